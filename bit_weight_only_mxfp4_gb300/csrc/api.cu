@@ -9,6 +9,7 @@
 #include "common.cuh"
 #include "launch.h"
 #include "layout.cuh"
+#include "paged.h"
 #include "tensor_map.h"
 
 namespace tt {
@@ -422,6 +423,130 @@ tt_status tt_gqa_decode_attention(const uint16_t* q_bf16, const uint16_t* k_cach
                             out_bf16, workspace, as_stream(stream), kPdl);
   if (e == cudaErrorInvalidConfiguration) return TT_ERR_UNSUPPORTED;
   return from_cuda(e);
+}
+
+namespace {
+
+// Checks a cache description and brings it into the kernels' form.
+tt_status check_paged_kv(const tt_paged_kv* kv, tt::PagedKv* out) {
+  if (!kv) return TT_ERR_NULL;
+  if (kv->type != TT_KV_BF16 && kv->type != TT_KV_FP8) return TT_ERR_SHAPE;
+  if (kv->num_pages < 1 || kv->kv_heads < 1 || kv->batch < 1 || kv->pages_per_seq < 1 ||
+      kv->head_dim < 1 || kv->page_size < 1)
+    return TT_ERR_SHAPE;
+  int shift = 4;
+  while (shift < 7 && (1 << shift) != kv->page_size) ++shift;
+  if ((1 << shift) != kv->page_size) return TT_ERR_UNSUPPORTED;
+  if (kv->head_dim != 64 && kv->head_dim != 128) return TT_ERR_UNSUPPORTED;
+  if (kv->kv_heads > tt::kGqaMaxKvHeads || kv->batch > tt::kPagedMaxBatch)
+    return TT_ERR_UNSUPPORTED;
+  // row and token numbers fit 32 bits
+  if (kv->num_pages > kMaxRows / kv->kv_heads / kv->page_size) return TT_ERR_UNSUPPORTED;
+  if (kv->pages_per_seq > kMaxRows / kv->page_size) return TT_ERR_UNSUPPORTED;
+  if (!kv->k || !kv->v || !kv->page_table || !kv->lens) return TT_ERR_NULL;
+  if (kv->type == TT_KV_FP8 && (!kv->k_scales || !kv->v_scales)) return TT_ERR_NULL;
+  if (!aligned(kv->k, 16) || !aligned(kv->v, 16) || !aligned(kv->page_table, 4) ||
+      !aligned(kv->lens, 4))
+    return TT_ERR_ALIGN;
+  if (kv->type == TT_KV_FP8 && (!aligned(kv->k_scales, 16) || !aligned(kv->v_scales, 16)))
+    return TT_ERR_ALIGN;
+  *out = tt::PagedKv{kv->k, kv->v, kv->k_scales, kv->v_scales, kv->page_table, kv->lens,
+                     int(kv->num_pages), shift, kv->kv_heads, kv->batch, kv->pages_per_seq};
+  return TT_OK;
+}
+
+tt_status check_paged_attention(const tt_paged_kv* kv, const tt::PagedAttnArgs& a,
+                                size_t ws_bytes, tt::PagedKv* out) {
+  if (tt_status st = check_paged_kv(kv, out)) return st;
+  if (a.heads < 1 || a.heads % kv->kv_heads != 0) return TT_ERR_SHAPE;
+  if (a.heads / kv->kv_heads > tt::kPagedMaxGroup) return TT_ERR_UNSUPPORTED;
+  if (!std::isfinite(a.scale) || !std::isfinite(a.softcap)) return TT_ERR_NONFINITE;
+  if (a.softcap < 0.f || a.window < 0) return TT_ERR_SHAPE;
+  if (a.q_stride % 8 != 0 || a.q_stride < int64_t(a.heads) * kv->head_dim) return TT_ERR_SHAPE;
+  if (a.tokens < 0 || a.tokens > kMaxRows / a.heads) return TT_ERR_SHAPE;
+  if (!a.q || !a.out || !a.ws) return TT_ERR_NULL;
+  if (ws_bytes < tt_paged_attention_workspace_bytes(a.heads, kv->kv_heads, kv->head_dim))
+    return TT_ERR_SIZE;
+  if (!aligned(a.q, 16) || !aligned(a.out, 16) || !aligned(a.ws, 16) || !aligned(a.lse, 4) ||
+      !aligned(a.slopes, 4) || !aligned(a.sinks, 4) || !aligned(a.prefix, 4) ||
+      !aligned(a.starts, 4))
+    return TT_ERR_ALIGN;
+  return TT_OK;
+}
+
+}  // namespace
+
+tt_status tt_rope_turns(const double* inv_freq, int32_t n, uint64_t* turns, void* stream) {
+  if (n < 1) return TT_ERR_SHAPE;
+  if (!inv_freq || !turns) return TT_ERR_NULL;
+  if (!aligned(inv_freq, 8) || !aligned(turns, 8)) return TT_ERR_ALIGN;
+  return from_cuda(tt::launch_rope_turns(inv_freq, n, turns, as_stream(stream)));
+}
+
+tt_status tt_paged_rope_append(const tt_paged_kv* kv, const uint16_t* q, const uint16_t* k,
+                               const uint16_t* v, int64_t q_stride, int64_t kv_stride,
+                               int64_t tokens, const int32_t* q_starts, int32_t heads,
+                               const uint64_t* turns, int32_t rot_dim, int32_t interleaved,
+                               const int32_t* positions, int32_t axes,
+                               const uint8_t* pair_axis, uint16_t* q_out, void* stream) {
+  tt::PagedKv c;
+  if (tt_status st = check_paged_kv(kv, &c)) return st;
+  const int64_t d = kv->head_dim;
+  if (heads < 0 || heads > kMaxRows / 256 || tokens < 0 || tokens > kMaxRows) return TT_ERR_SHAPE;
+  if (!q_starts && tokens != kv->batch) return TT_ERR_SHAPE;
+  if (kv_stride % 8 != 0 || kv_stride < kv->kv_heads * d) return TT_ERR_SHAPE;
+  if (heads > 0 && (q_stride % 8 != 0 || q_stride < heads * d)) return TT_ERR_SHAPE;
+  if (turns && (rot_dim % 16 != 0 || rot_dim < 16 || rot_dim > d)) return TT_ERR_SHAPE;
+  if (turns && (axes < 1 || axes > 4)) return TT_ERR_SHAPE;
+  if (turns && !positions && axes != 1) return TT_ERR_SHAPE;
+  if (!k || !v || (heads > 0 && (!q || !q_out))) return TT_ERR_NULL;
+  if (!aligned(k, 16) || !aligned(v, 16) ||
+      (heads > 0 && (!aligned(q, 16) || !aligned(q_out, 16))))
+    return TT_ERR_ALIGN;
+  if (!aligned(q_starts, 4) || !aligned(turns, 8) || !aligned(positions, 4)) return TT_ERR_ALIGN;
+  if (tokens == 0) return TT_OK;
+  const tt::RopeArgs rope{turns, rot_dim, interleaved != 0, positions, axes, pair_axis};
+  return from_cuda(tt::launch_paged_append(c, kv->head_dim, kv->type == TT_KV_FP8, q, k, v,
+                                           q_stride, kv_stride, tokens, q_starts, heads, rope,
+                                           q_out, as_stream(stream), kPdl));
+}
+
+size_t tt_paged_attention_workspace_bytes(int32_t heads, int32_t kv_heads, int32_t head_dim) {
+  if (heads < 1 || kv_heads < 1 || heads % kv_heads != 0) return 0;
+  if (head_dim != 64 && head_dim != 128) return 0;
+  if (heads / kv_heads > tt::kPagedMaxGroup || kv_heads > tt::kGqaMaxKvHeads) return 0;
+  const size_t a = tt::paged_decode_workspace_bytes(heads / kv_heads, head_dim);
+  const size_t b = tt::paged_prefill_workspace_bytes(head_dim);
+  return a > b ? a : b;
+}
+
+tt_status tt_paged_decode_attention(const tt_paged_kv* kv, const uint16_t* q, int64_t q_stride,
+                                    int32_t heads, float scale, float softcap, int32_t window,
+                                    const float* slopes, const float* sinks, uint16_t* out,
+                                    float* lse, void* workspace, size_t workspace_bytes,
+                                    void* stream) {
+  const tt::PagedAttnArgs a{q,      q_stride, nullptr, kv ? kv->batch : 0, heads, scale, softcap,
+                            window, slopes,   sinks,   nullptr,            out,   lse,   workspace};
+  tt::PagedKv c;
+  if (tt_status st = check_paged_attention(kv, a, workspace_bytes, &c)) return st;
+  return from_cuda(tt::launch_paged_decode(c, kv->head_dim, kv->type == TT_KV_FP8, a,
+                                           as_stream(stream), kPdl));
+}
+
+tt_status tt_paged_prefill_attention(const tt_paged_kv* kv, const uint16_t* q, int64_t q_stride,
+                                     const int32_t* q_starts, int64_t tokens, int32_t heads,
+                                     float scale, float softcap, int32_t window,
+                                     const float* slopes, const float* sinks,
+                                     const int32_t* prefix, uint16_t* out, float* lse,
+                                     void* workspace, size_t workspace_bytes, void* stream) {
+  const tt::PagedAttnArgs a{q,      q_stride, q_starts, tokens, heads, scale, softcap,
+                            window, slopes,   sinks,    prefix, out,   lse,   workspace};
+  tt::PagedKv c;
+  if (tt_status st = check_paged_attention(kv, a, workspace_bytes, &c)) return st;
+  if (!q_starts) return TT_ERR_NULL;
+  if (tokens == 0) return TT_OK;
+  return from_cuda(tt::launch_paged_prefill(c, kv->head_dim, kv->type == TT_KV_FP8, a,
+                                            as_stream(stream), kPdl));
 }
 
 size_t tt_lowbit_matrix_bytes(int32_t bits, int64_t n, int64_t k) {

@@ -60,3 +60,40 @@ def moe_expert_from_f32(w_gate_up: torch.Tensor, w_down: torch.Tensor):
     dn = torch.empty(nbytes, dtype=torch.uint8, device=w_down.device)
     thinmx.tt_mxfp4_pack_rows(dc, ds, hidden, inter, dn, nbytes)
     return gu, dn
+
+
+def paged_kv(k: torch.Tensor, v: torch.Tensor, page_table: torch.Tensor, lens: torch.Tensor,
+             k_scales: torch.Tensor | None = None, v_scales: torch.Tensor | None = None):
+    """The cache description the paged entry points take: k, v
+    [pages, kv_heads, page_size, head_dim] in bf16, or in float8_e4m3fn / uint8
+    codes with fp32 scales [pages, kv_heads, page_size]; page_table int32
+    [batch, pages_per_seq]; lens int32 [batch].  It keeps its tensors alive;
+    it is made once, and later steps write into page_table and lens."""
+    fp8 = k_scales is not None
+    for t in (k, v, page_table, lens, k_scales, v_scales):
+        assert t is None or (t.is_cuda and t.is_contiguous())
+    assert k.shape == v.shape and k.dtype == v.dtype and k.element_size() == (1 if fp8 else 2)
+    assert (v_scales is not None) == fp8
+    pages, kv_heads, page_size, head_dim = k.shape
+    assert page_table.dtype == lens.dtype == torch.int32
+    batch, width = page_table.shape
+    assert lens.shape == (batch,)
+    if fp8:
+        assert k_scales.shape == v_scales.shape == (pages, kv_heads, page_size)
+        assert k_scales.dtype == v_scales.dtype == torch.float32
+    kv = thinmx.tt_paged_kv(
+        k.data_ptr(), v.data_ptr(), k_scales.data_ptr() if fp8 else None,
+        v_scales.data_ptr() if fp8 else None, page_table.data_ptr(), lens.data_ptr(), pages,
+        thinmx.TT_KV_FP8 if fp8 else thinmx.TT_KV_BF16, page_size, kv_heads, head_dim, batch,
+        width)
+    kv.tensors = (k, v, page_table, lens, k_scales, v_scales)
+    return kv
+
+
+def rope_turns(inv_freq: torch.Tensor) -> torch.Tensor:
+    """Rotation frequencies, fp64 [n] in radians per position -> the table
+    tt_paged_rope_append takes."""
+    assert inv_freq.is_cuda and inv_freq.dtype == torch.float64 and inv_freq.is_contiguous()
+    turns = torch.empty(inv_freq.numel(), dtype=torch.int64, device=inv_freq.device)
+    thinmx.tt_rope_turns(inv_freq, inv_freq.numel(), turns)
+    return turns

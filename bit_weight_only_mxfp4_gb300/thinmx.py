@@ -63,7 +63,29 @@ SIGNATURES = {
     "tt_gqa_decode_workspace_bytes": (_SZ, [_I32, _I32, _I32]),
     "tt_gqa_decode_attention": (ctypes.c_int, [_P, _P, _P, _I32, _I32, _I32, _I64, _I64,
                                                 ctypes.c_float, _P, _P, _SZ, _P]),
+    "tt_rope_turns": (ctypes.c_int, [_P, _I32, _P, _P]),
+    "tt_paged_rope_append": (ctypes.c_int, [_P, _P, _P, _P, _I64, _I64, _I64, _P, _I32, _P, _I32,
+                                             _I32, _P, _I32, _P, _P, _P]),
+    "tt_paged_attention_workspace_bytes": (_SZ, [_I32, _I32, _I32]),
+    "tt_paged_decode_attention": (ctypes.c_int, [_P, _P, _I64, _I32, ctypes.c_float,
+                                                  ctypes.c_float, _I32, _P, _P, _P, _P, _P, _SZ,
+                                                  _P]),
+    "tt_paged_prefill_attention": (ctypes.c_int, [_P, _P, _I64, _P, _I64, _I32, ctypes.c_float,
+                                                   ctypes.c_float, _I32, _P, _P, _P, _P, _P, _P,
+                                                   _SZ, _P]),
 }
+
+
+TT_KV_BF16 = 0
+TT_KV_FP8 = 1
+
+
+class tt_paged_kv(ctypes.Structure):
+    """The paged key-value cache of one layer and the sequences of a step
+    (include/thinmx.h); loader.paged_kv fills one from tensors."""
+    _fields_ = [("k", _P), ("v", _P), ("k_scales", _P), ("v_scales", _P), ("page_table", _P),
+                ("lens", _P), ("num_pages", _I64), ("type", _I32), ("page_size", _I32),
+                ("kv_heads", _I32), ("head_dim", _I32), ("batch", _I32), ("pages_per_seq", _I32)]
 
 
 class ThinmxError(RuntimeError):
@@ -263,6 +285,43 @@ def tt_gqa_decode_attention(q_bf16, k_cache, v_cache, heads, kv_heads, head_dim,
     _check("tt_gqa_decode_attention", load().tt_gqa_decode_attention(
         _ptr(q_bf16), _ptr(k_cache), _ptr(v_cache), heads, kv_heads, head_dim, cap, length,
         float(scale), _ptr(out_bf16), _ptr(workspace), workspace_bytes, _stream(stream)))
+
+
+def tt_rope_turns(inv_freq, n, turns, stream=None):
+    _check("tt_rope_turns", load().tt_rope_turns(_ptr(inv_freq), n, _ptr(turns), _stream(stream)))
+
+
+def _kv(kv):
+    """Address of a tt_paged_kv (whose tensors the caller keeps alive)."""
+    return None if kv is None else ctypes.addressof(kv)
+
+
+def tt_paged_rope_append(kv, q, k, v, q_stride, kv_stride, tokens, q_starts, heads, turns, rot_dim,
+                         interleaved, positions, axes, pair_axis, q_out, stream=None):
+    _check("tt_paged_rope_append", load().tt_paged_rope_append(
+        _kv(kv), _ptr(q), _ptr(k), _ptr(v), q_stride, kv_stride, tokens, _ptr(q_starts), heads,
+        _ptr(turns), rot_dim, interleaved, _ptr(positions), axes, _ptr(pair_axis), _ptr(q_out),
+        _stream(stream)))
+
+
+def tt_paged_attention_workspace_bytes(heads, kv_heads, head_dim) -> int:
+    return int(load().tt_paged_attention_workspace_bytes(heads, kv_heads, head_dim))
+
+
+def tt_paged_decode_attention(kv, q, q_stride, heads, scale, softcap, window, slopes, sinks, out,
+                              lse, workspace, workspace_bytes, stream=None):
+    _check("tt_paged_decode_attention", load().tt_paged_decode_attention(
+        _kv(kv), _ptr(q), q_stride, heads, scale, softcap, window, _ptr(slopes), _ptr(sinks),
+        _ptr(out), _ptr(lse), _ptr(workspace), workspace_bytes, _stream(stream)))
+
+
+def tt_paged_prefill_attention(kv, q, q_stride, q_starts, tokens, heads, scale, softcap, window,
+                               slopes, sinks, prefix, out, lse, workspace, workspace_bytes,
+                               stream=None):
+    _check("tt_paged_prefill_attention", load().tt_paged_prefill_attention(
+        _kv(kv), _ptr(q), q_stride, _ptr(q_starts), tokens, heads, scale, softcap, window,
+        _ptr(slopes), _ptr(sinks), _ptr(prefix), _ptr(out), _ptr(lse), _ptr(workspace),
+        workspace_bytes, _stream(stream)))
 
 
 def tt_lowbit_matrix_bytes(bits, n, k) -> int:

@@ -10,6 +10,8 @@
  *   - bf16 gate/up SwiGLU matvec for the layers kept in bf16;
  *   - FP8 (E4M3, one scale per row) matvec and gate/up SwiGLU matvec;
  *   - single-token grouped-query attention over a bf16 KV cache;
+ *   - the paged KV cache (bf16 or FP8): append with position rotation,
+ *     attention of one or of several new tokens per sequence;
  *   - the MoE layer with Q1 / Q2 packed low-bit experts.
  *
  * Sources.  The method is the ThinTensor decode runtime's:
@@ -402,6 +404,129 @@ tt_status tt_gqa_decode_attention(const uint16_t* q_bf16, const uint16_t* k_cach
                                   int32_t head_dim, int64_t cap, int64_t len, float scale,
                                   uint16_t* out_bf16, void* workspace, size_t workspace_bytes,
                                   void* stream);
+
+/* ------------------------------------------------------------------------
+ * Paged key-value cache: append with position rotation, attention of one new
+ * token per sequence, attention of several new tokens per sequence.
+ *
+ * A tt_paged_kv (host memory, read during the call) describes the cache of
+ * one layer and the sequences of a step:
+ *   k, v        [num_pages][kv_heads][page_size][head_dim], bf16 (TT_KV_BF16)
+ *               or E4M3 codes (TT_KV_FP8);
+ *   k_scales, v_scales  TT_KV_FP8: fp32 [num_pages][kv_heads][page_size], one
+ *               scale per token and kv head (value = code * scale); else NULL;
+ *   page_table  int32 [batch][pages_per_seq]: token t of sequence b is row
+ *               t % page_size of page page_table[b][t / page_size].  A
+ *               negative entry is a hole: its tokens are masked in attention
+ *               and dropped by the append;
+ *   lens        int32 [batch]: tokens of each sequence, the step's new ones
+ *               included; 0 = an empty place of the batch.
+ * The step's new tokens are the last ones of their sequence.  q_starts NULL:
+ * one per sequence (flat token b belongs to sequence b); else int32
+ * [batch + 1] ascending: flat tokens q_starts[b] .. q_starts[b + 1] - 1
+ * belong to sequence b (flat tokens that no sequence has are ignored: their
+ * rows of the outputs are left as they are).
+ * With n_b new tokens, the i-th has the place p = lens[b] - n_b + i.
+ * A page number >= num_pages, or a length outside the table, is reported as
+ * TT_ERR_SHAPE in the device error word and treated as a hole (the length
+ * is clamped): nothing outside the pool is touched.  page_table, lens and
+ * q_starts are read after the call waits for the preceding kernel.
+ * Requires page_size 16, 32, 64 or 128; head_dim 64 or 128; kv_heads <= 64;
+ * batch <= 1024; num_pages * kv_heads * page_size and pages_per_seq *
+ * page_size <= 2^31 - 1 (else TT_ERR_UNSUPPORTED).  k, v and scales 16-byte
+ * aligned, int32 arrays 4-byte.
+ * --------------------------------------------------------------------- */
+#define TT_KV_BF16 0
+#define TT_KV_FP8 1
+#define TT_PAGED_MAX_BATCH 1024
+
+typedef struct {
+    void* k;
+    void* v;
+    float* k_scales;
+    float* v_scales;
+    const int32_t* page_table;
+    const int32_t* lens;
+    int64_t num_pages;
+    int32_t type;          /* TT_KV_BF16 or TT_KV_FP8 */
+    int32_t page_size;
+    int32_t kv_heads;
+    int32_t head_dim;
+    int32_t batch;
+    int32_t pages_per_seq;
+} tt_paged_kv;
+
+/* turns[i] = round(inv_freq[i] / 2 pi * 2^64) mod 2^64: the rotation
+   frequencies as fixed-point fractions of a turn, so that the phase of any
+   32-bit position is one exact integer product.  inv_freq fp64 [n], in
+   radians per position (scaled as the model wants it); turns uint64 [n].
+   Setup step. */
+tt_status tt_rope_turns(const double* inv_freq, int32_t n, uint64_t* turns, void* stream);
+
+/* Rotates the step's queries and keys and appends its keys and values.
+ *   pair i < rot_dim / 2 of a head: elements (i, i + rot_dim / 2), or
+ *   (2i, 2i + 1) if interleaved;  a = pos_i * inv_freq[i];
+ *   (x, y) -> (x cos a - y sin a, x sin a + y cos a);  the rest passes.
+ *   pos_i = p (the token's place) if positions is NULL, else
+ *   positions[pair_axis[i]][token] (int32 [axes][tokens]; several axes: time,
+ *   height, width; pair_axis uint8 [rot_dim / 2], NULL = axis 0).
+ *   q_out[token] = bf16_rne(rotated q)  [tokens][heads][head_dim];
+ *   cache row of the token = rotated k, and v: bf16_rne, or E4M3 with
+ *   scale = fp32(amax / 448) and code = e4m3_rne(x / scale), amax over the
+ *   unrounded row (an all-zero row: scale 0; a row with NaN or infinity:
+ *   scale NaN, codes 0).
+ * q, k, v: bf16, row of token t at t * stride elements (q_stride for q,
+ * kv_stride for k and v), heads contiguous within a row: slices of one fused
+ * QKV output will do.  heads = 0: no queries (q, q_out NULL).  turns NULL: no
+ * rotation.  A token whose place is negative (lens[b] < n_b) is not
+ * appended and its q_out row is zero.  A page table that lists one page
+ * twice makes two tokens share its rows (then either may win).
+ * q_out may be q itself when q_stride is heads * head_dim.
+ * Requires rot_dim % 16 == 0, 16 <= rot_dim <= head_dim, 1 <= axes <= 4,
+ * strides % 8 == 0 and at least a row, tokens >= 0 (== batch if q_starts is
+ * NULL); bf16 pointers 16-byte aligned. */
+tt_status tt_paged_rope_append(const tt_paged_kv* kv, const uint16_t* q, const uint16_t* k,
+                               const uint16_t* v, int64_t q_stride, int64_t kv_stride,
+                               int64_t tokens, const int32_t* q_starts, int32_t heads,
+                               const uint64_t* turns, int32_t rot_dim, int32_t interleaved,
+                               const int32_t* positions, int32_t axes,
+                               const uint8_t* pair_axis, uint16_t* q_out, void* stream);
+
+/* Attention of one new token per sequence (p = lens[b] - 1) over its pages.
+ *   j = h / (heads / kv_heads);  for the visible keys t of sequence b
+ *   (t <= p; t > p - window if window > 0; no hole):
+ *   z[h][t] = f(scale * q[b][h] . k[j][t]) + slopes[h] * (t - p),
+ *             f(s) = softcap * tanh(s / softcap) if softcap > 0, else s
+ *   out[b][h] = bf16_rne( sum_t e^z v[j][t] / (sum_t e^z + e^sinks[h]) )
+ *   lse[b][h] = log(sum_t e^z + e^sinks[h])
+ * slopes, sinks: fp32 [heads] or NULL (no bias; no sink).  lse fp32
+ * [batch][heads] or NULL.  A token that sees no key: out 0, lse = sinks[h]
+ * (-inf without sinks).  q: row of sequence b at b * q_stride elements; out
+ * [batch][heads][head_dim].
+ * Requires heads a multiple of kv_heads, heads / kv_heads <= 16, scale and
+ * softcap finite, softcap >= 0, window >= 0, q_stride % 8 == 0.
+ * workspace: device, >= tt_paged_attention_workspace_bytes(...) bytes,
+ * zero-filled once before its first use; each call leaves it ready for the
+ * next, whatever its sizes.  Calls that share one must be ordered on one
+ * stream.  After a TT_ERR_TIMEOUT zero it again. */
+size_t tt_paged_attention_workspace_bytes(int32_t heads, int32_t kv_heads, int32_t head_dim);
+tt_status tt_paged_decode_attention(const tt_paged_kv* kv, const uint16_t* q, int64_t q_stride,
+                                    int32_t heads, float scale, float softcap, int32_t window,
+                                    const float* slopes, const float* sinks, uint16_t* out,
+                                    float* lse, void* workspace, size_t workspace_bytes,
+                                    void* stream);
+
+/* The same for the new tokens of q_starts (required): each sees the keys
+ * t <= p, and also t < prefix[b] (int32 [batch] or NULL: the part of a
+ * sequence that its tokens see whole), t < lens[b], within the window.
+ * q rows at token * q_stride; out [tokens][heads][head_dim], lse
+ * [tokens][heads].  A token with p < 0 sees nothing. */
+tt_status tt_paged_prefill_attention(const tt_paged_kv* kv, const uint16_t* q, int64_t q_stride,
+                                     const int32_t* q_starts, int64_t tokens, int32_t heads,
+                                     float scale, float softcap, int32_t window,
+                                     const float* slopes, const float* sinks,
+                                     const int32_t* prefix, uint16_t* out, float* lse,
+                                     void* workspace, size_t workspace_bytes, void* stream);
 
 /* ------------------------------------------------------------------------
  * Q1 / Q2 packed low-bit experts  [SHIP 97.87 tok/s notes:
