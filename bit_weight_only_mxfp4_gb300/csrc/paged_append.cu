@@ -28,6 +28,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr uint32_t kAll = 0xffffffffu;
+constexpr int64_t kNowhere = INT64_MIN;  // the place of a token that no sequence has
 
 __global__ void rope_turns_kernel(const double* __restrict__ inv_freq, int n,
                                   uint64_t* __restrict__ turns) {
@@ -111,7 +112,7 @@ __global__ void __launch_bounds__(kThreads)
     int64_t place = int64_t(len) - 1;
     if (a.starts) {
       const int64_t s0 = __ldcg(a.starts + b), s1 = __ldcg(a.starts + b + 1);
-      place = t >= s0 && t < s1 ? len - (s1 - t) : -2;  // -2: no sequence has this token
+      place = t >= s0 && t < s1 ? len - (s1 - t) : kNowhere;
     }
     const int page = place >= 0 ? paged_page(kv, b, place, e) : -1;
     if (lane == 0) {
@@ -122,7 +123,7 @@ __global__ void __launch_bounds__(kThreads)
   __syncthreads();
   const int64_t place = s_place;
   const int page = s_page;
-  if (place == -2) return;
+  if (place == kNowhere) return;
   for (int i = tid; i < half; i += kThreads) {
     int64_t pos = place;
     if (a.rope.positions) {
