@@ -1,0 +1,1011 @@
+// Attention of one new token per sequence over the paged cache.
+//
+//   z[h][t] = f(scale * q[h] . k[j][t]) + slope[h] * (t - p),  j = h / G
+//   out[h]  = sum_t e^z v[j][t] / (sum_t e^z + e^sink[h])
+//
+// over the visible tokens t of each sequence, G = heads / kv_heads query
+// heads per kv head.  Every K and V row is needed once, for its G heads, so
+// the work is bound by the cache's bytes: the kernel is built to keep the
+// pages streaming.
+//
+// Split.  A sequence's tokens are cut into tiles (64 or 128 tokens); all
+// tiles of all (sequence, kv head) pairs form one line, and CTA c of the
+// C = min(SMs, tiles) takes the c-th C-th of it, whatever the lengths are:
+// no SM has more than one tile more than another, and the host needs to know
+// no length (the same launch serves a graph whose lengths grow).  A pair
+// whose tiles lie in several CTAs is joined by the last of them to finish
+// (a counter in the workspace), from the parts in CTA order, so that the
+// result does not depend on who comes last.
+//
+// Inside a CTA one warp issues the copies: per page and tile one TMA box of
+// K and one of V, straight into the swizzled layout that the fragment loads
+// read without bank conflicts; the ring spans pair boundaries, so the copies
+// run on while a pair is finished.  Two groups of four warps take the tiles
+// in turn, 16 (or 2 x 16) tokens a warp, each with its own running maximum,
+// sum and output; a pair's end joins them in shared memory.
+//
+// Products, on mma.sync m16n8k16 with the tokens (or dims) as the 16 rows and
+// the heads as the 8 columns, so that up to 8 heads fill it:
+//   S[token][head]  = K Q^T     O^T[dim][head] += V^T P^T
+// The order of the dims inside a contraction is free as long as both sides
+// agree, so K fragments are 16-byte pieces of the rows, and V^T fragments
+// are byte permutes of 16-byte pieces of two rows; P moves from the score
+// fragment to the B operand by a transposing movmatrix.  (tcgen05 would need
+// 128 rows of queries for a product of at most 16, and K and V would pass
+// shared memory all the same.)
+//   bf16: exact products; P as bf16 high + low parts (2^-16), since a decode
+//     step's output should not lose to the cache's own precision.
+//   FP8: codes become f16 exactly; q becomes f16 after an exact power-of-two
+//     prescale per head (its elements keep 11 bits down to 2^-29 of the
+//     largest); the scales multiply scores and weights in 32 bits; P * scale
+//     is rounded once to f16 (2^-11, against 2^-4 for a code), in units of
+//     the power of two of the largest scale so far, so that it is at most 2.
+#include <cmath>
+#include <type_traits>
+
+#include "launch.h"
+#include "paged.cuh"
+#include "tensor_map.h"
+
+namespace tt {
+namespace {
+
+constexpr uint32_t kFull = 0xffffffffu;
+constexpr int kGroups = 2;                    // tiles in work at once
+constexpr int kGroupWarps = 4;
+constexpr int kConsumers = kGroups * kGroupWarps * 32;
+constexpr int kThreads = kConsumers + 32;     // + the copying warp
+constexpr int kMaxCtas = 1024;                // counters in the workspace
+constexpr int kSmemMax = 220 * 1024;
+constexpr int kConsumerBar = 1;
+
+template <int D, int NH, bool FP8>
+struct Plan {
+  static constexpr int kEs = FP8 ? 1 : 2;
+  static constexpr int kRow = D * kEs;                    // bytes of a cache row
+  static constexpr int kBoxRow = kRow < 128 ? kRow : 128; // bytes of a box row (the swizzle span)
+  // 16-token chunks per warp and tile: 32 KB of K and V a tile, or 16 KB
+  // where the rows are 64 bytes
+  static constexpr int kTm = kRow == 256 ? 1 : 2;
+  static constexpr int kTok = 16 * kGroupWarps * kTm;
+  static constexpr int kPart = kTok * kRow;               // K (or V) bytes of a tile
+  static constexpr int kStage = 2 * kPart + (FP8 ? 2 * kTok * 4 : 0);
+  static constexpr int kSlot = 8 * NH * (D + 2);          // floats of one warp's part
+  static constexpr int kScratch = kGroupWarps * kSlot * 4;
+  static constexpr int kFixed = 1024 + kScratch + (kPagedMaxBatch + 1) * 8 + kPagedMaxBatch * 4 +
+                                512;  // alignment, parts, line, barriers
+  static constexpr int kRaw = (kSmemMax - kFixed) / kStage;
+  static constexpr int kStages = kRaw > 12 ? 12 : kRaw;
+  static constexpr int kSmem = kFixed + kStages * kStage;
+  static_assert(kStages >= 3, "ring");
+  static_assert(kStage % 1024 == 0, "swizzled boxes start on 1024 bytes");
+};
+
+// Floats of one CTA part: O [G][D], max [G], sum [G], padded to 16 bytes.
+__host__ __device__ constexpr int part_floats(int G, int D) { return (G * (D + 2) + 3) & ~3; }
+
+struct DecodeArgs {
+  const uint16_t* q;
+  int64_t q_stride;
+  int group;
+  float scale, softcap;
+  int window;
+  const float* slopes;
+  const float* sinks;
+  uint16_t* out;
+  float* lse;
+  int32_t* counters;
+  float* parts;
+  int32_t* err;
+};
+
+template <bool FP8>
+__device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                         uint32_t a3, uint32_t b0, uint32_t b1) {
+  if constexpr (FP8)
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
+        "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+  else
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 "
+        "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+  return r;
+}
+
+__device__ __forceinline__ uint32_t bf16x2(float a, float b) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ uint32_t f16x2(float a, float b) {
+  const __half2 h = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+// Four E4M3 codes -> two f16x2 (exact).
+__device__ __forceinline__ void e4m3x4(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(w));
+}
+__device__ __forceinline__ uint32_t word(const uint4& v, int i) {
+  return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
+}
+__device__ __forceinline__ uint32_t halves(uint32_t a, uint32_t b, int h) {
+  return __byte_perm(a, b, h ? 0x7632 : 0x5410);
+}
+
+__device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap* map, int row,
+                                        uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(row), "r"(0), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void bulk_copy(uint32_t dst, const void* src, uint32_t bytes,
+                                          uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cta.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+          dst),
+      "l"(src), "r"(bytes), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void consumer_sync() {
+  asm volatile("bar.sync %0, %1;" ::"r"(kConsumerBar), "r"(kConsumers) : "memory");
+}
+
+// The barrier, and whether any of its threads says so.
+__device__ __forceinline__ bool consumer_any(bool p) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
+      "barrier.cta.red.or.pred q, %2, %3, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(uint32_t(p)), "r"(kConsumerBar), "r"(kConsumers)
+      : "memory");
+  return r != 0;
+}
+
+// The line of tiles: sequence b has nt(b) tiles from tile t0(b) on for each
+// kv head; prefix[b] counts the tiles before it over all kv heads.
+struct Line {
+  const int64_t* prefix;
+  const int32_t* len;
+  int kv_heads, window, tok;
+  __device__ __forceinline__ int first_tile(int b) const {
+    const int n = len[b];
+    return window > 0 && n > window ? (n - window) / tok : 0;
+  }
+  __device__ __forceinline__ int tiles(int b) const {
+    const int n = len[b];
+    return n == 0 ? 0 : (n + tok - 1) / tok - first_tile(b);
+  }
+};
+
+// Where a CTA stands on the line.
+struct At {
+  int b, j, tile;  // tile counted from the pair's first
+};
+__device__ __forceinline__ At find(const Line& L, int batch, int64_t item) {
+  int lo = 0, hi = batch;  // the last b with prefix[b] <= item and tiles
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (L.prefix[mid] <= item) lo = mid; else hi = mid;
+  }
+  const int64_t rem = item - L.prefix[lo];
+  const int nt = L.tiles(lo);
+  return {lo, int(rem / nt), int(rem % nt)};
+}
+
+template <int D, int NH, bool FP8>
+__global__ void __launch_bounds__(kThreads, 1)
+    paged_decode_kernel(const __grid_constant__ CUtensorMap map_k,
+                        const __grid_constant__ CUtensorMap map_v, const PagedKv kv,
+                        const DecodeArgs a) {
+  using P = Plan<D, NH, FP8>;
+  constexpr int kTok = P::kTok, kTm = P::kTm;
+  extern __shared__ __align__(128) uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+  uint8_t* ring = smem;
+  float* scratch = reinterpret_cast<float*>(smem + P::kStages * P::kStage);
+  int64_t* prefix = reinterpret_cast<int64_t*>(scratch + P::kScratch / 4);
+  int32_t* slen = reinterpret_cast<int32_t*>(prefix + kPagedMaxBatch + 1);
+  uint64_t* full = reinterpret_cast<uint64_t*>(slen + kPagedMaxBatch);
+  uint64_t* empty = full + P::kStages;
+  uint32_t* mask = reinterpret_cast<uint32_t*>(empty + P::kStages);  // boxes present, per stage
+  int* flags = reinterpret_cast<int*>(mask + P::kStages);  // [0] last to finish, [1] gave up
+  int64_t* wsum = reinterpret_cast<int64_t*>(scratch);  // scan partials, before the main loop
+
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (tid == 0) {
+    for (int i = 0; i < P::kStages; ++i) {
+      mbar_init(smem_u32(&full[i]), 1);
+      mbar_init(smem_u32(&empty[i]), kGroupWarps);
+    }
+    flags[1] = 0;
+    fence_mbar_init();
+  }
+  pdl_allow_next_grid();
+  pdl_wait_prior_grid();
+
+  // ---- the line: lengths and the exclusive scan of the tiles
+  const Line L{prefix, slen, kv.kv_heads, a.window, kTok};
+  {
+    constexpr int kPer = (kPagedMaxBatch + kThreads - 1) / kThreads;
+    int64_t mine[kPer], sum = 0;
+    const int per = (kv.batch + kThreads - 1) / kThreads;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int b = tid * per + i;
+      mine[i] = 0;
+      if (i < per && b < kv.batch) {
+        slen[b] = paged_len(kv, b, blockIdx.x == 0 ? a.err : nullptr);
+        mine[i] = int64_t(L.tiles(b)) * kv.kv_heads;
+      }
+      sum += mine[i];
+    }
+    int64_t run = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t v = __shfl_up_sync(kFull, run, o);
+      if (lane >= o) run += v;
+    }
+    if (lane == 31) wsum[warp] = run;
+    __syncthreads();
+    int64_t base = run - sum;
+    for (int w = 0; w < warp; ++w) base += wsum[w];
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int b = tid * per + i;
+      if (i < per && b < kv.batch) prefix[b] = base;
+      base += mine[i];
+    }
+    if (tid == kThreads - 1) prefix[kv.batch] = base;
+    __syncthreads();
+  }
+  const int64_t T = prefix[kv.batch];
+  const int64_t C = T < gridDim.x ? T : gridDim.x;
+  const int64_t i0 = blockIdx.x < C ? T * blockIdx.x / C : 0;
+  const int64_t i1 = blockIdx.x < C ? T * (blockIdx.x + 1) / C : 0;
+  const int G = a.group, heads = G * kv.kv_heads;
+
+  if (warp == kGroups * kGroupWarps) {
+    // ================================================== the copying warp
+    if (i0 >= i1) return;
+    const int ps = 1 << kv.page_shift;
+    const int br = ps < kTok ? ps : kTok;  // rows of a box
+    const int nb = kTok / br;              // boxes of K (and of V) a tile
+    At at = find(L, kv.batch, i0);
+    int page = -1, t = 0;
+    auto look = [&](const At& w) {  // this lane's box of the tile: its page, or -1
+      t = (L.first_tile(w.b) + w.tile) * kTok + lane * br;
+      const int n = slen[w.b];
+      // boxes wholly before the window or past the length are not copied
+      const bool in = lane < nb && t < n && (a.window == 0 || t + br > n - a.window);
+      page = in ? paged_page(kv, w.b, t, a.err) : -1;
+    };
+    look(at);
+    for (int64_t it = i0; it < i1; ++it) {
+      const int idx = int(it - i0), st = idx % P::kStages;
+      const uint32_t bar = smem_u32(&full[st]);
+      const int my_page = page, my_t = t;
+      const int j = at.j;
+      // the next tile's pages, while this stage is awaited
+      if (++at.tile == L.tiles(at.b)) {
+        at.tile = 0;
+        if (++at.j == kv.kv_heads) {
+          at.j = 0;
+          do ++at.b;
+          while (at.b < kv.batch && L.tiles(at.b) == 0);
+        }
+      }
+      if (it + 1 < i1) look(at);
+      bool ok = true;
+      if (idx >= P::kStages)
+        ok = mbar_wait_bounded(smem_u32(&empty[st]), uint32_t((idx / P::kStages - 1) & 1));
+      if (!__all_sync(kFull, ok) || *static_cast<volatile int*>(&flags[1])) {
+        // gave up: the copies in flight land before the CTA may end
+        if (lane == 0) {
+          flag_error(a.err, kErrTimeout);
+          *static_cast<volatile int*>(&flags[1]) = 1;
+        }
+        for (int i = 1; i <= P::kStages && i <= idx; ++i)
+          (void)mbar_wait_bounded(smem_u32(&full[(idx - i) % P::kStages]),
+                                  uint32_t(((idx - i) / P::kStages) & 1));
+        return;
+      }
+      const uint32_t have = __ballot_sync(kFull, my_page >= 0);
+      if (lane == 0) {
+        mask[st] = have;
+        const uint32_t box = uint32_t(br) * (2 * P::kRow + (FP8 ? 8 : 0));
+        mbar_arrive_expect_tx(bar, __popc(have) * box);
+      }
+      __syncwarp();
+      if (my_page >= 0) {
+        const int64_t row = paged_row(kv, my_page, j, my_t);
+        const uint32_t base = smem_u32(ring + st * P::kStage);
+        // a box of both halves of 256-byte rows is [half][row][128 bytes]:
+        // the halves of a tile's boxes lie box by box
+        const uint32_t off = uint32_t(lane) * br * P::kRow;
+        tma_box(base + off, &map_k, int(row), bar);
+        tma_box(base + P::kPart + off, &map_v, int(row), bar);
+        if constexpr (FP8) {
+          const uint32_t so = base + 2 * P::kPart + uint32_t(lane) * br * 4;
+          bulk_copy(so, kv.k_scales + row, br * 4, bar);
+          bulk_copy(so + kTok * 4, kv.v_scales + row, br * 4, bar);
+        }
+      }
+    }
+    return;
+  }
+
+  // ==================================================== the computing warps
+  // sequences without a visible token: no tiles, but rows to write
+  for (int b = blockIdx.x; b < kv.batch; b += gridDim.x)
+    if (L.tiles(b) == 0)
+      for (int e = tid; e < heads * D / 8; e += kConsumers) {
+        reinterpret_cast<uint4*>(a.out + int64_t(b) * heads * D)[e] = make_uint4(0u, 0u, 0u, 0u);
+        if (a.lse && e < heads)
+          a.lse[int64_t(b) * heads + e] = a.sinks ? __ldcg(a.sinks + e) : -INFINITY;
+      }
+  if (i0 >= i1) return;
+  const int g = lane >> 2, qd = lane & 3;
+  const int grp = warp / kGroupWarps, gw = warp % kGroupWarps;
+  const int ps = 1 << kv.page_shift;
+  const int br_shift = ps < kTok ? kv.page_shift : (kTok == 64 ? 6 : 7);
+  constexpr int KP = P::kRow / 64;  // 16-byte pieces of a row per lane in the score product
+  constexpr int QR = D / 8;         // registers of q per lane and head tile
+  constexpr int MT = D / 16;        // 16-dim tiles of the output
+  const float inv_cap = a.softcap > 0.f ? 1.f / a.softcap : 0.f;
+  const bool plain = !(a.softcap > 0.f) && !a.slopes;
+
+  At at = find(L, kv.batch, i0);
+  for (int64_t it = i0; it < i1;) {
+    const int b = at.b, j = at.j, nt = L.tiles(b), k0 = at.tile;
+    const int here = int(i1 - it < nt - k0 ? i1 - it : nt - k0);
+    const int n = slen[b];
+    const int lo = a.window > 0 && n > a.window ? n - a.window : 0;
+    const int tok0 = L.first_tile(b) * kTok;
+
+    // ---- Q^T fragments: head g + 8 nh, the dims of this lane's pieces
+    uint32_t qf[NH][QR];
+    float fac[NH][2], slope[NH][2];  // heads 8 nh + 2 qd + {0, 1}
+#pragma unroll
+    for (int nh = 0; nh < NH; ++nh) {
+      const int h = g + 8 * nh;
+      const uint16_t* qp = a.q + int64_t(b) * a.q_stride + (int64_t(j) * G + (h < G ? h : 0)) * D;
+      if constexpr (FP8) {
+        float m = 0.f;
+        uint4 v[KP][2];
+#pragma unroll
+        for (int c = 0; c < KP; ++c) {
+          const int piece = D == 128 ? 2 * qd + c : qd;
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            v[c][e] = h < G ? __ldcg(reinterpret_cast<const uint4*>(qp + 16 * piece) + e)
+                            : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              m = fmaxf(m, fmaxf(fabsf(bf16_bits_to_f32(word(v[c][e], i) & 0xffffu)),
+                                 fabsf(bf16_bits_to_f32(word(v[c][e], i) >> 16))));
+          }
+        }
+        m = fmaxf(m, __shfl_xor_sync(kFull, m, 1));
+        m = fmaxf(m, __shfl_xor_sync(kFull, m, 2));
+        // 2^ex stays a normal number; a row whose largest element is below
+        // 2^-112 is brought up less far
+        const int ex = min(f16_prescale_exponent(m), 126);
+        const float up = __int_as_float((127 + ex) << 23);
+#pragma unroll
+        for (int c = 0; c < KP; ++c)
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              qf[nh][8 * c + 4 * e + i] =
+                  pack_f16x2_scaled(bf16_bits_to_f32(word(v[c][e], i) & 0xffffu),
+                                    bf16_bits_to_f32(word(v[c][e], i) >> 16), up);
+        const float down = __int_as_float((127 - ex) << 23);
+        fac[nh][0] = a.scale * __shfl_sync(kFull, down, 8 * qd);
+        fac[nh][1] = a.scale * __shfl_sync(kFull, down, 8 * qd + 4);
+      } else {
+#pragma unroll
+        for (int c = 0; c < KP; ++c) {
+          const int piece = 8 * (c >> 1) + 2 * qd + (c & 1);
+          const uint4 v = h < G ? __ldcg(reinterpret_cast<const uint4*>(qp) + piece)
+                                : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) qf[nh][4 * c + i] = word(v, i);
+        }
+        fac[nh][0] = fac[nh][1] = a.scale;
+      }
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int hc = 8 * nh + 2 * qd + e;
+        slope[nh][e] = a.slopes && hc < G ? __ldcg(a.slopes + j * G + hc) * kLog2e : 0.f;
+        if (plain) fac[nh][e] *= kLog2e;
+      }
+    }
+
+    float mrun[NH][2], lsum[NH][2], o[NH][MT][4];
+    float vref = 0x1p-120f;  // unit of o on an FP8 cache, a power of two
+#pragma unroll
+    for (int nh = 0; nh < NH; ++nh) {
+      mrun[nh][0] = mrun[nh][1] = -INFINITY;
+      lsum[nh][0] = lsum[nh][1] = 0.f;
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+        o[nh][mt][0] = o[nh][mt][1] = o[nh][mt][2] = o[nh][mt][3] = 0.f;
+    }
+
+    // ---- one tile; FULLT: every token of it is visible
+    auto tile = [&](auto full_tile, int st, int t0, uint32_t have) {
+      constexpr bool FULLT = decltype(full_tile)::value;
+      const uint8_t* kb = ring + st * P::kStage;
+      const uint8_t* vb = kb + P::kPart;
+      // byte address of 16-byte piece p of row r (swizzled box by box; a box
+      // of 256-byte rows holds its rows' first halves, then the second)
+      auto piece = [&](const uint8_t* base, int r, int p) {
+        if constexpr (P::kBoxRow == 64)
+          return base + r * 64 + ((p ^ ((r >> 1) & 3)) << 4);
+        else if constexpr (P::kRow == 128)
+          return base + r * 128 + ((p ^ (r & 7)) << 4);
+        else {
+          const int box = r >> br_shift, in = r & ((1 << br_shift) - 1);
+          return base + ((box * 2 + (p >> 3)) << (br_shift + 7)) + in * 128 +
+                 (((p & 7) ^ (r & 7)) << 4);
+        }
+      };
+      auto visible = [&](int r) {
+        const int t = t0 + r;
+        return t >= lo && t < n && ((have >> (r >> br_shift)) & 1u);
+      };
+      // scores sc[tm][nh]: tokens r0 + (g | g + 8) x heads 8 nh + 2qd + (0 | 1)
+      float sc[kTm][NH][4];
+#pragma unroll
+      for (int tm = 0; tm < kTm; ++tm) {
+        const int r0 = 16 * (tm * kGroupWarps + gw) + g;
+#pragma unroll
+        for (int nh = 0; nh < NH; ++nh)
+          sc[tm][nh][0] = sc[tm][nh][1] = sc[tm][nh][2] = sc[tm][nh][3] = 0.f;
+#pragma unroll
+        for (int c = 0; c < KP; ++c) {
+          const int p = FP8 ? (D == 128 ? 2 * qd + c : qd) : 8 * (c >> 1) + 2 * qd + (c & 1);
+          const uint4 x = *reinterpret_cast<const uint4*>(piece(kb, r0, p));
+          const uint4 y = *reinterpret_cast<const uint4*>(piece(kb, r0 + 8, p));
+          if constexpr (FP8) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              uint32_t x0, x1, y0, y1;
+              e4m3x4(word(x, i), x0, x1);
+              e4m3x4(word(y, i), y0, y1);
+#pragma unroll
+              for (int nh = 0; nh < NH; ++nh)
+                mma16816<true>(sc[tm][nh], x0, y0, x1, y1, qf[nh][8 * c + 2 * i],
+                               qf[nh][8 * c + 2 * i + 1]);
+            }
+          } else {
+#pragma unroll
+            for (int nh = 0; nh < NH; ++nh) {
+              mma16816<false>(sc[tm][nh], x.x, y.x, x.y, y.y, qf[nh][4 * c], qf[nh][4 * c + 1]);
+              mma16816<false>(sc[tm][nh], x.z, y.z, x.w, y.w, qf[nh][4 * c + 2],
+                              qf[nh][4 * c + 3]);
+            }
+          }
+        }
+      }
+      // the scales of this lane's tokens, and the unit of the weights
+      [[maybe_unused]] float vs[kTm][2];
+      [[maybe_unused]] float keep = 1.f;  // what the unit's change makes of o
+      if constexpr (FP8) {
+        const float* ss = reinterpret_cast<const float*>(vb + P::kPart);
+        float vmax = 0.f;
+#pragma unroll
+        for (int tm = 0; tm < kTm; ++tm)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int r = 16 * (tm * kGroupWarps + gw) + g + 8 * e;
+            const float ks = ss[r];
+            vs[tm][e] = ss[kTok + r];
+            if (!FULLT && !visible(r)) vs[tm][e] = 0.f;
+            vmax = fmaxf(vmax, fabsf(vs[tm][e]));
+#pragma unroll
+            for (int nh = 0; nh < NH; ++nh) {
+              sc[tm][nh][2 * e] *= ks;
+              sc[tm][nh][2 * e + 1] *= ks;
+            }
+          }
+        vmax = fmaxf(vmax, __shfl_xor_sync(kFull, vmax, 4));
+        vmax = fmaxf(vmax, __shfl_xor_sync(kFull, vmax, 8));
+        vmax = fmaxf(vmax, __shfl_xor_sync(kFull, vmax, 16));
+        const float top = fminf(__uint_as_float(__float_as_uint(vmax) & 0x7f800000u), 0x1p120f);
+        if (top > vref) {  // the same for the whole warp
+          keep = vref / top;
+          vref = top;
+        }
+        const float inv = __uint_as_float((254u << 23) - __float_as_uint(vref));
+#pragma unroll
+        for (int tm = 0; tm < kTm; ++tm) {
+          vs[tm][0] *= inv;
+          vs[tm][1] *= inv;
+        }
+      }
+      // to log2 units, mask, running maximum and sum
+#pragma unroll
+      for (int nh = 0; nh < NH; ++nh) {
+        float mx[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+        for (int tm = 0; tm < kTm; ++tm)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int r = 16 * (tm * kGroupWarps + gw) + g + 8 * (e >> 1);
+            float v = sc[tm][nh][e] * fac[nh][e & 1];
+            if (!plain) {
+              v = (a.softcap > 0.f ? cap_score(v, a.softcap, inv_cap) : v) * kLog2e;
+              v = fmaf(slope[nh][e & 1], float(t0 + r - (n - 1)), v);
+            }
+            if (!FULLT && !visible(r)) v = -INFINITY;
+            sc[tm][nh][e] = v;
+            mx[e & 1] = fmaxf(mx[e & 1], v);
+          }
+        float alpha[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          float m = mx[h];
+          m = fmaxf(m, __shfl_xor_sync(kFull, m, 4));
+          m = fmaxf(m, __shfl_xor_sync(kFull, m, 8));
+          m = fmaxf(m, __shfl_xor_sync(kFull, m, 16));
+          const float mn = fmaxf(mrun[nh][h], m);
+          const float ms = mn == -INFINITY ? 0.f : mn;  // nothing visible so far
+          alpha[h] = exp2f(mrun[nh][h] - ms);
+          mrun[nh][h] = mn;
+          mx[h] = ms;
+        }
+#pragma unroll
+        for (int tm = 0; tm < kTm; ++tm)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) sc[tm][nh][e] = exp2f(sc[tm][nh][e] - mx[e & 1]);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          float t = 0.f;
+#pragma unroll
+          for (int tm = 0; tm < kTm; ++tm) t += sc[tm][nh][h] + sc[tm][nh][h + 2];
+          lsum[nh][h] = lsum[nh][h] * alpha[h] + t;
+          if constexpr (FP8) alpha[h] *= keep;
+        }
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+          o[nh][mt][0] *= alpha[0];
+          o[nh][mt][1] *= alpha[1];
+          o[nh][mt][2] *= alpha[0];
+          o[nh][mt][3] *= alpha[1];
+        }
+      }
+      // O^T += V^T P^T
+#pragma unroll
+      for (int tm = 0; tm < kTm; ++tm) {
+        uint32_t ph[NH][2];
+        [[maybe_unused]] uint32_t pl[NH][2];
+#pragma unroll
+        for (int nh = 0; nh < NH; ++nh) {
+          const float* c = sc[tm][nh];
+          if constexpr (FP8) {
+            ph[nh][0] = transpose8x8(f16x2(c[0] * vs[tm][0], c[1] * vs[tm][0]));
+            ph[nh][1] = transpose8x8(f16x2(c[2] * vs[tm][1], c[3] * vs[tm][1]));
+          } else {
+            const uint32_t h0 = bf16x2(c[0], c[1]), h1 = bf16x2(c[2], c[3]);
+            ph[nh][0] = transpose8x8(h0);
+            ph[nh][1] = transpose8x8(h1);
+            pl[nh][0] = transpose8x8(bf16x2(c[0] - __uint_as_float(h0 << 16),
+                                            c[1] - __uint_as_float(h0 & 0xffff0000u)));
+            pl[nh][1] = transpose8x8(bf16x2(c[2] - __uint_as_float(h1 << 16),
+                                            c[3] - __uint_as_float(h1 & 0xffff0000u)));
+          }
+        }
+        const int rv = 16 * (tm * kGroupWarps + gw) + 2 * qd;
+        const int rr[4] = {rv, rv + 1, rv + 8, rv + 9};
+        if constexpr (FP8) {
+          // lane g: dims D/8 * g + (0 .. D/8 - 1); tile mt: row g is dim
+          // 2 mt of them, row g + 8 dim 2 mt + 1
+          uint32_t w[4][D / 32];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const bool ok = FULLT || visible(rr[i]);
+            if constexpr (D == 128) {
+              const uint4 x = ok ? *reinterpret_cast<const uint4*>(piece(vb, rr[i], g))
+                                 : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+              for (int u = 0; u < 4; ++u) w[i][u] = word(x, u);
+            } else {
+              const uint2 x = ok ? *reinterpret_cast<const uint2*>(piece(vb, rr[i], g >> 1) +
+                                                                   8 * (g & 1))
+                                 : make_uint2(0u, 0u);
+              w[i][0] = x.x;
+              w[i][1] = x.y;
+            }
+          }
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt) {
+            const int sel = (mt & 1) ? 0x7362 : 0x5140;  // bytes a, b of row 1 and 2 interleaved
+            uint32_t a0, a1, a2, a3;
+            e4m3x4(__byte_perm(w[0][mt >> 1], w[1][mt >> 1], sel), a0, a1);
+            e4m3x4(__byte_perm(w[2][mt >> 1], w[3][mt >> 1], sel), a2, a3);
+#pragma unroll
+            for (int nh = 0; nh < NH; ++nh)
+              mma16816<true>(o[nh][mt], a0, a1, a2, a3, ph[nh][0], ph[nh][1]);
+          }
+        } else {
+          constexpr int CH = D / 64;
+          uint4 v[4][CH];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const bool ok = FULLT || visible(rr[i]);
+#pragma unroll
+            for (int ch = 0; ch < CH; ++ch)
+              v[i][ch] = ok ? *reinterpret_cast<const uint4*>(piece(vb, rr[i], g + 8 * ch))
+                            : make_uint4(0u, 0u, 0u, 0u);
+          }
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt) {
+            // D = 64: rows g, g + 8 are dims 8g + 2mt, + 1; D = 128: dims
+            // 8g + mt and 64 + 8g + mt
+            uint32_t a0, a1, a2, a3;
+            if constexpr (D == 64) {
+              a0 = halves(word(v[0][0], mt), word(v[1][0], mt), 0);
+              a1 = halves(word(v[0][0], mt), word(v[1][0], mt), 1);
+              a2 = halves(word(v[2][0], mt), word(v[3][0], mt), 0);
+              a3 = halves(word(v[2][0], mt), word(v[3][0], mt), 1);
+            } else {
+              const int w = mt >> 1, hf = mt & 1;
+              a0 = halves(word(v[0][0], w), word(v[1][0], w), hf);
+              a1 = halves(word(v[0][CH - 1], w), word(v[1][CH - 1], w), hf);
+              a2 = halves(word(v[2][0], w), word(v[3][0], w), hf);
+              a3 = halves(word(v[2][CH - 1], w), word(v[3][CH - 1], w), hf);
+            }
+#pragma unroll
+            for (int nh = 0; nh < NH; ++nh) {
+              mma16816<false>(o[nh][mt], a0, a1, a2, a3, ph[nh][0], ph[nh][1]);
+              mma16816<false>(o[nh][mt], a0, a1, a2, a3, pl[nh][0], pl[nh][1]);
+            }
+          }
+        }
+      }
+    };
+
+    bool gave_up = false;
+    for (int x = 0; x < here; ++x) {
+      const int idx = int(it - i0) + x;
+      if (idx % kGroups != grp) continue;
+      const int st = idx % P::kStages;
+      if (!__all_sync(kFull, mbar_wait_bounded(smem_u32(&full[st]),
+                                               uint32_t((idx / P::kStages) & 1)))) {
+        if (lane == 0) {
+          flag_error(a.err, kErrTimeout);
+          *static_cast<volatile int*>(&flags[1]) = 1;
+        }
+        for (int i = idx; i < int(i1 - i0) && i < idx + P::kStages; ++i)  // copies in flight land
+          (void)mbar_wait_bounded(smem_u32(&full[i % P::kStages]),
+                                  uint32_t((i / P::kStages) & 1));
+        gave_up = true;
+        break;
+      }
+      const uint32_t have = mask[st];
+      const int t0 = tok0 + (k0 + x) * kTok;
+      const uint32_t all = kFull >> (32 - (kTok >> br_shift));
+      if (t0 >= lo && t0 + kTok <= n && have == all)
+        tile(std::true_type{}, st, t0, have);
+      else if (have)
+        tile(std::false_type{}, st, t0, have);
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // reads before the refill
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&empty[st]));
+    }
+
+    // ---- the pair's end: join the warps
+#pragma unroll
+    for (int nh = 0; nh < NH; ++nh) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        float l = lsum[nh][h];
+        l += __shfl_xor_sync(kFull, l, 4);
+        l += __shfl_xor_sync(kFull, l, 8);
+        l += __shfl_xor_sync(kFull, l, 16);
+        lsum[nh][h] = l;
+      }
+      if constexpr (FP8) {
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[nh][mt][e] *= vref;
+      }
+    }
+    // dims of fragment (mt, row g | g + 8)
+    auto dim = [&](int mt, int up) {
+      if constexpr (FP8) return D / 8 * g + 2 * mt + up;
+      else if constexpr (D == 64) return 8 * g + 2 * mt + up;
+      else return 8 * g + mt + 64 * up;
+    };
+    float* slot = scratch + gw * P::kSlot;  // [heads][D], max [heads], sum [heads]
+    auto put = [&] {
+#pragma unroll
+      for (int nh = 0; nh < NH; ++nh)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int hc = 8 * nh + 2 * qd + h;
+          if (hc < G) {
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) {
+              slot[hc * D + dim(mt, 0)] = o[nh][mt][h];
+              slot[hc * D + dim(mt, 1)] = o[nh][mt][h + 2];
+            }
+            if (g == 0) {
+              slot[8 * NH * D + hc] = mrun[nh][h];
+              slot[8 * NH * (D + 1) + hc] = lsum[nh][h];
+            }
+          }
+        }
+    };
+    const bool one = here == 1;  // a single tile: only its group has anything
+    const int only = int(it - i0) % kGroups;
+    if (!one) {
+      if (grp == 1) put();
+      consumer_sync();
+      if (grp == 0) {
+#pragma unroll
+        for (int nh = 0; nh < NH; ++nh)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int hc = 8 * nh + 2 * qd + h;
+            if (hc < G) {
+              const float m2 = slot[8 * NH * D + hc], l2 = slot[8 * NH * (D + 1) + hc];
+              const float M = fmaxf(mrun[nh][h], m2);
+              const float f1 = M == -INFINITY ? 0.f : exp2f(mrun[nh][h] - M);
+              const float f2 = M == -INFINITY ? 0.f : exp2f(m2 - M);
+              mrun[nh][h] = M;
+              lsum[nh][h] = lsum[nh][h] * f1 + l2 * f2;
+#pragma unroll
+              for (int mt = 0; mt < MT; ++mt) {
+                o[nh][mt][h] = o[nh][mt][h] * f1 + slot[hc * D + dim(mt, 0)] * f2;
+                o[nh][mt][h + 2] = o[nh][mt][h + 2] * f1 + slot[hc * D + dim(mt, 1)] * f2;
+              }
+            }
+          }
+        __syncwarp();
+        put();
+      }
+    } else if (grp == only) {
+      put();
+    }
+    // a wait that gave up: no result and no arrival, decided by all together
+    if (consumer_any(gave_up)) return;
+    const bool whole = k0 == 0 && here == nt;
+    // the joined value of head r, dims 4c .. 4c + 3, from the four slots
+    auto joined = [&](int r, int c, float& M, float& Lq) {
+      M = -INFINITY;
+#pragma unroll
+      for (int w = 0; w < kGroupWarps; ++w)
+        M = fmaxf(M, scratch[w * P::kSlot + 8 * NH * D + r]);
+      float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+      Lq = 0.f;
+#pragma unroll
+      for (int w = 0; w < kGroupWarps; ++w) {
+        const float* p = scratch + w * P::kSlot;
+        const float f = M == -INFINITY ? 0.f : exp2f(p[8 * NH * D + r] - M);
+        const float4 v = *reinterpret_cast<const float4*>(p + r * D + 4 * c);
+        s.x = fmaf(v.x, f, s.x);
+        s.y = fmaf(v.y, f, s.y);
+        s.z = fmaf(v.z, f, s.z);
+        s.w = fmaf(v.w, f, s.w);
+        Lq = fmaf(p[8 * NH * (D + 1) + r], f, Lq);
+      }
+      return s;
+    };
+    // final values from O, max (log2 units) and sum of head r
+    auto finish = [&](int r, int c, float4 s, float M, float Lq) {
+      const int h = j * G + r;
+      if (a.sinks) {
+        const float z = __ldcg(a.sinks + h) * kLog2e;
+        const float M2 = fmaxf(M, z);
+        const float f = M == -INFINITY ? 0.f : exp2f(M - M2);
+        Lq = Lq * f + exp2f(z - M2);
+        s.x *= f;
+        s.y *= f;
+        s.z *= f;
+        s.w *= f;
+        M = M2;
+      }
+      const float inv = Lq > 0.f ? 1.f / Lq : Lq == 0.f ? 0.f : Lq;  // a NaN stays one
+      const int64_t row = int64_t(b) * heads + h;
+      *reinterpret_cast<uint2*>(a.out + row * D + 4 * c) =
+          make_uint2(bf16x2(s.x * inv, s.y * inv), bf16x2(s.z * inv, s.w * inv));
+      if (a.lse && c == 0)
+        a.lse[row] = Lq == 0.f ? -INFINITY : (M + log2f(Lq)) * 0.6931471805599453f;
+    };
+    const int quads = G * (D / 4);
+    if (whole) {
+      for (int e = tid; e < quads; e += kConsumers) {
+        float M, Lq;
+        const int r = e / (D / 4), c = e % (D / 4);
+        const float4 s = joined(r, c, M, Lq);
+        finish(r, c, s, M, Lq);
+      }
+    } else {
+      const int PS = part_floats(G, D);
+      const int64_t s0 = L.prefix[b] + int64_t(j) * nt;  // the pair's first item
+      const int cf = int(((s0 + 1) * C - 1) / T);        // CTAs of its first and last items
+      const int cl = int(((s0 + nt) * C - 1) / T);
+      float* part = a.parts + (int64_t(blockIdx.x) * 2 + (k0 == 0)) * PS;
+      for (int e = tid; e < quads; e += kConsumers) {
+        float M, Lq;
+        const int r = e / (D / 4), c = e % (D / 4);
+        const float4 s = joined(r, c, M, Lq);
+        *reinterpret_cast<float4*>(part + r * D + 4 * c) = s;
+        if (c == 0) {
+          part[G * D + r] = M;
+          part[G * D + G + r] = Lq;
+        }
+      }
+      __threadfence();
+      consumer_sync();
+      if (tid == 0) flags[0] = atomicAdd(a.counters + cf, 1) == cl - cf;
+      consumer_sync();
+      if (flags[0]) {
+        __threadfence();
+        const int np = cl - cf + 1;
+        auto part_of = [&](int p) {
+          return a.parts + (int64_t(cf + p) * 2 + (p == 0)) * PS;
+        };
+        float* hm = scratch;  // [16] max, [16] sum of the pair's heads
+        for (int r = warp; r < G; r += kConsumers / 32) {
+          float M = -INFINITY, Lq = 0.f;
+          for (int p = lane; p < np; p += 32) M = fmaxf(M, __ldcg(part_of(p) + G * D + r));
+          M = warp_max(M);
+          for (int p = lane; p < np; p += 32)
+            Lq += M == -INFINITY ? 0.f
+                                 : exp2f(__ldcg(part_of(p) + G * D + r) - M) *
+                                       __ldcg(part_of(p) + G * D + G + r);
+          Lq = warp_sum(Lq);
+          if (lane == 0) {
+            hm[r] = M;
+            hm[16 + r] = Lq;
+          }
+        }
+        consumer_sync();
+        for (int e = tid; e < quads; e += kConsumers) {
+          const int r = e / (D / 4), c = e % (D / 4);
+          const float M = hm[r];
+          float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+          for (int p0 = 0; p0 < np; p0 += 8) {
+            float4 v[8];
+            float m[8];
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+              const bool in = p0 + u < np;
+              const float* pp = part_of(in ? p0 + u : 0);
+              v[u] = in ? __ldcg(reinterpret_cast<const float4*>(pp + r * D + 4 * c))
+                        : make_float4(0.f, 0.f, 0.f, 0.f);
+              m[u] = in ? __ldcg(pp + G * D + r) : -INFINITY;
+            }
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+              const float f = M == -INFINITY ? 0.f : exp2f(m[u] - M);
+              s.x = fmaf(v[u].x, f, s.x);
+              s.y = fmaf(v[u].y, f, s.y);
+              s.z = fmaf(v[u].z, f, s.z);
+              s.w = fmaf(v[u].w, f, s.w);
+            }
+          }
+          finish(r, c, s, M, hm[16 + r]);
+        }
+        if (tid == 0) a.counters[cf] = 0;  // ready for the next call
+      }
+    }
+    consumer_sync();  // the scratch is free again
+    it += here;
+    at.tile = 0;
+    if (k0 + here == nt) {
+      if (++at.j == kv.kv_heads) {
+        at.j = 0;
+        do ++at.b;
+        while (at.b < kv.batch && L.tiles(at.b) == 0);
+      }
+    }
+  }
+}
+
+// Rows of head_dim elements as boxes of `rows` rows x (one or two) spans of
+// at most 128 bytes, written with the swizzle of that span.
+cudaError_t pool_map(CUtensorMap* map, const void* base, int D, bool fp8, int64_t rows_total,
+                     int rows) {
+  EncodeTiledFn enc = tensor_map_encoder();
+  if (!enc) return cudaErrorNotSupported;
+  const int es = fp8 ? 1 : 2, row = D * es, span = row < 128 ? row : 128;
+  const cuuint64_t dims[3] = {cuuint64_t(span / es), cuuint64_t(rows_total),
+                              cuuint64_t(row / span)};
+  const cuuint64_t strides[2] = {cuuint64_t(row), cuuint64_t(span)};
+  const cuuint32_t box[3] = {cuuint32_t(span / es), cuuint32_t(rows), cuuint32_t(row / span)};
+  const cuuint32_t estr[3] = {1u, 1u, 1u};
+  if (enc(map, fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
+          const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+          span == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+    return cudaErrorInvalidValue;
+  return cudaSuccess;
+}
+
+template <int D, int NH, bool FP8>
+cudaError_t launch(const DeviceInfo& di, const PagedKv& kv, const PagedAttnArgs& a,
+                   cudaStream_t s, bool pdl) {
+  using P = Plan<D, NH, FP8>;
+  auto kern = paged_decode_kernel<D, NH, FP8>;
+  const int ps = 1 << kv.page_shift, br = ps < P::kTok ? ps : P::kTok;
+  const int64_t rows = (int64_t(kv.num_pages) * kv.kv_heads) << kv.page_shift;
+  CUtensorMap mk, mv;
+  if (cudaError_t e = pool_map(&mk, kv.k, D, FP8, rows, br)) return e;
+  if (cudaError_t e = pool_map(&mv, kv.v, D, FP8, rows, br)) return e;
+  if (cudaError_t e = ensure_smem(di, kern, P::kSmem)) return e;
+  // one CTA per SM, or one per tile that the table could hold where that is less
+  const int64_t most =
+      ((int64_t(kv.pages_per_seq) << kv.page_shift) + P::kTok - 1) / P::kTok * kv.batch *
+      kv.kv_heads;
+  int64_t grid = di.sms < kMaxCtas ? di.sms : kMaxCtas;
+  if (grid > most) grid = most;
+  DecodeArgs d;
+  d.q = a.q;
+  d.q_stride = a.q_stride;
+  d.group = a.heads / kv.kv_heads;
+  d.scale = a.scale;
+  d.softcap = a.softcap;
+  d.window = a.window;
+  d.slopes = a.slopes;
+  d.sinks = a.sinks;
+  d.out = a.out;
+  d.lse = a.lse;
+  d.counters = static_cast<int32_t*>(a.ws);
+  d.parts = reinterpret_cast<float*>(static_cast<uint8_t*>(a.ws) + kMaxCtas * 4);
+  d.err = di.error_word;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(unsigned(grid));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = P::kSmem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = pdl ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kern, mk, mv, kv, d);
+}
+
+}  // namespace
+
+size_t paged_decode_workspace_bytes(int group, int head_dim) {
+  const DeviceInfo* di = device_info();
+  const int64_t ctas = di && di->sms < kMaxCtas ? di->sms : kMaxCtas;
+  return size_t(kMaxCtas) * 4 + size_t(ctas) * 2 * part_floats(group, head_dim) * 4;
+}
+
+cudaError_t launch_paged_decode(const PagedKv& kv, int head_dim, bool fp8,
+                                const PagedAttnArgs& a, cudaStream_t s, bool pdl) {
+  const DeviceInfo* di = device_info();
+  if (!di) return cudaErrorNoDevice;
+  const bool wide = a.heads / kv.kv_heads > 8;
+  if (head_dim == 64) {
+    if (fp8)
+      return wide ? launch<64, 2, true>(*di, kv, a, s, pdl) : launch<64, 1, true>(*di, kv, a, s, pdl);
+    return wide ? launch<64, 2, false>(*di, kv, a, s, pdl) : launch<64, 1, false>(*di, kv, a, s, pdl);
+  }
+  if (fp8)
+    return wide ? launch<128, 2, true>(*di, kv, a, s, pdl) : launch<128, 1, true>(*di, kv, a, s, pdl);
+  return wide ? launch<128, 2, false>(*di, kv, a, s, pdl) : launch<128, 1, false>(*di, kv, a, s, pdl);
+}
+
+}  // namespace tt

@@ -125,12 +125,7 @@ cudaError_t launch(const PagedKv& kv, int D, bool fp8, const PagedAttnArgs& a, c
 
 }  // namespace
 
-size_t paged_decode_workspace_bytes(int, int) { return 16; }
 size_t paged_prefill_workspace_bytes(int) { return 16; }
-cudaError_t launch_paged_decode(const PagedKv& kv, int head_dim, bool fp8,
-                                const PagedAttnArgs& a, cudaStream_t s, bool pdl) {
-  return launch(kv, head_dim, fp8, a, s, pdl);
-}
 cudaError_t launch_paged_prefill(const PagedKv& kv, int head_dim, bool fp8,
                                  const PagedAttnArgs& a, cudaStream_t s, bool pdl) {
   return launch(kv, head_dim, fp8, a, s, pdl);
