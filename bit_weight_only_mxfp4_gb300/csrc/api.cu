@@ -529,6 +529,9 @@ tt_status tt_paged_decode_attention(const tt_paged_kv* kv, const uint16_t* q, in
                             window, slopes,   sinks,   nullptr,            out,   lse,   workspace};
   tt::PagedKv c;
   if (tt_status st = check_paged_attention(kv, a, workspace_bytes, &c)) return st;
+  // tiles of all sequences and kv heads (of at least 64 tokens) are counted in 32 bits
+  const int64_t tiles = ((int64_t(kv->pages_per_seq) * kv->page_size + 63) / 64) * kv->batch;
+  if (tiles > kMaxRows / kv->kv_heads) return TT_ERR_UNSUPPORTED;
   return from_cuda(tt::launch_paged_decode(c, kv->head_dim, kv->type == TT_KV_FP8, a,
                                            as_stream(stream), kPdl));
 }

@@ -56,7 +56,7 @@ constexpr int kGroupWarps = 4;
 constexpr int kConsumers = kGroups * kGroupWarps * 32;
 constexpr int kThreads = kConsumers + 32;     // + the copying warp
 constexpr int kMaxCtas = 1024;                // counters in the workspace
-constexpr int kSmemMax = 220 * 1024;
+constexpr int kSmemMax = 227 * 1024;
 constexpr int kConsumerBar = 1;
 
 template <int D, int NH, bool FP8>
@@ -72,12 +72,16 @@ struct Plan {
   static constexpr int kStage = 2 * kPart + (FP8 ? 2 * kTok * 4 : 0);
   static constexpr int kSlot = 8 * NH * (D + 2);          // floats of one warp's part
   static constexpr int kScratch = kGroupWarps * kSlot * 4;
-  static constexpr int kFixed = 1024 + kScratch + (kPagedMaxBatch + 1) * 8 + kPagedMaxBatch * 4 +
-                                512;  // alignment, parts, line, barriers
-  static constexpr int kRaw = (kSmemMax - kFixed) / kStage;
+  static constexpr int kFixed =
+      1024 + kScratch + (2 * kPagedMaxBatch + 2) * 4 + 512;  // alignment, parts, line, barriers
+  // A multiple of the groups, so that a stage is always the same group's: a
+  // group then waits for every phase of its stages' barriers in turn.  (With
+  // a stage that changes hands, a group that is ahead can find the phase
+  // before last and take it for its own.)
+  static constexpr int kRaw = (kSmemMax - kFixed) / kStage / kGroups * kGroups;
   static constexpr int kStages = kRaw > 12 ? 12 : kRaw;
   static constexpr int kSmem = kFixed + kStages * kStage;
-  static_assert(kStages >= 3, "ring");
+  static_assert(kStages >= 4 && kStages % kGroups == 0, "ring");
   static_assert(kStage % 1024 == 0, "swizzled boxes start on 1024 bytes");
 };
 
@@ -177,7 +181,7 @@ __device__ __forceinline__ bool consumer_any(bool p) {
 // The line of tiles: sequence b has nt(b) tiles from tile t0(b) on for each
 // kv head; prefix[b] counts the tiles before it over all kv heads.
 struct Line {
-  const int64_t* prefix;
+  const int32_t* prefix;
   const int32_t* len;
   int kv_heads, window, tok;
   __device__ __forceinline__ int first_tile(int b) const {
@@ -194,15 +198,14 @@ struct Line {
 struct At {
   int b, j, tile;  // tile counted from the pair's first
 };
-__device__ __forceinline__ At find(const Line& L, int batch, int64_t item) {
+__device__ __forceinline__ At find(const Line& L, int batch, int item) {
   int lo = 0, hi = batch;  // the last b with prefix[b] <= item and tiles
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
     if (L.prefix[mid] <= item) lo = mid; else hi = mid;
   }
-  const int64_t rem = item - L.prefix[lo];
-  const int nt = L.tiles(lo);
-  return {lo, int(rem / nt), int(rem % nt)};
+  const int rem = item - L.prefix[lo], nt = L.tiles(lo);
+  return {lo, rem / nt, rem % nt};
 }
 
 template <int D, int NH, bool FP8>
@@ -216,13 +219,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
   uint8_t* ring = smem;
   float* scratch = reinterpret_cast<float*>(smem + P::kStages * P::kStage);
-  int64_t* prefix = reinterpret_cast<int64_t*>(scratch + P::kScratch / 4);
-  int32_t* slen = reinterpret_cast<int32_t*>(prefix + kPagedMaxBatch + 1);
+  int32_t* prefix = reinterpret_cast<int32_t*>(scratch + P::kScratch / 4);
+  int32_t* slen = prefix + kPagedMaxBatch + 2;
   uint64_t* full = reinterpret_cast<uint64_t*>(slen + kPagedMaxBatch);
   uint64_t* empty = full + P::kStages;
   uint32_t* mask = reinterpret_cast<uint32_t*>(empty + P::kStages);  // boxes present, per stage
   int* flags = reinterpret_cast<int*>(mask + P::kStages);  // [0] last to finish, [1] gave up
-  int64_t* wsum = reinterpret_cast<int64_t*>(scratch);  // scan partials, before the main loop
+  int32_t* wsum = reinterpret_cast<int32_t*>(scratch);  // scan partials, before the main loop
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if (tid == 0) {
@@ -240,7 +243,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const Line L{prefix, slen, kv.kv_heads, a.window, kTok};
   {
     constexpr int kPer = (kPagedMaxBatch + kThreads - 1) / kThreads;
-    int64_t mine[kPer], sum = 0;
+    int mine[kPer], sum = 0;
     const int per = (kv.batch + kThreads - 1) / kThreads;
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
@@ -248,19 +251,19 @@ __global__ void __launch_bounds__(kThreads, 1)
       mine[i] = 0;
       if (i < per && b < kv.batch) {
         slen[b] = paged_len(kv, b, blockIdx.x == 0 ? a.err : nullptr);
-        mine[i] = int64_t(L.tiles(b)) * kv.kv_heads;
+        mine[i] = L.tiles(b) * kv.kv_heads;
       }
       sum += mine[i];
     }
-    int64_t run = sum;
+    int run = sum;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const int64_t v = __shfl_up_sync(kFull, run, o);
+      const int v = __shfl_up_sync(kFull, run, o);
       if (lane >= o) run += v;
     }
     if (lane == 31) wsum[warp] = run;
     __syncthreads();
-    int64_t base = run - sum;
+    int base = run - sum;
     for (int w = 0; w < warp; ++w) base += wsum[w];
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
@@ -273,8 +276,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   const int64_t T = prefix[kv.batch];
   const int64_t C = T < gridDim.x ? T : gridDim.x;
-  const int64_t i0 = blockIdx.x < C ? T * blockIdx.x / C : 0;
-  const int64_t i1 = blockIdx.x < C ? T * (blockIdx.x + 1) / C : 0;
+  const int i0 = blockIdx.x < C ? int(T * blockIdx.x / C) : 0;
+  const int i1 = blockIdx.x < C ? int(T * (blockIdx.x + 1) / C) : 0;
   const int G = a.group, heads = G * kv.kv_heads;
 
   if (warp == kGroups * kGroupWarps) {
@@ -293,8 +296,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       page = in ? paged_page(kv, w.b, t, a.err) : -1;
     };
     look(at);
-    for (int64_t it = i0; it < i1; ++it) {
-      const int idx = int(it - i0), st = idx % P::kStages;
+    for (int it = i0; it < i1; ++it) {
+      const int idx = it - i0, st = idx % P::kStages;
       const uint32_t bar = smem_u32(&full[st]);
       const int my_page = page, my_t = t;
       const int j = at.j;
@@ -368,9 +371,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   const bool plain = !(a.softcap > 0.f) && !a.slopes;
 
   At at = find(L, kv.batch, i0);
-  for (int64_t it = i0; it < i1;) {
+  for (int it = i0; it < i1;) {
     const int b = at.b, j = at.j, nt = L.tiles(b), k0 = at.tile;
-    const int here = int(i1 - it < nt - k0 ? i1 - it : nt - k0);
+    const int here = i1 - it < nt - k0 ? i1 - it : nt - k0;
     const int n = slen[b];
     const int lo = a.window > 0 && n > a.window ? n - a.window : 0;
     const int tok0 = L.first_tile(b) * kTok;
@@ -682,7 +685,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     bool gave_up = false;
     for (int x = 0; x < here; ++x) {
-      const int idx = int(it - i0) + x;
+      const int idx = (it - i0) + x;
       if (idx % kGroups != grp) continue;
       const int st = idx % P::kStages;
       if (!__all_sync(kFull, mbar_wait_bounded(smem_u32(&full[st]),
@@ -691,7 +694,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           flag_error(a.err, kErrTimeout);
           *static_cast<volatile int*>(&flags[1]) = 1;
         }
-        for (int i = idx; i < int(i1 - i0) && i < idx + P::kStages; ++i)  // copies in flight land
+        for (int i = idx; i < i1 - i0 && i < idx + P::kStages; ++i)  // copies in flight land
           (void)mbar_wait_bounded(smem_u32(&full[i % P::kStages]),
                                   uint32_t((i / P::kStages) & 1));
         gave_up = true;
@@ -754,7 +757,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     };
     const bool one = here == 1;  // a single tile: only its group has anything
-    const int only = int(it - i0) % kGroups;
+    const int only = (it - i0) % kGroups;
     if (!one) {
       if (grp == 1) put();
       consumer_sync();

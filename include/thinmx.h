@@ -504,7 +504,8 @@ tt_status tt_paged_rope_append(const tt_paged_kv* kv, const uint16_t* q, const u
  * (-inf without sinks).  q: row of sequence b at b * q_stride elements; out
  * [batch][heads][head_dim].
  * Requires heads a multiple of kv_heads, heads / kv_heads <= 16, scale and
- * softcap finite, softcap >= 0, window >= 0, q_stride % 8 == 0.
+ * softcap finite, softcap >= 0, window >= 0, q_stride % 8 == 0, and batch *
+ * kv_heads * pages_per_seq * page_size / 64 < 2^31.
  * workspace: device, >= tt_paged_attention_workspace_bytes(...) bytes,
  * zero-filled once before its first use; each call leaves it ready for the
  * next, whatever its sizes.  Calls that share one must be ordered on one

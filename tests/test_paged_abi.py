@@ -116,6 +116,8 @@ def test_attention_refusals(lib):
         assert call(c, lse=A + 2) == 3
         assert call(c, slopes=A + 1) == 3
         assert call(c, sinks=A + 3) == 3
+    # more tiles than 32 bits count
+    assert decode(kv(batch=1024, pages_per_seq=(1 << 31) // 16 - 1)) == 5
     assert prefill(c, starts=None) == 1
     assert prefill(c, tokens=-1) == 2
     assert prefill(c, tokens=1 << 31) == 2
