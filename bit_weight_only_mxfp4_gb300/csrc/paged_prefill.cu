@@ -1,134 +1,1062 @@
-// Attention over the paged cache, one warp per new token and query head.
+// Attention of several new tokens per sequence over the paged cache: the
+// attention of a prompt, or of a chunk of one.
 //
-//   z_j = f(scale * q . k_j) + slope * (j - p),  f(s) = cap tanh(s / cap)
-//   over the visible keys j: j < len, j <= p or j < prefix, j > p - window;
-//   out = sum_j e^z_j v_j / (sum_j e^z_j + e^sink),  lse = log of the divisor
+//   z[r][t] = f(scale * q[r] . k[j][t]) + slope[h] * (t - p)
+//   out[r]  = sum_t e^z v[j][t] / (sum_t e^z + e^sink[h])
 //
-// with the running maximum and sum of the softmax, 32-bit throughout.
-#include <cuda_fp8.h>
+// A row r is one new token (place p) and one of the G query heads of kv head
+// j; it sees the tokens [rlo, rhi): rhi = max(p + 1, prefix) up to the length,
+// rlo = p + 1 - window.  The work is 4 head_dim operations per row and
+// token, so it belongs to the tensor cores:
+//   S = Q K^T   128 rows x 128 tokens, tcgen05.mma, accumulator in TMEM
+//   P = 2^(S - m) in bf16, back to TMEM over S
+//   O += P V    A operand P from TMEM, B operand V as it lies in the cache
+//               (token rows: the "transposed" B of the instruction), O in TMEM
+//
+// Tiles.  A row tile packs floor(128 / G) tokens x G heads, so a K and V tile
+// serves the whole group and short chunks still fill rows.  A CTA works on
+// two row tiles at once (A and B), each with a warpgroup for its softmax, one
+// thread a row, while the tensor cores are busy with the other's products:
+//   warps 0-3, 4-7  softmax of A and B (208 registers: a row's 128 scores)
+//   warp 8          the products, one thread
+//   warp 9          the copies (TMA: one box per page and 64 dims)
+//   warps 10-11     make the V tiles safe (below); FP8: E4M3 -> bf16 tiles
+// The running maximum is only raised (and O rescaled, which takes a TMEM round
+// trip) when a row's maximum has grown by more than 2^8: the weights are then
+// at most 2^8, which costs no precision in bf16 and 32 bits.
+//
+// Rounding.  Q and K products are exact, sums 32-bit; P is rounded once to
+// bf16 (2^-8 of each weight; its errors average out over the tokens, and the
+// output is rounded to the same 8 bits).  The sum of weights is taken from
+// the unrounded ones.  FP8: codes become bf16 exactly, the key scales
+// multiply S, the value scales multiply P, in 32 bits.
+//
+// Masked values.  0 * NaN is NaN, so a V row that some rows of the tile must
+// not see may not enter the product with NaN or infinities in it: rows of no
+// token (past the length, holes) are zeroed, and where the mask cuts a tile the
+// elements that are not finite are zeroed and the rows that do see them get
+// them added at the end.  Tiles that all rows see whole need nothing of it.
+//
+// Work.  Row tiles x kv heads are dealt to one CTA per SM, the last (longest)
+// first; where there are fewer than half as many as SMs, each is split along
+// its tokens and joined by the last part to finish, from the parts in order.
+// What the lengths are is read on the device.
+#include <cmath>
 
 #include "launch.h"
 #include "paged.cuh"
+#include "tensor_map.h"
 
 namespace tt {
 namespace {
 
-__device__ __forceinline__ float e4m3_f32(uint8_t c) {
-  return __half2float(__half(__nv_cvt_fp8_to_halfraw(c, __NV_E4M3)));
+constexpr int kRows = 128;   // rows of a row tile
+constexpr int kKeys = 128;   // tokens of a K / V tile
+constexpr int kWarps = 12;
+constexpr int kThreads = 32 * kWarps;
+constexpr int kMmaWarp = 8, kLoadWarp = 9, kFixWarp = 10;
+constexpr int kFixers = 64;
+constexpr int kCounters = 1024;  // as in the decode kernel's part of the workspace
+constexpr int kMaxSplit = 32;
+constexpr uint32_t kAll = 0xffffffffu;
+
+template <int D, bool FP8>
+struct Plan {
+  static constexpr int kHalves = D / 64;            // 128-byte spans of a bf16 row
+  static constexpr int kSpan = kKeys * 128;         // bytes of a tile's one span
+  static constexpr int kTile = kSpan * kHalves;     // a K or V tile, or a Q tile
+  static constexpr int kSlots = FP8 ? (D == 128 ? 3 : 6) : (D == 128 ? 4 : 8);
+  static constexpr int kRaw = FP8 ? kKeys * D + 2 * kKeys * 4 : 0;  // codes, both scales (with K)
+  static constexpr int kRaws = FP8 ? (D == 128 ? 2 : 4) : 0;
+  static constexpr int kOffKv = 2 * kTile;
+  static constexpr int kOffRaw = kOffKv + kSlots * kTile;
+  static constexpr int kOffScale = kOffRaw + kRaws * kRaw;      // [4 tiles][key, value][128]
+  static constexpr int kOffLine = kOffScale + (FP8 ? 4 * 2 * kKeys * 4 : 0);
+  static constexpr int kOffBar = kOffLine + (kPagedMaxBatch + 1) * 4 + 12;
+  static constexpr int kSmem = 1024 + kOffBar + 512;
+  static_assert(kSmem <= 227 * 1024, "shared memory");
+  static_assert(kOffBar % 8 == 0, "barriers");
+  // TMEM columns: S (and P over it) of A and B, O of A and B
+  static constexpr int kColS = 0, kColO = 256;
+};
+
+struct PrefillArgs {
+  const int32_t* starts;
+  int64_t tokens;
+  int group, per_tile;  // heads per kv head, tokens per row tile
+  float scale, softcap;
+  int window;
+  const float* slopes;
+  const float* sinks;
+  const int32_t* prefix;
+  uint16_t* out;
+  float* lse;
+  int32_t* counters;
+  float* parts;
+  int32_t* err;
+};
+
+// ---- tcgen05
+__device__ __forceinline__ uint64_t desc_base() {
+  return (uint64_t(1024 >> 4) << 32)  // stride: 8 rows of 128 bytes
+         | (uint64_t(1) << 46)        // descriptor version
+         | (uint64_t(2) << 61);       // 128-byte swizzle
+}
+// K-major operand (rows of 64 contiguous elements of the contraction).
+__device__ __forceinline__ uint64_t desc_k(uint32_t addr) {
+  return desc_base() | (uint64_t(1) << 16) | uint64_t((addr >> 4) & 0x3fffu);
+}
+// MN-major operand (rows = steps of the contraction); `leading` bytes from
+// one 64-element span of the outer dimension to the next.
+__device__ __forceinline__ uint64_t desc_mn(uint32_t addr, uint32_t leading) {
+  return desc_base() | (uint64_t(leading >> 4) << 16) | uint64_t((addr >> 4) & 0x3fffu);
+}
+// bf16 x bf16 -> f32, 128 rows, n columns; mn: B is MN-major.
+__device__ __forceinline__ constexpr uint32_t idesc(int n, bool mn) {
+  return (1u << 4) | (1u << 7) | (1u << 10) | (mn ? 1u << 16 : 0u) | (uint32_t(n >> 3) << 17) |
+         (uint32_t(kRows >> 4) << 24);
+}
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t id,
+                                       uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(id), "r"(acc)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t id,
+                                       uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(id), "r"(acc)
+      : "memory");
+}
+__device__ __forceinline__ void commit(uint64_t* bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
+          smem_u32(bar))
+      : "memory");
+}
+__device__ __forceinline__ void fence_after() {
+  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+}
+__device__ __forceinline__ void fence_before() {
+  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+}
+__device__ __forceinline__ void wait_ld() {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void wait_st() {
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+// 32 columns of this warp's 32 lanes (complete after wait_ld).
+__device__ __forceinline__ void tmem_ld32(uint32_t addr, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]),
+        "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]),
+        "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(addr));
+}
+__device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
+      "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(
+          addr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
+      "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]),
+      "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]),
+      "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+
+__device__ __forceinline__ void tma_q(uint32_t dst, const CUtensorMap* map, int x, int h, int t,
+                                      uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(h), "r"(t), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void tma_rows(uint32_t dst, const CUtensorMap* map, int x, int row,
+                                         uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(row), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void bulk_copy(uint32_t dst, const void* src, uint32_t bytes,
+                                          uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cta.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+          dst),
+      "l"(src), "r"(bytes), "r"(bar)
+      : "memory");
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t bf16x2(float a, float b) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+// Two E4M3 codes (low 16 bits) -> bf16x2, exact.
+__device__ __forceinline__ uint32_t e4m3x2_bf16x2(uint32_t w) {
+  uint32_t h;
+  asm("{\n\t.reg .b16 l, u;\n\tmov.b32 {l, u}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\t}"
+      : "=r"(h)
+      : "r"(w));
+  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
+  return bf16x2(f.x, f.y);
+}
+
+// What one piece of work is: the row tiles A and B of q tile `qt` of sequence
+// b, kv head j, the part [k0, k1) of its K / V tiles.
+struct Item {
+  int b, j, len, pre;
+  int tok0, new_tokens;  // first flat token of tile A; the sequence's tokens from it on
+  int p0;                // place of tok0
+  int lo, hi;            // tokens that some row sees
+  int all_lo, all_hi;    // tokens that every row sees
+  int k0, k1, parts, part;
+  int base;              // number among the joined pieces
+};
+
+// Waits for a phase; gives up after kWaitLimitNs, or when another thread has.
+__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile int* quit,
+                                     int32_t* err) {
+  const uint32_t a = smem_u32(bar);
+  if (mbar_try_wait(a, parity)) return true;
+  const uint64_t t0 = globaltimer_ns();
+  for (uint32_t it = 1;; ++it) {
+    if (mbar_try_wait(a, parity)) return true;
+    if ((it & 15u) == 0u) {
+      if (*quit) return false;
+      if (globaltimer_ns() - t0 > kWaitLimitNs) {
+        *quit = 1;
+        flag_error(err, kErrTimeout);
+        return false;
+      }
+    }
+  }
 }
 
 template <int D, bool FP8>
-__global__ void __launch_bounds__(128)
-    paged_attention_kernel(const PagedKv kv, const PagedAttnArgs a, int32_t* err) {
-  constexpr int E = D / 32;
-  const int lane = threadIdx.x & 31;
-  const int64_t item = int64_t(blockIdx.x) * 4 + (threadIdx.x >> 5);
-  const int64_t t = item / a.heads;
-  const int h = int(item - t * a.heads);
+__global__ void __launch_bounds__(kThreads, 1)
+    paged_prefill_kernel(const __grid_constant__ CUtensorMap map_q,
+                         const __grid_constant__ CUtensorMap map_k,
+                         const __grid_constant__ CUtensorMap map_v, const PagedKv kv,
+                         const PrefillArgs a) {
+  using P = Plan<D, FP8>;
+  extern __shared__ __align__(128) uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+  const uint32_t sbase = smem_u32(smem);
+  float* scales = reinterpret_cast<float*>(smem + P::kOffScale);
+  int32_t* line = reinterpret_cast<int32_t*>(smem + P::kOffLine);  // q tiles before sequence b
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + P::kOffBar);
+  uint64_t* empty = full + P::kSlots;
+  uint64_t* ready = empty + P::kSlots;   // slot made safe, or converted
+  uint64_t* raw_full = ready + P::kSlots;
+  uint64_t* raw_empty = raw_full + 4;
+  uint64_t* q_full = raw_empty + 4;      // [2]
+  uint64_t* q_free = q_full + 2;         // [2]
+  uint64_t* s_full = q_free + 2;         // [2]
+  uint64_t* p_full = s_full + 2;         // [2]
+  uint64_t* o_done = p_full + 2;         // [2]
+  uint64_t* join = o_done + 2;           // [2]
+  uint64_t* drained = join + 2;
+  uint32_t* have = reinterpret_cast<uint32_t*>(drained + 1);  // [8] boxes present, per tile
+  int* dirty = reinterpret_cast<int*>(have + 8);              // [4] item number + 1
+  int* misc = dirty + 4;  // [0] TMEM address, [1] quit, [2 + g] last to finish, [4..] scan
+  volatile int* quit = misc + 1;
+
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (tid == 0) {
+    for (int i = 0; i < P::kSlots; ++i) {
+      mbar_init(smem_u32(&full[i]), 1);
+      mbar_init(smem_u32(&empty[i]), 1);
+      mbar_init(smem_u32(&ready[i]), kFixers);
+    }
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(smem_u32(&raw_full[i]), 1);
+      mbar_init(smem_u32(&raw_empty[i]), kFixers);
+    }
+    for (int g = 0; g < 2; ++g) {
+      mbar_init(smem_u32(&q_full[g]), 1);
+      mbar_init(smem_u32(&q_free[g]), 1);
+      mbar_init(smem_u32(&s_full[g]), 1);
+      mbar_init(smem_u32(&p_full[g]), kRows);
+      mbar_init(smem_u32(&o_done[g]), 1);
+      mbar_init(smem_u32(&join[g]), kRows);
+    }
+    mbar_init(smem_u32(drained), 1);
+    for (int i = 0; i < 4; ++i) dirty[i] = 0;
+    misc[1] = 0;
+    fence_mbar_init();
+  }
+  if (warp == kMmaWarp) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     smem_u32(&misc[0])),
+                 "r"(512)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
   pdl_allow_next_grid();
   pdl_wait_prior_grid();
-  if (t >= a.tokens) return;
-  const int b = a.starts ? paged_seq_of(a.starts, kv.batch, t, lane) : int(t);
-  int32_t* e1 = lane == 0 ? err : nullptr;
-  const int64_t len = paged_len(kv, b, e1);
-  int64_t p = len - 1;
-  if (a.starts) {
-    const int64_t s0 = __ldcg(a.starts + b), s1 = __ldcg(a.starts + b + 1);
-    if (t < s0 || t >= s1) return;
-    p = len - (s1 - t);
-  }
-  const int64_t pre = a.prefix ? __ldcg(a.prefix + b) : 0;
-  int64_t hi = p + 1 > pre ? p + 1 : pre;
-  if (hi > len) hi = len;
-  if (p < 0) hi = 0;
-  const int64_t lo = a.window > 0 && p + 1 > a.window ? p + 1 - a.window : 0;
-  const int j = h / (a.heads / kv.kv_heads);
-  float q[E], o[E];
+
+  // ---- the pieces of work: q tiles of every sequence, scanned
+  const int64_t tokens = a.tokens;
+  auto start_of = [&](int b) {
+    const int64_t s = __ldcg(a.starts + b);
+    return int(s < 0 ? 0 : s > tokens ? tokens : s);
+  };
+  {
+    constexpr int kPer = (kPagedMaxBatch + kThreads - 1) / kThreads;
+    const int per = (kv.batch + kThreads - 1) / kThreads;
+    int mine[kPer], sum = 0;
 #pragma unroll
-  for (int i = 0; i < E; ++i) {
-    q[i] = bf16_bits_to_f32(__ldcg(a.q + t * a.q_stride + int64_t(h) * D + lane * E + i));
-    o[i] = 0.f;
-  }
-  float m = -INFINITY, l = 0.f;
-  const float slope = a.slopes ? __ldcg(a.slopes + h) : 0.f;
-  for (int64_t x = lo; x < hi; ++x) {
-    const int page = paged_page(kv, b, x, e1);
-    if (page < 0) continue;
-    const int64_t row = paged_row(kv, page, j, x);
-    float k[E], v[E];
+    for (int i = 0; i < kPer; ++i) {
+      const int b = tid * per + i;
+      mine[i] = 0;
+      if (i < per && b < kv.batch) {
+        const int n = start_of(b + 1) - start_of(b);
+        if (blockIdx.x == 0) (void)paged_len(kv, b, a.err);
+        mine[i] = n > 0 ? (n + 2 * a.per_tile - 1) / (2 * a.per_tile) : 0;
+      }
+      sum += mine[i];
+    }
+    int run = sum;
 #pragma unroll
-    for (int i = 0; i < E; ++i) {
-      const int64_t at = row * D + lane * E + i;
-      if constexpr (FP8) {
-        k[i] = e4m3_f32(static_cast<const uint8_t*>(kv.k)[at]);
-        v[i] = e4m3_f32(static_cast<const uint8_t*>(kv.v)[at]);
-      } else {
-        k[i] = bf16_bits_to_f32(static_cast<const uint16_t*>(kv.k)[at]);
-        v[i] = bf16_bits_to_f32(static_cast<const uint16_t*>(kv.v)[at]);
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(kAll, run, o);
+      if (lane >= o) run += v;
+    }
+    if (lane == 31) misc[4 + warp] = run;
+    __syncthreads();
+    int before = run - sum;
+    for (int w = 0; w < warp; ++w) before += misc[4 + w];
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int b = tid * per + i;
+      if (i < per && b < kv.batch) line[b] = before;
+      before += mine[i];
+    }
+    if (tid == kThreads - 1) line[kv.batch] = before;
+    fence_before();
+    __syncthreads();
+    fence_after();
+  }
+  const uint32_t tmem = uint32_t(misc[0]);
+  const int tiles = line[kv.batch];
+  const int64_t pieces = int64_t(tiles) * kv.kv_heads;
+  const int sms = gridDim.x;
+  int split = pieces > 0 && pieces * 2 <= sms ? int(sms / pieces) : 1;
+  split = split < kMaxSplit ? split : kMaxSplit;
+  const int64_t items = pieces * split;
+  const int G = a.group, heads = G * kv.kv_heads, TT = a.per_tile;
+
+  auto item_of = [&](int64_t idx) {
+    Item w;
+    w.part = int(idx % split);
+    const int64_t piece = idx / split;
+    w.base = split > 1 ? int(piece) : 0;
+    w.j = int(piece % kv.kv_heads);
+    const int u = tiles - 1 - int(piece / kv.kv_heads);  // the longest first
+    int lo = 0, hi = kv.batch;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (line[mid] <= u) lo = mid; else hi = mid;
+    }
+    w.b = lo;
+    const int s0 = start_of(lo), s1 = start_of(lo + 1);
+    const int q0 = (u - line[lo]) * 2 * TT;
+    w.tok0 = s0 + q0;
+    w.new_tokens = s1 - w.tok0;
+    w.len = paged_len(kv, lo, nullptr);
+    w.p0 = w.len - w.new_tokens;
+    w.pre = a.prefix ? __ldcg(a.prefix + lo) : 0;
+    const int rows = w.new_tokens < 2 * TT ? w.new_tokens : 2 * TT;
+    const int plast = w.p0 + rows - 1;
+    int top = plast + 1 > w.pre ? plast + 1 : w.pre;
+    top = top < w.len ? top : w.len;
+    w.hi = plast < 0 ? 0 : top;
+    const int pf = w.p0 > 0 ? w.p0 : 0;  // the first row with a place
+    w.lo = a.window > 0 && pf + 1 > a.window ? pf + 1 - a.window : 0;
+    if (w.lo > w.hi) w.lo = w.hi;
+    w.all_hi = w.p0 < 0 ? 0 : w.p0 + 1 > w.pre ? w.p0 + 1 : w.pre;
+    w.all_hi = w.all_hi < w.hi ? w.all_hi : w.hi;
+    w.all_lo = a.window > 0 && plast + 1 > a.window ? plast + 1 - a.window : 0;
+    const int ka = w.lo / kKeys, kb = (w.hi + kKeys - 1) / kKeys;
+    const int nk = w.hi > w.lo ? kb - ka : 0;
+    w.parts = split < nk ? split : nk > 0 ? nk : 1;
+    w.k0 = w.k1 = ka;
+    if (w.part < w.parts) {
+      w.k0 = ka + int(int64_t(nk) * w.part / w.parts);
+      w.k1 = ka + int(int64_t(nk) * (w.part + 1) / w.parts);
+    }
+    return w;
+  };
+  auto has_b = [&](const Item& w) { return w.new_tokens > TT; };
+  const int br_shift = kv.page_shift;  // rows of a box: a page, 16 .. 128
+  const int boxes = kKeys >> br_shift;
+
+  if (warp >= kMmaWarp) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+    if (warp == kLoadWarp) {
+      // ============================================================ copies
+      uint32_t n = 0;  // slots used
+      int seq = 0;     // items done
+      uint32_t nt = 0; // tiles
+      bool ok = true;
+      for (int64_t idx = blockIdx.x; ok && idx < items; idx += sms) {
+        const Item w = item_of(idx);
+        if (w.k1 <= w.k0) continue;
+        const int groups = has_b(w) ? 2 : 1;
+        // Q is free when the last score product of the item before is done
+        // (of either tile: the products of B follow A's)
+        if (seq > 0) ok = __all_sync(kAll, wait(&q_free[0], uint32_t(seq - 1) & 1u, quit, a.err));
+        if (!ok) break;
+        if (lane < groups) {
+          const uint32_t bar = smem_u32(&q_full[lane]);
+          mbar_arrive_expect_tx(bar, uint32_t(TT * G * 128 * P::kHalves));
+          for (int h = 0; h < P::kHalves; ++h)
+            tma_q(sbase + lane * P::kTile + h * P::kSpan, &map_q, 64 * h, w.j * G,
+                  w.tok0 + lane * TT, bar);
+        }
+        __syncwarp();
+        ++seq;
+        for (int kt = w.k0; ok && kt < w.k1; ++kt, ++nt) {
+          const int t = kt * kKeys + (lane << br_shift);
+          const bool in = lane < boxes && t < w.hi && t + (1 << br_shift) > w.lo;
+          const int page = in ? paged_page(kv, w.b, t, a.err) : -1;
+          const uint32_t got = __ballot_sync(kAll, page >= 0);
+          const int64_t row = page >= 0 ? paged_row(kv, page, w.j, t) : 0;
+          const uint32_t bytes_row = 128u * P::kHalves;
+          for (int part = 0; part < 2; ++part, ++n) {  // K, then V
+            if constexpr (FP8) {
+              const uint32_t s = n % P::kRaws, turn = n / P::kRaws;
+              ok = turn == 0 || wait(&raw_empty[s], (turn - 1) & 1u, quit, a.err);
+              ok = __all_sync(kAll, ok);
+              if (!ok) break;
+              const uint32_t bar = smem_u32(&raw_full[s]);
+              if (lane == 0) {
+                have[nt & 7u] = got;
+                mbar_arrive_expect_tx(bar, __popc(got) * (uint32_t(part ? D : D + 8) << br_shift));
+              }
+              __syncwarp();
+              if (page >= 0) {
+                const uint32_t dst = sbase + P::kOffRaw + s * P::kRaw;
+                const uint8_t* src = static_cast<const uint8_t*>(part ? kv.v : kv.k) + row * D;
+                bulk_copy(dst + ((uint32_t(lane) * D) << br_shift), src, uint32_t(D) << br_shift,
+                          bar);
+                if (part == 0) {  // both scales with K: the softmax needs them after S
+                  const uint32_t so = dst + kKeys * D + (uint32_t(lane) << (br_shift + 2));
+                  bulk_copy(so, kv.k_scales + row, 4u << br_shift, bar);
+                  bulk_copy(so + kKeys * 4, kv.v_scales + row, 4u << br_shift, bar);
+                }
+              }
+            } else {
+              const uint32_t s = n % P::kSlots, turn = n / P::kSlots;
+              ok = turn == 0 || wait(&empty[s], (turn - 1) & 1u, quit, a.err);
+              ok = __all_sync(kAll, ok);
+              if (!ok) break;
+              const uint32_t bar = smem_u32(&full[s]);
+              if (lane == 0) {
+                have[nt & 7u] = got;
+                mbar_arrive_expect_tx(bar, __popc(got) * (bytes_row << br_shift));
+              }
+              __syncwarp();
+              if (page >= 0) {
+                const uint32_t dst =
+                    sbase + P::kOffKv + s * P::kTile + (uint32_t(lane) << (br_shift + 7));
+                for (int h = 0; h < P::kHalves; ++h)
+                  tma_rows(dst + h * P::kSpan, part ? &map_v : &map_k, 64 * h, int(row), bar);
+              }
+            }
+          }
+        }
+      }
+      if (!ok) {  // gave up: the copies in flight land before the CTA ends
+        uint64_t* f = FP8 ? raw_full : full;
+        const uint32_t m = FP8 ? (P::kRaws ? P::kRaws : 1) : P::kSlots;
+        for (uint32_t i = 1; i <= m && i <= n; ++i)
+          (void)mbar_wait_bounded(smem_u32(&f[(n - i) % m]), ((n - i) / m) & 1u);
+        for (int g = 0; g < 2; ++g) (void)mbar_wait_bounded(smem_u32(&q_full[g]), uint32_t(seq - 1) & 1u);
+      }
+    } else if (warp == kMmaWarp) {
+      // ========================================================== products
+      if (lane == 0) {
+        uint32_t n = 0, ca = 0, cb = 0, seq = 0, qb = 0;  // slots; tiles of A, of B; items
+        bool ok = true;
+        auto scores = [&](int g, uint32_t slot) {
+          const uint32_t q = sbase + g * P::kTile, k = sbase + P::kOffKv + slot * P::kTile;
+#pragma unroll
+          for (int i = 0; i < D / 16; ++i) {
+            const uint32_t off = (i >> 2) * P::kSpan + (i & 3) * 32;
+            mma_ss(tmem + P::kColS + g * 128, desc_k(q + off), desc_k(k + off),
+                   idesc(kKeys, false), i > 0);
+          }
+        };
+        auto values = [&](int g, uint32_t slot, bool first) {
+          const uint32_t v = sbase + P::kOffKv + slot * P::kTile;
+#pragma unroll
+          for (int i = 0; i < kKeys / 16; ++i)
+            mma_ts(tmem + P::kColO + g * 128, tmem + P::kColS + g * 128 + 8 * i,
+                   desc_mn(v + i * 2048, P::kHalves > 1 ? P::kSpan : 1024), idesc(D, true),
+                   !first || i > 0);
+        };
+        auto key_ready = [&](uint32_t m) {
+          return wait(FP8 ? &ready[m % P::kSlots] : &full[m % P::kSlots], (m / P::kSlots) & 1u,
+                      quit, a.err);
+        };
+        // (bf16: an even number of slots, so that a slot is K's or V's for good)
+        auto value_ready = [&](uint32_t m) {
+          return wait(&ready[m % P::kSlots], (m / P::kSlots) & 1u, quit, a.err);
+        };
+        for (int64_t idx = blockIdx.x; ok && idx < items; idx += sms) {
+          const Item w = item_of(idx);
+          const int nk = w.k1 - w.k0;
+          if (nk <= 0) continue;
+          const bool b = has_b(w);
+          ok = wait(&q_full[0], seq & 1u, quit, a.err) && (!b || wait(&q_full[1], qb & 1u, quit, a.err)) &&
+               key_ready(n);
+          if (!ok) break;
+          fence_after();
+          scores(0, n % P::kSlots);
+          commit(&s_full[0]);
+          if (b) {
+            scores(1, n % P::kSlots);
+            commit(&s_full[1]);
+          }
+          commit(&empty[n % P::kSlots]);
+          if (nk == 1) commit(&q_free[0]);
+          for (int i = 0; i < nk; ++i, n += 2) {
+            const bool next = i + 1 < nk;
+            const uint32_t vs = (n + 1) % P::kSlots, ks = (n + 2) % P::kSlots;
+            ok = value_ready(n + 1) && (!next || key_ready(n + 2)) &&
+                 wait(&p_full[0], ca & 1u, quit, a.err);
+            if (!ok) break;
+            fence_after();
+            values(0, vs, i == 0);
+            commit(&o_done[0]);
+            ++ca;
+            if (next) {
+              scores(0, ks);
+              commit(&s_full[0]);
+            }
+            if (b) {
+              ok = wait(&p_full[1], cb & 1u, quit, a.err);
+              if (!ok) break;
+              fence_after();
+              values(1, vs, i == 0);
+              commit(&o_done[1]);
+              ++cb;
+            }
+            commit(&empty[vs]);
+            if (next) {
+              if (b) {
+                scores(1, ks);
+                commit(&s_full[1]);
+              }
+              commit(&empty[ks]);
+              if (i + 2 == nk) commit(&q_free[0]);
+            }
+          }
+          ++seq;
+          qb += b;
+        }
+        // nothing of the tensor cores is under way when the CTA ends
+        commit(drained);
+        (void)mbar_wait_bounded(smem_u32(drained), 0);
+      }
+      __syncwarp();
+    } else {
+      // ===================================== V tiles made safe; FP8 -> bf16
+      const int ft = tid - kFixWarp * 32;
+      uint32_t n = 0, nt = 0;
+      int seq = 0;
+      bool ok = true;
+      for (int64_t idx = blockIdx.x; ok && idx < items; idx += sms) {
+        const Item w = item_of(idx);
+        if (w.k1 <= w.k0) continue;
+        ++seq;
+        for (int kt = w.k0; ok && kt < w.k1; ++kt, ++nt) {
+          const int t0 = kt * kKeys;
+          for (int part = 0; part < 2; ++part, ++n) {
+            const uint32_t s = n % P::kSlots, turn = n / P::kSlots;
+            uint8_t* tile = smem + P::kOffKv + s * P::kTile;
+            if constexpr (FP8) {
+              const uint32_t rs = n % P::kRaws;
+              ok = wait(&raw_full[rs], (n / P::kRaws) & 1u, quit, a.err) &&
+                   (turn == 0 || wait(&empty[s], (turn - 1) & 1u, quit, a.err));
+              if (!ok) break;
+              const uint8_t* raw = smem + P::kOffRaw + rs * P::kRaw;
+              const uint32_t got = have[nt & 7u];
+              const bool cut = t0 < w.all_lo || t0 + kKeys > w.all_hi;
+              const uint32_t whole = kAll >> (32 - boxes);
+              const bool sure = !cut && got == whole;
+              bool bad = false;
+              constexpr int kC = D / 16;  // 16-byte pieces of a raw row
+#pragma unroll 4
+              for (int i = 0; i < kKeys * kC / kFixers; ++i) {
+                const int u = i * kFixers + ft, r = u / kC, c = u % kC;
+                uint4 x = *reinterpret_cast<const uint4*>(raw + u * 16);
+                if (!sure) {
+                  const int t = t0 + r;
+                  if (t < w.lo || t >= w.hi || !((got >> (r >> br_shift)) & 1u)) {
+                    x = make_uint4(0u, 0u, 0u, 0u);
+                  } else if (part) {
+                    uint32_t* xs[4] = {&x.x, &x.y, &x.z, &x.w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+#pragma unroll
+                      for (int o = 0; o < 32; o += 8)
+                        if (((*xs[e] >> o) & 0x7fu) == 0x7fu) {
+                          *xs[e] &= ~(0xffu << o);
+                          bad = true;
+                        }
+                  }
+                }
+                const uint4 d0 = make_uint4(e4m3x2_bf16x2(x.x), e4m3x2_bf16x2(x.x >> 16),
+                                            e4m3x2_bf16x2(x.y), e4m3x2_bf16x2(x.y >> 16));
+                const uint4 d1 = make_uint4(e4m3x2_bf16x2(x.z), e4m3x2_bf16x2(x.z >> 16),
+                                            e4m3x2_bf16x2(x.w), e4m3x2_bf16x2(x.w >> 16));
+                uint8_t* dst = tile + (c >> 2) * P::kSpan + r * 128;
+                const int ch = (c & 3) * 2;
+                *reinterpret_cast<uint4*>(dst + ((ch ^ (r & 7)) << 4)) = d0;
+                *reinterpret_cast<uint4*>(dst + (((ch + 1) ^ (r & 7)) << 4)) = d1;
+              }
+              if (part == 0) {
+                const float* sc = reinterpret_cast<const float*>(raw + kKeys * D);
+                for (int i = ft; i < 2 * kKeys; i += kFixers)
+                  scales[(nt & 3u) * 2 * kKeys + i] = sc[i];
+              }
+              if (bad) dirty[seq & 3] = seq;
+              asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+              mbar_arrive(smem_u32(&raw_empty[rs]));
+              mbar_arrive(smem_u32(&ready[s]));
+            } else {
+              if (part == 0) continue;  // K: scores of masked tokens are replaced
+              ok = wait(&full[s], turn & 1u, quit, a.err);
+              if (!ok) break;
+              const uint32_t got = have[nt & 7u];
+              const bool cut = t0 < w.all_lo || t0 + kKeys > w.all_hi;
+              if (cut || got != kAll >> (32 - boxes)) {
+                bool bad = false;
+                for (int r = ft; r < kKeys; r += kFixers) {
+                  const int t = t0 + r;
+                  const bool none =
+                      t < w.lo || t >= w.hi || !((got >> (r >> br_shift)) & 1u);
+                  for (int c = 0; c < 8 * P::kHalves; ++c) {
+                    // pieces in another order for every row: no bank conflicts
+                    uint4* p = reinterpret_cast<uint4*>(tile + (c >> 3) * P::kSpan + r * 128 +
+                                                        ((((c & 7) + r) & 7) << 4));
+                    if (none) {
+                      *p = make_uint4(0u, 0u, 0u, 0u);
+                      continue;
+                    }
+                    uint4 x = *p;
+                    uint32_t* xs[4] = {&x.x, &x.y, &x.z, &x.w};
+                    bool hit = false;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                      if ((*xs[e] & 0x7f80u) == 0x7f80u) {
+                        *xs[e] &= 0xffff0000u;
+                        hit = true;
+                      }
+                      if ((*xs[e] & 0x7f800000u) == 0x7f800000u) {
+                        *xs[e] &= 0x0000ffffu;
+                        hit = true;
+                      }
+                    }
+                    if (hit) {
+                      *p = x;
+                      bad = true;
+                    }
+                  }
+                }
+                if (bad) dirty[seq & 3] = seq;
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+              }
+              mbar_arrive(smem_u32(&ready[s]));
+            }
+          }
+        }
       }
     }
-    float s = 0.f;
+  } else {
+    // ============================================================== softmax
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+    const int g = warp >> 2, r = tid & (kRows - 1);
+    const uint32_t lanes = uint32_t((warp & 3) * 32) << 16;
+    const uint32_t ts = tmem + lanes + P::kColS + g * 128, to = tmem + lanes + P::kColO + g * 128;
+    const bool plain = !FP8 && !(a.softcap > 0.f) && !a.slopes && a.scale > 0.f;
+    const float inv_cap = a.softcap > 0.f ? 1.f / a.softcap : 0.f;
+    const int rt = r / G, rh = r - rt * G;
+    uint32_t nt = 0, my = 0;  // tiles of the CTA; tiles of this row tile
+    uint32_t met = 0;
+    int seq = 0;
+    bool ok = true;
+    // the row tile's four warps meet (a barrier that can give up)
+    auto meet = [&] {
+      mbar_arrive(smem_u32(&join[g]));
+      return __all_sync(kAll, wait(&join[g], met++ & 1u, quit, a.err)) != 0;
+    };
+    for (int64_t idx = blockIdx.x; ok && idx < items; idx += sms) {
+      const Item w = item_of(idx);
+      if (w.part >= w.parts) continue;
+      const int nk = w.k1 - w.k0;
+      if (nk > 0) ++seq;
+      const int tok = g * TT + rt;  // among the item's tokens
+      const bool mine = rt < TT && tok < w.new_tokens;
+      if (g == 1 && !has_b(w)) {
+        nt += nk;
+        continue;
+      }
+      const int p = w.p0 + tok, h = w.j * G + rh;
+      // the tokens this row sees; a row of no token takes whatever comes
+      int rhi = 0x7fffffff, rlo = 0;
+      if (mine) {
+        rhi = p < 0 ? 0 : p + 1 > w.pre ? p + 1 : w.pre;
+        rhi = rhi < w.len ? rhi : w.len;
+        rlo = a.window > 0 && p + 1 > a.window ? p + 1 - a.window : 0;
+      }
+      const float slope = a.slopes && mine ? __ldcg(a.slopes + h) * kLog2e : 0.f;
+      float m = -INFINITY, l = 0.f;
+      bool holes = false;  // in any tile
+      for (int i = 0; i < nk; ++i, ++nt, ++my) {
+        ok = __all_sync(kAll, wait(&s_full[g], my & 1u, quit, a.err));
+        if (!ok) break;
+        fence_after();
+        const int t0 = (w.k0 + i) * kKeys;
+        const uint32_t got = have[nt & 7u];
+        uint32_t s[4][32];
 #pragma unroll
-    for (int i = 0; i < E; ++i) s = fmaf(q[i], k[i], s);
-    s = warp_sum(s) * a.scale;
-    if constexpr (FP8) s *= kv.k_scales[row];
-    if (a.softcap > 0.f) s = cap_score(s, a.softcap, 1.f / a.softcap);
-    s += slope * float(x - p);
-    const float mn = fmaxf(m, s);
-    const float al = mn == -INFINITY ? 1.f : expf(m - mn);
-    const float w = mn == -INFINITY ? 0.f : expf(s - mn);
-    m = mn;
-    l = l * al + w;
-    const float wv = FP8 ? w * kv.v_scales[row] : w;
+        for (int c = 0; c < 4; ++c) tmem_ld32(ts + 32 * c, s[c]);
+        wait_ld();
+        const bool whole = got == kAll >> (32 - boxes);
+        holes |= !whole;
+        const bool clear = __all_sync(kAll, t0 >= rlo && t0 + kKeys <= rhi) && whole;
+        float mul = a.scale * kLog2e;
+        const float* ks = scales + ((nt & 3u) * 2) * kKeys;
+        if (!plain) {
 #pragma unroll
-    for (int i = 0; i < E; ++i) o[i] = o[i] * al + wv * v[i];
+          for (int c = 0; c < 4; ++c)
+#pragma unroll
+            for (int e = 0; e < 32; ++e) {
+              float v = __uint_as_float(s[c][e]) * a.scale;
+              if constexpr (FP8) v *= ks[32 * c + e];
+              if (a.softcap > 0.f) v = cap_score(v, a.softcap, inv_cap);
+              s[c][e] = __float_as_uint(fmaf(slope, float(t0 + 32 * c + e - p), v * kLog2e));
+            }
+          mul = 1.f;
+        }
+        if (!clear) {
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+#pragma unroll
+            for (int e = 0; e < 32; ++e) {
+              const int t = t0 + 32 * c + e;
+              if (t < rlo || t >= rhi || !((got >> ((32 * c + e) >> br_shift)) & 1u))
+                s[c][e] = 0xff800000u;
+            }
+        }
+        float mx[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          mx[c] = __uint_as_float(s[c][0]);
+#pragma unroll
+          for (int e = 1; e < 32; ++e) mx[c] = fmaxf(mx[c], __uint_as_float(s[c][e]));
+        }
+        const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * mul;
+        if (i == 0) {
+          m = mt;
+        } else {
+          const bool up = mt > m + 8.f;  // also from -inf, where nothing was seen yet
+          if (__any_sync(kAll, up)) {
+            const float f = up ? ex2(m - mt) : 1.f;
+            if (up) m = mt;
+            l *= f;
+            ok = __all_sync(kAll, wait(&o_done[g], (my - 1) & 1u, quit, a.err));
+            if (!ok) break;
+            fence_after();
+#pragma unroll 1
+            for (int c = 0; c < D / 32; ++c) {
+              uint32_t o[32];
+              tmem_ld32(to + 32 * c, o);
+              wait_ld();
+#pragma unroll
+              for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+              tmem_st32(to + 32 * c, o);
+            }
+          }
+        }
+        const float off = m == -INFINITY ? 0.f : -m;
+        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+        const float* vsc = ks + kKeys;
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          uint32_t pk[32];
+#pragma unroll
+          for (int e = 0; e < 32; ++e) {
+            const int x = 2 * e & 31;
+            float p0 = ex2(fmaf(__uint_as_float(s[2 * c + (e >> 4)][x]), mul, off));
+            float p1 = ex2(fmaf(__uint_as_float(s[2 * c + (e >> 4)][x + 1]), mul, off));
+            sum[e & 3] += p0 + p1;
+            if constexpr (FP8) {
+              // a masked token's scale may be anything
+              const float2 v = *reinterpret_cast<const float2*>(vsc + 64 * c + 2 * e);
+              p0 = clear || p0 > 0.f ? p0 * v.x : 0.f;
+              p1 = clear || p1 > 0.f ? p1 * v.y : 0.f;
+            }
+            pk[e] = bf16x2(p0, p1);
+          }
+          tmem_st32(ts + 32 * c, pk);
+        }
+        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        wait_st();
+        fence_before();
+        mbar_arrive(smem_u32(&p_full[g]));
+      }
+      if (!ok) break;
+
+      // ---- the item's end
+      if (nk > 0) {
+        ok = __all_sync(kAll, wait(&o_done[g], (my - 1) & 1u, quit, a.err));
+        if (!ok) break;
+        fence_after();
+      }
+      const int64_t row = int64_t(w.tok0 + tok) * heads + h;
+      const bool poisoned = nk > 0 && *static_cast<volatile int*>(&dirty[seq & 3]) == seq;
+      // values that are not finite and were kept out of the product, from the
+      // tiles where that was done
+      auto add_not_finite = [&](float* o, int d0) {
+        for (int t = rlo > w.k0 * kKeys ? rlo : w.k0 * kKeys; t < rhi && t < w.k1 * kKeys; ++t) {
+          const int t0 = t / kKeys * kKeys;
+          if (!holes && t0 >= w.all_lo && t0 + kKeys <= w.all_hi) {
+            t = t0 + kKeys - 1;
+            continue;
+          }
+          const int page = paged_page(kv, w.b, t, nullptr);
+          if (page < 0) continue;
+          const int64_t at = paged_row(kv, page, w.j, t) * D + d0;
+          for (int d = 0; d < 32; ++d) {
+            if constexpr (FP8) {
+              if ((__ldcg(static_cast<const uint8_t*>(kv.v) + at + d) & 0x7f) == 0x7f) o[d] = NAN;
+            } else {
+              const float x = bf16_bits_to_f32(__ldcg(static_cast<const uint16_t*>(kv.v) + at + d));
+              if (!(fabsf(x) <= 3.4028234663852886e38f)) o[d] += x;
+            }
+          }
+        }
+      };
+      auto store = [&](const float* o, int c, float inv) {  // 32 dims from 32 c on
+        uint4* dst = reinterpret_cast<uint4*>(a.out + row * D + 32 * c);
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          dst[e] = make_uint4(bf16x2(o[8 * e] * inv, o[8 * e + 1] * inv),
+                              bf16x2(o[8 * e + 2] * inv, o[8 * e + 3] * inv),
+                              bf16x2(o[8 * e + 4] * inv, o[8 * e + 5] * inv),
+                              bf16x2(o[8 * e + 6] * inv, o[8 * e + 7] * inv));
+      };
+      auto close = [&](float& mm, float& ll) {  // the sink; returns the factor of O
+        float f = 1.f;
+        if (a.sinks) {
+          const float z = __ldcg(a.sinks + h) * kLog2e;
+          const float m2 = fmaxf(mm, z);
+          f = mm == -INFINITY ? 0.f : ex2(mm - m2);
+          ll = ll * f + ex2(z - m2);
+          mm = m2;
+        }
+        if (a.lse)
+          a.lse[row] = ll == 0.f ? -INFINITY : (mm + log2f(ll)) * 0.6931471805599453f;
+        return f * (ll > 0.f ? 1.f / ll : ll == 0.f ? 0.f : ll);
+      };
+      if (w.parts == 1) {
+        float inv = 0.f;
+        if (mine) inv = close(m, l);
+#pragma unroll 1
+        for (int c = 0; c < D / 32; ++c) {
+          uint32_t o[32];
+          if (nk > 0) {
+            tmem_ld32(to + 32 * c, o);
+            wait_ld();
+          } else {
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = 0u;
+          }
+          float of[32];
+#pragma unroll
+          for (int e = 0; e < 32; ++e) of[e] = __uint_as_float(o[e]);
+          if (mine) {
+            if (poisoned) add_not_finite(of, 32 * c);
+            store(of, c, inv);
+          }
+        }
+        fence_before();
+        continue;
+      }
+      // a part: O [D / 4][128 rows] float4, max [128], sum [128]
+      constexpr int kPartFloats = kRows * (D + 2);
+      auto part_at = [&](int q) {
+        return a.parts + (int64_t(w.base) * split + q) * 2 * kPartFloats + g * kPartFloats;
+      };
+      float* mypart = part_at(w.part);
+#pragma unroll 1
+      for (int c = 0; c < D / 32; ++c) {
+        uint32_t o[32];
+        tmem_ld32(to + 32 * c, o);
+        wait_ld();
+        float of[32];
+#pragma unroll
+        for (int e = 0; e < 32; ++e) of[e] = __uint_as_float(o[e]);
+        if (mine && poisoned) add_not_finite(of, 32 * c);
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          *reinterpret_cast<float4*>(mypart + ((8 * c + e) * kRows + r) * 4) =
+              make_float4(of[4 * e], of[4 * e + 1], of[4 * e + 2], of[4 * e + 3]);
+      }
+      mypart[kRows * D + r] = m;
+      mypart[kRows * (D + 1) + r] = l;
+      fence_before();
+      __threadfence();
+      if (!(ok = meet())) break;
+      if (r == 0)
+        misc[2 + g] = atomicAdd(a.counters + 2 * w.base + g, 1) == w.parts - 1;
+      if (!(ok = meet())) break;
+      if (misc[2 + g]) {
+        __threadfence();
+        if (r == 0) a.counters[2 * w.base + g] = 0;  // ready for the next call
+        float M = -INFINITY, L = 0.f;
+        for (int q = 0; q < w.parts; ++q) M = fmaxf(M, __ldcg(part_at(q) + kRows * D + r));
+        for (int q = 0; q < w.parts; ++q)
+          L += M == -INFINITY ? 0.f
+                              : ex2(__ldcg(part_at(q) + kRows * D + r) - M) *
+                                    __ldcg(part_at(q) + kRows * (D + 1) + r);
+        const float Mraw = M;
+        float inv = 0.f;
+        if (mine) inv = close(M, L);
+#pragma unroll 1
+        for (int c = 0; c < D / 32; ++c) {
+          float of[32];
+#pragma unroll
+          for (int e = 0; e < 32; ++e) of[e] = 0.f;
+          for (int q = 0; q < w.parts; ++q) {
+            const float* pq = part_at(q);
+            const float f = Mraw == -INFINITY ? 0.f : ex2(__ldcg(pq + kRows * D + r) - Mraw);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              const float4 v =
+                  __ldcg(reinterpret_cast<const float4*>(pq + ((8 * c + e) * kRows + r) * 4));
+              of[4 * e] = fmaf(v.x, f, of[4 * e]);
+              of[4 * e + 1] = fmaf(v.y, f, of[4 * e + 1]);
+              of[4 * e + 2] = fmaf(v.z, f, of[4 * e + 2]);
+              of[4 * e + 3] = fmaf(v.w, f, of[4 * e + 3]);
+            }
+          }
+          if (mine) store(of, c, inv);
+        }
+      }
+    }
   }
-  if (a.sinks) {
-    const float s = __ldcg(a.sinks + h);
-    const float mn = fmaxf(m, s);
-    const float al = m == -INFINITY ? 0.f : expf(m - mn);
-    m = mn;
-    l = l * al + expf(s - mn);
-#pragma unroll
-    for (int i = 0; i < E; ++i) o[i] *= al;
-  }
-  const float inv = l > 0.f ? 1.f / l : 0.f;
-#pragma unroll
-  for (int i = 0; i < E; ++i) {
-    const __nv_bfloat16 r = __float2bfloat16_rn(o[i] * inv);
-    a.out[(t * a.heads + h) * D + lane * E + i] = *reinterpret_cast<const uint16_t*>(&r);
-  }
-  if (a.lse && lane == 0) a.lse[t * a.heads + h] = l > 0.f ? m + logf(l) : -INFINITY;
+  // ---- every role is done (or has given up): free the tensor memory
+  fence_before();
+  __syncthreads();
+  if (warp == kMmaWarp)
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512)
+                 : "memory");
 }
 
-cudaError_t launch(const PagedKv& kv, int D, bool fp8, const PagedAttnArgs& a, cudaStream_t s,
-                   bool pdl) {
-  const DeviceInfo* di = device_info();
-  if (!di) return cudaErrorNoDevice;
+cudaError_t encode(CUtensorMap* map, const void* base, int rank, const cuuint64_t* dims,
+                   const cuuint64_t* strides, const cuuint32_t* box) {
+  EncodeTiledFn enc = tensor_map_encoder();
+  if (!enc) return cudaErrorNotSupported;
+  const cuuint32_t estr[3] = {1u, 1u, 1u};
+  if (enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, cuuint32_t(rank), const_cast<void*>(base), dims,
+          strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+    return cudaErrorInvalidValue;
+  return cudaSuccess;
+}
+
+template <int D, bool FP8>
+cudaError_t launch(const DeviceInfo& di, const PagedKv& kv, const PagedAttnArgs& a,
+                   cudaStream_t s, bool pdl) {
+  using P = Plan<D, FP8>;
+  auto kern = paged_prefill_kernel<D, FP8>;
+  const int G = a.heads / kv.kv_heads, TT = kRows / G;
+  CUtensorMap mq, mk = {}, mv = {};
+  {
+    const cuuint64_t dims[3] = {cuuint64_t(D), cuuint64_t(a.heads), cuuint64_t(a.tokens)};
+    const cuuint64_t strides[2] = {cuuint64_t(D) * 2, cuuint64_t(a.q_stride) * 2};
+    const cuuint32_t box[3] = {64u, cuuint32_t(G), cuuint32_t(TT)};
+    if (cudaError_t e = encode(&mq, a.q, 3, dims, strides, box)) return e;
+  }
+  if (!FP8) {
+    const cuuint64_t dims[2] = {cuuint64_t(D),
+                                (cuuint64_t(kv.num_pages) * kv.kv_heads) << kv.page_shift};
+    const cuuint64_t strides[1] = {cuuint64_t(D) * 2};
+    const cuuint32_t box[2] = {64u, 1u << kv.page_shift};
+    if (cudaError_t e = encode(&mk, kv.k, 2, dims, strides, box)) return e;
+    if (cudaError_t e = encode(&mv, kv.v, 2, dims, strides, box)) return e;
+  }
+  if (cudaError_t e = ensure_smem(di, kern, P::kSmem)) return e;
+  PrefillArgs d;
+  d.starts = a.starts;
+  d.tokens = a.tokens;
+  d.group = G;
+  d.per_tile = TT;
+  d.scale = a.scale;
+  d.softcap = a.softcap;
+  d.window = a.window;
+  d.slopes = a.slopes;
+  d.sinks = a.sinks;
+  d.prefix = a.prefix;
+  d.out = a.out;
+  d.lse = a.lse;
+  d.counters = static_cast<int32_t*>(a.ws);
+  d.parts = reinterpret_cast<float*>(static_cast<uint8_t*>(a.ws) + kCounters * 4);
+  d.err = di.error_word;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(unsigned((a.tokens * a.heads + 3) / 4));
-  cfg.blockDim = dim3(128);
+  cfg.gridDim = dim3(unsigned(di.sms < kCounters ? di.sms : kCounters));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = P::kSmem;
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = pdl ? 1 : 0;
-  if (D == 64)
-    return fp8 ? cudaLaunchKernelEx(&cfg, paged_attention_kernel<64, true>, kv, a, di->error_word)
-               : cudaLaunchKernelEx(&cfg, paged_attention_kernel<64, false>, kv, a,
-                                    di->error_word);
-  return fp8 ? cudaLaunchKernelEx(&cfg, paged_attention_kernel<128, true>, kv, a, di->error_word)
-             : cudaLaunchKernelEx(&cfg, paged_attention_kernel<128, false>, kv, a,
-                                  di->error_word);
+  return cudaLaunchKernelEx(&cfg, kern, mq, mk, mv, kv, d);
 }
 
 }  // namespace
 
-size_t paged_prefill_workspace_bytes(int) { return 16; }
+size_t paged_prefill_workspace_bytes(int head_dim) {
+  // counters, and one part of two row tiles per CTA
+  const DeviceInfo* di = device_info();
+  const int64_t ctas = di && di->sms < kCounters ? di->sms : kCounters;
+  return size_t(kCounters) * 4 + size_t(ctas) * 2 * kRows * (head_dim + 2) * 4;
+}
+
 cudaError_t launch_paged_prefill(const PagedKv& kv, int head_dim, bool fp8,
                                  const PagedAttnArgs& a, cudaStream_t s, bool pdl) {
-  return launch(kv, head_dim, fp8, a, s, pdl);
+  const DeviceInfo* di = device_info();
+  if (!di) return cudaErrorNoDevice;
+  if (head_dim == 64)
+    return fp8 ? launch<64, true>(*di, kv, a, s, pdl) : launch<64, false>(*di, kv, a, s, pdl);
+  return fp8 ? launch<128, true>(*di, kv, a, s, pdl) : launch<128, false>(*di, kv, a, s, pdl);
 }
 
 }  // namespace tt
