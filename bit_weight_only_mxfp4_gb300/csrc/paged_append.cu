@@ -15,11 +15,11 @@
 // sincospi, rounded to 2^-24 of the half turn.
 //
 // Bound by bytes for a prompt (every row read and written once) and by
-// latency for a decode step.  A CTA takes one token and a share of its
-// heads: it computes the rot/2 sines and cosines once into shared memory
-// while its first rows of q, k and v are already on their way, and each
-// group of head_dim/8 lanes then rotates one row: 16 bytes a lane, the
-// partner elements by shuffle.
+// latency for a decode step.  A CTA takes one or four tokens: its threads look
+// up the tokens' places and compute each sine and cosine once, into shared
+// memory, and after one barrier each group of head_dim/16 lanes rotates one
+// row at a time, a lane both elements of its eight pairs (two 16-byte pieces),
+// with the next rows' loads in flight.
 #include "launch.h"
 #include "paged.cuh"
 
@@ -78,139 +78,190 @@ __device__ __forceinline__ uint32_t e4m3x2(float a, float b) {
   return r;
 }
 
-template <int D, bool FP8>
+// kTok tokens per CTA; blockIdx.y: a share of their rows.
+template <int D, bool FP8, int kTok>
 __global__ void __launch_bounds__(kThreads)
-    paged_append_kernel(const PagedKv kv, const AppendArgs a) {
-  constexpr int LPR = D / 8;           // lanes per row
-  constexpr int RPC = kThreads / LPR;  // rows per CTA and round
-  __shared__ float2 cs[D / 2];
-  __shared__ int s_page;
-  __shared__ int64_t s_place;
+    paged_append_kernel(const PagedKv kv, const AppendArgs a, int64_t tokens) {
+  constexpr int U = D / 16;            // lanes per row
+  constexpr int RPC = kThreads / U;    // rows per round
+  constexpr int kPairs = D / 2;
+  __shared__ float2 cs[kTok][kPairs];  // pair 8u + k at [k * U + u]: lanes read side by side
+  __shared__ int s_page[kTok];
+  __shared__ int64_t s_place[kTok];
   const int tid = threadIdx.x, lane = tid & 31;
-  const int64_t t = blockIdx.x;
-  const int sub = tid % LPR;
+  const int64_t t0 = int64_t(blockIdx.x) * kTok;
+  const int unit = tid % U;
   const int rows = a.heads + 2 * kv.kv_heads;
-  const int rot = a.rope.turns ? a.rope.rot : 0, half = rot >> 1;
+  const int rot = a.rope.turns ? a.rope.rot : 0;
+  // this lane's two pieces of 8 elements: the elements of its pairs, or two
+  // neighbours past the rotated part
+  const bool turns = unit < rot / 16;
+  const bool halved = turns && !a.rope.interleaved;
+  const int p0 = halved ? unit : 2 * unit;
+  const int p1 = halved ? unit + rot / 16 : 2 * unit + 1;
   pdl_allow_next_grid();
   pdl_wait_prior_grid();
 
-  auto source = [&](int r) {
+  struct Two {
+    uint4 x, y;
+  };
+  auto source = [&](int tk, int r) {
+    const int64_t t = t0 + tk;
     const uint16_t* p = r < a.heads ? a.q + t * a.q_stride + int64_t(r) * D
                         : r < a.heads + kv.kv_heads
                             ? a.k + t * a.kv_stride + int64_t(r - a.heads) * D
                             : a.v + t * a.kv_stride + int64_t(r - a.heads - kv.kv_heads) * D;
-    return __ldcg(reinterpret_cast<const uint4*>(p) + sub);
+    const uint4* u = reinterpret_cast<const uint4*>(p);
+    return Two{__ldcg(u + p0), __ldcg(u + p1)};
   };
-  int r = blockIdx.y * RPC + tid / LPR;
-  uint4 raw = r < rows ? source(r) : make_uint4(0u, 0u, 0u, 0u);
-
-  // Warp 0: the token's sequence, place and page.
-  if (tid < 32) {
-    const int b = a.starts ? paged_seq_of(a.starts, kv.batch, t, lane) : int(t);
-    int32_t* e = lane == 0 ? a.err : nullptr;
-    const int len = paged_len(kv, b, e);
-    int64_t place = int64_t(len) - 1;
-    if (a.starts) {
-      const int64_t s0 = __ldcg(a.starts + b), s1 = __ldcg(a.starts + b + 1);
-      place = t >= s0 && t < s1 ? len - (s1 - t) : kNowhere;
-    }
-    const int page = place >= 0 ? paged_page(kv, b, place, e) : -1;
-    if (lane == 0) {
-      s_page = page;
-      s_place = place;
-    }
-  }
-  __syncthreads();
-  const int64_t place = s_place;
-  const int page = s_page;
-  if (place == kNowhere) return;
-  for (int i = tid; i < half; i += kThreads) {
-    int64_t pos = place;
-    if (a.rope.positions) {
-      int ax = a.rope.pair_axis ? a.rope.pair_axis[i] : 0;
-      ax = ax < a.rope.axes ? ax : a.rope.axes - 1;
-      pos = __ldcg(a.rope.positions + int64_t(ax) * gridDim.x + t);
-    }
-    const uint64_t ph = uint64_t(pos) * a.rope.turns[i];
-    float sn, cn;
-    sincospif(float(int32_t(ph >> 32)) * 0x1p-31f, &sn, &cn);
-    cs[i] = make_float2(cn, sn);
-  }
-  __syncthreads();
-
+  // this thread's rows: (token, row), RPC rows further each round
+  int tk = 0, r = blockIdx.y * RPC + tid / U;
   const int step = gridDim.y * RPC;
-  for (; r - tid / LPR < rows; r += step) {
-    const uint4 next = r + step < rows ? source(r + step) : make_uint4(0u, 0u, 0u, 0u);
-    float x[8];
-    unpack8(raw, x);
-    if (rot) {
-      float y[8];
-      if (a.rope.interleaved) {
+  const int ntok = tokens - t0 < kTok ? int(tokens - t0) : kTok;
+  auto settle = [&] {
+    while (r >= rows && tk < ntok) {
+      r -= rows;
+      ++tk;
+    }
+  };
+  settle();
+  Two raw{};
+  if (tk < ntok) raw = source(tk, r);
+
+  // ---- places and angles: one pair of one token a thread
+  constexpr int kShare = kThreads / kTok < kPairs ? kThreads / kTok : kPairs;
+  if (tid < kTok * kShare) {
+    const int my = tid / kShare;  // a warp has one token
+    const int64_t t = t0 + my;
+    if (my < ntok) {
+      const int b = a.starts ? paged_seq_of(a.starts, kv.batch, t, lane) : int(t);
+      const bool says = tid % kShare == 0;
+      int32_t* e = says ? a.err : nullptr;
+      const int len = paged_len(kv, b, e);
+      int64_t place = int64_t(len) - 1;
+      if (a.starts) {
+        const int64_t s0 = __ldcg(a.starts + b), s1 = __ldcg(a.starts + b + 1);
+        place = t >= s0 && t < s1 ? len - (s1 - t) : kNowhere;
+      }
+      if (says) {
+        s_place[my] = place;
+        s_page[my] = place >= 0 ? paged_page(kv, b, place, e) : -1;
+      }
+      for (int i = tid % kShare; i < rot / 2; i += kShare) {
+        int64_t pos = place;
+        if (a.rope.positions) {
+          int ax = a.rope.pair_axis ? a.rope.pair_axis[i] : 0;
+          ax = ax < a.rope.axes ? ax : a.rope.axes - 1;
+          pos = __ldcg(a.rope.positions + int64_t(ax) * tokens + t);
+        }
+        const uint64_t ph = uint64_t(pos) * a.rope.turns[i];
+        float sn, cn;
+        sincospif(float(int32_t(ph >> 32)) * 0x1p-31f, &sn, &cn);
+        cs[my][(i & 7) * U + (i >> 3)] = make_float2(cn, sn);
+      }
+    }
+  }
+  __syncthreads();
+
+  // ---- rows: the whole warp stays while any of its lanes has one
+  while (__any_sync(kAll, tk < ntok)) {
+    const bool have = tk < ntok;
+    const int ct = have ? tk : 0, cr = r;
+    float x[8], y[8];
+    unpack8(raw.x, x);
+    unpack8(raw.y, y);
+    r += step;
+    settle();
+    if (tk < ntok) raw = source(tk, r);
+    const bool is_v = cr >= a.heads + kv.kv_heads;
+    if (turns && !is_v) {
+      if (halved) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float2 c = 8 * sub < rot ? cs[4 * sub + i] : make_float2(1.f, 0.f);
-          y[2 * i] = x[2 * i] * c.x - x[2 * i + 1] * c.y;
-          y[2 * i + 1] = x[2 * i] * c.y + x[2 * i + 1] * c.x;
+        for (int k = 0; k < 8; ++k) {
+          const float2 c = cs[ct][k * U + unit];
+          const float u = x[k] * c.x - y[k] * c.y;
+          y[k] = x[k] * c.y + y[k] * c.x;
+          x[k] = u;
         }
       } else {
-        const int hl = half >> 3;  // lanes of the first half
-        const bool first = sub < hl, in = 8 * sub < rot;
-        const int from = !in ? lane : first ? lane + hl : lane - hl;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float o = __shfl_sync(kAll, x[i], from);
-          const float2 c = in ? cs[8 * (first ? sub : sub - hl) + i] : make_float2(1.f, 0.f);
-          y[i] = x[i] * c.x + (first ? -o : o) * c.y;
-          if (!in) y[i] = x[i];
+        for (int k = 0; k < 8; ++k) {
+          const float2 c = cs[ct][k * U + unit];
+          float* z = k < 4 ? x + 2 * k : y + 2 * (k - 4);
+          const float u = z[0] * c.x - z[1] * c.y;
+          z[1] = z[0] * c.y + z[1] * c.x;
+          z[0] = u;
         }
       }
-      if (8 * sub < rot && r < a.heads + kv.kv_heads) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = y[i];
-      }
     }
-    if (r < a.heads) {
-      const uint4 w = place >= 0 ? pack8(x) : make_uint4(0u, 0u, 0u, 0u);
-      *reinterpret_cast<uint4*>(a.q_out + (t * a.heads + r) * D + 8 * sub) = w;
+    const int64_t place = s_place[ct];
+    const int page = s_page[ct];
+    if (have && cr < a.heads && place != kNowhere) {
+      const bool in = place >= 0;
+      uint4* o = reinterpret_cast<uint4*>(a.q_out + ((t0 + ct) * a.heads + cr) * D);
+      o[p0] = in ? pack8(x) : make_uint4(0u, 0u, 0u, 0u);
+      o[p1] = in ? pack8(y) : make_uint4(0u, 0u, 0u, 0u);
     }
-    const int jr = r - a.heads;  // k head, or kv_heads + v head
-    const bool is_k = jr < kv.kv_heads;
-    const int j = is_k ? jr : jr - kv.kv_heads;
-    const bool store = jr >= 0 && r < rows && page >= 0;
+    const bool store = have && cr >= a.heads && page >= 0 && place >= 0;
+    const int j = cr - a.heads - (is_v ? kv.kv_heads : 0);
     const int64_t row = store ? paged_row(kv, page, j, place) : 0;
     if constexpr (FP8) {
       // a NaN or an infinity gives the row a NaN scale and zero codes
       float m = 0.f;
       bool bad = false;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        m = fmaxf(m, fabsf(x[i]));
-        bad |= !(fabsf(x[i]) <= 3.4028234663852886e38f);
+      for (int k = 0; k < 8; ++k) {
+        m = fmaxf(m, fmaxf(fabsf(x[k]), fabsf(y[k])));
+        bad |= !(fabsf(x[k]) <= 3.4028234663852886e38f) || !(fabsf(y[k]) <= 3.4028234663852886e38f);
       }
+      if (bad) m = INFINITY;
 #pragma unroll
-      for (int o = LPR / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kAll, m, o));
-      const uint32_t votes = __ballot_sync(kAll, bad);
-      const uint32_t row_lanes = ((1u << LPR) - 1) << (lane & ~(LPR - 1));
+      for (int o = U / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kAll, m, o));
       if (store) {
-        const bool ok = (votes & row_lanes) == 0u;
+        const bool ok = m < INFINITY;
         const float s = m / 448.f;
-        uint32_t c[4] = {0u, 0u, 0u, 0u};
+        uint32_t c[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
         if (ok && s > 0.f) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) c[i] = e4m3x2(x[2 * i] / s, x[2 * i + 1] / s);
+          for (int k = 0; k < 4; ++k) {
+            c[k] = e4m3x2(x[2 * k] / s, x[2 * k + 1] / s);
+            c[k + 4] = e4m3x2(y[2 * k] / s, y[2 * k + 1] / s);
+          }
         }
-        uint8_t* base = static_cast<uint8_t*>(is_k ? kv.k : kv.v);
-        *reinterpret_cast<uint2*>(base + row * D + 8 * sub) =
-            make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
-        if (sub == 0)
-          (is_k ? kv.k_scales : kv.v_scales)[row] = ok ? s : __int_as_float(0x7fc00000);
+        uint2* o = reinterpret_cast<uint2*>(static_cast<uint8_t*>(is_v ? kv.v : kv.k) + row * D);
+        o[p0] = make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
+        o[p1] = make_uint2(c[4] | (c[5] << 16), c[6] | (c[7] << 16));
+        if (unit == 0)
+          (is_v ? kv.v_scales : kv.k_scales)[row] = ok ? s : __int_as_float(0x7fc00000);
       }
     } else if (store) {
-      uint16_t* base = static_cast<uint16_t*>(is_k ? kv.k : kv.v);
-      *reinterpret_cast<uint4*>(base + row * D + 8 * sub) = pack8(x);
+      uint4* o = reinterpret_cast<uint4*>(static_cast<uint16_t*>(is_v ? kv.v : kv.k) + row * D);
+      o[p0] = pack8(x);
+      o[p1] = pack8(y);
     }
-    raw = next;
   }
+}
+
+template <int D, bool FP8>
+cudaError_t launch(const DeviceInfo& di, const PagedKv& kv, const AppendArgs& a, int64_t tokens,
+                   cudaStream_t s, bool pdl) {
+  const int per = kThreads / (D / 16);
+  const int rounds = (a.heads + 2 * kv.kv_heads + per - 1) / per;
+  // Few tokens (a decode step): a CTA per token and round of rows, so that no
+  // row waits for another.  From eight tokens per SM on, four tokens a CTA:
+  // a barrier and the angles serve four times the rows.
+  const bool many = tokens >= 8 * di.sms;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = many ? dim3(unsigned((tokens + 3) / 4)) : dim3(unsigned(tokens), unsigned(rounds));
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = pdl ? 1 : 0;
+  return many ? cudaLaunchKernelEx(&cfg, paged_append_kernel<D, FP8, 4>, kv, a, tokens)
+              : cudaLaunchKernelEx(&cfg, paged_append_kernel<D, FP8, 1>, kv, a, tokens);
 }
 
 }  // namespace
@@ -228,25 +279,11 @@ cudaError_t launch_paged_append(const PagedKv& kv, int head_dim, bool fp8, const
   const DeviceInfo* di = device_info();
   if (!di) return cudaErrorNoDevice;
   const AppendArgs a{q, k, v, q_stride, kv_stride, starts, heads, rope, q_out, di->error_word};
-  const int per = kThreads / (head_dim / 8);
-  const int rounds = (heads + 2 * kv.kv_heads + per - 1) / per;
-  // Few tokens: a CTA per round of rows, so that no row waits for another;
-  // many: one CTA goes through all of a token's rows on one set of angles.
-  const int share = tokens * rounds <= 4 * di->sms ? rounds : 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(unsigned(tokens), unsigned(share));
-  cfg.blockDim = dim3(kThreads);
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = pdl ? 1 : 0;
   if (head_dim == 64)
-    return fp8 ? cudaLaunchKernelEx(&cfg, paged_append_kernel<64, true>, kv, a)
-               : cudaLaunchKernelEx(&cfg, paged_append_kernel<64, false>, kv, a);
-  return fp8 ? cudaLaunchKernelEx(&cfg, paged_append_kernel<128, true>, kv, a)
-             : cudaLaunchKernelEx(&cfg, paged_append_kernel<128, false>, kv, a);
+    return fp8 ? launch<64, true>(*di, kv, a, tokens, s, pdl)
+               : launch<64, false>(*di, kv, a, tokens, s, pdl);
+  return fp8 ? launch<128, true>(*di, kv, a, tokens, s, pdl)
+             : launch<128, false>(*di, kv, a, tokens, s, pdl);
 }
 
 }  // namespace tt

@@ -286,64 +286,65 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int ps = 1 << kv.page_shift;
     const int br = ps < kTok ? ps : kTok;  // rows of a box
     const int nb = kTok / br;              // boxes of K (and of V) a tile
-    At at = find(L, kv.batch, i0);
-    int page = -1, t = 0;
-    auto look = [&](const At& w) {  // this lane's box of the tile: its page, or -1
-      t = (L.first_tile(w.b) + w.tile) * kTok + lane * br;
-      const int n = slen[w.b];
-      // boxes wholly before the window or past the length are not copied
-      const bool in = lane < nb && t < n && (a.window == 0 || t + br > n - a.window);
-      page = in ? paged_page(kv, w.b, t, a.err) : -1;
+    // Lane l looks up box l % nb of the tile l / nb of a batch of 32 / nb
+    // tiles, one batch ahead of the copies, and issues that box's copies when
+    // its tile's turn comes: no table entry is waited for in the loop.
+    const int nb_shift = __popc(nb - 1), tb = 32 >> nb_shift;
+    int page, j, t;
+    auto look = [&](int base) {
+      const int it = base + (lane >> nb_shift);
+      page = -1;
+      if (it < i1) {
+        const At w = find(L, kv.batch, it);
+        const int n = slen[w.b];
+        j = w.j;
+        t = (L.first_tile(w.b) + w.tile) * kTok + (lane & (nb - 1)) * br;
+        // boxes wholly before the window or past the length are not copied
+        if (t < n && (a.window == 0 || t + br > n - a.window))
+          page = paged_page(kv, w.b, t, a.err);
+      }
     };
-    look(at);
-    for (int it = i0; it < i1; ++it) {
-      const int idx = it - i0, st = idx % P::kStages;
-      const uint32_t bar = smem_u32(&full[st]);
-      const int my_page = page, my_t = t;
-      const int j = at.j;
-      // the next tile's pages, while this stage is awaited
-      if (++at.tile == L.tiles(at.b)) {
-        at.tile = 0;
-        if (++at.j == kv.kv_heads) {
-          at.j = 0;
-          do ++at.b;
-          while (at.b < kv.batch && L.tiles(at.b) == 0);
+    look(i0);
+    for (int base = i0; base < i1; base += tb) {
+      const int my_page = page, my_j = j, my_t = t;
+      look(base + tb);
+      const uint32_t got = __ballot_sync(kFull, my_page >= 0);
+      const int64_t row = my_page >= 0 ? paged_row(kv, my_page, my_j, my_t) : 0;
+      for (int x = 0; x < tb && base + x < i1; ++x) {
+        const int idx = base + x - i0, st = idx % P::kStages;
+        const uint32_t bar = smem_u32(&full[st]);
+        bool ok = true;
+        if (idx >= P::kStages)
+          ok = mbar_wait_bounded(smem_u32(&empty[st]), uint32_t((idx / P::kStages - 1) & 1));
+        if (!__all_sync(kFull, ok) || *static_cast<volatile int*>(&flags[1])) {
+          // gave up: the copies in flight land before the CTA may end
+          if (lane == 0) {
+            flag_error(a.err, kErrTimeout);
+            *static_cast<volatile int*>(&flags[1]) = 1;
+          }
+          for (int i = 1; i <= P::kStages && i <= idx; ++i)
+            (void)mbar_wait_bounded(smem_u32(&full[(idx - i) % P::kStages]),
+                                    uint32_t(((idx - i) / P::kStages) & 1));
+          return;
         }
-      }
-      if (it + 1 < i1) look(at);
-      bool ok = true;
-      if (idx >= P::kStages)
-        ok = mbar_wait_bounded(smem_u32(&empty[st]), uint32_t((idx / P::kStages - 1) & 1));
-      if (!__all_sync(kFull, ok) || *static_cast<volatile int*>(&flags[1])) {
-        // gave up: the copies in flight land before the CTA may end
         if (lane == 0) {
-          flag_error(a.err, kErrTimeout);
-          *static_cast<volatile int*>(&flags[1]) = 1;
+          const uint32_t have = (got >> (x << nb_shift)) & (kFull >> (32 - nb));
+          const uint32_t box = uint32_t(br) * (2 * P::kRow + (FP8 ? 8 : 0));
+          mask[st] = have;
+          mbar_arrive_expect_tx(bar, __popc(have) * box);
         }
-        for (int i = 1; i <= P::kStages && i <= idx; ++i)
-          (void)mbar_wait_bounded(smem_u32(&full[(idx - i) % P::kStages]),
-                                  uint32_t(((idx - i) / P::kStages) & 1));
-        return;
-      }
-      const uint32_t have = __ballot_sync(kFull, my_page >= 0);
-      if (lane == 0) {
-        mask[st] = have;
-        const uint32_t box = uint32_t(br) * (2 * P::kRow + (FP8 ? 8 : 0));
-        mbar_arrive_expect_tx(bar, __popc(have) * box);
-      }
-      __syncwarp();
-      if (my_page >= 0) {
-        const int64_t row = paged_row(kv, my_page, j, my_t);
-        const uint32_t base = smem_u32(ring + st * P::kStage);
-        // a box of both halves of 256-byte rows is [half][row][128 bytes]:
-        // the halves of a tile's boxes lie box by box
-        const uint32_t off = uint32_t(lane) * br * P::kRow;
-        tma_box(base + off, &map_k, int(row), bar);
-        tma_box(base + P::kPart + off, &map_v, int(row), bar);
-        if constexpr (FP8) {
-          const uint32_t so = base + 2 * P::kPart + uint32_t(lane) * br * 4;
-          bulk_copy(so, kv.k_scales + row, br * 4, bar);
-          bulk_copy(so + kTok * 4, kv.v_scales + row, br * 4, bar);
+        __syncwarp();
+        if ((lane >> nb_shift) == x && my_page >= 0) {
+          const uint32_t base_st = smem_u32(ring + st * P::kStage);
+          // a box of 256-byte rows is [half][row][128 bytes]
+          const uint32_t off = uint32_t(lane & (nb - 1)) * br;
+          tma_box(base_st + off * P::kRow, &map_k, int(row), bar);
+          tma_box(base_st + P::kPart + off * P::kRow, &map_v, int(row), bar);
+          if constexpr (FP8) {
+            const uint32_t so = base_st + 2 * P::kPart + off * 4;
+            bulk_copy(so, kv.k_scales + row, br * 4, bar);
+            bulk_copy(so + kTok * 4, kv.v_scales + row, br * 4, bar);
+          }
         }
       }
     }
@@ -476,9 +477,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
       for (int tm = 0; tm < kTm; ++tm) {
         const int r0 = 16 * (tm * kGroupWarps + gw) + g;
+        float s2[NH][4];  // a second chain of products: half the latency
 #pragma unroll
         for (int nh = 0; nh < NH; ++nh)
-          sc[tm][nh][0] = sc[tm][nh][1] = sc[tm][nh][2] = sc[tm][nh][3] = 0.f;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) sc[tm][nh][e] = s2[nh][e] = 0.f;
 #pragma unroll
         for (int c = 0; c < KP; ++c) {
           const int p = FP8 ? (D == 128 ? 2 * qd + c : qd) : 8 * (c >> 1) + 2 * qd + (c & 1);
@@ -492,18 +495,22 @@ __global__ void __launch_bounds__(kThreads, 1)
               e4m3x4(word(y, i), y0, y1);
 #pragma unroll
               for (int nh = 0; nh < NH; ++nh)
-                mma16816<true>(sc[tm][nh], x0, y0, x1, y1, qf[nh][8 * c + 2 * i],
+                mma16816<true>(i & 1 ? s2[nh] : sc[tm][nh], x0, y0, x1, y1, qf[nh][8 * c + 2 * i],
                                qf[nh][8 * c + 2 * i + 1]);
             }
           } else {
 #pragma unroll
             for (int nh = 0; nh < NH; ++nh) {
               mma16816<false>(sc[tm][nh], x.x, y.x, x.y, y.y, qf[nh][4 * c], qf[nh][4 * c + 1]);
-              mma16816<false>(sc[tm][nh], x.z, y.z, x.w, y.w, qf[nh][4 * c + 2],
+              mma16816<false>(s2[nh], x.z, y.z, x.w, y.w, qf[nh][4 * c + 2],
                               qf[nh][4 * c + 3]);
             }
           }
         }
+#pragma unroll
+        for (int nh = 0; nh < NH; ++nh)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) sc[tm][nh][e] += s2[nh][e];
       }
       // the scales of this lane's tokens, and the unit of the weights
       [[maybe_unused]] float vs[kTm][2];

@@ -207,6 +207,38 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+// Two 32-bit lanes at once.
+__device__ __forceinline__ uint64_t f2(uint32_t lo, uint32_t hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(lo), "r"(hi));
+  return r;
+}
+__device__ __forceinline__ uint64_t f2(float lo, float hi) {
+  return f2(__float_as_uint(lo), __float_as_uint(hi));
+}
+__device__ __forceinline__ void un2(uint64_t v, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ float rcp(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
 __device__ __forceinline__ uint32_t bf16x2(float a, float b) {
   const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
   return *reinterpret_cast<const uint32_t*>(&h);
@@ -273,7 +305,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* q_free = q_full + 2;         // [2]
   uint64_t* s_full = q_free + 2;         // [2]
   uint64_t* p_full = s_full + 2;         // [2]
-  uint64_t* o_done = p_full + 2;         // [2]
+  uint64_t* p_half = p_full + 2;         // [2]
+  uint64_t* o_done = p_half + 2;         // [2]
   uint64_t* join = o_done + 2;           // [2]
   uint64_t* drained = join + 2;
   uint32_t* have = reinterpret_cast<uint32_t*>(drained + 1);  // [8] boxes present, per tile
@@ -297,6 +330,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(smem_u32(&q_free[g]), 1);
       mbar_init(smem_u32(&s_full[g]), 1);
       mbar_init(smem_u32(&p_full[g]), kRows);
+      mbar_init(smem_u32(&p_half[g]), kRows);
       mbar_init(smem_u32(&o_done[g]), 1);
       mbar_init(smem_u32(&join[g]), kRows);
     }
@@ -366,6 +400,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int64_t items = pieces * split;
   const int G = a.group, heads = G * kv.kv_heads, TT = a.per_tile;
 
+  // The CTA's turns: the items, longest first, are dealt to the CTAs to and
+  // fro, which evens out what a falling order leaves uneven; -1 at the end.
+  auto turn_of = [&](int64_t turn) {
+    if (turn * sms >= items) return int64_t(-1);
+    return turn * sms + (turn & 1 ? sms - 1 - int(blockIdx.x) : int(blockIdx.x));
+  };
   auto item_of = [&](int64_t idx) {
     Item w;
     w.part = int(idx % split);
@@ -419,7 +459,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       int seq = 0;     // items done
       uint32_t nt = 0; // tiles
       bool ok = true;
-      for (int64_t idx = blockIdx.x; ok && idx < items; idx += sms) {
+      for (int64_t turn = 0, idx; ok && (idx = turn_of(turn)) >= 0; ++turn) {
+        if (idx >= items) continue;
         const Item w = item_of(idx);
         if (w.k1 <= w.k0) continue;
         const int groups = has_b(w) ? 2 : 1;
@@ -436,12 +477,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         __syncwarp();
         ++seq;
-        for (int kt = w.k0; ok && kt < w.k1; ++kt, ++nt) {
+        auto look = [&](int kt) {
           const int t = kt * kKeys + (lane << br_shift);
           const bool in = lane < boxes && t < w.hi && t + (1 << br_shift) > w.lo;
-          const int page = in ? paged_page(kv, w.b, t, a.err) : -1;
+          return in ? paged_page(kv, w.b, t, a.err) : -1;
+        };
+        int ahead = look(w.k0);
+        for (int kt = w.k0; ok && kt < w.k1; ++kt, ++nt) {
+          const int page = ahead;
+          if (kt + 1 < w.k1) ahead = look(kt + 1);  // the next tile's, while this one is copied
           const uint32_t got = __ballot_sync(kAll, page >= 0);
-          const int64_t row = page >= 0 ? paged_row(kv, page, w.j, t) : 0;
+          const int64_t row =
+              page >= 0 ? paged_row(kv, page, w.j, kt * kKeys + (lane << br_shift)) : 0;
           const uint32_t bytes_row = 128u * P::kHalves;
           for (int part = 0; part < 2; ++part, ++n) {  // K, then V
             if constexpr (FP8) {
@@ -508,13 +555,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                    idesc(kKeys, false), i > 0);
           }
         };
-        auto values = [&](int g, uint32_t slot, bool first) {
+        // half 0, 1: the first and the last 64 tokens
+        auto values = [&](int g, uint32_t slot, bool first, int half) {
           const uint32_t v = sbase + P::kOffKv + slot * P::kTile;
 #pragma unroll
-          for (int i = 0; i < kKeys / 16; ++i)
-            mma_ts(tmem + P::kColO + g * 128, tmem + P::kColS + g * 128 + 8 * i,
-                   desc_mn(v + i * 2048, P::kHalves > 1 ? P::kSpan : 1024), idesc(D, true),
-                   !first || i > 0);
+          for (int i = 0; i < kKeys / 32; ++i) {
+            const int k = half * (kKeys / 32) + i;
+            mma_ts(tmem + P::kColO + g * 128, tmem + P::kColS + g * 128 + 8 * k,
+                   desc_mn(v + k * 2048, P::kHalves > 1 ? P::kSpan : 1024), idesc(D, true),
+                   !first || k > 0);
+          }
         };
         auto key_ready = [&](uint32_t m) {
           return wait(FP8 ? &ready[m % P::kSlots] : &full[m % P::kSlots], (m / P::kSlots) & 1u,
@@ -524,7 +574,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         auto value_ready = [&](uint32_t m) {
           return wait(&ready[m % P::kSlots], (m / P::kSlots) & 1u, quit, a.err);
         };
-        for (int64_t idx = blockIdx.x; ok && idx < items; idx += sms) {
+        for (int64_t turn = 0, idx; ok && (idx = turn_of(turn)) >= 0; ++turn) {
+          if (idx >= items) continue;
           const Item w = item_of(idx);
           const int nk = w.k1 - w.k0;
           if (nk <= 0) continue;
@@ -544,11 +595,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int i = 0; i < nk; ++i, n += 2) {
             const bool next = i + 1 < nk;
             const uint32_t vs = (n + 1) % P::kSlots, ks = (n + 2) % P::kSlots;
-            ok = value_ready(n + 1) && (!next || key_ready(n + 2)) &&
-                 wait(&p_full[0], ca & 1u, quit, a.err);
+            ok = value_ready(n + 1) && wait(&p_half[0], ca & 1u, quit, a.err);
             if (!ok) break;
             fence_after();
-            values(0, vs, i == 0);
+            values(0, vs, i == 0, 0);
+            ok = (!next || key_ready(n + 2)) && wait(&p_full[0], ca & 1u, quit, a.err);
+            if (!ok) break;
+            fence_after();
+            values(0, vs, i == 0, 1);
             commit(&o_done[0]);
             ++ca;
             if (next) {
@@ -556,10 +610,14 @@ __global__ void __launch_bounds__(kThreads, 1)
               commit(&s_full[0]);
             }
             if (b) {
+              ok = wait(&p_half[1], cb & 1u, quit, a.err);
+              if (!ok) break;
+              fence_after();
+              values(1, vs, i == 0, 0);
               ok = wait(&p_full[1], cb & 1u, quit, a.err);
               if (!ok) break;
               fence_after();
-              values(1, vs, i == 0);
+              values(1, vs, i == 0, 1);
               commit(&o_done[1]);
               ++cb;
             }
@@ -587,7 +645,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t n = 0, nt = 0;
       int seq = 0;
       bool ok = true;
-      for (int64_t idx = blockIdx.x; ok && idx < items; idx += sms) {
+      for (int64_t turn = 0, idx; ok && (idx = turn_of(turn)) >= 0; ++turn) {
+        if (idx >= items) continue;
         const Item w = item_of(idx);
         if (w.k1 <= w.k0) continue;
         ++seq;
@@ -639,8 +698,19 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
               if (part == 0) {
                 const float* sc = reinterpret_cast<const float*>(raw + kKeys * D);
-                for (int i = ft; i < 2 * kKeys; i += kFixers)
-                  scales[(nt & 3u) * 2 * kKeys + i] = sc[i];
+                for (int i = ft; i < 2 * kKeys; i += kFixers) {
+                  const int r = i & (kKeys - 1), t = t0 + r;
+                  float v = sc[i];
+                  if (!sure) {
+                    if (t < w.lo || t >= w.hi || !((got >> (r >> br_shift)) & 1u)) {
+                      v = 0.f;
+                    } else if (i >= kKeys && !(fabsf(v) <= 3.4028234663852886e38f)) {
+                      v = 0.f;  // a value row that some must not see: as an element of V
+                      bad = true;
+                    }
+                  }
+                  scales[(nt & 3u) * 2 * kKeys + i] = v;
+                }
               }
               if (bad) dirty[seq & 3] = seq;
               asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -701,7 +771,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int g = warp >> 2, r = tid & (kRows - 1);
     const uint32_t lanes = uint32_t((warp & 3) * 32) << 16;
     const uint32_t ts = tmem + lanes + P::kColS + g * 128, to = tmem + lanes + P::kColO + g * 128;
-    const bool plain = !FP8 && !(a.softcap > 0.f) && !a.slopes && a.scale > 0.f;
+    const bool plain = !(a.softcap > 0.f) && !a.slopes && a.scale > 0.f;
     const float inv_cap = a.softcap > 0.f ? 1.f / a.softcap : 0.f;
     const int rt = r / G, rh = r - rt * G;
     uint32_t nt = 0, my = 0;  // tiles of the CTA; tiles of this row tile
@@ -713,7 +783,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_arrive(smem_u32(&join[g]));
       return __all_sync(kAll, wait(&join[g], met++ & 1u, quit, a.err)) != 0;
     };
-    for (int64_t idx = blockIdx.x; ok && idx < items; idx += sms) {
+    for (int64_t turn = 0, idx; ok && (idx = turn_of(turn)) >= 0; ++turn) {
+      if (idx >= items) continue;
       const Item w = item_of(idx);
       if (w.part >= w.parts) continue;
       const int nk = w.k1 - w.k0;
@@ -748,36 +819,76 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool whole = got == kAll >> (32 - boxes);
         holes |= !whole;
         const bool clear = __all_sync(kAll, t0 >= rlo && t0 + kKeys <= rhi) && whole;
-        float mul = a.scale * kLog2e;
+        float mul = a.scale * kLog2e;  // what turns s into log2 units
         const float* ks = scales + ((nt & 3u) * 2) * kKeys;
-        if (!plain) {
+        if constexpr (FP8) {
 #pragma unroll
           for (int c = 0; c < 4; ++c)
 #pragma unroll
-            for (int e = 0; e < 32; ++e) {
-              float v = __uint_as_float(s[c][e]) * a.scale;
-              if constexpr (FP8) v *= ks[32 * c + e];
-              if (a.softcap > 0.f) v = cap_score(v, a.softcap, inv_cap);
-              s[c][e] = __float_as_uint(fmaf(slope, float(t0 + 32 * c + e - p), v * kLog2e));
+            for (int e = 0; e < 32; e += 4) {
+              const float4 k = *reinterpret_cast<const float4*>(ks + 32 * c + e);
+              const float kk[4] = {k.x, k.y, k.z, k.w};
+#pragma unroll
+              for (int u = 0; u < 4; u += 2) {
+                float lo, hi;
+                un2(mul2(f2(s[c][e + u], s[c][e + u + 1]), f2(kk[u], kk[u + 1])), lo, hi);
+                s[c][e + u] = __float_as_uint(lo);
+                s[c][e + u + 1] = __float_as_uint(hi);
+              }
             }
+        }
+        if (!plain) {
+          if (a.softcap > 0.f) {
+            // cap tanh(x) = cap - 2 cap / (1 + e^2x), x = s scale / cap; e^2x
+            // may be infinite, its reciprocal is then 0.  Off by cap * 2^-22
+            // absolutely, which is what counts in the exponent.
+            const float cl = a.softcap * kLog2e, xm = 2.f * kLog2e * a.scale * inv_cap;
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+#pragma unroll
+              for (int e = 0; e < 32; ++e) {
+                const float x = ex2(__uint_as_float(s[c][e]) * xm);
+                s[c][e] = __float_as_uint(fmaf(-2.f * cl, rcp(1.f + x), cl));
+              }
+          } else {
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+#pragma unroll
+              for (int e = 0; e < 32; ++e)
+                s[c][e] = __float_as_uint(__uint_as_float(s[c][e]) * mul);
+          }
           mul = 1.f;
+          if (a.slopes) {
+            const float base = slope * float(t0 - p);
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+#pragma unroll
+              for (int e = 0; e < 32; ++e)
+                s[c][e] = __float_as_uint(__uint_as_float(s[c][e]) +
+                                          fmaf(slope, float(32 * c + e), base));
+          }
         }
         if (!clear) {
+          // this row's tokens of the tile, one bit each
 #pragma unroll
-          for (int c = 0; c < 4; ++c)
+          for (int c = 0; c < 4; ++c) {
+            const int a0 = rlo - t0 - 32 * c, a1 = rhi - t0 - 32 * c;
+            uint32_t see = a0 <= 0 ? kAll : a0 >= 32 ? 0u : kAll << a0;
+            see &= a1 <= 0 ? 0u : a1 >= 32 ? kAll : kAll >> (32 - a1);
+            if (!((got >> ((32 * c) >> br_shift)) & 1u)) see &= 0xffff0000u;
+            if (!((got >> ((32 * c + 16) >> br_shift)) & 1u)) see &= 0x0000ffffu;
 #pragma unroll
-            for (int e = 0; e < 32; ++e) {
-              const int t = t0 + 32 * c + e;
-              if (t < rlo || t >= rhi || !((got >> ((32 * c + e) >> br_shift)) & 1u))
-                s[c][e] = 0xff800000u;
-            }
+            for (int e = 0; e < 32; ++e)
+              if (!((see >> e) & 1u)) s[c][e] = 0xff800000u;
+          }
         }
         float mx[4];
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-          mx[c] = __uint_as_float(s[c][0]);
+          mx[c] = fmaxf(__uint_as_float(s[c][0]), __uint_as_float(s[c][1]));
 #pragma unroll
-          for (int e = 1; e < 32; ++e) mx[c] = fmaxf(mx[c], __uint_as_float(s[c][e]));
+          for (int e = 2; e < 32; e += 2)
+            mx[c] = fmaxf(fmaxf(mx[c], __uint_as_float(s[c][e])), __uint_as_float(s[c][e + 1]));
         }
         const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * mul;
         if (i == 0) {
@@ -803,28 +914,44 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         const float off = m == -INFINITY ? 0.f : -m;
-        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+        const uint64_t mul_2 = f2(mul, mul), off_2 = f2(off, off);
+        uint64_t sum[2] = {0ull, 0ull};
         const float* vsc = ks + kKeys;
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
           uint32_t pk[32];
 #pragma unroll
-          for (int e = 0; e < 32; ++e) {
-            const int x = 2 * e & 31;
-            float p0 = ex2(fmaf(__uint_as_float(s[2 * c + (e >> 4)][x]), mul, off));
-            float p1 = ex2(fmaf(__uint_as_float(s[2 * c + (e >> 4)][x + 1]), mul, off));
-            sum[e & 3] += p0 + p1;
-            if constexpr (FP8) {
-              // a masked token's scale may be anything
-              const float2 v = *reinterpret_cast<const float2*>(vsc + 64 * c + 2 * e);
-              p0 = clear || p0 > 0.f ? p0 * v.x : 0.f;
-              p1 = clear || p1 > 0.f ? p1 * v.y : 0.f;
+          for (int e = 0; e < 32; e += 2) {
+            float w[4];
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+              const int x = 2 * (e + u) & 31, cc = 2 * c + (e >> 4);
+              float z0, z1;
+              un2(fma2(f2(s[cc][x], s[cc][x + 1]), mul_2, off_2), z0, z1);
+              w[2 * u] = ex2(z0);
+              w[2 * u + 1] = ex2(z1);
+              sum[u] = add2(sum[u], f2(w[2 * u], w[2 * u + 1]));
             }
-            pk[e] = bf16x2(p0, p1);
+            if constexpr (FP8) {
+              const float4 v = *reinterpret_cast<const float4*>(vsc + 64 * c + 2 * e);
+              un2(mul2(f2(w[0], w[1]), f2(v.x, v.y)), w[0], w[1]);
+              un2(mul2(f2(w[2], w[3]), f2(v.z, v.w)), w[2], w[3]);
+            }
+            pk[e] = bf16x2(w[0], w[1]);
+            pk[e + 1] = bf16x2(w[2], w[3]);
           }
           tmem_st32(ts + 32 * c, pk);
+          if (c == 0) {  // the products may begin with the first half
+            wait_st();
+            fence_before();
+            mbar_arrive(smem_u32(&p_half[g]));
+          }
         }
-        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        {
+          float s0, s1;
+          un2(add2(sum[0], sum[1]), s0, s1);
+          l += s0 + s1;
+        }
         wait_st();
         fence_before();
         mbar_arrive(smem_u32(&p_full[g]));
@@ -853,7 +980,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int64_t at = paged_row(kv, page, w.j, t) * D + d0;
           for (int d = 0; d < 32; ++d) {
             if constexpr (FP8) {
-              if ((__ldcg(static_cast<const uint8_t*>(kv.v) + at + d) & 0x7f) == 0x7f) o[d] = NAN;
+              const float x = __ldcg(kv.v_scales + at / D);
+              if ((__ldcg(static_cast<const uint8_t*>(kv.v) + at + d) & 0x7f) == 0x7f ||
+                  !(fabsf(x) <= 3.4028234663852886e38f))
+                o[d] = NAN;
             } else {
               const float x = bf16_bits_to_f32(__ldcg(static_cast<const uint16_t*>(kv.v) + at + d));
               if (!(fabsf(x) <= 3.4028234663852886e38f)) o[d] += x;
