@@ -45,7 +45,6 @@
 
 #include "launch.h"
 #include "paged.cuh"
-#include "tensor_map.h"
 
 namespace tt {
 namespace {
@@ -54,7 +53,8 @@ constexpr uint32_t kFull = 0xffffffffu;
 constexpr int kGroups = 2;                    // tiles in work at once
 constexpr int kGroupWarps = 4;
 constexpr int kConsumers = kGroups * kGroupWarps * 32;
-constexpr int kThreads = kConsumers + 32;     // + the copying warp
+constexpr int kCopiers = 128;
+constexpr int kThreads = kConsumers + kCopiers;
 constexpr int kMaxCtas = 1024;                // counters in the workspace
 constexpr int kSmemMax = 227 * 1024;
 constexpr int kConsumerBar = 1;
@@ -63,7 +63,6 @@ template <int D, int NH, bool FP8>
 struct Plan {
   static constexpr int kEs = FP8 ? 1 : 2;
   static constexpr int kRow = D * kEs;                    // bytes of a cache row
-  static constexpr int kBoxRow = kRow < 128 ? kRow : 128; // bytes of a box row (the swizzle span)
   // 16-token chunks per warp and tile: 32 KB of K and V a tile, or 16 KB
   // where the rows are 64 bytes
   static constexpr int kTm = kRow == 256 ? 1 : 2;
@@ -72,6 +71,10 @@ struct Plan {
   static constexpr int kStage = 2 * kPart + (FP8 ? 2 * kTok * 4 : 0);
   static constexpr int kSlot = 8 * NH * (D + 2);          // floats of one warp's part
   static constexpr int kScratch = kGroupWarps * kSlot * 4;
+  // XOR of a 16-byte piece's number within its row: the eight lanes of one
+  // shared-memory phase then read eight different bank groups, both where
+  // they read two rows (K) and where they read four (V)
+  __device__ static constexpr int swizzle(int r) { return kRow == 64 ? (r >> 1) & 3 : r & 7; }
   static constexpr int kFixed =
       1024 + kScratch + (2 * kPagedMaxBatch + 2) * 4 + 512;  // alignment, parts, line, barriers
   // A multiple of the groups, so that a stage is always the same group's: a
@@ -82,7 +85,6 @@ struct Plan {
   static constexpr int kStages = kRaw > 12 ? 12 : kRaw;
   static constexpr int kSmem = kFixed + kStages * kStage;
   static_assert(kStages >= 4 && kStages % kGroups == 0, "ring");
-  static_assert(kStage % 1024 == 0, "swizzled boxes start on 1024 bytes");
 };
 
 // Floats of one CTA part: O [G][D], max [G], sum [G], padded to 16 bytes.
@@ -146,21 +148,19 @@ __device__ __forceinline__ uint32_t halves(uint32_t a, uint32_t b, int h) {
   return __byte_perm(a, b, h ? 0x7632 : 0x5410);
 }
 
-__device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap* map, int row,
-                                        uint32_t bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(row), "r"(0), "r"(bar)
-      : "memory");
+// 16 bytes to shared memory, past L1; counted by the thread's next
+// copies_arrive.
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
-__device__ __forceinline__ void bulk_copy(uint32_t dst, const void* src, uint32_t bytes,
-                                          uint32_t bar) {
-  asm volatile(
-      "cp.async.bulk.shared::cta.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-          dst),
-      "l"(src), "r"(bytes), "r"(bar)
-      : "memory");
+// Arrives on the barrier when this thread's copies so far have landed.
+__device__ __forceinline__ void copies_arrive(uint32_t bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
 }
 __device__ __forceinline__ void consumer_sync() {
   asm volatile("bar.sync %0, %1;" ::"r"(kConsumerBar), "r"(kConsumers) : "memory");
@@ -210,9 +210,7 @@ __device__ __forceinline__ At find(const Line& L, int batch, int item) {
 
 template <int D, int NH, bool FP8>
 __global__ void __launch_bounds__(kThreads, 1)
-    paged_decode_kernel(const __grid_constant__ CUtensorMap map_k,
-                        const __grid_constant__ CUtensorMap map_v, const PagedKv kv,
-                        const DecodeArgs a) {
+    paged_decode_kernel(const PagedKv kv, const DecodeArgs a) {
   using P = Plan<D, NH, FP8>;
   constexpr int kTok = P::kTok, kTm = P::kTm;
   extern __shared__ __align__(128) uint8_t smem_raw[];
@@ -223,14 +221,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   int32_t* slen = prefix + kPagedMaxBatch + 2;
   uint64_t* full = reinterpret_cast<uint64_t*>(slen + kPagedMaxBatch);
   uint64_t* empty = full + P::kStages;
-  uint32_t* mask = reinterpret_cast<uint32_t*>(empty + P::kStages);  // boxes present, per stage
+  uint32_t* mask = reinterpret_cast<uint32_t*>(empty + P::kStages);  // granules present, per stage
   int* flags = reinterpret_cast<int*>(mask + P::kStages);  // [0] last to finish, [1] gave up
   int32_t* wsum = reinterpret_cast<int32_t*>(scratch);  // scan partials, before the main loop
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if (tid == 0) {
     for (int i = 0; i < P::kStages; ++i) {
-      mbar_init(smem_u32(&full[i]), 1);
+      mbar_init(smem_u32(&full[i]), kCopiers + 1);
       mbar_init(smem_u32(&empty[i]), kGroupWarps);
     }
     flags[1] = 0;
@@ -280,72 +278,81 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int i1 = blockIdx.x < C ? int(T * (blockIdx.x + 1) / C) : 0;
   const int G = a.group, heads = G * kv.kv_heads;
 
-  if (warp == kGroups * kGroupWarps) {
-    // ================================================== the copying warp
+  constexpr int kGran = kTok / 16;  // granules of 16 tokens in a tile: each lies within a page
+  if (warp >= kGroups * kGroupWarps) {
+    // ================================================= the copying warps
     if (i0 >= i1) return;
-    const int ps = 1 << kv.page_shift;
-    const int br = ps < kTok ? ps : kTok;  // rows of a box
-    const int nb = kTok / br;              // boxes of K (and of V) a tile
-    // Lane l looks up box l % nb of the tile l / nb of a batch of 32 / nb
-    // tiles, one batch ahead of the copies, and issues that box's copies when
-    // its tile's turn comes: no table entry is waited for in the loop.
-    const int nb_shift = __popc(nb - 1), tb = 32 >> nb_shift;
-    int page, j, t;
+    // Lane l looks up granule l % kGran of tile l / kGran of a batch of
+    // tiles, one batch ahead of the copies: no table entry is waited for in
+    // the loop.  Each warp has the same batch.
+    constexpr int kBatch = 32 / kGran;
+    const int pw = warp - kGroups * kGroupWarps, pt = tid - kConsumers;
+    int row;  // the granule's first row in the pool, or -1
     auto look = [&](int base) {
-      const int it = base + (lane >> nb_shift);
-      page = -1;
+      const int it = base + lane / kGran;
+      row = -1;
       if (it < i1) {
         const At w = find(L, kv.batch, it);
-        const int n = slen[w.b];
-        j = w.j;
-        t = (L.first_tile(w.b) + w.tile) * kTok + (lane & (nb - 1)) * br;
-        // boxes wholly before the window or past the length are not copied
-        if (t < n && (a.window == 0 || t + br > n - a.window))
-          page = paged_page(kv, w.b, t, a.err);
+        const int n = slen[w.b], t = (L.first_tile(w.b) + w.tile) * kTok + lane % kGran * 16;
+        // granules wholly before the window or past the length are not copied
+        if (t < n && (a.window == 0 || t + 16 > n - a.window)) {
+          const int page = paged_page(kv, w.b, t, a.err);
+          if (page >= 0) row = int(paged_row(kv, page, w.j, t));
+        }
       }
     };
+    // this lane's piece of a granule's i-th 512 bytes: row and swizzled place
+    constexpr int kLr = P::kRow / 16;  // lanes a row
+    const int lr = lane / kLr, lc = lane % kLr;
     look(i0);
-    for (int base = i0; base < i1; base += tb) {
-      const int my_page = page, my_j = j, my_t = t;
-      look(base + tb);
-      const uint32_t got = __ballot_sync(kFull, my_page >= 0);
-      const int64_t row = my_page >= 0 ? paged_row(kv, my_page, my_j, my_t) : 0;
-      for (int x = 0; x < tb && base + x < i1; ++x) {
+    for (int base = i0; base < i1; base += kBatch) {
+      const int my_row = row;
+      look(base + kBatch);
+      const uint32_t got = __ballot_sync(kFull, my_row >= 0);
+      for (int x = 0; x < kBatch && base + x < i1; ++x) {
         const int idx = base + x - i0, st = idx % P::kStages;
-        const uint32_t bar = smem_u32(&full[st]);
         bool ok = true;
         if (idx >= P::kStages)
           ok = mbar_wait_bounded(smem_u32(&empty[st]), uint32_t((idx / P::kStages - 1) & 1));
         if (!__all_sync(kFull, ok) || *static_cast<volatile int*>(&flags[1])) {
-          // gave up: the copies in flight land before the CTA may end
           if (lane == 0) {
             flag_error(a.err, kErrTimeout);
             *static_cast<volatile int*>(&flags[1]) = 1;
           }
-          for (int i = 1; i <= P::kStages && i <= idx; ++i)
-            (void)mbar_wait_bounded(smem_u32(&full[(idx - i) % P::kStages]),
-                                    uint32_t(((idx - i) / P::kStages) & 1));
+          asm volatile("cp.async.wait_all;" ::: "memory");
           return;
         }
-        if (lane == 0) {
-          const uint32_t have = (got >> (x << nb_shift)) & (kFull >> (32 - nb));
-          const uint32_t box = uint32_t(br) * (2 * P::kRow + (FP8 ? 8 : 0));
-          mask[st] = have;
-          mbar_arrive_expect_tx(bar, __popc(have) * box);
-        }
-        __syncwarp();
-        if ((lane >> nb_shift) == x && my_page >= 0) {
-          const uint32_t base_st = smem_u32(ring + st * P::kStage);
-          // a box of 256-byte rows is [half][row][128 bytes]
-          const uint32_t off = uint32_t(lane & (nb - 1)) * br;
-          tma_box(base_st + off * P::kRow, &map_k, int(row), bar);
-          tma_box(base_st + P::kPart + off * P::kRow, &map_v, int(row), bar);
-          if constexpr (FP8) {
-            const uint32_t so = base_st + 2 * P::kPart + off * 4;
-            bulk_copy(so, kv.k_scales + row, br * 4, bar);
-            bulk_copy(so + kTok * 4, kv.v_scales + row, br * 4, bar);
+        const uint32_t have = (got >> (x * kGran)) & (kFull >> (32 - kGran));
+        const uint32_t stage = smem_u32(ring + st * P::kStage);
+#pragma unroll
+        for (int u0 = 0; u0 < 2 * kGran / 4; ++u0) {
+          const int u = u0 * 4 + pw, gr = u >> 1;  // granule; even u: K, odd: V
+          const int r = __shfl_sync(kFull, my_row, x * kGran + gr);
+          if (r >= 0) {
+            const uint8_t* src = static_cast<const uint8_t*>(u & 1 ? kv.v : kv.k) +
+                                 int64_t(r) * P::kRow + lane * 16;
+            const uint32_t dst = stage + (u & 1 ? P::kPart : 0) + gr * 16 * P::kRow;
+#pragma unroll
+            for (int i = 0; i < P::kRow / 32; ++i) {
+              const int q = lr + i * (512 / P::kRow);
+              copy16(dst + q * P::kRow + ((lc ^ P::swizzle(q)) << 4), src + i * 512);
+            }
           }
         }
+        if constexpr (FP8) {
+          const int gr = (pt >> 3) % kGran;
+          const int r = __shfl_sync(kFull, my_row, x * kGran + gr);
+          if (pt < 8 * kGran && r >= 0) {
+            const int w = (pt >> 2) & 1, q = pt & 3;
+            copy16(stage + 2 * P::kPart + (w * kTok + gr * 16 + q * 4) * 4,
+                   (w ? kv.v_scales : kv.k_scales) + int64_t(r) + q * 4);
+          }
+        }
+        if (pt == 0) {
+          mask[st] = have;
+          mbar_arrive(smem_u32(&full[st]));
+        }
+        copies_arrive(smem_u32(&full[st]));
       }
     }
     return;
@@ -363,8 +370,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (i0 >= i1) return;
   const int g = lane >> 2, qd = lane & 3;
   const int grp = warp / kGroupWarps, gw = warp % kGroupWarps;
-  const int ps = 1 << kv.page_shift;
-  const int br_shift = ps < kTok ? kv.page_shift : (kTok == 64 ? 6 : 7);
   constexpr int KP = P::kRow / 64;  // 16-byte pieces of a row per lane in the score product
   constexpr int QR = D / 8;         // registers of q per lane and head tile
   constexpr int MT = D / 16;        // 16-dim tiles of the output
@@ -455,22 +460,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       constexpr bool FULLT = decltype(full_tile)::value;
       const uint8_t* kb = ring + st * P::kStage;
       const uint8_t* vb = kb + P::kPart;
-      // byte address of 16-byte piece p of row r (swizzled box by box; a box
-      // of 256-byte rows holds its rows' first halves, then the second)
+      // 16-byte piece p of row r
       auto piece = [&](const uint8_t* base, int r, int p) {
-        if constexpr (P::kBoxRow == 64)
-          return base + r * 64 + ((p ^ ((r >> 1) & 3)) << 4);
-        else if constexpr (P::kRow == 128)
-          return base + r * 128 + ((p ^ (r & 7)) << 4);
-        else {
-          const int box = r >> br_shift, in = r & ((1 << br_shift) - 1);
-          return base + ((box * 2 + (p >> 3)) << (br_shift + 7)) + in * 128 +
-                 (((p & 7) ^ (r & 7)) << 4);
-        }
+        return base + r * P::kRow + ((p ^ P::swizzle(r)) << 4);
       };
       auto visible = [&](int r) {
         const int t = t0 + r;
-        return t >= lo && t < n && ((have >> (r >> br_shift)) & 1u);
+        return t >= lo && t < n && ((have >> (r >> 4)) & 1u);
       };
       // scores sc[tm][nh]: tokens r0 + (g | g + 8) x heads 8 nh + 2qd + (0 | 1)
       float sc[kTm][NH][4];
@@ -575,14 +571,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           m = fmaxf(m, __shfl_xor_sync(kFull, m, 16));
           const float mn = fmaxf(mrun[nh][h], m);
           const float ms = mn == -INFINITY ? 0.f : mn;  // nothing visible so far
-          alpha[h] = exp2f(mrun[nh][h] - ms);
+          alpha[h] = ex2(mrun[nh][h] - ms);
           mrun[nh][h] = mn;
           mx[h] = ms;
         }
 #pragma unroll
         for (int tm = 0; tm < kTm; ++tm)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) sc[tm][nh][e] = exp2f(sc[tm][nh][e] - mx[e & 1]);
+          for (int e = 0; e < 4; ++e) sc[tm][nh][e] = ex2(sc[tm][nh][e] - mx[e & 1]);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           float t = 0.f;
@@ -701,20 +697,16 @@ __global__ void __launch_bounds__(kThreads, 1)
           flag_error(a.err, kErrTimeout);
           *static_cast<volatile int*>(&flags[1]) = 1;
         }
-        for (int i = idx; i < i1 - i0 && i < idx + P::kStages; ++i)  // copies in flight land
-          (void)mbar_wait_bounded(smem_u32(&full[i % P::kStages]),
-                                  uint32_t((i / P::kStages) & 1));
         gave_up = true;
         break;
       }
       const uint32_t have = mask[st];
       const int t0 = tok0 + (k0 + x) * kTok;
-      const uint32_t all = kFull >> (32 - (kTok >> br_shift));
+      const uint32_t all = kFull >> (32 - kGran);
       if (t0 >= lo && t0 + kTok <= n && have == all)
         tile(std::true_type{}, st, t0, have);
       else if (have)
         tile(std::false_type{}, st, t0, have);
-      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // reads before the refill
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&empty[st]));
     }
@@ -777,8 +769,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (hc < G) {
               const float m2 = slot[8 * NH * D + hc], l2 = slot[8 * NH * (D + 1) + hc];
               const float M = fmaxf(mrun[nh][h], m2);
-              const float f1 = M == -INFINITY ? 0.f : exp2f(mrun[nh][h] - M);
-              const float f2 = M == -INFINITY ? 0.f : exp2f(m2 - M);
+              const float f1 = M == -INFINITY ? 0.f : ex2(mrun[nh][h] - M);
+              const float f2 = M == -INFINITY ? 0.f : ex2(m2 - M);
               mrun[nh][h] = M;
               lsum[nh][h] = lsum[nh][h] * f1 + l2 * f2;
 #pragma unroll
@@ -808,7 +800,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
       for (int w = 0; w < kGroupWarps; ++w) {
         const float* p = scratch + w * P::kSlot;
-        const float f = M == -INFINITY ? 0.f : exp2f(p[8 * NH * D + r] - M);
+        const float f = M == -INFINITY ? 0.f : ex2(p[8 * NH * D + r] - M);
         const float4 v = *reinterpret_cast<const float4*>(p + r * D + 4 * c);
         s.x = fmaf(v.x, f, s.x);
         s.y = fmaf(v.y, f, s.y);
@@ -824,8 +816,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (a.sinks) {
         const float z = __ldcg(a.sinks + h) * kLog2e;
         const float M2 = fmaxf(M, z);
-        const float f = M == -INFINITY ? 0.f : exp2f(M - M2);
-        Lq = Lq * f + exp2f(z - M2);
+        const float f = M == -INFINITY ? 0.f : ex2(M - M2);
+        Lq = Lq * f + ex2(z - M2);
         s.x *= f;
         s.y *= f;
         s.z *= f;
@@ -880,7 +872,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           M = warp_max(M);
           for (int p = lane; p < np; p += 32)
             Lq += M == -INFINITY ? 0.f
-                                 : exp2f(__ldcg(part_of(p) + G * D + r) - M) *
+                                 : ex2(__ldcg(part_of(p) + G * D + r) - M) *
                                        __ldcg(part_of(p) + G * D + G + r);
           Lq = warp_sum(Lq);
           if (lane == 0) {
@@ -906,7 +898,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
 #pragma unroll
             for (int u = 0; u < 8; ++u) {
-              const float f = M == -INFINITY ? 0.f : exp2f(m[u] - M);
+              const float f = M == -INFINITY ? 0.f : ex2(m[u] - M);
               s.x = fmaf(v[u].x, f, s.x);
               s.y = fmaf(v[u].y, f, s.y);
               s.z = fmaf(v[u].z, f, s.z);
@@ -931,36 +923,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-// Rows of head_dim elements as boxes of `rows` rows x (one or two) spans of
-// at most 128 bytes, written with the swizzle of that span.
-cudaError_t pool_map(CUtensorMap* map, const void* base, int D, bool fp8, int64_t rows_total,
-                     int rows) {
-  EncodeTiledFn enc = tensor_map_encoder();
-  if (!enc) return cudaErrorNotSupported;
-  const int es = fp8 ? 1 : 2, row = D * es, span = row < 128 ? row : 128;
-  const cuuint64_t dims[3] = {cuuint64_t(span / es), cuuint64_t(rows_total),
-                              cuuint64_t(row / span)};
-  const cuuint64_t strides[2] = {cuuint64_t(row), cuuint64_t(span)};
-  const cuuint32_t box[3] = {cuuint32_t(span / es), cuuint32_t(rows), cuuint32_t(row / span)};
-  const cuuint32_t estr[3] = {1u, 1u, 1u};
-  if (enc(map, fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
-          const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-          span == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
-          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
-    return cudaErrorInvalidValue;
-  return cudaSuccess;
-}
-
 template <int D, int NH, bool FP8>
 cudaError_t launch(const DeviceInfo& di, const PagedKv& kv, const PagedAttnArgs& a,
                    cudaStream_t s, bool pdl) {
   using P = Plan<D, NH, FP8>;
   auto kern = paged_decode_kernel<D, NH, FP8>;
-  const int ps = 1 << kv.page_shift, br = ps < P::kTok ? ps : P::kTok;
-  const int64_t rows = (int64_t(kv.num_pages) * kv.kv_heads) << kv.page_shift;
-  CUtensorMap mk, mv;
-  if (cudaError_t e = pool_map(&mk, kv.k, D, FP8, rows, br)) return e;
-  if (cudaError_t e = pool_map(&mv, kv.v, D, FP8, rows, br)) return e;
   if (cudaError_t e = ensure_smem(di, kern, P::kSmem)) return e;
   // one CTA per SM, or one per tile that the table could hold where that is less
   const int64_t most =
@@ -992,7 +959,7 @@ cudaError_t launch(const DeviceInfo& di, const PagedKv& kv, const PagedAttnArgs&
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = pdl ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, kern, mk, mv, kv, d);
+  return cudaLaunchKernelEx(&cfg, kern, kv, d);
 }
 
 }  // namespace
