@@ -1,5 +1,5 @@
-// The paged key-value cache as the kernels see it: addressing and the score
-// cap shared by the append and the attention kernels.
+// The paged key-value cache as the kernels see it: the addressing that the
+// append and the attention kernels share.
 //
 // Token t of sequence b is row t % page_size of page table[b][t / page_size];
 // a page holds, for every kv head, page_size rows of head_dim elements:
@@ -49,15 +49,6 @@ __device__ __forceinline__ int paged_seq_of(const int32_t* starts, int batch, in
   int n = 0;
   for (int i = 1 + lane; i < batch; i += 32) n += __ldcg(starts + i) <= t;
   return __reduce_add_sync(0xffffffffu, n);
-}
-
-// cap * tanh(s / cap) by tanh(x) = 1 - 2 / (1 + e^2x): off by about 2^-23
-// absolutely, so the capped score is off by cap * 2^-23, which is what counts
-// in the softmax's exponent.  The exponent is held below 100, where tanh has
-// long been 1, so that the quick division never meets a divisor beyond 2^126.
-__device__ __forceinline__ float cap_score(float s, float cap, float inv_cap) {
-  const float e = exp2f(fminf(2.f * kLog2e * (s * inv_cap), 100.f));
-  return cap * (1.f - __fdividef(2.f, 1.f + e));
 }
 
 }  // namespace tt

@@ -44,6 +44,15 @@ struct PagedAttnArgs {
   void* ws;
 };
 
+// Whether a kernel whose warps trade registers (setmaxnreg) was compiled with
+// the registers per thread that its shares add up to: with fewer, a warp
+// would wait for registers that the CTA does not have.  Asked once a kernel.
+template <typename Kern>
+bool has_registers(Kern kern, int regs) {
+  cudaFuncAttributes at;
+  return cudaFuncGetAttributes(&at, kern) == cudaSuccess && at.numRegs >= regs;
+}
+
 constexpr int kPagedMaxBatch = 1024;
 constexpr int kPagedMaxGroup = 16;  // query heads per kv head
 

@@ -50,11 +50,8 @@ namespace tt {
 namespace {
 
 constexpr uint32_t kFull = 0xffffffffu;
-constexpr int kGroups = 2;                    // tiles in work at once
 constexpr int kGroupWarps = 4;
-constexpr int kConsumers = kGroups * kGroupWarps * 32;
 constexpr int kCopiers = 128;
-constexpr int kThreads = kConsumers + kCopiers;
 constexpr int kMaxCtas = 1024;                // counters in the workspace
 constexpr int kSmemMax = 227 * 1024;
 constexpr int kConsumerBar = 1;
@@ -63,14 +60,29 @@ template <int D, int NH, bool FP8>
 struct Plan {
   static constexpr int kEs = FP8 ? 1 : 2;
   static constexpr int kRow = D * kEs;                    // bytes of a cache row
+  static constexpr int kGroups = 2;  // tiles in work at once
+  static constexpr int kConsumers = kGroups * kGroupWarps * 32;
+  static constexpr int kThreads = kConsumers + kCopiers;
+  // registers a thread: 65,536 less the copying warps' share
+  static constexpr int kCopyRegs = 56;
+  static constexpr int kLaunchRegs = 65536 / kThreads / 8 * 8;
+  static constexpr int kRegs = (kLaunchRegs * kThreads - kCopyRegs * kCopiers) / kConsumers / 8 * 8;
   // 16-token chunks per warp and tile: 32 KB of K and V a tile, or 16 KB
   // where the rows are 64 bytes
   static constexpr int kTm = kRow == 256 ? 1 : 2;
   static constexpr int kTok = 16 * kGroupWarps * kTm;
   static constexpr int kPart = kTok * kRow;               // K (or V) bytes of a tile
-  static constexpr int kStage = 2 * kPart + (FP8 ? 2 * kTok * 4 : 0);
-  static constexpr int kSlot = 8 * NH * (D + 2);          // floats of one warp's part
-  static constexpr int kScratch = kGroupWarps * kSlot * 4;
+  static constexpr int kOffScale = 2 * kPart;
+  static constexpr int kOffQ = kOffScale + (FP8 ? 2 * kTok * 4 : 0);
+  static constexpr int kStage = kOffQ + 8 * NH * D * 2;   // K, V, scales, the pair's queries
+  // A warp's result: its output fragments as float4 units [2 NH][D / 32][32
+  // lanes], then the heads' maxima and sums.  Two sets of slots where they
+  // fit, so that a pair's result is read while the next is worked on.
+  static constexpr int kUnits = 2 * NH * D;
+  static constexpr int kSlot = 4 * kUnits + 16 * NH;      // floats
+  static constexpr int kWarps = kGroups * kGroupWarps;
+  static constexpr int kSets = NH * D > 128 ? 1 : 2;
+  static constexpr int kScratch = kSets * kWarps * kSlot * 4;
   // XOR of a 16-byte piece's number within its row: the eight lanes of one
   // shared-memory phase then read eight different bank groups, both where
   // they read two rows (K) and where they read four (V)
@@ -84,11 +96,15 @@ struct Plan {
   static constexpr int kRaw = (kSmemMax - kFixed) / kStage / kGroups * kGroups;
   static constexpr int kStages = kRaw > 12 ? 12 : kRaw;
   static constexpr int kSmem = kFixed + kStages * kStage;
+  static_assert(kScratch / kSets >= (kConsumers > kUnits ? kConsumers : 0) * 24, "join");
   static_assert(kStages >= 4 && kStages % kGroups == 0, "ring");
 };
 
-// Floats of one CTA part: O [G][D], max [G], sum [G], padded to 16 bytes.
-__host__ __device__ constexpr int part_floats(int G, int D) { return (G * (D + 2) + 3) & ~3; }
+// Floats of one CTA part: a slot as above.
+constexpr int part_floats(int group, int D) {
+  const int nh = group > 8 ? 2 : 1;
+  return 8 * nh * D + 16 * nh;
+}
 
 struct DecodeArgs {
   const uint16_t* q;
@@ -157,23 +173,33 @@ __device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
 __device__ __forceinline__ void copies_arrive(uint32_t bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
 }
+__device__ __forceinline__ float rcp(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ void prefetch_l2(const void* p) {
+  asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
+}
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+template <int kConsumers>
 __device__ __forceinline__ void consumer_sync() {
-  asm volatile("bar.sync %0, %1;" ::"r"(kConsumerBar), "r"(kConsumers) : "memory");
+  asm volatile("bar.sync %0, %1;" ::"r"(kConsumerBar), "n"(kConsumers) : "memory");
 }
 
 // The barrier, and whether any of its threads says so.
+template <int kConsumers>
 __device__ __forceinline__ bool consumer_any(bool p) {
   uint32_t r;
   asm volatile(
       "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
       "barrier.cta.red.or.pred q, %2, %3, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
       : "=r"(r)
-      : "r"(uint32_t(p)), "r"(kConsumerBar), "r"(kConsumers)
+      : "r"(uint32_t(p)), "r"(kConsumerBar), "n"(kConsumers)
       : "memory");
   return r != 0;
 }
@@ -209,10 +235,11 @@ __device__ __forceinline__ At find(const Line& L, int batch, int item) {
 }
 
 template <int D, int NH, bool FP8>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(Plan<D, NH, FP8>::kThreads, 1)
     paged_decode_kernel(const PagedKv kv, const DecodeArgs a) {
   using P = Plan<D, NH, FP8>;
   constexpr int kTok = P::kTok, kTm = P::kTm;
+  constexpr int kGroups = P::kGroups, kConsumers = P::kConsumers, kThreads = P::kThreads;
   extern __shared__ __align__(128) uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
   uint8_t* ring = smem;
@@ -235,6 +262,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     fence_mbar_init();
   }
   pdl_allow_next_grid();
+  // The lengths and the table come into L2 while the preceding kernel ends (it
+  // may still write them: L2 is where writes land, so nothing stale is kept).
+  if (warp >= kGroups * kGroupWarps) {
+    const int pt = tid - kConsumers;
+    for (int i = pt * 32; i < kv.batch; i += kCopiers * 32) prefetch_l2(kv.lens + i);
+    const int64_t entries = int64_t(kv.batch) * kv.pages_per_seq;
+    const int64_t each = (entries + gridDim.x - 1) / gridDim.x;
+    for (int64_t i = each * blockIdx.x + pt * 32; i < each * (blockIdx.x + 1) && i < entries;
+         i += kCopiers * 32)
+      prefetch_l2(kv.page_table + i);
+  }
   pdl_wait_prior_grid();
 
   // ---- the line: lengths and the exclusive scan of the tiles
@@ -273,7 +311,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
   }
   const int64_t T = prefix[kv.batch];
-  const int64_t C = T < gridDim.x ? T : gridDim.x;
+  // a CTA has a tile for each of its groups at least: fewer CTAs, fewer parts
+  const int64_t Tg = (T + kGroups - 1) / kGroups;
+  const int64_t C = Tg < gridDim.x ? Tg : gridDim.x;
   const int i0 = blockIdx.x < C ? int(T * blockIdx.x / C) : 0;
   const int i1 = blockIdx.x < C ? int(T * (blockIdx.x + 1) / C) : 0;
   const int G = a.group, heads = G * kv.kv_heads;
@@ -281,6 +321,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   constexpr int kGran = kTok / 16;  // granules of 16 tokens in a tile: each lies within a page
   if (warp >= kGroups * kGroupWarps) {
     // ================================================= the copying warps
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(P::kCopyRegs));
     if (i0 >= i1) return;
     // Lane l looks up granule l % kGran of tile l / kGran of a batch of
     // tiles, one batch ahead of the copies: no table entry is waited for in
@@ -288,11 +329,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr int kBatch = 32 / kGran;
     const int pw = warp - kGroups * kGroupWarps, pt = tid - kConsumers;
     int row;  // the granule's first row in the pool, or -1
+    int query;  // the tile is its group's first of a pair: the pair's first query row, or -1
     auto look = [&](int base) {
       const int it = base + lane / kGran;
-      row = -1;
+      row = query = -1;
       if (it < i1) {
         const At w = find(L, kv.batch, it);
+        const int first = it - w.tile > i0 ? it - w.tile : i0;
+        if (it - first < kGroups) query = w.b * kv.kv_heads + w.j;
         const int n = slen[w.b], t = (L.first_tile(w.b) + w.tile) * kTok + lane % kGran * 16;
         // granules wholly before the window or past the length are not copied
         if (t < n && (a.window == 0 || t + 16 > n - a.window)) {
@@ -306,7 +350,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int lr = lane / kLr, lc = lane % kLr;
     look(i0);
     for (int base = i0; base < i1; base += kBatch) {
-      const int my_row = row;
+      const int my_row = row, my_query = query;
       look(base + kBatch);
       const uint32_t got = __ballot_sync(kFull, my_row >= 0);
       for (int x = 0; x < kBatch && base + x < i1; ++x) {
@@ -339,12 +383,19 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
         }
+        const int bj = __shfl_sync(kFull, my_query, x * kGran);
+        if (bj >= 0) {
+          const int b = bj / kv.kv_heads, j = bj - b * kv.kv_heads;
+          const uint16_t* src = a.q + int64_t(b) * a.q_stride + int64_t(j) * G * D;
+          for (int i = pt; i < G * D / 8; i += kCopiers)
+            copy16(stage + P::kOffQ + i * 16, src + i * 8);
+        }
         if constexpr (FP8) {
           const int gr = (pt >> 3) % kGran;
           const int r = __shfl_sync(kFull, my_row, x * kGran + gr);
           if (pt < 8 * kGran && r >= 0) {
             const int w = (pt >> 2) & 1, q = pt & 3;
-            copy16(stage + 2 * P::kPart + (w * kTok + gr * 16 + q * 4) * 4,
+            copy16(stage + P::kOffScale + (w * kTok + gr * 16 + q * 4) * 4,
                    (w ? kv.v_scales : kv.k_scales) + int64_t(r) + q * 4);
           }
         }
@@ -359,6 +410,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 
   // ==================================================== the computing warps
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(P::kRegs));
   // sequences without a visible token: no tiles, but rows to write
   for (int b = blockIdx.x; b < kv.batch; b += gridDim.x)
     if (L.tiles(b) == 0)
@@ -373,9 +425,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   constexpr int KP = P::kRow / 64;  // 16-byte pieces of a row per lane in the score product
   constexpr int QR = D / 8;         // registers of q per lane and head tile
   constexpr int MT = D / 16;        // 16-dim tiles of the output
-  const float inv_cap = a.softcap > 0.f ? 1.f / a.softcap : 0.f;
+  // to log2 units; with a cap, cap tanh(x) = cap - 2 cap / (1 + e^2x) from
+  // v = 2x log2 e (e^2x may be infinite, its reciprocal is then 0): off by
+  // about cap 2^-22 absolutely, which is what counts in the exponent
+  const float cap2 = a.softcap * kLog2e;
+  const float unit = a.softcap > 0.f ? 2.f * kLog2e / a.softcap : kLog2e;
   const bool plain = !(a.softcap > 0.f) && !a.slopes;
 
+  uint32_t pairs = 0;  // done so far
   At at = find(L, kv.batch, i0);
   for (int it = i0; it < i1;) {
     const int b = at.b, j = at.j, nt = L.tiles(b), k0 = at.tile;
@@ -388,61 +445,64 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t qf[NH][QR];
     float fac[NH][2], slope[NH][2];  // heads 8 nh + 2 qd + {0, 1}
 #pragma unroll
-    for (int nh = 0; nh < NH; ++nh) {
-      const int h = g + 8 * nh;
-      const uint16_t* qp = a.q + int64_t(b) * a.q_stride + (int64_t(j) * G + (h < G ? h : 0)) * D;
-      if constexpr (FP8) {
-        float m = 0.f;
-        uint4 v[KP][2];
-#pragma unroll
-        for (int c = 0; c < KP; ++c) {
-          const int piece = D == 128 ? 2 * qd + c : qd;
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            v[c][e] = h < G ? __ldcg(reinterpret_cast<const uint4*>(qp + 16 * piece) + e)
-                            : make_uint4(0u, 0u, 0u, 0u);
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              m = fmaxf(m, fmaxf(fabsf(bf16_bits_to_f32(word(v[c][e], i) & 0xffffu)),
-                                 fabsf(bf16_bits_to_f32(word(v[c][e], i) >> 16))));
-          }
-        }
-        m = fmaxf(m, __shfl_xor_sync(kFull, m, 1));
-        m = fmaxf(m, __shfl_xor_sync(kFull, m, 2));
-        // 2^ex stays a normal number; a row whose largest element is below
-        // 2^-112 is brought up less far
-        const int ex = min(f16_prescale_exponent(m), 126);
-        const float up = __int_as_float((127 + ex) << 23);
-#pragma unroll
-        for (int c = 0; c < KP; ++c)
-#pragma unroll
-          for (int e = 0; e < 2; ++e)
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              qf[nh][8 * c + 4 * e + i] =
-                  pack_f16x2_scaled(bf16_bits_to_f32(word(v[c][e], i) & 0xffffu),
-                                    bf16_bits_to_f32(word(v[c][e], i) >> 16), up);
-        const float down = __int_as_float((127 - ex) << 23);
-        fac[nh][0] = a.scale * __shfl_sync(kFull, down, 8 * qd);
-        fac[nh][1] = a.scale * __shfl_sync(kFull, down, 8 * qd + 4);
-      } else {
-#pragma unroll
-        for (int c = 0; c < KP; ++c) {
-          const int piece = 8 * (c >> 1) + 2 * qd + (c & 1);
-          const uint4 v = h < G ? __ldcg(reinterpret_cast<const uint4*>(qp) + piece)
-                                : make_uint4(0u, 0u, 0u, 0u);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) qf[nh][4 * c + i] = word(v, i);
-        }
-        fac[nh][0] = fac[nh][1] = a.scale;
-      }
+    for (int nh = 0; nh < NH; ++nh)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const int hc = 8 * nh + 2 * qd + e;
         slope[nh][e] = a.slopes && hc < G ? __ldcg(a.slopes + j * G + hc) * kLog2e : 0.f;
-        if (plain) fac[nh][e] *= kLog2e;
       }
-    }
+    auto load_q = [&](const uint8_t* qs) {
+#pragma unroll
+      for (int nh = 0; nh < NH; ++nh) {
+        const int h = g + 8 * nh;
+        const uint4* qp = reinterpret_cast<const uint4*>(qs + h * D * 2);
+        if constexpr (FP8) {
+          float m = 0.f;
+          uint4 v[KP][2];
+#pragma unroll
+          for (int c = 0; c < KP; ++c) {
+            const int pc = D == 128 ? 2 * qd + c : qd;
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              v[c][e] = h < G ? qp[2 * pc + e] : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                m = fmaxf(m, fmaxf(fabsf(bf16_bits_to_f32(word(v[c][e], i) & 0xffffu)),
+                                   fabsf(bf16_bits_to_f32(word(v[c][e], i) >> 16))));
+            }
+          }
+          m = fmaxf(m, __shfl_xor_sync(kFull, m, 1));
+          m = fmaxf(m, __shfl_xor_sync(kFull, m, 2));
+          // 2^ex stays a normal number; a row whose largest element is below
+          // 2^-112 is brought up less far
+          const int ex = min(f16_prescale_exponent(m), 126);
+          const float up = __int_as_float((127 + ex) << 23);
+#pragma unroll
+          for (int c = 0; c < KP; ++c)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                qf[nh][8 * c + 4 * e + i] =
+                    pack_f16x2_scaled(bf16_bits_to_f32(word(v[c][e], i) & 0xffffu),
+                                      bf16_bits_to_f32(word(v[c][e], i) >> 16), up);
+          const float down = __int_as_float((127 - ex) << 23);
+          fac[nh][0] = a.scale * __shfl_sync(kFull, down, 8 * qd);
+          fac[nh][1] = a.scale * __shfl_sync(kFull, down, 8 * qd + 4);
+        } else {
+#pragma unroll
+          for (int c = 0; c < KP; ++c) {
+            const int pc = 8 * (c >> 1) + 2 * qd + (c & 1);
+            const uint4 v = h < G ? qp[pc] : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) qf[nh][4 * c + i] = word(v, i);
+          }
+          fac[nh][0] = fac[nh][1] = a.scale;
+        }
+        fac[nh][0] *= unit;
+        fac[nh][1] *= unit;
+      }
+    };
 
     float mrun[NH][2], lsum[NH][2], o[NH][MT][4];
     float vref = 0x1p-120f;  // unit of o on an FP8 cache, a power of two
@@ -555,7 +615,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int r = 16 * (tm * kGroupWarps + gw) + g + 8 * (e >> 1);
             float v = sc[tm][nh][e] * fac[nh][e & 1];
             if (!plain) {
-              v = (a.softcap > 0.f ? cap_score(v, a.softcap, inv_cap) : v) * kLog2e;
+              if (a.softcap > 0.f) v = fmaf(-2.f * cap2, rcp(1.f + ex2(v)), cap2);
               v = fmaf(slope[nh][e & 1], float(t0 + r - (n - 1)), v);
             }
             if (!FULLT && !visible(r)) v = -INFINITY;
@@ -700,6 +760,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         gave_up = true;
         break;
       }
+      if (x < kGroups) load_q(ring + st * P::kStage + P::kOffQ);  // the group's first tile
       const uint32_t have = mask[st];
       const int t0 = tok0 + (k0 + x) * kTok;
       const uint32_t all = kFull >> (32 - kGran);
@@ -729,90 +790,69 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int e = 0; e < 4; ++e) o[nh][mt][e] *= vref;
       }
     }
-    // dims of fragment (mt, row g | g + 8)
-    auto dim = [&](int mt, int up) {
-      if constexpr (FP8) return D / 8 * g + 2 * mt + up;
-      else if constexpr (D == 64) return 8 * g + 2 * mt + up;
-      else return 8 * g + mt + 64 * up;
+    // Unit (hf, qi) of a lane: head 8 (hf / 2) + 2 qd + hf % 2, four
+    // consecutive dims from first_dim(qi, g) on.
+    constexpr int QI = D / 32;
+    constexpr bool kSplitDims = !FP8 && D == 128;  // rows g, g + 8 are 64 dims apart
+    auto first_dim = [](int qi, int gg) {
+      return kSplitDims ? 8 * gg + 4 * (qi & 1) + 64 * (qi >> 1) : D / 8 * gg + 4 * qi;
     };
-    float* slot = scratch + gw * P::kSlot;  // [heads][D], max [heads], sum [heads]
-    auto put = [&] {
+    float* set = scratch + (P::kSets > 1 ? pairs & 1 : 0) * (P::kWarps * P::kSlot);
+    ++pairs;
+    const bool one = here == 1;  // a single tile: only its group has anything
+    const int w0 = one ? (it - i0) % kGroups * kGroupWarps : 0;
+    const int nw = one ? kGroupWarps : P::kWarps;
+    if (warp >= w0 && warp < w0 + nw) {
+      float* slot = set + warp * P::kSlot;
 #pragma unroll
       for (int nh = 0; nh < NH; ++nh)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const int hc = 8 * nh + 2 * qd + h;
-          if (hc < G) {
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt) {
-              slot[hc * D + dim(mt, 0)] = o[nh][mt][h];
-              slot[hc * D + dim(mt, 1)] = o[nh][mt][h + 2];
+          for (int qi = 0; qi < QI; ++qi) {
+            float4 v;
+            if constexpr (kSplitDims) {
+              const int up = 2 * (qi >> 1), mt = 4 * (qi & 1);
+              v = make_float4(o[nh][mt][h + up], o[nh][mt + 1][h + up], o[nh][mt + 2][h + up],
+                              o[nh][mt + 3][h + up]);
+            } else {
+              v = make_float4(o[nh][2 * qi][h], o[nh][2 * qi][h + 2], o[nh][2 * qi + 1][h],
+                              o[nh][2 * qi + 1][h + 2]);
             }
-            if (g == 0) {
-              slot[8 * NH * D + hc] = mrun[nh][h];
-              slot[8 * NH * (D + 1) + hc] = lsum[nh][h];
-            }
+            reinterpret_cast<float4*>(slot)[((2 * nh + h) * QI + qi) * 32 + lane] = v;
+          }
+          if (g == 0) {
+            slot[4 * P::kUnits + 8 * nh + 2 * qd + h] = mrun[nh][h];
+            slot[4 * P::kUnits + 8 * NH + 8 * nh + 2 * qd + h] = lsum[nh][h];
           }
         }
-    };
-    const bool one = here == 1;  // a single tile: only its group has anything
-    const int only = (it - i0) % kGroups;
-    if (!one) {
-      if (grp == 1) put();
-      consumer_sync();
-      if (grp == 0) {
-#pragma unroll
-        for (int nh = 0; nh < NH; ++nh)
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const int hc = 8 * nh + 2 * qd + h;
-            if (hc < G) {
-              const float m2 = slot[8 * NH * D + hc], l2 = slot[8 * NH * (D + 1) + hc];
-              const float M = fmaxf(mrun[nh][h], m2);
-              const float f1 = M == -INFINITY ? 0.f : ex2(mrun[nh][h] - M);
-              const float f2 = M == -INFINITY ? 0.f : ex2(m2 - M);
-              mrun[nh][h] = M;
-              lsum[nh][h] = lsum[nh][h] * f1 + l2 * f2;
-#pragma unroll
-              for (int mt = 0; mt < MT; ++mt) {
-                o[nh][mt][h] = o[nh][mt][h] * f1 + slot[hc * D + dim(mt, 0)] * f2;
-                o[nh][mt][h + 2] = o[nh][mt][h + 2] * f1 + slot[hc * D + dim(mt, 1)] * f2;
-              }
-            }
-          }
-        __syncwarp();
-        put();
-      }
-    } else if (grp == only) {
-      put();
     }
     // a wait that gave up: no result and no arrival, decided by all together
-    if (consumer_any(gave_up)) return;
+    if (consumer_any<P::kConsumers>(gave_up)) return;
     const bool whole = k0 == 0 && here == nt;
-    // the joined value of head r, dims 4c .. 4c + 3, from the four slots
-    auto joined = [&](int r, int c, float& M, float& Lq) {
+    // the warps' values of unit u of head r
+    auto joined = [&](int r, int u, float& M, float& Lq) {
       M = -INFINITY;
-#pragma unroll
-      for (int w = 0; w < kGroupWarps; ++w)
-        M = fmaxf(M, scratch[w * P::kSlot + 8 * NH * D + r]);
+      for (int w = 0; w < nw; ++w) M = fmaxf(M, set[(w0 + w) * P::kSlot + 4 * P::kUnits + r]);
       float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
       Lq = 0.f;
-#pragma unroll
-      for (int w = 0; w < kGroupWarps; ++w) {
-        const float* p = scratch + w * P::kSlot;
-        const float f = M == -INFINITY ? 0.f : ex2(p[8 * NH * D + r] - M);
-        const float4 v = *reinterpret_cast<const float4*>(p + r * D + 4 * c);
+      const float ms = M == -INFINITY ? 0.f : M;
+#pragma unroll 4
+      for (int w = 0; w < nw; ++w) {
+        const float* p = set + (w0 + w) * P::kSlot;
+        const float f = ex2(p[4 * P::kUnits + r] - ms);
+        const float4 v = reinterpret_cast<const float4*>(p)[u];
         s.x = fmaf(v.x, f, s.x);
         s.y = fmaf(v.y, f, s.y);
         s.z = fmaf(v.z, f, s.z);
         s.w = fmaf(v.w, f, s.w);
-        Lq = fmaf(p[8 * NH * (D + 1) + r], f, Lq);
+        Lq = fmaf(p[4 * P::kUnits + 8 * NH + r], f, Lq);
       }
       return s;
     };
     // final values from O, max (log2 units) and sum of head r
-    auto finish = [&](int r, int c, float4 s, float M, float Lq) {
-      const int h = j * G + r;
+    auto finish = [&](int r, int u, float4 s, float M, float Lq) {
+      const int h = j * G + r, ul = u & 31, qi = (u >> 5) % QI;
       if (a.sinks) {
         const float z = __ldcg(a.sinks + h) * kLog2e;
         const float M2 = fmaxf(M, z);
@@ -826,91 +866,122 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       const float inv = Lq > 0.f ? 1.f / Lq : Lq == 0.f ? 0.f : Lq;  // a NaN stays one
       const int64_t row = int64_t(b) * heads + h;
-      *reinterpret_cast<uint2*>(a.out + row * D + 4 * c) =
+      const int d0 = first_dim(qi, ul >> 2);
+      *reinterpret_cast<uint2*>(a.out + row * D + d0) =
           make_uint2(bf16x2(s.x * inv, s.y * inv), bf16x2(s.z * inv, s.w * inv));
-      if (a.lse && c == 0)
+      if (a.lse && d0 == 0)
         a.lse[row] = Lq == 0.f ? -INFINITY : (M + log2f(Lq)) * 0.6931471805599453f;
     };
-    const int quads = G * (D / 4);
+    // head of unit u
+    auto head_of = [](int u) {
+      const int hf = (u >> 5) / QI;
+      return 8 * (hf >> 1) + 2 * (u & 3) + (hf & 1);
+    };
     if (whole) {
-      for (int e = tid; e < quads; e += kConsumers) {
+      for (int u = tid; u < P::kUnits; u += kConsumers) {
+        const int r = head_of(u);
+        if (r >= G) continue;
         float M, Lq;
-        const int r = e / (D / 4), c = e % (D / 4);
-        const float4 s = joined(r, c, M, Lq);
-        finish(r, c, s, M, Lq);
+        const float4 s = joined(r, u, M, Lq);
+        finish(r, u, s, M, Lq);
       }
     } else {
-      const int PS = part_floats(G, D);
       const int64_t s0 = L.prefix[b] + int64_t(j) * nt;  // the pair's first item
       const int cf = int(((s0 + 1) * C - 1) / T);        // CTAs of its first and last items
       const int cl = int(((s0 + nt) * C - 1) / T);
-      float* part = a.parts + (int64_t(blockIdx.x) * 2 + (k0 == 0)) * PS;
-      for (int e = tid; e < quads; e += kConsumers) {
+      float* part = a.parts + (int64_t(blockIdx.x) * 2 + (k0 == 0)) * P::kSlot;
+      for (int u = tid; u < P::kUnits; u += kConsumers) {
+        const int r = head_of(u);
+        if (r >= G) continue;
         float M, Lq;
-        const int r = e / (D / 4), c = e % (D / 4);
-        const float4 s = joined(r, c, M, Lq);
-        *reinterpret_cast<float4*>(part + r * D + 4 * c) = s;
-        if (c == 0) {
-          part[G * D + r] = M;
-          part[G * D + G + r] = Lq;
+        const float4 s = joined(r, u, M, Lq);
+        reinterpret_cast<float4*>(part)[u] = s;
+        if (first_dim((u >> 5) % QI, (u & 31) >> 2) == 0) {
+          part[4 * P::kUnits + r] = M;
+          part[4 * P::kUnits + 8 * NH + r] = Lq;
         }
       }
       __threadfence();
-      consumer_sync();
+      consumer_sync<P::kConsumers>();
       if (tid == 0) flags[0] = atomicAdd(a.counters + cf, 1) == cl - cf;
-      consumer_sync();
+      consumer_sync<P::kConsumers>();
       if (flags[0]) {
         __threadfence();
         const int np = cl - cf + 1;
-        auto part_of = [&](int p) {
-          return a.parts + (int64_t(cf + p) * 2 + (p == 0)) * PS;
-        };
-        float* hm = scratch;  // [16] max, [16] sum of the pair's heads
-        for (int r = warp; r < G; r += kConsumers / 32) {
-          float M = -INFINITY, Lq = 0.f;
-          for (int p = lane; p < np; p += 32) M = fmaxf(M, __ldcg(part_of(p) + G * D + r));
-          M = warp_max(M);
-          for (int p = lane; p < np; p += 32)
-            Lq += M == -INFINITY ? 0.f
-                                 : ex2(__ldcg(part_of(p) + G * D + r) - M) *
-                                       __ldcg(part_of(p) + G * D + G + r);
-          Lq = warp_sum(Lq);
-          if (lane == 0) {
-            hm[r] = M;
-            hm[16 + r] = Lq;
-          }
-        }
-        consumer_sync();
-        for (int e = tid; e < quads; e += kConsumers) {
-          const int r = e / (D / 4), c = e % (D / 4);
-          const float M = hm[r];
+        // Each thread one unit: the parts in turn with the running maximum,
+        // kJoin parts' loads in flight.  Where there are more threads than
+        // units, kSub of them share a unit's parts and are joined after.
+        constexpr int kJoin = 16;
+        constexpr int kSub = kConsumers > P::kUnits ? kConsumers / P::kUnits : 1;
+        for (int u0 = tid; u0 < P::kUnits * kSub; u0 += kConsumers) {
+          const int u = u0 % P::kUnits, sub = u0 / P::kUnits, r = head_of(u);
           float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-          for (int p0 = 0; p0 < np; p0 += 8) {
-            float4 v[8];
-            float m[8];
+          float M = -INFINITY, Lq = 0.f;
+          for (int p0 = sub; p0 < np && r < G; p0 += kJoin * kSub) {
+            float4 v[kJoin];
+            float m[kJoin], l[kJoin], mx = M;
 #pragma unroll
-            for (int u = 0; u < 8; ++u) {
-              const bool in = p0 + u < np;
-              const float* pp = part_of(in ? p0 + u : 0);
-              v[u] = in ? __ldcg(reinterpret_cast<const float4*>(pp + r * D + 4 * c))
+            for (int e = 0; e < kJoin; ++e) {
+              const int p = p0 + e * kSub;
+              const bool in = p < np;
+              const float* pp = a.parts + (int64_t(cf + (in ? p : 0)) * 2 + (!in || p == 0)) * P::kSlot;
+              v[e] = in ? __ldcg(reinterpret_cast<const float4*>(pp) + u)
                         : make_float4(0.f, 0.f, 0.f, 0.f);
-              m[u] = in ? __ldcg(pp + G * D + r) : -INFINITY;
+              m[e] = in ? __ldcg(pp + 4 * P::kUnits + r) : -INFINITY;
+              l[e] = in ? __ldcg(pp + 4 * P::kUnits + 8 * NH + r) : 0.f;
             }
 #pragma unroll
-            for (int u = 0; u < 8; ++u) {
-              const float f = M == -INFINITY ? 0.f : ex2(m[u] - M);
-              s.x = fmaf(v[u].x, f, s.x);
-              s.y = fmaf(v[u].y, f, s.y);
-              s.z = fmaf(v[u].z, f, s.z);
-              s.w = fmaf(v[u].w, f, s.w);
+            for (int e = 0; e < kJoin; ++e) mx = fmaxf(mx, m[e]);
+            const float ms = mx == -INFINITY ? 0.f : mx;
+            const float old = ex2(M - ms);
+            M = mx;
+            s.x *= old;
+            s.y *= old;
+            s.z *= old;
+            s.w *= old;
+            Lq *= old;
+#pragma unroll
+            for (int e = 0; e < kJoin; ++e) {
+              const float f = ex2(m[e] - ms);
+              s.x = fmaf(v[e].x, f, s.x);
+              s.y = fmaf(v[e].y, f, s.y);
+              s.z = fmaf(v[e].z, f, s.z);
+              s.w = fmaf(v[e].w, f, s.w);
+              Lq = fmaf(l[e], f, Lq);
             }
           }
-          finish(r, c, s, M, hm[16 + r]);
+          if constexpr (kSub > 1) {
+            // [sub][unit] values, then maxima, then sums, in the slots
+            float4* sv = reinterpret_cast<float4*>(set);
+            float* sm = set + 4 * kSub * P::kUnits;
+            sv[u0] = s;
+            sm[u0] = M;
+            sm[kSub * P::kUnits + u0] = Lq;
+            consumer_sync<P::kConsumers>();
+            if (sub == 0) {
+              float mx = M;
+              for (int e = 1; e < kSub; ++e) mx = fmaxf(mx, sm[e * P::kUnits + u]);
+              const float ms = mx == -INFINITY ? 0.f : mx;
+              s = make_float4(0.f, 0.f, 0.f, 0.f);
+              Lq = 0.f;
+              for (int e = 0; e < kSub; ++e) {
+                const float f = ex2(sm[e * P::kUnits + u] - ms);
+                const float4 v = sv[e * P::kUnits + u];
+                s.x = fmaf(v.x, f, s.x);
+                s.y = fmaf(v.y, f, s.y);
+                s.z = fmaf(v.z, f, s.z);
+                s.w = fmaf(v.w, f, s.w);
+                Lq = fmaf(sm[kSub * P::kUnits + e * P::kUnits + u], f, Lq);
+              }
+              M = mx;
+            }
+          }
+          if (sub == 0 && r < G) finish(r, u, s, M, Lq);
         }
         if (tid == 0) a.counters[cf] = 0;  // ready for the next call
       }
     }
-    consumer_sync();  // the scratch is free again
+    if (P::kSets == 1) consumer_sync<P::kConsumers>();  // the slots are free again
     it += here;
     at.tile = 0;
     if (k0 + here == nt) {
@@ -928,6 +999,8 @@ cudaError_t launch(const DeviceInfo& di, const PagedKv& kv, const PagedAttnArgs&
                    cudaStream_t s, bool pdl) {
   using P = Plan<D, NH, FP8>;
   auto kern = paged_decode_kernel<D, NH, FP8>;
+  static const bool fits = has_registers(kern, P::kLaunchRegs);
+  if (!fits) return cudaErrorInvalidDeviceFunction;
   if (cudaError_t e = ensure_smem(di, kern, P::kSmem)) return e;
   // one CTA per SM, or one per tile that the table could hold where that is less
   const int64_t most =
@@ -951,7 +1024,7 @@ cudaError_t launch(const DeviceInfo& di, const PagedKv& kv, const PagedAttnArgs&
   d.err = di.error_word;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(unsigned(grid));
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(P::kThreads);
   cfg.dynamicSmemBytes = P::kSmem;
   cfg.stream = s;
   cudaLaunchAttribute attr[1];

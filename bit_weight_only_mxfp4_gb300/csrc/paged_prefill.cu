@@ -54,6 +54,9 @@ constexpr int kRows = 128;   // rows of a row tile
 constexpr int kKeys = 128;   // tokens of a K / V tile
 constexpr int kWarps = 12;
 constexpr int kThreads = 32 * kWarps;
+// registers a thread: at launch, for the softmax warps, for the others
+constexpr int kLaunchRegs = 168, kSoftmaxRegs = 208, kOtherRegs = 88;
+static_assert(256 * kSoftmaxRegs + 128 * kOtherRegs <= kThreads * kLaunchRegs, "register shares");
 constexpr int kMmaWarp = 8, kLoadWarp = 9, kFixWarp = 10;
 constexpr int kFixers = 64;
 constexpr int kCounters = 1024;  // as in the decode kernel's part of the workspace
@@ -452,7 +455,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int boxes = kKeys >> br_shift;
 
   if (warp >= kMmaWarp) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
     if (warp == kLoadWarp) {
       // ============================================================ copies
       uint32_t n = 0;  // slots used
@@ -767,7 +770,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else {
     // ============================================================== softmax
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
     const int g = warp >> 2, r = tid & (kRows - 1);
     const uint32_t lanes = uint32_t((warp & 3) * 32) << 16;
     const uint32_t ts = tmem + lanes + P::kColS + g * 128, to = tmem + lanes + P::kColO + g * 128;
@@ -1141,6 +1144,8 @@ cudaError_t launch(const DeviceInfo& di, const PagedKv& kv, const PagedAttnArgs&
     if (cudaError_t e = encode(&mk, kv.k, 2, dims, strides, box)) return e;
     if (cudaError_t e = encode(&mv, kv.v, 2, dims, strides, box)) return e;
   }
+  static const bool fits = has_registers(kern, kLaunchRegs);
+  if (!fits) return cudaErrorInvalidDeviceFunction;
   if (cudaError_t e = ensure_smem(di, kern, P::kSmem)) return e;
   PrefillArgs d;
   d.starts = a.starts;
