@@ -17,10 +17,11 @@
 // serves the whole group and short chunks still fill rows.  A CTA works on
 // two row tiles at once (A and B), each with a warpgroup for its softmax, one
 // thread a row, while the tensor cores are busy with the other's products:
-//   warps 0-3, 4-7  softmax of A and B (208 registers: a row's 128 scores)
+//   warps 0-3, 4-7  softmax of A and B (a thread holds a row's 128 scores)
 //   warp 8          the products, one thread
 //   warp 9          the copies (TMA: one box per page and 64 dims)
-//   warps 10-11     make the V tiles safe (below); FP8: E4M3 -> bf16 tiles
+//   warps 10, 11    make the V tiles safe (below); FP8: warps 10-15, which
+//                   also turn E4M3 pages into bf16 tiles
 // The running maximum is only raised (and O rescaled, which takes a TMEM round
 // trip) when a row's maximum has grown by more than 2^8: the weights are then
 // at most 2^8, which costs no precision in bf16 and 32 bits.
@@ -42,6 +43,7 @@
 // its tokens and joined by the last part to finish, from the parts in order.
 // What the lengths are is read on the device.
 #include <cmath>
+#include <type_traits>
 
 #include "launch.h"
 #include "paged.cuh"
@@ -52,19 +54,24 @@ namespace {
 
 constexpr int kRows = 128;   // rows of a row tile
 constexpr int kKeys = 128;   // tokens of a K / V tile
-constexpr int kWarps = 12;
-constexpr int kThreads = 32 * kWarps;
-// registers a thread: at launch, for the softmax warps, for the others
-constexpr int kLaunchRegs = 168, kSoftmaxRegs = 208, kOtherRegs = 88;
-static_assert(256 * kSoftmaxRegs + 128 * kOtherRegs <= kThreads * kLaunchRegs, "register shares");
 constexpr int kMmaWarp = 8, kLoadWarp = 9, kFixWarp = 10;
-constexpr int kFixers = 64;
 constexpr int kCounters = 1024;  // as in the decode kernel's part of the workspace
 constexpr int kMaxSplit = 32;
 constexpr uint32_t kAll = 0xffffffffu;
 
 template <int D, bool FP8>
 struct Plan {
+  // warps 0-7 softmax, 8 products, 9 copies, and from kFixWarp on those that
+  // make the V tiles safe: two; FP8: six, which convert.  Registers a thread:
+  // at launch, for the softmax warps (a thread holds a row's 128 scores), for
+  // the others.
+  static constexpr int kThreads = FP8 ? 512 : 384;
+  static constexpr int kFixers = kThreads - 32 * kFixWarp;
+  static constexpr int kLaunchRegs = FP8 ? 128 : 168;
+  static constexpr int kSoftmaxRegs = FP8 ? 184 : 208;
+  static constexpr int kOtherRegs = FP8 ? 72 : 88;
+  static_assert(256 * kSoftmaxRegs + (kThreads - 256) * kOtherRegs <= kThreads * kLaunchRegs,
+                "register shares");
   static constexpr int kHalves = D / 64;            // 128-byte spans of a bf16 row
   static constexpr int kSpan = kKeys * 128;         // bytes of a tile's one span
   static constexpr int kTile = kSpan * kHalves;     // a K or V tile, or a Q tile
@@ -76,7 +83,7 @@ struct Plan {
   static constexpr int kOffScale = kOffRaw + kRaws * kRaw;      // [4 tiles][key, value][128]
   static constexpr int kOffLine = kOffScale + (FP8 ? 4 * 2 * kKeys * 4 : 0);
   static constexpr int kOffBar = kOffLine + (kPagedMaxBatch + 1) * 4 + 12;
-  static constexpr int kSmem = 1024 + kOffBar + 512;
+  static constexpr int kSmem = 1024 + kOffBar + 640;
   static_assert(kSmem <= 227 * 1024, "shared memory");
   static_assert(kOffBar % 8 == 0, "barriers");
   // TMEM columns: S (and P over it) of A and B, O of A and B
@@ -119,26 +126,32 @@ __device__ __forceinline__ constexpr uint32_t idesc(int n, bool mn) {
   return (1u << 4) | (1u << 7) | (1u << 10) | (mn ? 1u << 16 : 0u) | (uint32_t(n >> 3) << 17) |
          (uint32_t(kRows >> 4) << 24);
 }
+// The products are issued by a whole warp in step, one elected lane each:
+// the compiler then knows that their operands are the same in all lanes and
+// keeps them in uniform registers.  (In a branch of one lane every operand is
+// moved there first: 60 to 110 cycles an instruction, more than the products
+// themselves take.)
 __device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t id,
                                        uint32_t acc) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "{\n\t.reg .pred p, e;\n\tsetp.ne.b32 p, %4, 0;\n\telect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
       "l"(a), "l"(b), "r"(id), "r"(acc)
       : "memory");
 }
 __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t id,
                                        uint32_t acc) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "{\n\t.reg .pred p, e;\n\tsetp.ne.b32 p, %4, 0;\n\telect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
       "r"(a), "l"(b), "r"(id), "r"(acc)
       : "memory");
 }
-__device__ __forceinline__ void commit(uint64_t* bar) {
+__device__ __forceinline__ void commit(uint32_t bar) {
   asm volatile(
-      "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
-          smem_u32(bar))
+      "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(
+          bar)
       : "memory");
 }
 __device__ __forceinline__ void fence_after() {
@@ -147,8 +160,17 @@ __device__ __forceinline__ void fence_after() {
 __device__ __forceinline__ void fence_before() {
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
 }
-__device__ __forceinline__ void wait_ld() {
-  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+// Waits for this thread's tcgen05.ld; the registers pass through, so that
+// nothing that uses them is moved before it.
+__device__ __forceinline__ void wait_ld(uint32_t (&r)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]),
+                 "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]),
+                 "+r"(r[14]), "+r"(r[15]), "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]),
+                 "+r"(r[21]), "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]),
+                 "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
+               :
+               : "memory");
 }
 __device__ __forceinline__ void wait_st() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
@@ -177,6 +199,75 @@ __device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t (&r)[32]
       "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]),
       "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]),
       "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+
+// 64 columns of this warp's 32 lanes into r[first ..] (complete after
+// wait_ld128).
+template <int first>
+__device__ __forceinline__ void tmem_ld64(uint32_t addr, uint32_t (&r)[128]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x64.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17,"
+      "%18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32, %33,"
+      "%34, %35, %36, %37, %38, %39, %40, %41, %42, %43, %44, %45, %46, %47, %48, %49,"
+      "%50, %51, %52, %53, %54, %55, %56, %57, %58, %59, %60, %61, %62, %63}, [%64];"
+      : "=r"(r[first + 0]), "=r"(r[first + 1]), "=r"(r[first + 2]), "=r"(r[first + 3]), "=r"(r[first + 4]), "=r"(r[first + 5]), "=r"(r[first + 6]),
+      "=r"(r[first + 7]), "=r"(r[first + 8]), "=r"(r[first + 9]), "=r"(r[first + 10]), "=r"(r[first + 11]), "=r"(r[first + 12]), "=r"(r[first + 13]),
+      "=r"(r[first + 14]), "=r"(r[first + 15]), "=r"(r[first + 16]), "=r"(r[first + 17]), "=r"(r[first + 18]), "=r"(r[first + 19]), "=r"(r[first + 20]),
+      "=r"(r[first + 21]), "=r"(r[first + 22]), "=r"(r[first + 23]), "=r"(r[first + 24]), "=r"(r[first + 25]), "=r"(r[first + 26]), "=r"(r[first + 27]),
+      "=r"(r[first + 28]), "=r"(r[first + 29]), "=r"(r[first + 30]), "=r"(r[first + 31]), "=r"(r[first + 32]), "=r"(r[first + 33]), "=r"(r[first + 34]),
+      "=r"(r[first + 35]), "=r"(r[first + 36]), "=r"(r[first + 37]), "=r"(r[first + 38]), "=r"(r[first + 39]), "=r"(r[first + 40]), "=r"(r[first + 41]),
+      "=r"(r[first + 42]), "=r"(r[first + 43]), "=r"(r[first + 44]), "=r"(r[first + 45]), "=r"(r[first + 46]), "=r"(r[first + 47]), "=r"(r[first + 48]),
+      "=r"(r[first + 49]), "=r"(r[first + 50]), "=r"(r[first + 51]), "=r"(r[first + 52]), "=r"(r[first + 53]), "=r"(r[first + 54]), "=r"(r[first + 55]),
+      "=r"(r[first + 56]), "=r"(r[first + 57]), "=r"(r[first + 58]), "=r"(r[first + 59]), "=r"(r[first + 60]), "=r"(r[first + 61]), "=r"(r[first + 62]),
+      "=r"(r[first + 63])
+      : "r"(addr));
+}
+// Waits for this thread's loads; the registers pass through, so that nothing
+// that uses them is moved before.
+__device__ __forceinline__ void wait_ld128(uint32_t (&r)[128]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+      : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]),
+      "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]),
+      "+r"(r[14]), "+r"(r[15]), "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]),
+      "+r"(r[21]), "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]),
+      "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31]), "+r"(r[32]), "+r"(r[33]), "+r"(r[34]),
+      "+r"(r[35]), "+r"(r[36]), "+r"(r[37]), "+r"(r[38]), "+r"(r[39]), "+r"(r[40]), "+r"(r[41]),
+      "+r"(r[42]), "+r"(r[43]), "+r"(r[44]), "+r"(r[45]), "+r"(r[46]), "+r"(r[47]), "+r"(r[48]),
+      "+r"(r[49]), "+r"(r[50]), "+r"(r[51]), "+r"(r[52]), "+r"(r[53]), "+r"(r[54]), "+r"(r[55]),
+      "+r"(r[56]), "+r"(r[57]), "+r"(r[58]), "+r"(r[59]), "+r"(r[60]), "+r"(r[61]), "+r"(r[62]),
+      "+r"(r[63])
+      :
+      : "memory");
+  asm volatile(""
+      : "+r"(r[64]), "+r"(r[65]), "+r"(r[66]), "+r"(r[67]), "+r"(r[68]), "+r"(r[69]), "+r"(r[70]),
+      "+r"(r[71]), "+r"(r[72]), "+r"(r[73]), "+r"(r[74]), "+r"(r[75]), "+r"(r[76]), "+r"(r[77]),
+      "+r"(r[78]), "+r"(r[79]), "+r"(r[80]), "+r"(r[81]), "+r"(r[82]), "+r"(r[83]), "+r"(r[84]),
+      "+r"(r[85]), "+r"(r[86]), "+r"(r[87]), "+r"(r[88]), "+r"(r[89]), "+r"(r[90]), "+r"(r[91]),
+      "+r"(r[92]), "+r"(r[93]), "+r"(r[94]), "+r"(r[95]), "+r"(r[96]), "+r"(r[97]), "+r"(r[98]),
+      "+r"(r[99]), "+r"(r[100]), "+r"(r[101]), "+r"(r[102]), "+r"(r[103]), "+r"(r[104]),
+      "+r"(r[105]), "+r"(r[106]), "+r"(r[107]), "+r"(r[108]), "+r"(r[109]), "+r"(r[110]),
+      "+r"(r[111]), "+r"(r[112]), "+r"(r[113]), "+r"(r[114]), "+r"(r[115]), "+r"(r[116]),
+      "+r"(r[117]), "+r"(r[118]), "+r"(r[119]), "+r"(r[120]), "+r"(r[121]), "+r"(r[122]),
+      "+r"(r[123]), "+r"(r[124]), "+r"(r[125]), "+r"(r[126]), "+r"(r[127])
+      :
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st64(uint32_t addr, const uint32_t (&r)[64]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x64.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18,"
+      "%19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32, %33, %34,"
+      "%35, %36, %37, %38, %39, %40, %41, %42, %43, %44, %45, %46, %47, %48, %49, %50,"
+      "%51, %52, %53, %54, %55, %56, %57, %58, %59, %60, %61, %62, %63, %64};" ::"r"(addr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
+      "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]),
+      "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]),
+      "r"(r[29]), "r"(r[30]), "r"(r[31]), "r"(r[32]), "r"(r[33]), "r"(r[34]), "r"(r[35]),
+      "r"(r[36]), "r"(r[37]), "r"(r[38]), "r"(r[39]), "r"(r[40]), "r"(r[41]), "r"(r[42]),
+      "r"(r[43]), "r"(r[44]), "r"(r[45]), "r"(r[46]), "r"(r[47]), "r"(r[48]), "r"(r[49]),
+      "r"(r[50]), "r"(r[51]), "r"(r[52]), "r"(r[53]), "r"(r[54]), "r"(r[55]), "r"(r[56]),
+      "r"(r[57]), "r"(r[58]), "r"(r[59]), "r"(r[60]), "r"(r[61]), "r"(r[62]), "r"(r[63])
       : "memory");
 }
 
@@ -237,6 +328,11 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
 }
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float y;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+  return y;
+}
 __device__ __forceinline__ float rcp(float x) {
   float y;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -287,13 +383,16 @@ __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile in
   }
 }
 
-template <int D, bool FP8>
-__global__ void __launch_bounds__(kThreads, 1)
+// GEN: a cap, a bias or a scale that is not positive (the plain kernel's loop
+// stays short without them).
+template <int D, bool FP8, bool GEN>
+__global__ void __launch_bounds__(Plan<D, FP8>::kThreads, 1)
     paged_prefill_kernel(const __grid_constant__ CUtensorMap map_q,
                          const __grid_constant__ CUtensorMap map_k,
                          const __grid_constant__ CUtensorMap map_v, const PagedKv kv,
                          const PrefillArgs a) {
   using P = Plan<D, FP8>;
+  constexpr int kThreads = P::kThreads, kFixers = P::kFixers;
   extern __shared__ __align__(128) uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
   const uint32_t sbase = smem_u32(smem);
@@ -305,23 +404,22 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* raw_full = ready + P::kSlots;
   uint64_t* raw_empty = raw_full + 4;
   uint64_t* q_full = raw_empty + 4;      // [2]
-  uint64_t* q_free = q_full + 2;         // [2]
-  uint64_t* s_full = q_free + 2;         // [2]
+  uint64_t* q_free = q_full + 2;
+  uint64_t* s_full = q_free + 1;         // [2]
   uint64_t* p_full = s_full + 2;         // [2]
-  uint64_t* p_half = p_full + 2;         // [2]
-  uint64_t* o_done = p_half + 2;         // [2]
+  uint64_t* o_done = p_full + 2;         // [2]
   uint64_t* join = o_done + 2;           // [2]
   uint64_t* drained = join + 2;
   uint32_t* have = reinterpret_cast<uint32_t*>(drained + 1);  // [8] boxes present, per tile
   int* dirty = reinterpret_cast<int*>(have + 8);              // [4] item number + 1
-  int* misc = dirty + 4;  // [0] TMEM address, [1] quit, [2 + g] last to finish, [4..] scan
+  int* misc = dirty + 4;  // [0] TMEM address, [1] quit, [2 + g] last to finish, [4 .. 19] scan
   volatile int* quit = misc + 1;
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if (tid == 0) {
     for (int i = 0; i < P::kSlots; ++i) {
       mbar_init(smem_u32(&full[i]), 1);
-      mbar_init(smem_u32(&empty[i]), 1);
+      mbar_init(smem_u32(&empty[i]), 2);  // both row tiles
       mbar_init(smem_u32(&ready[i]), kFixers);
     }
     for (int i = 0; i < 4; ++i) {
@@ -330,13 +428,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int g = 0; g < 2; ++g) {
       mbar_init(smem_u32(&q_full[g]), 1);
-      mbar_init(smem_u32(&q_free[g]), 1);
       mbar_init(smem_u32(&s_full[g]), 1);
       mbar_init(smem_u32(&p_full[g]), kRows);
-      mbar_init(smem_u32(&p_half[g]), kRows);
       mbar_init(smem_u32(&o_done[g]), 1);
       mbar_init(smem_u32(&join[g]), kRows);
     }
+    mbar_init(smem_u32(q_free), 2);
     mbar_init(smem_u32(drained), 1);
     for (int i = 0; i < 4; ++i) dirty[i] = 0;
     misc[1] = 0;
@@ -455,7 +552,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int boxes = kKeys >> br_shift;
 
   if (warp >= kMmaWarp) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(P::kOtherRegs));
     if (warp == kLoadWarp) {
       // ============================================================ copies
       uint32_t n = 0;  // slots used
@@ -467,9 +564,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const Item w = item_of(idx);
         if (w.k1 <= w.k0) continue;
         const int groups = has_b(w) ? 2 : 1;
-        // Q is free when the last score product of the item before is done
-        // (of either tile: the products of B follow A's)
-        if (seq > 0) ok = __all_sync(kAll, wait(&q_free[0], uint32_t(seq - 1) & 1u, quit, a.err));
+        // Q is free when the last score products of the item before are done
+        if (seq > 0) ok = __all_sync(kAll, wait(q_free, uint32_t(seq - 1) & 1u, quit, a.err));
         if (!ok) break;
         if (lane < groups) {
           const uint32_t bar = smem_u32(&q_full[lane]);
@@ -546,103 +642,109 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     } else if (warp == kMmaWarp) {
       // ========================================================== products
-      if (lane == 0) {
-        uint32_t n = 0, ca = 0, cb = 0, seq = 0, qb = 0;  // slots; tiles of A, of B; items
-        bool ok = true;
-        auto scores = [&](int g, uint32_t slot) {
-          const uint32_t q = sbase + g * P::kTile, k = sbase + P::kOffKv + slot * P::kTile;
+      // One warp for both row tiles, whichever is ready, so that a tile's
+      // products (P V, then the next scores) go to the tensor cores in one
+      // piece.  (With an issuer for each they are taken in turn, both tiles
+      // wait for both, and softmax and products do not overlap: a softmax
+      // warp waited 2275 of 4190 cycles a tile.)  One commit a tile: products
+      // finish in order, so scores that are there say that the P V before
+      // them is done.
+      const uint32_t kv0 = sbase + P::kOffKv;
+      uint32_t n = 0, my0 = 0, my1 = 0, seq0 = 0, seq1 = 0;  // slots; tiles, items of A and B
+      bool ok = tmem == 0;  // all columns are ours, so they begin at 0
+      if (!ok && lane == 0) {
+        *quit = 1;
+        flag_error(a.err, kErrShape);
+      }
+      auto scores = [&](auto gc, uint32_t slot) {
+        constexpr int g = decltype(gc)::value;
+        const uint64_t q = desc_k(sbase + g * P::kTile), k = desc_k(kv0 + slot * P::kTile);
 #pragma unroll
-          for (int i = 0; i < D / 16; ++i) {
-            const uint32_t off = (i >> 2) * P::kSpan + (i & 3) * 32;
-            mma_ss(tmem + P::kColS + g * 128, desc_k(q + off), desc_k(k + off),
-                   idesc(kKeys, false), i > 0);
-          }
-        };
-        // half 0, 1: the first and the last 64 tokens
-        auto values = [&](int g, uint32_t slot, bool first, int half) {
-          const uint32_t v = sbase + P::kOffKv + slot * P::kTile;
+        for (int i = 0; i < D / 16; ++i) {
+          const uint64_t off = ((i >> 2) * P::kSpan + (i & 3) * 32) >> 4;
+          mma_ss(P::kColS + g * 128, q + off, k + off, idesc(kKeys, false), i > 0);
+        }
+        commit(smem_u32(&s_full[g]));
+      };
+      auto values = [&](auto gc, uint32_t slot, uint32_t more) {
+        constexpr int g = decltype(gc)::value;
+        const uint64_t v = desc_mn(kv0 + slot * P::kTile, P::kHalves > 1 ? P::kSpan : 1024);
 #pragma unroll
-          for (int i = 0; i < kKeys / 32; ++i) {
-            const int k = half * (kKeys / 32) + i;
-            mma_ts(tmem + P::kColO + g * 128, tmem + P::kColS + g * 128 + 8 * k,
-                   desc_mn(v + k * 2048, P::kHalves > 1 ? P::kSpan : 1024), idesc(D, true),
-                   !first || k > 0);
-          }
-        };
-        auto key_ready = [&](uint32_t m) {
-          return wait(FP8 ? &ready[m % P::kSlots] : &full[m % P::kSlots], (m / P::kSlots) & 1u,
-                      quit, a.err);
-        };
-        // (bf16: an even number of slots, so that a slot is K's or V's for good)
-        auto value_ready = [&](uint32_t m) {
-          return wait(&ready[m % P::kSlots], (m / P::kSlots) & 1u, quit, a.err);
-        };
-        for (int64_t turn = 0, idx; ok && (idx = turn_of(turn)) >= 0; ++turn) {
-          if (idx >= items) continue;
-          const Item w = item_of(idx);
-          const int nk = w.k1 - w.k0;
-          if (nk <= 0) continue;
-          const bool b = has_b(w);
-          ok = wait(&q_full[0], seq & 1u, quit, a.err) && (!b || wait(&q_full[1], qb & 1u, quit, a.err)) &&
-               key_ready(n);
+        for (int k = 0; k < kKeys / 16; ++k)
+          mma_ts(P::kColO + g * 128, P::kColS + g * 128 + 8 * k, v + k * (2048 >> 4),
+                 idesc(D, true), k > 0 ? 1u : more);
+      };
+      // slot use m has its K tile, its V tile (bf16: an even number of slots,
+      // so that a slot is K's or V's for good)
+      auto key_bar = [&](uint32_t m) {
+        return smem_u32(FP8 ? &ready[m % P::kSlots] : &full[m % P::kSlots]);
+      };
+      auto phase = [&](uint32_t m) { return (m / P::kSlots) & 1u; };
+      using G0 = std::integral_constant<int, 0>;
+      using G1 = std::integral_constant<int, 1>;
+      for (int64_t turn = 0, idx; ok && (idx = turn_of(turn)) >= 0; ++turn) {
+        if (idx >= items) continue;
+        const Item w = item_of(idx);
+        const int nk = __shfl_sync(kAll, w.k1 - w.k0, 0);
+        if (nk <= 0) continue;
+        const bool b = __shfl_sync(kAll, int(has_b(w)), 0) != 0;
+        ok = __all_sync(kAll, wait(&q_full[0], seq0++ & 1u, quit, a.err) &&
+                                  wait(FP8 ? &ready[n % P::kSlots] : &full[n % P::kSlots],
+                                       phase(n), quit, a.err));
+        if (!ok) break;
+        fence_after();
+        scores(G0{}, n % P::kSlots);
+        if (b) {
+          ok = __all_sync(kAll, wait(&q_full[1], seq1++ & 1u, quit, a.err));
           if (!ok) break;
           fence_after();
-          scores(0, n % P::kSlots);
-          commit(&s_full[0]);
-          if (b) {
-            scores(1, n % P::kSlots);
-            commit(&s_full[1]);
-          }
-          commit(&empty[n % P::kSlots]);
-          if (nk == 1) commit(&q_free[0]);
-          for (int i = 0; i < nk; ++i, n += 2) {
-            const bool next = i + 1 < nk;
-            const uint32_t vs = (n + 1) % P::kSlots, ks = (n + 2) % P::kSlots;
-            ok = value_ready(n + 1) && wait(&p_half[0], ca & 1u, quit, a.err);
-            if (!ok) break;
-            fence_after();
-            values(0, vs, i == 0, 0);
-            ok = (!next || key_ready(n + 2)) && wait(&p_full[0], ca & 1u, quit, a.err);
-            if (!ok) break;
-            fence_after();
-            values(0, vs, i == 0, 1);
-            commit(&o_done[0]);
-            ++ca;
-            if (next) {
-              scores(0, ks);
-              commit(&s_full[0]);
-            }
-            if (b) {
-              ok = wait(&p_half[1], cb & 1u, quit, a.err);
-              if (!ok) break;
-              fence_after();
-              values(1, vs, i == 0, 0);
-              ok = wait(&p_full[1], cb & 1u, quit, a.err);
-              if (!ok) break;
-              fence_after();
-              values(1, vs, i == 0, 1);
-              commit(&o_done[1]);
-              ++cb;
-            }
-            commit(&empty[vs]);
-            if (next) {
-              if (b) {
-                scores(1, ks);
-                commit(&s_full[1]);
-              }
-              commit(&empty[ks]);
-              if (i + 2 == nk) commit(&q_free[0]);
-            }
-          }
-          ++seq;
-          qb += b;
+          scores(G1{}, n % P::kSlots);
         }
-        // nothing of the tensor cores is under way when the CTA ends
-        commit(drained);
-        (void)mbar_wait_bounded(smem_u32(drained), 0);
+        uint32_t i0 = 0, i1 = b ? 0 : nk;
+        uint64_t since = 0;  // of the idle stretch
+        auto tile = [&](auto gc, uint32_t& i, uint32_t& my) {
+          constexpr int g = decltype(gc)::value;
+          if (i >= uint32_t(nk)) return false;
+          const uint32_t m = n + 2 * i;
+          const bool next = i + 1 < uint32_t(nk);
+          const bool go =
+              mbar_test_wait(smem_u32(&p_full[g]), my & 1u) &&
+              mbar_test_wait(smem_u32(&ready[(m + 1) % P::kSlots]), phase(m + 1)) &&
+              (!next || mbar_test_wait(key_bar(m + 2), phase(m + 2)));
+          if (!__all_sync(kAll, go)) return false;
+          fence_after();
+          values(gc, (m + 1) % P::kSlots, i > 0);
+          if (next) scores(gc, (m + 2) % P::kSlots);
+          else commit(smem_u32(&o_done[g]));
+          ++i;
+          ++my;
+          return true;
+        };
+        for (uint32_t idle = 0; i0 < uint32_t(nk) || i1 < uint32_t(nk);) {
+          bool did = tile(G0{}, i0, my0);
+          did |= tile(G1{}, i1, my1);
+          if (did) {
+            idle = 0;
+          } else if ((++idle & 63u) == 0u) {
+            if (idle == 64u) since = globaltimer_ns();
+            if (globaltimer_ns() - since > kWaitLimitNs && lane == 0) {
+              *quit = 1;
+              flag_error(a.err, kErrTimeout);
+            }
+            if (__any_sync(kAll, *quit)) {
+              ok = false;
+              break;
+            }
+          }
+        }
+        if (!ok) break;
+        n += 2 * nk;
       }
+      // nothing of the tensor cores is under way when the CTA ends
+      commit(smem_u32(drained));
+      (void)mbar_wait_bounded(smem_u32(drained), 0);
       __syncwarp();
-    } else {
+    } else if (warp >= kFixWarp) {
       // ===================================== V tiles made safe; FP8 -> bf16
       const int ft = tid - kFixWarp * 32;
       uint32_t n = 0, nt = 0;
@@ -670,34 +772,45 @@ __global__ void __launch_bounds__(kThreads, 1)
               const bool sure = !cut && got == whole;
               bool bad = false;
               constexpr int kC = D / 16;  // 16-byte pieces of a raw row
-#pragma unroll 4
-              for (int i = 0; i < kKeys * kC / kFixers; ++i) {
-                const int u = i * kFixers + ft, r = u / kC, c = u % kC;
-                uint4 x = *reinterpret_cast<const uint4*>(raw + u * 16);
-                if (!sure) {
-                  const int t = t0 + r;
-                  if (t < w.lo || t >= w.hi || !((got >> (r >> br_shift)) & 1u)) {
-                    x = make_uint4(0u, 0u, 0u, 0u);
-                  } else if (part) {
-                    uint32_t* xs[4] = {&x.x, &x.y, &x.z, &x.w};
+constexpr int kIlp = 4;  // pieces in work at once
+#pragma unroll 1
+              for (int i0 = 0; i0 < kKeys * kC; i0 += kIlp * kFixers) {
+                uint4 x4[kIlp];
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
-#pragma unroll
-                      for (int o = 0; o < 32; o += 8)
-                        if (((*xs[e] >> o) & 0x7fu) == 0x7fu) {
-                          *xs[e] &= ~(0xffu << o);
-                          bad = true;
-                        }
-                  }
+                for (int i = 0; i < kIlp; ++i) {
+                  const int u = i0 + i * kFixers + ft;
+                  x4[i] = u < kKeys * kC ? *reinterpret_cast<const uint4*>(raw + u * 16)
+                                         : make_uint4(0u, 0u, 0u, 0u);
                 }
-                const uint4 d0 = make_uint4(e4m3x2_bf16x2(x.x), e4m3x2_bf16x2(x.x >> 16),
-                                            e4m3x2_bf16x2(x.y), e4m3x2_bf16x2(x.y >> 16));
-                const uint4 d1 = make_uint4(e4m3x2_bf16x2(x.z), e4m3x2_bf16x2(x.z >> 16),
-                                            e4m3x2_bf16x2(x.w), e4m3x2_bf16x2(x.w >> 16));
-                uint8_t* dst = tile + (c >> 2) * P::kSpan + r * 128;
-                const int ch = (c & 3) * 2;
-                *reinterpret_cast<uint4*>(dst + ((ch ^ (r & 7)) << 4)) = d0;
-                *reinterpret_cast<uint4*>(dst + (((ch + 1) ^ (r & 7)) << 4)) = d1;
+#pragma unroll
+                for (int i = 0; i < kIlp; ++i) {
+                  const int u = i0 + i * kFixers + ft, r = u / kC, c = u % kC;
+                  if (u >= kKeys * kC) break;
+                  uint4 x = x4[i];
+                  if (!sure) {
+                    const int t = t0 + r;
+                    if (t < w.lo || t >= w.hi || !((got >> (r >> br_shift)) & 1u)) {
+                      x = make_uint4(0u, 0u, 0u, 0u);
+                    } else if (part) {
+                      uint32_t* xs[4] = {&x.x, &x.y, &x.z, &x.w};
+#pragma unroll
+                      for (int e = 0; e < 4; ++e) {
+                        // bytes 0x7f and 0xff, NaN, become 0
+                        const uint32_t nan = __vcmpeq4(*xs[e] & 0x7f7f7f7fu, 0x7f7f7f7fu);
+                        bad |= nan != 0u;
+                        *xs[e] &= ~nan;
+                      }
+                    }
+                  }
+                  const uint4 d0 = make_uint4(e4m3x2_bf16x2(x.x), e4m3x2_bf16x2(x.x >> 16),
+                                              e4m3x2_bf16x2(x.y), e4m3x2_bf16x2(x.y >> 16));
+                  const uint4 d1 = make_uint4(e4m3x2_bf16x2(x.z), e4m3x2_bf16x2(x.z >> 16),
+                                              e4m3x2_bf16x2(x.w), e4m3x2_bf16x2(x.w >> 16));
+                  uint8_t* dst = tile + (c >> 2) * P::kSpan + r * 128;
+                  const int ch = (c & 3) * 2;
+                  *reinterpret_cast<uint4*>(dst + ((ch ^ (r & 7)) << 4)) = d0;
+                  *reinterpret_cast<uint4*>(dst + (((ch + 1) ^ (r & 7)) << 4)) = d1;
+                }
               }
               if (part == 0) {
                 const float* sc = reinterpret_cast<const float*>(raw + kKeys * D);
@@ -770,15 +883,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else {
     // ============================================================== softmax
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(P::kSoftmaxRegs));
     const int g = warp >> 2, r = tid & (kRows - 1);
     const uint32_t lanes = uint32_t((warp & 3) * 32) << 16;
     const uint32_t ts = tmem + lanes + P::kColS + g * 128, to = tmem + lanes + P::kColO + g * 128;
-    const bool plain = !(a.softcap > 0.f) && !a.slopes && a.scale > 0.f;
-    const float inv_cap = a.softcap > 0.f ? 1.f / a.softcap : 0.f;
+    // scores to log2 units: z = s mul without a cap; with one, e^2x is 2^(s cap_mul)
+    const float mul = a.scale * kLog2e;
+    const float cap2 = a.softcap * kLog2e;
+    const float cap_mul = a.softcap > 0.f ? 2.f * mul / a.softcap : 0.f;
     const int rt = r / G, rh = r - rt * G;
     uint32_t nt = 0, my = 0;  // tiles of the CTA; tiles of this row tile
-    uint32_t met = 0;
+    uint32_t met = 0, slot = 0, done = 0;  // meetings; slot uses of the CTA; items of this row tile
     int seq = 0;
     bool ok = true;
     // the row tile's four warps meet (a barrier that can give up)
@@ -794,8 +909,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (nk > 0) ++seq;
       const int tok = g * TT + rt;  // among the item's tokens
       const bool mine = rt < TT && tok < w.new_tokens;
-      if (g == 1 && !has_b(w)) {
+      const int groups = has_b(w) ? 2 : 1;
+      if (g == 1 && groups == 1) {
         nt += nk;
+        slot += 2 * nk;
         continue;
       }
       const int p = w.p0 + tok, h = w.j * G + rh;
@@ -813,87 +930,94 @@ __global__ void __launch_bounds__(kThreads, 1)
         ok = __all_sync(kAll, wait(&s_full[g], my & 1u, quit, a.err));
         if (!ok) break;
         fence_after();
+        if (r == 0) {
+          // these scores are there: their K tile is done with, and the V tile
+          // before; the only row tile of an item arrives for both
+          for (int e = groups; e <= 2; ++e) {
+            mbar_arrive(smem_u32(&empty[slot % P::kSlots]));
+            if (i > 0) mbar_arrive(smem_u32(&empty[(slot - 1) % P::kSlots]));
+            if (i + 1 == nk) mbar_arrive(smem_u32(q_free));
+          }
+        }
+        slot += 2;
         const int t0 = (w.k0 + i) * kKeys;
         const uint32_t got = have[nt & 7u];
-        uint32_t s[4][32];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_ld32(ts + 32 * c, s[c]);
-        wait_ld();
         const bool whole = got == kAll >> (32 - boxes);
         holes |= !whole;
         const bool clear = __all_sync(kAll, t0 >= rlo && t0 + kKeys <= rhi) && whole;
-        float mul = a.scale * kLog2e;  // what turns s into log2 units
         const float* ks = scales + ((nt & 3u) * 2) * kKeys;
-        if constexpr (FP8) {
-#pragma unroll
-          for (int c = 0; c < 4; ++c)
+        // All of the row's scores at once, and its weights at once: a TMEM access
+        // takes hundreds of cycles whatever its size.  (Read twice in pieces of
+        // 32 columns, for the maximum and for the weights: 1177 against 761 us at
+        // 8192 tokens, 64 heads of 64; written in four pieces: 897.)
+        uint32_t s[128];
+        tmem_ld64<0>(ts, s);
+        tmem_ld64<64>(ts + 64, s);
+        wait_ld128(s);
+        // FP8: the key scales
+        auto scaled = [&](uint32_t* x, int c) {
+          {
 #pragma unroll
             for (int e = 0; e < 32; e += 4) {
               const float4 k = *reinterpret_cast<const float4*>(ks + 32 * c + e);
-              const float kk[4] = {k.x, k.y, k.z, k.w};
+              float f[4];
+              un2(mul2(f2(x[e], x[e + 1]), f2(k.x, k.y)), f[0], f[1]);
+              un2(mul2(f2(x[e + 2], x[e + 3]), f2(k.z, k.w)), f[2], f[3]);
 #pragma unroll
-              for (int u = 0; u < 4; u += 2) {
-                float lo, hi;
-                un2(mul2(f2(s[c][e + u], s[c][e + u + 1]), f2(kk[u], kk[u + 1])), lo, hi);
-                s[c][e + u] = __float_as_uint(lo);
-                s[c][e + u + 1] = __float_as_uint(hi);
-              }
+              for (int u = 0; u < 4; ++u) x[e + u] = __float_as_uint(f[u]);
             }
+          }
+        };
+        // to log2 units, the long way: the cap, the bias, a scale <= 0.
+        // cap tanh(x) = cap - 2 cap / (1 + e^2x); e^2x may be infinite, its
+        // reciprocal is then 0.  Off by cap * 2^-22 absolutely, which is what
+        // counts in the exponent.
+        auto capped = [&](float v) {
+          return fmaf(-2.f * cap2, rcp(1.f + ex2(v * cap_mul)), cap2);
+        };
+        auto general = [&](uint32_t* x, int c) {
+          const float base = slope * float(t0 + 32 * c - p);
+#pragma unroll
+          for (int e = 0; e < 32; ++e) {
+            float v = __uint_as_float(x[e]);
+            v = a.softcap > 0.f ? capped(v) : v * mul;
+            x[e] = __float_as_uint(v + fmaf(slope, float(e), base));
+          }
+        };
+        auto masked = [&](uint32_t* x, int c) {
+          // this row's tokens of the columns, one bit each
+          const int a0 = rlo - t0 - 32 * c, a1 = rhi - t0 - 32 * c;
+          uint32_t see = a0 <= 0 ? kAll : a0 >= 32 ? 0u : kAll << a0;
+          see &= a1 <= 0 ? 0u : a1 >= 32 ? kAll : kAll >> (32 - a1);
+          if (!((got >> ((32 * c) >> br_shift)) & 1u)) see &= 0xffff0000u;
+          if (!((got >> ((32 * c + 16) >> br_shift)) & 1u)) see &= 0x0000ffffu;
+#pragma unroll
+          for (int e = 0; e < 32; ++e)
+            if (!((see >> e) & 1u)) x[e] = 0xff800000u;
+        };
+        if constexpr (FP8) {
+#pragma unroll
+          for (int c = 0; c < 4; ++c) scaled(s + 32 * c, c);
         }
-        if (!plain) {
-          if (a.softcap > 0.f) {
-            // cap tanh(x) = cap - 2 cap / (1 + e^2x), x = s scale / cap; e^2x
-            // may be infinite, its reciprocal is then 0.  Off by cap * 2^-22
-            // absolutely, which is what counts in the exponent.
-            const float cl = a.softcap * kLog2e, xm = 2.f * kLog2e * a.scale * inv_cap;
+        if constexpr (GEN) {
 #pragma unroll
-            for (int c = 0; c < 4; ++c)
-#pragma unroll
-              for (int e = 0; e < 32; ++e) {
-                const float x = ex2(__uint_as_float(s[c][e]) * xm);
-                s[c][e] = __float_as_uint(fmaf(-2.f * cl, rcp(1.f + x), cl));
-              }
-          } else {
-#pragma unroll
-            for (int c = 0; c < 4; ++c)
-#pragma unroll
-              for (int e = 0; e < 32; ++e)
-                s[c][e] = __float_as_uint(__uint_as_float(s[c][e]) * mul);
-          }
-          mul = 1.f;
-          if (a.slopes) {
-            const float base = slope * float(t0 - p);
-#pragma unroll
-            for (int c = 0; c < 4; ++c)
-#pragma unroll
-              for (int e = 0; e < 32; ++e)
-                s[c][e] = __float_as_uint(__uint_as_float(s[c][e]) +
-                                          fmaf(slope, float(32 * c + e), base));
-          }
+          for (int c = 0; c < 4; ++c) general(s + 32 * c, c);
         }
-        if (!clear) {
-          // this row's tokens of the tile, one bit each
+        if (__builtin_expect(!clear, 0)) {
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            const int a0 = rlo - t0 - 32 * c, a1 = rhi - t0 - 32 * c;
-            uint32_t see = a0 <= 0 ? kAll : a0 >= 32 ? 0u : kAll << a0;
-            see &= a1 <= 0 ? 0u : a1 >= 32 ? kAll : kAll >> (32 - a1);
-            if (!((got >> ((32 * c) >> br_shift)) & 1u)) see &= 0xffff0000u;
-            if (!((got >> ((32 * c + 16) >> br_shift)) & 1u)) see &= 0x0000ffffu;
-#pragma unroll
-            for (int e = 0; e < 32; ++e)
-              if (!((see >> e) & 1u)) s[c][e] = 0xff800000u;
-          }
+          for (int c = 0; c < 4; ++c) masked(s + 32 * c, c);
         }
         float mx[4];
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-          mx[c] = fmaxf(__uint_as_float(s[c][0]), __uint_as_float(s[c][1]));
+          const uint32_t* x = s + 32 * c;
+          mx[c] = fmaxf(__uint_as_float(x[0]), __uint_as_float(x[1]));
 #pragma unroll
           for (int e = 2; e < 32; e += 2)
-            mx[c] = fmaxf(fmaxf(mx[c], __uint_as_float(s[c][e])), __uint_as_float(s[c][e + 1]));
+            mx[c] = max3(mx[c], __uint_as_float(x[e]), __uint_as_float(x[e + 1]));
         }
-        const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * mul;
+        float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+        if (!GEN) mt *= mul;
         if (i == 0) {
           m = mt;
         } else {
@@ -902,14 +1026,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float f = up ? ex2(m - mt) : 1.f;
             if (up) m = mt;
             l *= f;
-            ok = __all_sync(kAll, wait(&o_done[g], (my - 1) & 1u, quit, a.err));
-            if (!ok) break;
-            fence_after();
+            // (the tile before is in O: its product came before these scores)
 #pragma unroll 1
             for (int c = 0; c < D / 32; ++c) {
               uint32_t o[32];
               tmem_ld32(to + 32 * c, o);
-              wait_ld();
+              wait_ld(o);
 #pragma unroll
               for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
               tmem_st32(to + 32 * c, o);
@@ -917,39 +1039,29 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         const float off = m == -INFINITY ? 0.f : -m;
-        const uint64_t mul_2 = f2(mul, mul), off_2 = f2(off, off);
+        const uint64_t off_2 = f2(off, off);
+        const uint64_t mul_2 = GEN ? f2(1.f, 1.f) : f2(mul, mul);
         uint64_t sum[2] = {0ull, 0ull};
         const float* vsc = ks + kKeys;
+        uint32_t pk[64];
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          uint32_t pk[32];
+        for (int e = 0; e < 128; e += 4) {
+          float z[4];
+          un2(fma2(f2(s[e], s[e + 1]), mul_2, off_2), z[0], z[1]);
+          un2(fma2(f2(s[e + 2], s[e + 3]), mul_2, off_2), z[2], z[3]);
 #pragma unroll
-          for (int e = 0; e < 32; e += 2) {
-            float w[4];
-#pragma unroll
-            for (int u = 0; u < 2; ++u) {
-              const int x = 2 * (e + u) & 31, cc = 2 * c + (e >> 4);
-              float z0, z1;
-              un2(fma2(f2(s[cc][x], s[cc][x + 1]), mul_2, off_2), z0, z1);
-              w[2 * u] = ex2(z0);
-              w[2 * u + 1] = ex2(z1);
-              sum[u] = add2(sum[u], f2(w[2 * u], w[2 * u + 1]));
-            }
-            if constexpr (FP8) {
-              const float4 v = *reinterpret_cast<const float4*>(vsc + 64 * c + 2 * e);
-              un2(mul2(f2(w[0], w[1]), f2(v.x, v.y)), w[0], w[1]);
-              un2(mul2(f2(w[2], w[3]), f2(v.z, v.w)), w[2], w[3]);
-            }
-            pk[e] = bf16x2(w[0], w[1]);
-            pk[e + 1] = bf16x2(w[2], w[3]);
+          for (int u = 0; u < 4; ++u) z[u] = ex2(z[u]);
+          sum[0] = add2(sum[0], f2(z[0], z[1]));
+          sum[1] = add2(sum[1], f2(z[2], z[3]));
+          if constexpr (FP8) {
+            const float4 v = *reinterpret_cast<const float4*>(vsc + e);
+            un2(mul2(f2(z[0], z[1]), f2(v.x, v.y)), z[0], z[1]);
+            un2(mul2(f2(z[2], z[3]), f2(v.z, v.w)), z[2], z[3]);
           }
-          tmem_st32(ts + 32 * c, pk);
-          if (c == 0) {  // the products may begin with the first half
-            wait_st();
-            fence_before();
-            mbar_arrive(smem_u32(&p_half[g]));
-          }
+          pk[e / 2] = bf16x2(z[0], z[1]);
+          pk[e / 2 + 1] = bf16x2(z[2], z[3]);
         }
+        tmem_st64(ts, pk);
         {
           float s0, s1;
           un2(add2(sum[0], sum[1]), s0, s1);
@@ -963,9 +1075,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 
       // ---- the item's end
       if (nk > 0) {
-        ok = __all_sync(kAll, wait(&o_done[g], (my - 1) & 1u, quit, a.err));
+        ok = __all_sync(kAll, wait(&o_done[g], uint32_t(done++) & 1u, quit, a.err));
         if (!ok) break;
         fence_after();
+        if (r == 0)
+          for (int e = groups; e <= 2; ++e) mbar_arrive(smem_u32(&empty[(slot - 1) % P::kSlots]));
       }
       const int64_t row = int64_t(w.tok0 + tok) * heads + h;
       const bool poisoned = nk > 0 && *static_cast<volatile int*>(&dirty[seq & 3]) == seq;
@@ -1024,7 +1138,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           uint32_t o[32];
           if (nk > 0) {
             tmem_ld32(to + 32 * c, o);
-            wait_ld();
+            wait_ld(o);
           } else {
 #pragma unroll
             for (int e = 0; e < 32; ++e) o[e] = 0u;
@@ -1050,7 +1164,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int c = 0; c < D / 32; ++c) {
         uint32_t o[32];
         tmem_ld32(to + 32 * c, o);
-        wait_ld();
+        wait_ld(o);
         float of[32];
 #pragma unroll
         for (int e = 0; e < 32; ++e) of[e] = __uint_as_float(o[e]);
@@ -1123,11 +1237,11 @@ cudaError_t encode(CUtensorMap* map, const void* base, int rank, const cuuint64_
   return cudaSuccess;
 }
 
-template <int D, bool FP8>
+template <int D, bool FP8, bool GEN>
 cudaError_t launch(const DeviceInfo& di, const PagedKv& kv, const PagedAttnArgs& a,
                    cudaStream_t s, bool pdl) {
   using P = Plan<D, FP8>;
-  auto kern = paged_prefill_kernel<D, FP8>;
+  auto kern = paged_prefill_kernel<D, FP8, GEN>;
   const int G = a.heads / kv.kv_heads, TT = kRows / G;
   CUtensorMap mq, mk = {}, mv = {};
   {
@@ -1144,7 +1258,7 @@ cudaError_t launch(const DeviceInfo& di, const PagedKv& kv, const PagedAttnArgs&
     if (cudaError_t e = encode(&mk, kv.k, 2, dims, strides, box)) return e;
     if (cudaError_t e = encode(&mv, kv.v, 2, dims, strides, box)) return e;
   }
-  static const bool fits = has_registers(kern, kLaunchRegs);
+  static const bool fits = has_registers(kern, P::kLaunchRegs);
   if (!fits) return cudaErrorInvalidDeviceFunction;
   if (cudaError_t e = ensure_smem(di, kern, P::kSmem)) return e;
   PrefillArgs d;
@@ -1165,7 +1279,7 @@ cudaError_t launch(const DeviceInfo& di, const PagedKv& kv, const PagedAttnArgs&
   d.err = di.error_word;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(unsigned(di.sms < kCounters ? di.sms : kCounters));
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(P::kThreads);
   cfg.dynamicSmemBytes = P::kSmem;
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
@@ -1189,9 +1303,19 @@ cudaError_t launch_paged_prefill(const PagedKv& kv, int head_dim, bool fp8,
                                  const PagedAttnArgs& a, cudaStream_t s, bool pdl) {
   const DeviceInfo* di = device_info();
   if (!di) return cudaErrorNoDevice;
-  if (head_dim == 64)
-    return fp8 ? launch<64, true>(*di, kv, a, s, pdl) : launch<64, false>(*di, kv, a, s, pdl);
-  return fp8 ? launch<128, true>(*di, kv, a, s, pdl) : launch<128, false>(*di, kv, a, s, pdl);
+  const bool gen = a.softcap > 0.f || a.slopes || !(a.scale > 0.f);
+  if (head_dim == 64) {
+    if (gen)
+      return fp8 ? launch<64, true, true>(*di, kv, a, s, pdl)
+                 : launch<64, false, true>(*di, kv, a, s, pdl);
+    return fp8 ? launch<64, true, false>(*di, kv, a, s, pdl)
+               : launch<64, false, false>(*di, kv, a, s, pdl);
+  }
+  if (gen)
+    return fp8 ? launch<128, true, true>(*di, kv, a, s, pdl)
+               : launch<128, false, true>(*di, kv, a, s, pdl);
+  return fp8 ? launch<128, true, false>(*di, kv, a, s, pdl)
+             : launch<128, false, false>(*di, kv, a, s, pdl);
 }
 
 }  // namespace tt
