@@ -86,8 +86,13 @@ struct Plan {
   static constexpr int kSmem = 1024 + kOffBar + 640;
   static_assert(kSmem <= 227 * 1024, "shared memory");
   static_assert(kOffBar % 8 == 0, "barriers");
-  // TMEM columns: S (and P over it) of A and B, O of A and B
-  static constexpr int kColS = 0, kColO = 256;
+  // TMEM columns of A and B: S, O and P.  With 128 dims P lies over S (all
+  // 512 columns are taken) and the next scores wait for P V; with 64 it has
+  // its own, and they wait only until S is read.
+  static constexpr bool kOwnP = D == 64;
+  __host__ __device__ static constexpr int kColS(int g) { return 128 * g; }
+  __host__ __device__ static constexpr int kColO(int g) { return 256 + D * g; }
+  __host__ __device__ static constexpr int kColP(int g) { return kOwnP ? 384 + 64 * g : kColS(g); }
 };
 
 struct PrefillArgs {
@@ -408,7 +413,8 @@ __global__ void __launch_bounds__(Plan<D, FP8>::kThreads, 1)
   uint64_t* s_full = q_free + 1;         // [2]
   uint64_t* p_full = s_full + 2;         // [2]
   uint64_t* o_done = p_full + 2;         // [2]
-  uint64_t* join = o_done + 2;           // [2]
+  uint64_t* s_read = o_done + 2;         // [2]
+  uint64_t* join = s_read + 2;           // [2]
   uint64_t* drained = join + 2;
   uint32_t* have = reinterpret_cast<uint32_t*>(drained + 1);  // [8] boxes present, per tile
   int* dirty = reinterpret_cast<int*>(have + 8);              // [4] item number + 1
@@ -431,6 +437,7 @@ __global__ void __launch_bounds__(Plan<D, FP8>::kThreads, 1)
       mbar_init(smem_u32(&s_full[g]), 1);
       mbar_init(smem_u32(&p_full[g]), kRows);
       mbar_init(smem_u32(&o_done[g]), 1);
+      mbar_init(smem_u32(&s_read[g]), kRows);
       mbar_init(smem_u32(&join[g]), kRows);
     }
     mbar_init(smem_u32(q_free), 2);
@@ -662,7 +669,7 @@ __global__ void __launch_bounds__(Plan<D, FP8>::kThreads, 1)
 #pragma unroll
         for (int i = 0; i < D / 16; ++i) {
           const uint64_t off = ((i >> 2) * P::kSpan + (i & 3) * 32) >> 4;
-          mma_ss(P::kColS + g * 128, q + off, k + off, idesc(kKeys, false), i > 0);
+          mma_ss(P::kColS(g), q + off, k + off, idesc(kKeys, false), i > 0);
         }
         commit(smem_u32(&s_full[g]));
       };
@@ -671,7 +678,7 @@ __global__ void __launch_bounds__(Plan<D, FP8>::kThreads, 1)
         const uint64_t v = desc_mn(kv0 + slot * P::kTile, P::kHalves > 1 ? P::kSpan : 1024);
 #pragma unroll
         for (int k = 0; k < kKeys / 16; ++k)
-          mma_ts(P::kColO + g * 128, P::kColS + g * 128 + 8 * k, v + k * (2048 >> 4),
+          mma_ts(P::kColO(g), P::kColP(g) + 8 * k, v + k * (2048 >> 4),
                  idesc(D, true), k > 0 ? 1u : more);
       };
       // slot use m has its K tile, its V tile (bf16: an even number of slots,
@@ -700,29 +707,49 @@ __global__ void __launch_bounds__(Plan<D, FP8>::kThreads, 1)
           fence_after();
           scores(G1{}, n % P::kSlots);
         }
-        uint32_t i0 = 0, i1 = b ? 0 : nk;
+        // of each row tile: products P V issued, scores issued
+        uint32_t v0 = 0, v1 = b ? 0 : nk, s0 = 1, s1 = b ? 1 : nk;
         uint64_t since = 0;  // of the idle stretch
-        auto tile = [&](auto gc, uint32_t& i, uint32_t& my) {
+        auto tile = [&](auto gc, uint32_t& vi, uint32_t& si, uint32_t& my) {
           constexpr int g = decltype(gc)::value;
-          if (i >= uint32_t(nk)) return false;
-          const uint32_t m = n + 2 * i;
-          const bool next = i + 1 < uint32_t(nk);
-          const bool go =
-              mbar_test_wait(smem_u32(&p_full[g]), my & 1u) &&
-              mbar_test_wait(smem_u32(&ready[(m + 1) % P::kSlots]), phase(m + 1)) &&
-              (!next || mbar_test_wait(key_bar(m + 2), phase(m + 2)));
-          if (!__all_sync(kAll, go)) return false;
-          fence_after();
-          values(gc, (m + 1) % P::kSlots, i > 0);
-          if (next) scores(gc, (m + 2) % P::kSlots);
-          else commit(smem_u32(&o_done[g]));
-          ++i;
-          ++my;
-          return true;
+          bool did = false;
+          const uint32_t m = n + 2 * vi;
+          if (vi < uint32_t(nk)) {
+            const bool next = vi + 1 < uint32_t(nk);
+            const bool go =
+                mbar_test_wait(smem_u32(&p_full[g]), my & 1u) &&
+                mbar_test_wait(smem_u32(&ready[(m + 1) % P::kSlots]), phase(m + 1)) &&
+                (P::kOwnP || !next || mbar_test_wait(key_bar(m + 2), phase(m + 2)));
+            if (__all_sync(kAll, go)) {
+              fence_after();
+              values(gc, (m + 1) % P::kSlots, vi > 0);
+              if (P::kOwnP || !next) commit(smem_u32(&o_done[g]));
+              if (!P::kOwnP && next) scores(gc, (m + 2) % P::kSlots);
+              ++vi;
+              ++my;
+              did = true;
+            }
+          }
+          if constexpr (P::kOwnP) {
+            // tile si's scores, once those before are read (my - vi tiles
+            // were before this item)
+            if (si < uint32_t(nk)) {
+              const uint32_t ms = n + 2 * si;
+              const bool go = mbar_test_wait(smem_u32(&s_read[g]), (my - vi + si - 1) & 1u) &&
+                              mbar_test_wait(key_bar(ms), phase(ms));
+              if (__all_sync(kAll, go)) {
+                fence_after();
+                scores(gc, ms % P::kSlots);
+                ++si;
+                did = true;
+              }
+            }
+          }
+          return did;
         };
-        for (uint32_t idle = 0; i0 < uint32_t(nk) || i1 < uint32_t(nk);) {
-          bool did = tile(G0{}, i0, my0);
-          did |= tile(G1{}, i1, my1);
+        for (uint32_t idle = 0; v0 < uint32_t(nk) || v1 < uint32_t(nk);) {
+          bool did = tile(G0{}, v0, s0, my0);
+          did |= tile(G1{}, v1, s1, my1);
           if (did) {
             idle = 0;
           } else if ((++idle & 63u) == 0u) {
@@ -886,7 +913,8 @@ constexpr int kIlp = 4;  // pieces in work at once
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(P::kSoftmaxRegs));
     const int g = warp >> 2, r = tid & (kRows - 1);
     const uint32_t lanes = uint32_t((warp & 3) * 32) << 16;
-    const uint32_t ts = tmem + lanes + P::kColS + g * 128, to = tmem + lanes + P::kColO + g * 128;
+    const uint32_t ts = tmem + lanes + P::kColS(g), to = tmem + lanes + P::kColO(g),
+                   tp = tmem + lanes + P::kColP(g);
     // scores to log2 units: z = s mul without a cap; with one, e^2x is 2^(s cap_mul)
     const float mul = a.scale * kLog2e;
     const float cap2 = a.softcap * kLog2e;
@@ -924,22 +952,25 @@ constexpr int kIlp = 4;  // pieces in work at once
         rlo = a.window > 0 && p + 1 > a.window ? p + 1 - a.window : 0;
       }
       const float slope = a.slopes && mine ? __ldcg(a.slopes + h) * kLog2e : 0.f;
+      // one arrival of each row tile; the only row tile of an item arrives for both
+      auto free_slot = [&](uint32_t use) {
+        if (r == 0)
+          for (int e = groups; e <= 2; ++e) mbar_arrive(smem_u32(&empty[use % P::kSlots]));
+      };
       float m = -INFINITY, l = 0.f;
       bool holes = false;  // in any tile
       for (int i = 0; i < nk; ++i, ++nt, ++my) {
         ok = __all_sync(kAll, wait(&s_full[g], my & 1u, quit, a.err));
         if (!ok) break;
         fence_after();
-        if (r == 0) {
-          // these scores are there: their K tile is done with, and the V tile
-          // before; the only row tile of an item arrives for both
-          for (int e = groups; e <= 2; ++e) {
-            mbar_arrive(smem_u32(&empty[slot % P::kSlots]));
-            if (i > 0) mbar_arrive(smem_u32(&empty[(slot - 1) % P::kSlots]));
-            if (i + 1 == nk) mbar_arrive(smem_u32(q_free));
-          }
-        }
+        // these scores are there: their K tile is done with, and where they
+        // waited for it the V tile before
+        free_slot(slot);
+        if (!P::kOwnP && i > 0) free_slot(slot - 1);
+        if (i + 1 == nk && r == 0)
+          for (int e = groups; e <= 2; ++e) mbar_arrive(smem_u32(q_free));
         slot += 2;
+        [[maybe_unused]] bool seen_o = false;
         const int t0 = (w.k0 + i) * kKeys;
         const uint32_t got = have[nt & 7u];
         const bool whole = got == kAll >> (32 - boxes);
@@ -954,6 +985,10 @@ constexpr int kIlp = 4;  // pieces in work at once
         tmem_ld64<0>(ts, s);
         tmem_ld64<64>(ts + 64, s);
         wait_ld128(s);
+        if constexpr (P::kOwnP) {
+          fence_before();
+          mbar_arrive(smem_u32(&s_read[g]));
+        }
         // FP8: the key scales
         auto scaled = [&](uint32_t* x, int c) {
           {
@@ -1026,7 +1061,13 @@ constexpr int kIlp = 4;  // pieces in work at once
             const float f = up ? ex2(m - mt) : 1.f;
             if (up) m = mt;
             l *= f;
-            // (the tile before is in O: its product came before these scores)
+            // the tile before has to be in O (where the scores waited for it, it is)
+            if constexpr (P::kOwnP) {
+              ok = __all_sync(kAll, wait(&o_done[g], (my - 1) & 1u, quit, a.err));
+              if (!ok) break;
+              fence_after();
+              seen_o = true;
+            }
 #pragma unroll 1
             for (int c = 0; c < D / 32; ++c) {
               uint32_t o[32];
@@ -1061,7 +1102,15 @@ constexpr int kIlp = 4;  // pieces in work at once
           pk[e / 2] = bf16x2(z[0], z[1]);
           pk[e / 2 + 1] = bf16x2(z[2], z[3]);
         }
-        tmem_st64(ts, pk);
+        if constexpr (P::kOwnP) {  // the weights before these are read, their V tile done with
+          if (!seen_o) {
+            ok = __all_sync(kAll, i == 0 || wait(&o_done[g], (my - 1) & 1u, quit, a.err));
+            if (!ok) break;
+            fence_after();
+          }
+          if (i > 0) free_slot(slot - 3);
+        }
+        tmem_st64(tp, pk);
         {
           float s0, s1;
           un2(add2(sum[0], sum[1]), s0, s1);
@@ -1075,11 +1124,10 @@ constexpr int kIlp = 4;  // pieces in work at once
 
       // ---- the item's end
       if (nk > 0) {
-        ok = __all_sync(kAll, wait(&o_done[g], uint32_t(done++) & 1u, quit, a.err));
+        ok = __all_sync(kAll, wait(&o_done[g], (P::kOwnP ? my - 1 : done++) & 1u, quit, a.err));
         if (!ok) break;
         fence_after();
-        if (r == 0)
-          for (int e = groups; e <= 2; ++e) mbar_arrive(smem_u32(&empty[(slot - 1) % P::kSlots]));
+        free_slot(slot - 1);
       }
       const int64_t row = int64_t(w.tok0 + tok) * heads + h;
       const bool poisoned = nk > 0 && *static_cast<volatile int*>(&dirty[seq & 3]) == seq;
