@@ -68,8 +68,8 @@ struct Plan {
   static constexpr int kThreads = FP8 ? 512 : 384;
   static constexpr int kFixers = kThreads - 32 * kFixWarp;
   static constexpr int kLaunchRegs = FP8 ? 128 : 168;
-  static constexpr int kSoftmaxRegs = FP8 ? 184 : 208;
-  static constexpr int kOtherRegs = FP8 ? 72 : 88;
+  static constexpr int kSoftmaxRegs = FP8 ? 200 : 208;
+  static constexpr int kOtherRegs = FP8 ? 56 : 88;
   static_assert(256 * kSoftmaxRegs + (kThreads - 256) * kOtherRegs <= kThreads * kLaunchRegs,
                 "register shares");
   static constexpr int kHalves = D / 64;            // 128-byte spans of a bf16 row
@@ -546,7 +546,12 @@ __global__ void __launch_bounds__(Plan<D, FP8>::kThreads, 1)
     w.all_lo = a.window > 0 && plast + 1 > a.window ? plast + 1 - a.window : 0;
     const int ka = w.lo / kKeys, kb = (w.hi + kKeys - 1) / kKeys;
     const int nk = w.hi > w.lo ? kb - ka : 0;
-    w.parts = split < nk ? split : nk > 0 ? nk : 1;
+    // Parts cost the tiles that each still has, and the joining of all of
+    // them by one CTA, about as long a part as a tile: the sum is least
+    // at the root of the tiles.
+    int most = 1;
+    while (most * most < nk) ++most;
+    w.parts = split < most ? split : most;
     w.k0 = w.k1 = ka;
     if (w.part < w.parts) {
       w.k0 = ka + int(int64_t(nk) * w.part / w.parts);
@@ -752,7 +757,7 @@ __global__ void __launch_bounds__(Plan<D, FP8>::kThreads, 1)
           did |= tile(G1{}, v1, s1, my1);
           if (did) {
             idle = 0;
-          } else if ((++idle & 63u) == 0u) {
+          } else if ((__nanosleep(20), (++idle & 63u) == 0u)) {
             if (idle == 64u) since = globaltimer_ns();
             if (globaltimer_ns() - since > kWaitLimitNs && lane == 0) {
               *quit = 1;
@@ -1247,17 +1252,31 @@ constexpr int kIlp = 4;  // pieces in work at once
           float of[32];
 #pragma unroll
           for (int e = 0; e < 32; ++e) of[e] = 0.f;
-          for (int q = 0; q < w.parts; ++q) {
-            const float* pq = part_at(q);
-            const float f = Mraw == -INFINITY ? 0.f : ex2(__ldcg(pq + kRows * D + r) - Mraw);
+          constexpr int kJoin = 3;  // parts whose loads are in flight together
+          for (int q0 = 0; q0 < w.parts; q0 += kJoin) {
+            float4 v[kJoin][8];
+            float f[kJoin];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              const float4 v =
-                  __ldcg(reinterpret_cast<const float4*>(pq + ((8 * c + e) * kRows + r) * 4));
-              of[4 * e] = fmaf(v.x, f, of[4 * e]);
-              of[4 * e + 1] = fmaf(v.y, f, of[4 * e + 1]);
-              of[4 * e + 2] = fmaf(v.z, f, of[4 * e + 2]);
-              of[4 * e + 3] = fmaf(v.w, f, of[4 * e + 3]);
+            for (int u = 0; u < kJoin; ++u) {
+              const bool in = q0 + u < w.parts;
+              const float* pq = part_at(in ? q0 + u : 0);
+              f[u] = in ? __ldcg(pq + kRows * D + r) : -INFINITY;
+#pragma unroll
+              for (int e = 0; e < 8; ++e)
+                v[u][e] = in ? __ldcg(reinterpret_cast<const float4*>(
+                                   pq + ((8 * c + e) * kRows + r) * 4))
+                             : make_float4(0.f, 0.f, 0.f, 0.f);
+            }
+#pragma unroll
+            for (int u = 0; u < kJoin; ++u) {
+              const float x = ex2(f[u] - (Mraw == -INFINITY ? 0.f : Mraw));
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {
+                of[4 * e] = fmaf(v[u][e].x, x, of[4 * e]);
+                of[4 * e + 1] = fmaf(v[u][e].y, x, of[4 * e + 1]);
+                of[4 * e + 2] = fmaf(v[u][e].z, x, of[4 * e + 2]);
+                of[4 * e + 3] = fmaf(v[u][e].w, x, of[4 * e + 3]);
+              }
             }
           }
           if (mine) store(of, c, inv);
