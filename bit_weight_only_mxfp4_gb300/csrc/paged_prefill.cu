@@ -40,7 +40,7 @@
 //
 // Work.  Row tiles x kv heads are dealt to one CTA per SM, the last (longest)
 // first; where there are fewer than half as many as SMs, each is split along
-// its tokens and joined by the last part to finish, from the parts in order.
+// its tokens, and a second kernel joins the parts, in order.
 // What the lengths are is read on the device.
 #include <cmath>
 #include <type_traits>
@@ -55,7 +55,8 @@ namespace {
 constexpr int kRows = 128;   // rows of a row tile
 constexpr int kKeys = 128;   // tokens of a K / V tile
 constexpr int kMmaWarp = 8, kLoadWarp = 9, kFixWarp = 10;
-constexpr int kCounters = 1024;  // as in the decode kernel's part of the workspace
+constexpr int kCounters = 1024;  // the decode kernel's, at the workspace's start: left alone
+constexpr int kJoinBytes = (kCounters + 1) * 16;
 constexpr int kMaxSplit = 32;
 constexpr uint32_t kAll = 0xffffffffu;
 
@@ -82,7 +83,9 @@ struct Plan {
   static constexpr int kOffRaw = kOffKv + kSlots * kTile;
   static constexpr int kOffScale = kOffRaw + kRaws * kRaw;      // [4 tiles][key, value][128]
   static constexpr int kOffLine = kOffScale + (FP8 ? 4 * 2 * kKeys * 4 : 0);
-  static constexpr int kOffBar = kOffLine + (kPagedMaxBatch + 1) * 4 + 12;
+  static constexpr int kOffStart = kOffLine + (kPagedMaxBatch + 4) * 4;
+  static constexpr int kOffLen = kOffStart + (kPagedMaxBatch + 4) * 4;
+  static constexpr int kOffBar = kOffLen + kPagedMaxBatch * 4;
   static constexpr int kSmem = 1024 + kOffBar + 640;
   static_assert(kSmem <= 227 * 1024, "shared memory");
   static_assert(kOffBar % 8 == 0, "barriers");
@@ -106,7 +109,8 @@ struct PrefillArgs {
   const int32_t* prefix;
   uint16_t* out;
   float* lse;
-  int32_t* counters;
+  bool may_split;   // the join kernel follows
+  int4* joins;      // for it: [0].x the pieces, then a record per piece and row tile
   float* parts;
   int32_t* err;
 };
@@ -388,6 +392,22 @@ __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile in
   }
 }
 
+// The end of a row from its maximum (log2 units) and sum: the sink, the
+// logarithm; returns the factor of O.
+__device__ __forceinline__ float close_row(float m, float l, const float* sinks, int h,
+                                           float* lse, int64_t row) {
+  float f = 1.f;
+  if (sinks) {
+    const float z = __ldcg(sinks + h) * kLog2e;
+    const float m2 = fmaxf(m, z);
+    f = m == -INFINITY ? 0.f : ex2(m - m2);
+    l = l * f + ex2(z - m2);
+    m = m2;
+  }
+  if (lse) lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+  return f * (l > 0.f ? 1.f / l : l == 0.f ? 0.f : l);  // a NaN stays one
+}
+
 // GEN: a cap, a bias or a scale that is not positive (the plain kernel's loop
 // stays short without them).
 template <int D, bool FP8, bool GEN>
@@ -403,6 +423,8 @@ __global__ void __launch_bounds__(Plan<D, FP8>::kThreads, 1)
   const uint32_t sbase = smem_u32(smem);
   float* scales = reinterpret_cast<float*>(smem + P::kOffScale);
   int32_t* line = reinterpret_cast<int32_t*>(smem + P::kOffLine);  // q tiles before sequence b
+  int32_t* first = reinterpret_cast<int32_t*>(smem + P::kOffStart);  // its first flat token
+  int32_t* lens = reinterpret_cast<int32_t*>(smem + P::kOffLen);
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + P::kOffBar);
   uint64_t* empty = full + P::kSlots;
   uint64_t* ready = empty + P::kSlots;   // slot made safe, or converted
@@ -414,11 +436,10 @@ __global__ void __launch_bounds__(Plan<D, FP8>::kThreads, 1)
   uint64_t* p_full = s_full + 2;         // [2]
   uint64_t* o_done = p_full + 2;         // [2]
   uint64_t* s_read = o_done + 2;         // [2]
-  uint64_t* join = s_read + 2;           // [2]
-  uint64_t* drained = join + 2;
+  uint64_t* drained = s_read + 2;
   uint32_t* have = reinterpret_cast<uint32_t*>(drained + 1);  // [8] boxes present, per tile
   int* dirty = reinterpret_cast<int*>(have + 8);              // [4] item number + 1
-  int* misc = dirty + 4;  // [0] TMEM address, [1] quit, [2 + g] last to finish, [4 .. 19] scan
+  int* misc = dirty + 4;  // [0] TMEM address, [1] quit, [4 .. 19] scan
   volatile int* quit = misc + 1;
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -438,7 +459,6 @@ __global__ void __launch_bounds__(Plan<D, FP8>::kThreads, 1)
       mbar_init(smem_u32(&p_full[g]), kRows);
       mbar_init(smem_u32(&o_done[g]), 1);
       mbar_init(smem_u32(&s_read[g]), kRows);
-      mbar_init(smem_u32(&join[g]), kRows);
     }
     mbar_init(smem_u32(q_free), 2);
     mbar_init(smem_u32(drained), 1);
@@ -458,10 +478,12 @@ __global__ void __launch_bounds__(Plan<D, FP8>::kThreads, 1)
 
   // ---- the pieces of work: q tiles of every sequence, scanned
   const int64_t tokens = a.tokens;
-  auto start_of = [&](int b) {
+  for (int b = tid; b <= kv.batch; b += kThreads) {
     const int64_t s = __ldcg(a.starts + b);
-    return int(s < 0 ? 0 : s > tokens ? tokens : s);
-  };
+    first[b] = int(s < 0 ? 0 : s > tokens ? tokens : s);
+    if (b < kv.batch) lens[b] = paged_len(kv, b, blockIdx.x == 0 ? a.err : nullptr);
+  }
+  __syncthreads();
   {
     constexpr int kPer = (kPagedMaxBatch + kThreads - 1) / kThreads;
     const int per = (kv.batch + kThreads - 1) / kThreads;
@@ -471,8 +493,7 @@ __global__ void __launch_bounds__(Plan<D, FP8>::kThreads, 1)
       const int b = tid * per + i;
       mine[i] = 0;
       if (i < per && b < kv.batch) {
-        const int n = start_of(b + 1) - start_of(b);
-        if (blockIdx.x == 0) (void)paged_len(kv, b, a.err);
+        const int n = first[b + 1] - first[b];
         mine[i] = n > 0 ? (n + 2 * a.per_tile - 1) / (2 * a.per_tile) : 0;
       }
       sum += mine[i];
@@ -502,9 +523,11 @@ __global__ void __launch_bounds__(Plan<D, FP8>::kThreads, 1)
   const int tiles = line[kv.batch];
   const int64_t pieces = int64_t(tiles) * kv.kv_heads;
   const int sms = gridDim.x;
-  int split = pieces > 0 && pieces * 2 <= sms ? int(sms / pieces) : 1;
+  int split = a.may_split && pieces > 0 && pieces * 2 <= sms ? int(sms / pieces) : 1;
   split = split < kMaxSplit ? split : kMaxSplit;
   const int64_t items = pieces * split;
+  if (a.may_split && blockIdx.x == 0 && tid == 0)
+    a.joins[0] = make_int4(split > 1 ? int(pieces) : 0, split, 0, 0);
   const int G = a.group, heads = G * kv.kv_heads, TT = a.per_tile;
 
   // The CTA's turns: the items, longest first, are dealt to the CTAs to and
@@ -526,11 +549,11 @@ __global__ void __launch_bounds__(Plan<D, FP8>::kThreads, 1)
       if (line[mid] <= u) lo = mid; else hi = mid;
     }
     w.b = lo;
-    const int s0 = start_of(lo), s1 = start_of(lo + 1);
+    const int s0 = first[lo], s1 = first[lo + 1];
     const int q0 = (u - line[lo]) * 2 * TT;
     w.tok0 = s0 + q0;
     w.new_tokens = s1 - w.tok0;
-    w.len = paged_len(kv, lo, nullptr);
+    w.len = lens[lo];
     w.p0 = w.len - w.new_tokens;
     w.pre = a.prefix ? __ldcg(a.prefix + lo) : 0;
     const int rows = w.new_tokens < 2 * TT ? w.new_tokens : 2 * TT;
@@ -546,11 +569,8 @@ __global__ void __launch_bounds__(Plan<D, FP8>::kThreads, 1)
     w.all_lo = a.window > 0 && plast + 1 > a.window ? plast + 1 - a.window : 0;
     const int ka = w.lo / kKeys, kb = (w.hi + kKeys - 1) / kKeys;
     const int nk = w.hi > w.lo ? kb - ka : 0;
-    // Parts cost the tiles that each still has, and the joining of all of
-    // them by one CTA, about as long a part as a tile: the sum is least
-    // at the root of the tiles.
-    int most = 1;
-    while (most * most < nk) ++most;
+    // two tiles a part at least (a part's start costs about as much)
+    const int most = nk > 3 ? nk / 2 : 1;
     w.parts = split < most ? split : most;
     w.k0 = w.k1 = ka;
     if (w.part < w.parts) {
@@ -926,14 +946,9 @@ constexpr int kIlp = 4;  // pieces in work at once
     const float cap_mul = a.softcap > 0.f ? 2.f * mul / a.softcap : 0.f;
     const int rt = r / G, rh = r - rt * G;
     uint32_t nt = 0, my = 0;  // tiles of the CTA; tiles of this row tile
-    uint32_t met = 0, slot = 0, done = 0;  // meetings; slot uses of the CTA; items of this row tile
+    uint32_t slot = 0, done = 0;  // slot uses of the CTA; items of this row tile
     int seq = 0;
     bool ok = true;
-    // the row tile's four warps meet (a barrier that can give up)
-    auto meet = [&] {
-      mbar_arrive(smem_u32(&join[g]));
-      return __all_sync(kAll, wait(&join[g], met++ & 1u, quit, a.err)) != 0;
-    };
     for (int64_t turn = 0, idx; ok && (idx = turn_of(turn)) >= 0; ++turn) {
       if (idx >= items) continue;
       const Item w = item_of(idx);
@@ -943,6 +958,8 @@ constexpr int kIlp = 4;  // pieces in work at once
       const int tok = g * TT + rt;  // among the item's tokens
       const bool mine = rt < TT && tok < w.new_tokens;
       const int groups = has_b(w) ? 2 : 1;
+      if (split > 1 && w.part == 0 && r == 0 && (w.parts == 1 || (g == 1 && groups == 1)))
+        a.joins[1 + 2 * w.base + g] = make_int4(0, 0, 0, 0);
       if (g == 1 && groups == 1) {
         nt += nk;
         slot += 2 * nk;
@@ -1170,22 +1187,9 @@ constexpr int kIlp = 4;  // pieces in work at once
                               bf16x2(o[8 * e + 4] * inv, o[8 * e + 5] * inv),
                               bf16x2(o[8 * e + 6] * inv, o[8 * e + 7] * inv));
       };
-      auto close = [&](float& mm, float& ll) {  // the sink; returns the factor of O
-        float f = 1.f;
-        if (a.sinks) {
-          const float z = __ldcg(a.sinks + h) * kLog2e;
-          const float m2 = fmaxf(mm, z);
-          f = mm == -INFINITY ? 0.f : ex2(mm - m2);
-          ll = ll * f + ex2(z - m2);
-          mm = m2;
-        }
-        if (a.lse)
-          a.lse[row] = ll == 0.f ? -INFINITY : (mm + log2f(ll)) * 0.6931471805599453f;
-        return f * (ll > 0.f ? 1.f / ll : ll == 0.f ? 0.f : ll);
-      };
       if (w.parts == 1) {
         float inv = 0.f;
-        if (mine) inv = close(m, l);
+        if (mine) inv = close_row(m, l, a.sinks, h, a.lse, row);
 #pragma unroll 1
         for (int c = 0; c < D / 32; ++c) {
           uint32_t o[32];
@@ -1229,59 +1233,12 @@ constexpr int kIlp = 4;  // pieces in work at once
       }
       mypart[kRows * D + r] = m;
       mypart[kRows * (D + 1) + r] = l;
-      fence_before();
-      __threadfence();
-      if (!(ok = meet())) break;
-      if (r == 0)
-        misc[2 + g] = atomicAdd(a.counters + 2 * w.base + g, 1) == w.parts - 1;
-      if (!(ok = meet())) break;
-      if (misc[2 + g]) {
-        __threadfence();
-        if (r == 0) a.counters[2 * w.base + g] = 0;  // ready for the next call
-        float M = -INFINITY, L = 0.f;
-        for (int q = 0; q < w.parts; ++q) M = fmaxf(M, __ldcg(part_at(q) + kRows * D + r));
-        for (int q = 0; q < w.parts; ++q)
-          L += M == -INFINITY ? 0.f
-                              : ex2(__ldcg(part_at(q) + kRows * D + r) - M) *
-                                    __ldcg(part_at(q) + kRows * (D + 1) + r);
-        const float Mraw = M;
-        float inv = 0.f;
-        if (mine) inv = close(M, L);
-#pragma unroll 1
-        for (int c = 0; c < D / 32; ++c) {
-          float of[32];
-#pragma unroll
-          for (int e = 0; e < 32; ++e) of[e] = 0.f;
-          constexpr int kJoin = 3;  // parts whose loads are in flight together
-          for (int q0 = 0; q0 < w.parts; q0 += kJoin) {
-            float4 v[kJoin][8];
-            float f[kJoin];
-#pragma unroll
-            for (int u = 0; u < kJoin; ++u) {
-              const bool in = q0 + u < w.parts;
-              const float* pq = part_at(in ? q0 + u : 0);
-              f[u] = in ? __ldcg(pq + kRows * D + r) : -INFINITY;
-#pragma unroll
-              for (int e = 0; e < 8; ++e)
-                v[u][e] = in ? __ldcg(reinterpret_cast<const float4*>(
-                                   pq + ((8 * c + e) * kRows + r) * 4))
-                             : make_float4(0.f, 0.f, 0.f, 0.f);
-            }
-#pragma unroll
-            for (int u = 0; u < kJoin; ++u) {
-              const float x = ex2(f[u] - (Mraw == -INFINITY ? 0.f : Mraw));
-#pragma unroll
-              for (int e = 0; e < 8; ++e) {
-                of[4 * e] = fmaf(v[u][e].x, x, of[4 * e]);
-                of[4 * e + 1] = fmaf(v[u][e].y, x, of[4 * e + 1]);
-                of[4 * e + 2] = fmaf(v[u][e].z, x, of[4 * e + 2]);
-                of[4 * e + 3] = fmaf(v[u][e].w, x, of[4 * e + 3]);
-              }
-            }
-          }
-          if (mine) store(of, c, inv);
-        }
+      if (w.part == 0 && r == 0) {
+        const int left = w.new_tokens - g * TT;
+        a.joins[1 + 2 * w.base + g] =
+            make_int4(w.parts, w.tok0 + g * TT, left < TT ? left : TT, w.j);
       }
+      fence_before();
     }
   }
   // ---- every role is done (or has given up): free the tensor memory
@@ -1290,6 +1247,72 @@ constexpr int kIlp = 4;  // pieces in work at once
   if (warp == kMmaWarp)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512)
                  : "memory");
+}
+
+// Joins the parts of split pieces, launched behind the kernel above: a block
+// takes eight dims of a row tile at a time, a thread a row, with kJoin parts'
+// loads in flight.  (Joined by the last CTA of a piece, 12 parts of a piece
+// took 27 us: 1.6 MB through one SM.)
+constexpr int kJoinThreads = kRows;
+template <int D>
+__global__ void __launch_bounds__(kJoinThreads)
+    paged_prefill_join_kernel(const PrefillArgs a, int heads) {
+  constexpr int kJoin = 8;
+  constexpr int kPartFloats = kRows * (D + 2);
+  const int r = threadIdx.x;
+  pdl_allow_next_grid();
+  pdl_wait_prior_grid();
+  const int4 head = __ldcg(a.joins);
+  const int units = head.x * 2 * (D / 8), split = head.y;
+  const int rt = r / a.group, rh = r - rt * a.group;
+  for (int u = blockIdx.x; u < units; u += gridDim.x) {
+    const int tile = u / (D / 8), c = u % (D / 8);  // piece and row tile; dims 8c ..
+    const int4 rec = __ldcg(a.joins + 1 + tile);    // parts, first token, tokens, kv head
+    if (rt >= rec.z) continue;                      // (no parts: no tokens)
+    const float* part = a.parts + (int64_t(tile >> 1) * split * 2 + (tile & 1)) * kPartFloats;
+    float o[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    float m = -INFINITY, l = 0.f;
+    for (int q0 = 0; q0 < rec.x; q0 += kJoin) {
+      float4 v[kJoin][2];
+      float pm[kJoin], pl[kJoin], mx = m;
+#pragma unroll
+      for (int e = 0; e < kJoin; ++e) {
+        const bool in = q0 + e < rec.x;
+        const float* p = part + int64_t(in ? q0 + e : 0) * 2 * kPartFloats;
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          v[e][i] = in ? __ldcg(reinterpret_cast<const float4*>(p + ((2 * c + i) * kRows + r) * 4))
+                       : make_float4(0.f, 0.f, 0.f, 0.f);
+        pm[e] = in ? __ldcg(p + kRows * D + r) : -INFINITY;
+        pl[e] = in ? __ldcg(p + kRows * (D + 1) + r) : 0.f;
+      }
+#pragma unroll
+      for (int e = 0; e < kJoin; ++e) mx = fmaxf(mx, pm[e]);
+      const float ms = mx == -INFINITY ? 0.f : mx, old = ex2(m - ms);
+      m = mx;
+      l *= old;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) o[i] *= old;
+#pragma unroll
+      for (int e = 0; e < kJoin; ++e) {
+        const float f = ex2(pm[e] - ms);
+        l = fmaf(pl[e], f, l);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          o[4 * i] = fmaf(v[e][i].x, f, o[4 * i]);
+          o[4 * i + 1] = fmaf(v[e][i].y, f, o[4 * i + 1]);
+          o[4 * i + 2] = fmaf(v[e][i].z, f, o[4 * i + 2]);
+          o[4 * i + 3] = fmaf(v[e][i].w, f, o[4 * i + 3]);
+        }
+      }
+    }
+    const int h = rec.w * a.group + rh;
+    const int64_t row = int64_t(rec.y + rt) * heads + h;
+    const float inv = close_row(m, l, a.sinks, h, c == 0 ? a.lse : nullptr, row);
+    *reinterpret_cast<uint4*>(a.out + row * D + 8 * c) =
+        make_uint4(bf16x2(o[0] * inv, o[1] * inv), bf16x2(o[2] * inv, o[3] * inv),
+                   bf16x2(o[4] * inv, o[5] * inv), bf16x2(o[6] * inv, o[7] * inv));
+  }
 }
 
 cudaError_t encode(CUtensorMap* map, const void* base, int rank, const cuuint64_t* dims,
@@ -1341,8 +1364,12 @@ cudaError_t launch(const DeviceInfo& di, const PagedKv& kv, const PagedAttnArgs&
   d.prefix = a.prefix;
   d.out = a.out;
   d.lse = a.lse;
-  d.counters = static_cast<int32_t*>(a.ws);
-  d.parts = reinterpret_cast<float*>(static_cast<uint8_t*>(a.ws) + kCounters * 4);
+  // Split where there may be fewer than half as many pieces as SMs (tokens
+  // that no sequence has only make this too careful).
+  const int64_t pieces = (a.tokens + 2 * TT - 1) / (2 * TT) * kv.kv_heads;
+  d.may_split = pieces * 2 <= di.sms;
+  d.joins = reinterpret_cast<int4*>(static_cast<uint8_t*>(a.ws) + kCounters * 4);
+  d.parts = reinterpret_cast<float*>(static_cast<uint8_t*>(a.ws) + kCounters * 4 + kJoinBytes);
   d.err = di.error_word;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(unsigned(di.sms < kCounters ? di.sms : kCounters));
@@ -1354,16 +1381,23 @@ cudaError_t launch(const DeviceInfo& di, const PagedKv& kv, const PagedAttnArgs&
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = pdl ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, kern, mq, mk, mv, kv, d);
+  if (cudaError_t e = cudaLaunchKernelEx(&cfg, kern, mq, mk, mv, kv, d)) return e;
+  if (!d.may_split) return cudaSuccess;
+  cfg.gridDim = dim3(unsigned(di.sms * 4));
+  cfg.blockDim = dim3(kJoinThreads);
+  cfg.dynamicSmemBytes = 0;
+  cfg.numAttrs = 1;  // the join always follows programmatically
+  return cudaLaunchKernelEx(&cfg, paged_prefill_join_kernel<D>, d, a.heads);
 }
 
 }  // namespace
 
 size_t paged_prefill_workspace_bytes(int head_dim) {
-  // counters, and one part of two row tiles per CTA
+  // (the decode kernel's counters,) the records of the join, and one part of
+  // two row tiles per CTA
   const DeviceInfo* di = device_info();
   const int64_t ctas = di && di->sms < kCounters ? di->sms : kCounters;
-  return size_t(kCounters) * 4 + size_t(ctas) * 2 * kRows * (head_dim + 2) * 4;
+  return size_t(kCounters) * 4 + kJoinBytes + size_t(ctas) * 2 * kRows * (head_dim + 2) * 4;
 }
 
 cudaError_t launch_paged_prefill(const PagedKv& kv, int head_dim, bool fp8,
