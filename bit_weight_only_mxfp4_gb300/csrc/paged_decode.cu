@@ -51,7 +51,8 @@ namespace {
 
 constexpr uint32_t kFull = 0xffffffffu;
 constexpr int kGroupWarps = 4;
-constexpr int kCopiers = 128;
+constexpr int kCopyWarps = 4;
+constexpr int kCopiers = 32 * kCopyWarps;
 constexpr int kMaxCtas = 1024;                // counters in the workspace
 constexpr int kSmemMax = 227 * 1024;
 constexpr int kConsumerBar = 1;
@@ -89,15 +90,16 @@ struct Plan {
   __device__ static constexpr int swizzle(int r) { return kRow == 64 ? (r >> 1) & 3 : r & 7; }
   static constexpr int kFixed =
       1024 + kScratch + (2 * kPagedMaxBatch + 2) * 4 + 512;  // alignment, parts, line, barriers
-  // A multiple of the groups, so that a stage is always the same group's: a
-  // group then waits for every phase of its stages' barriers in turn.  (With
-  // a stage that changes hands, a group that is ahead can find the phase
-  // before last and take it for its own.)
-  static constexpr int kRaw = (kSmemMax - kFixed) / kStage / kGroups * kGroups;
+  // A multiple of the groups and of the copying warps, so that a stage is
+  // always the same group's and the same warp's: they then wait for every
+  // phase of its barriers in turn.  (With a stage that changes hands, one that
+  // is ahead can find the phase before last and take it for its own.)
+  static constexpr int kUnit = kGroups > kCopyWarps ? kGroups : kCopyWarps;
+  static constexpr int kRaw = (kSmemMax - kFixed) / kStage / kUnit * kUnit;
   static constexpr int kStages = kRaw > 12 ? 12 : kRaw;
   static constexpr int kSmem = kFixed + kStages * kStage;
   static_assert(kScratch / kSets >= (kConsumers > kUnits ? kConsumers : 0) * 24, "join");
-  static_assert(kStages >= 4 && kStages % kGroups == 0, "ring");
+  static_assert(kStages >= 4 && kStages % kGroups == 0 && kStages % kCopyWarps == 0, "ring");
 };
 
 // Floats of one CTA part: a slot as above.
@@ -255,7 +257,7 @@ __global__ void __launch_bounds__(Plan<D, NH, FP8>::kThreads, 1)
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if (tid == 0) {
     for (int i = 0; i < P::kStages; ++i) {
-      mbar_init(smem_u32(&full[i]), kCopiers + 1);
+      mbar_init(smem_u32(&full[i]), 32 + 1);  // a copying warp's lanes and its word
       mbar_init(smem_u32(&empty[i]), kGroupWarps);
     }
     flags[1] = 0;
@@ -327,7 +329,7 @@ __global__ void __launch_bounds__(Plan<D, NH, FP8>::kThreads, 1)
     // tiles, one batch ahead of the copies: no table entry is waited for in
     // the loop.  Each warp has the same batch.
     constexpr int kBatch = 32 / kGran;
-    const int pw = warp - kGroups * kGroupWarps, pt = tid - kConsumers;
+    const int pw = warp - kGroups * kGroupWarps;
     int row;  // the granule's first row in the pool, or -1
     int query;  // the tile is its group's first of a pair: the pair's first query row, or -1
     auto look = [&](int base) {
@@ -355,6 +357,7 @@ __global__ void __launch_bounds__(Plan<D, NH, FP8>::kThreads, 1)
       const uint32_t got = __ballot_sync(kFull, my_row >= 0);
       for (int x = 0; x < kBatch && base + x < i1; ++x) {
         const int idx = base + x - i0, st = idx % P::kStages;
+        if (idx % kCopyWarps != pw) continue;
         bool ok = true;
         if (idx >= P::kStages)
           ok = mbar_wait_bounded(smem_u32(&empty[st]), uint32_t((idx / P::kStages - 1) & 1));
@@ -369,17 +372,19 @@ __global__ void __launch_bounds__(Plan<D, NH, FP8>::kThreads, 1)
         const uint32_t have = (got >> (x * kGran)) & (kFull >> (32 - kGran));
         const uint32_t stage = smem_u32(ring + st * P::kStage);
 #pragma unroll
-        for (int u0 = 0; u0 < 2 * kGran / 4; ++u0) {
-          const int u = u0 * 4 + pw, gr = u >> 1;  // granule; even u: K, odd: V
+        for (int gr = 0; gr < kGran; ++gr) {
           const int r = __shfl_sync(kFull, my_row, x * kGran + gr);
           if (r >= 0) {
-            const uint8_t* src = static_cast<const uint8_t*>(u & 1 ? kv.v : kv.k) +
-                                 int64_t(r) * P::kRow + lane * 16;
-            const uint32_t dst = stage + (u & 1 ? P::kPart : 0) + gr * 16 * P::kRow;
+            const int64_t from = int64_t(r) * P::kRow + lane * 16;
 #pragma unroll
-            for (int i = 0; i < P::kRow / 32; ++i) {
-              const int q = lr + i * (512 / P::kRow);
-              copy16(dst + q * P::kRow + ((lc ^ P::swizzle(q)) << 4), src + i * 512);
+            for (int w = 0; w < 2; ++w) {  // K, V
+              const uint8_t* src = static_cast<const uint8_t*>(w ? kv.v : kv.k) + from;
+              const uint32_t dst = stage + w * P::kPart + gr * 16 * P::kRow;
+#pragma unroll
+              for (int i = 0; i < P::kRow / 32; ++i) {
+                const int q = lr + i * (512 / P::kRow);
+                copy16(dst + q * P::kRow + ((lc ^ P::swizzle(q)) << 4), src + i * 512);
+              }
             }
           }
         }
@@ -387,19 +392,21 @@ __global__ void __launch_bounds__(Plan<D, NH, FP8>::kThreads, 1)
         if (bj >= 0) {
           const int b = bj / kv.kv_heads, j = bj - b * kv.kv_heads;
           const uint16_t* src = a.q + int64_t(b) * a.q_stride + int64_t(j) * G * D;
-          for (int i = pt; i < G * D / 8; i += kCopiers)
+          for (int i = lane; i < G * D / 8; i += 32)
             copy16(stage + P::kOffQ + i * 16, src + i * 8);
         }
         if constexpr (FP8) {
-          const int gr = (pt >> 3) % kGran;
-          const int r = __shfl_sync(kFull, my_row, x * kGran + gr);
-          if (pt < 8 * kGran && r >= 0) {
-            const int w = (pt >> 2) & 1, q = pt & 3;
-            copy16(stage + P::kOffScale + (w * kTok + gr * 16 + q * 4) * 4,
-                   (w ? kv.v_scales : kv.k_scales) + int64_t(r) + q * 4);
+          constexpr int kPieces = 8 * kGran;  // 16 bytes: 4 of K, 4 of V a granule
+#pragma unroll
+          for (int u = 0; u < kPieces / 32; ++u) {
+            const int e = u * 32 + lane, gr = e >> 3, w = (e >> 2) & 1, q = e & 3;
+            const int r = __shfl_sync(kFull, my_row, x * kGran + gr);
+            if (r >= 0)
+              copy16(stage + P::kOffScale + (w * kTok + gr * 16 + q * 4) * 4,
+                     (w ? kv.v_scales : kv.k_scales) + int64_t(r) + q * 4);
           }
         }
-        if (pt == 0) {
+        if (lane == 0) {
           mask[st] = have;
           mbar_arrive(smem_u32(&full[st]));
         }
