@@ -15,7 +15,7 @@
 // sincospi, rounded to 2^-24 of the half turn.
 //
 // Bound by bytes for a prompt (every row read and written once) and by
-// latency for a decode step.  A CTA takes one or four tokens: its threads look
+// latency for a decode step.  A CTA takes one or two tokens: its threads look
 // up the tokens' places and compute each sine and cosine once, into shared
 // memory, and after one barrier each group of head_dim/16 lanes rotates one
 // row at a time, a lane both elements of its eight pairs (two 16-byte pieces),
@@ -26,7 +26,7 @@
 namespace tt {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 constexpr uint32_t kAll = 0xffffffffu;
 constexpr int64_t kNowhere = INT64_MIN;  // the place of a token that no sequence has
 
@@ -134,14 +134,25 @@ __global__ void __launch_bounds__(kThreads)
     const int my = tid / kShare;  // a warp has one token
     const int64_t t = t0 + my;
     if (my < ntok) {
-      const int b = a.starts ? paged_seq_of(a.starts, kv.batch, t, lane) : int(t);
       const bool says = tid % kShare == 0;
       int32_t* e = says ? a.err : nullptr;
-      const int len = paged_len(kv, b, e);
-      int64_t place = int64_t(len) - 1;
-      if (a.starts) {
-        const int64_t s0 = __ldcg(a.starts + b), s1 = __ldcg(a.starts + b + 1);
+      int b = int(t);
+      int64_t place;
+      if (a.starts && kv.batch < 32) {
+        // all starts and lengths in one round trip
+        const int s = lane <= kv.batch ? __ldcg(a.starts + lane) : INT32_MAX;
+        const int n = lane < kv.batch ? paged_len(kv, lane, a.err) : 0;
+        b = __popc(__ballot_sync(kAll, lane > 0 && lane < kv.batch && s <= t));
+        const int s0 = __shfl_sync(kAll, s, b), s1 = __shfl_sync(kAll, s, b + 1);
+        const int len = __shfl_sync(kAll, n, b);
         place = t >= s0 && t < s1 ? len - (s1 - t) : kNowhere;
+      } else if (a.starts) {
+        b = paged_seq_of(a.starts, kv.batch, t, lane);
+        const int64_t s0 = __ldcg(a.starts + b), s1 = __ldcg(a.starts + b + 1);
+        const int n = paged_len(kv, b, e);
+        place = t >= s0 && t < s1 ? n - (s1 - t) : kNowhere;
+      } else {
+        place = int64_t(paged_len(kv, b, e)) - 1;
       }
       if (says) {
         s_place[my] = place;
@@ -248,11 +259,13 @@ cudaError_t launch(const DeviceInfo& di, const PagedKv& kv, const AppendArgs& a,
   const int per = kThreads / (D / 16);
   const int rounds = (a.heads + 2 * kv.kv_heads + per - 1) / per;
   // Few tokens (a decode step): a CTA per token and round of rows, so that no
-  // row waits for another.  From eight tokens per SM on, four tokens a CTA:
-  // a barrier and the angles serve four times the rows.
+  // row waits for another.  From eight tokens per SM on, two tokens a CTA, which
+  // goes through all of their rows: 128 threads and 2 tokens took 23.6 / 44.7 us
+  // on the bf16 / FP8 prompts of 6484 / 8191 tokens, 256 and 4 24.6 / 48.1, 512
+  // and 8 25.9 / 49.2.
   const bool many = tokens >= 8 * di.sms;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = many ? dim3(unsigned((tokens + 3) / 4)) : dim3(unsigned(tokens), unsigned(rounds));
+  cfg.gridDim = many ? dim3(unsigned((tokens + 1) / 2)) : dim3(unsigned(tokens), unsigned(rounds));
   cfg.blockDim = dim3(kThreads);
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
@@ -260,7 +273,7 @@ cudaError_t launch(const DeviceInfo& di, const PagedKv& kv, const AppendArgs& a,
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = pdl ? 1 : 0;
-  return many ? cudaLaunchKernelEx(&cfg, paged_append_kernel<D, FP8, 4>, kv, a, tokens)
+  return many ? cudaLaunchKernelEx(&cfg, paged_append_kernel<D, FP8, 2>, kv, a, tokens)
               : cudaLaunchKernelEx(&cfg, paged_append_kernel<D, FP8, 1>, kv, a, tokens);
 }
 
