@@ -583,3 +583,98 @@ def test_prompt_then_decode_agree():
         want = ref.attention(c, q[-1:], None, 0.125)
         ref.check_attention(a[0][-1:], a[1][-1:], want, PREFILL_EPS, "prompt")
         ref.check_attention(*b, want, DECODE_EPS[fp8], "decode")
+
+
+# ------------------------------------------------------------------------------------------- larger and stranger cases
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("heads,kvh,d,batch,rot,interleaved", [(5, 1, 128, 3, 128, False), (16, 4, 64, 40, 32, True),
+                                                              (8, 8, 128, 31, 64, False), (12, 1, 64, 33, 64, False)])
+def test_append_many_tokens(heads, kvh, d, batch, rot, interleaved, fp8):
+    """From eight tokens per SM on a CTA takes several tokens; an odd number of them, few and many sequences."""
+    r = synth.rng(WID, batch, 6)
+    new = r.integers(0, 2 * 1300 // batch, batch)
+    new[0] += max(0, 1301 - int(new.sum()))
+    if int(new.sum()) % 2 == 0:
+        new[0] += 1
+    _append_case(92 + batch, heads, kvh, d, 32, fp8, [int(n + r.integers(0, 40)) for n in new], [int(n) for n in new],
+                 rot, interleaved)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("heads,kvh,d,batch,most", [(40, 10, 128, 64, 40), (8, 8, 64, 50, 300), (64, 8, 64, 90, 30)])
+def test_prefill_more_pieces_than_sms(heads, kvh, d, batch, most, fp8):
+    """Several pieces a CTA, with one and with two row tiles."""
+    r = synth.rng(WID, batch, 7)
+    new = [int(n) for n in r.integers(0, most, batch)]
+    _prefill_case(batch, heads, kvh, d, 16, fp8, new, [int(n) for n in r.integers(0, 60, batch)])
+
+
+@pytest.mark.parametrize("parts", [True, False])
+@pytest.mark.parametrize("bad", [0x7FC0, 0x7F80, 0xFF80], ids=["nan", "inf", "-inf"])
+def test_prefill_values_not_finite_reach_only_rows_that_see_them(bad, parts):
+    """A value that is not finite makes its dimension so in the rows that see its token, and in no other: causal rows
+    before it, rows whose window has left it behind, and every row of another kv head."""
+    heads, kvh, d, n = (16, 4, 128, 300) if parts else (64, 16, 64, 1100)
+    window, at, dim = 200, (70, 133, 260), 17
+    c = ref.Cache(95, [n], kvh, d, 32, False, junk=False)
+    for t in at:
+        c.v[c.table[0, t // 32], 1, t % 32, dim] = bad
+    starts = np.array([0, n], np.int32)
+    q = synth.normal_bf16(synth.rng(WID, 95, 2), (n, heads, d), 1.0)
+    got = bf16_to_f64(_attend(_handle(c), q, starts, 0.125, window=window)[0]).reshape(n, heads, d)
+    clean = ref.Cache(95, [n], kvh, d, 32, False, junk=False)
+    want = bf16_to_f64(_attend(_handle(clean), q, starts, 0.125, window=window)[0]).reshape(n, heads, d)
+    p = np.arange(n)
+    sees = np.zeros(n, bool)
+    for t in at:
+        sees |= (p >= t) & (p < t + window)
+    hit = np.zeros((n, heads, d), bool)
+    group = heads // kvh
+    hit[sees, group:2 * group, dim] = True
+    assert np.array_equal(~np.isfinite(got), hit)
+    if bad != 0x7FC0:
+        assert (got[hit] == bf16_to_f64(np.uint16(bad))).all()
+    assert np.array_equal(got[~hit], want[~hit])
+
+
+@pytest.mark.parametrize("what", ["code", "scale"])
+def test_prefill_fp8_values_not_finite(what):
+    """The same for an E4M3 NaN code, and for a row whose scale is NaN (what the append writes for a row that is not
+    finite): the whole row of values."""
+    n, t = 300, 140
+    c, clean = (ref.Cache(96, [n], 4, 128, 32, True, junk=False) for _ in range(2))
+    at = (c.table[0, t // 32], 2, t % 32)
+    if what == "code":
+        c.v[at][5] = 0x7F
+    else:
+        c.v_scales[at] = np.nan
+    starts = np.array([0, n], np.int32)
+    q = synth.normal_bf16(synth.rng(WID, 96, 2), (n, 16, 128), 1.0)
+    got, want = (bf16_to_f64(_attend(_handle(x), q, starts, 0.125)[0]).reshape(n, 16, 128) for x in (c, clean))
+    hit = np.zeros((n, 16, 128), bool)
+    hit[t:, 8:12, 5 if what == "code" else slice(None)] = True
+    assert np.array_equal(~np.isfinite(got), hit)
+    # the scale stands beside all weights of the rows' products, so those rows are the only ones that may differ
+    assert np.array_equal(got[~hit], want[~hit])
+
+
+def test_decode_values_not_finite_in_sight():
+    c = ref.Cache(97, [100, 60], 8, 64, 16, False, junk=False)
+    c.v[c.table[0, 2], 3, 5, 9] = 0x7F80
+    q = synth.normal_bf16(synth.rng(WID, 97, 1), (2, 64, 64), 1.0)
+    got = bf16_to_f64(_attend(_handle(c), q, None, 0.125)[0]).reshape(2, 64, 64)
+    hit = np.zeros((2, 64, 64), bool)
+    hit[0, 24:32, 9] = True
+    assert np.array_equal(~np.isfinite(got), hit)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_example_layer(fp8):
+    """A prompt and steps of a layer, decoded in a graph, against one prompt over all tokens.  Between the two lie the
+    weights' rounding to bf16 in the prompt kernel (2^-8) and, after it, three bf16 roundings of the rows (2^-8 each)
+    that a different last bit can turn the other way, once for each of the two."""
+    from examples import paged_layer
+    one, whole = paged_layer.serve(fp8, steps=9)
+    one, whole = one.double().cpu().numpy(), whole.double().cpu().numpy()
+    far = np.linalg.norm(one - whole, axis=-1) / np.linalg.norm(whole, axis=-1)
+    assert far.max() <= 7 * 2.0 ** -8, far.max()
