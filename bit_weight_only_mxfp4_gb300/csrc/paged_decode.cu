@@ -65,7 +65,7 @@ struct Plan {
   static constexpr int kConsumers = kGroups * kGroupWarps * 32;
   static constexpr int kThreads = kConsumers + kCopiers;
   // registers a thread: 65,536 less the copying warps' share
-  static constexpr int kCopyRegs = 56;
+  static constexpr int kCopyRegs = 72;
   static constexpr int kLaunchRegs = 65536 / kThreads / 8 * 8;
   static constexpr int kRegs = (kLaunchRegs * kThreads - kCopyRegs * kCopiers) / kConsumers / 8 * 8;
   // 16-token chunks per warp and tile: 32 KB of K and V a tile, or 16 KB
