@@ -777,7 +777,7 @@ __global__ void __launch_bounds__(Plan<D, FP8>::kThreads, 1)
           did |= tile(G1{}, v1, s1, my1);
           if (did) {
             idle = 0;
-          } else if ((__nanosleep(20), (++idle & 63u) == 0u)) {
+          } else if ((++idle & 63u) == 0u) {
             if (idle == 64u) since = globaltimer_ns();
             if (globaltimer_ns() - since > kWaitLimitNs && lane == 0) {
               *quit = 1;
