@@ -38,10 +38,12 @@
 // elements that are not finite are zeroed and the rows that do see them get
 // them added at the end.  Tiles that all rows see whole need nothing of it.
 //
-// Work.  Row tiles x kv heads are dealt to one CTA per SM, the last (longest)
-// first; where there are fewer than half as many as SMs, each is split along
-// its tokens, and a second kernel joins the parts, in order.
-// What the lengths are is read on the device.
+// Work.  A piece (two row tiles of a kv head) goes to one CTA; the pieces, longest
+// first, are dealt to one CTA per SM in rounds, to and fro.  Where the last round
+// (or the only one) has a piece for every second CTA at most, its pieces are
+// split along their tokens and a second kernel joins the parts, in order: 512
+// pieces of 64 tiles on 152 SMs are three rounds and a half then, not four (420
+// -> 384 us).  What the lengths are is read on the device.
 #include <cmath>
 #include <type_traits>
 
@@ -58,6 +60,8 @@ constexpr int kMmaWarp = 8, kLoadWarp = 9, kFixWarp = 10;
 constexpr int kCounters = 1024;  // the decode kernel's, at the workspace's start: left alone
 constexpr int kJoinBytes = (kCounters + 1) * 16;
 constexpr int kMaxSplit = 32;
+constexpr int kMaxSorted = 64;   // sequences that are put in order of length
+constexpr int kTailTiles = 8;    // tiles a piece of the last round has to have to be split
 constexpr uint32_t kAll = 0xffffffffu;
 
 template <int D, bool FP8>
@@ -84,8 +88,10 @@ struct Plan {
   static constexpr int kOffScale = kOffRaw + kRaws * kRaw;      // [4 tiles][key, value][128]
   static constexpr int kOffLine = kOffScale + (FP8 ? 4 * 2 * kKeys * 4 : 0);
   static constexpr int kOffStart = kOffLine + (kPagedMaxBatch + 4) * 4;
-  static constexpr int kOffLen = kOffStart + (kPagedMaxBatch + 4) * 4;
-  static constexpr int kOffBar = kOffLen + kPagedMaxBatch * 4;
+  static constexpr int kOffEnd = kOffStart + kPagedMaxBatch * 4;
+  static constexpr int kOffLen = kOffEnd + kPagedMaxBatch * 4;
+  static constexpr int kOffOrder = kOffLen + kPagedMaxBatch * 4;
+  static constexpr int kOffBar = kOffOrder + kPagedMaxBatch * 4;
   static constexpr int kSmem = 1024 + kOffBar + 640;
   static_assert(kSmem <= 227 * 1024, "shared memory");
   static_assert(kOffBar % 8 == 0, "barriers");
@@ -370,7 +376,7 @@ struct Item {
   int lo, hi;            // tokens that some row sees
   int all_lo, all_hi;    // tokens that every row sees
   int k0, k1, parts, part;
-  int base;              // number among the joined pieces
+  int base;              // number among the joined pieces, or -1
 };
 
 // Waits for a phase; gives up after kWaitLimitNs, or when another thread has.
@@ -422,9 +428,13 @@ __global__ void __launch_bounds__(Plan<D, FP8>::kThreads, 1)
   uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
   const uint32_t sbase = smem_u32(smem);
   float* scales = reinterpret_cast<float*>(smem + P::kOffScale);
-  int32_t* line = reinterpret_cast<int32_t*>(smem + P::kOffLine);  // q tiles before sequence b
-  int32_t* first = reinterpret_cast<int32_t*>(smem + P::kOffStart);  // its first flat token
+  // of the i-th sequence taken: the q tiles before it, its first flat token and
+  // the one after its last, its length, its number
+  int32_t* line = reinterpret_cast<int32_t*>(smem + P::kOffLine);
+  int32_t* first = reinterpret_cast<int32_t*>(smem + P::kOffStart);
+  int32_t* ends = reinterpret_cast<int32_t*>(smem + P::kOffEnd);
   int32_t* lens = reinterpret_cast<int32_t*>(smem + P::kOffLen);
+  int32_t* order = reinterpret_cast<int32_t*>(smem + P::kOffOrder);
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + P::kOffBar);
   uint64_t* empty = full + P::kSlots;
   uint64_t* ready = empty + P::kSlots;   // slot made safe, or converted
@@ -476,24 +486,44 @@ __global__ void __launch_bounds__(Plan<D, FP8>::kThreads, 1)
   pdl_allow_next_grid();
   pdl_wait_prior_grid();
 
-  // ---- the pieces of work: q tiles of every sequence, scanned
+  // ---- the pieces of work: q tiles of every sequence, scanned.  Where there are
+  // more than about one for every CTA, the sequences are taken in order of their
+  // lengths, so that the longest pieces come first (three ragged chunks of 64
+  // heads of 64 over FP8 pages: 746 us, in the order given 790); up to 64 of
+  // them, as each is ranked against all.
   const int64_t tokens = a.tokens;
-  for (int b = tid; b <= kv.batch; b += kThreads) {
+  auto start_of = [&](int b) {
     const int64_t s = __ldcg(a.starts + b);
-    first[b] = int(s < 0 ? 0 : s > tokens ? tokens : s);
-    if (b < kv.batch) lens[b] = paged_len(kv, b, blockIdx.x == 0 ? a.err : nullptr);
+    return int(s < 0 ? 0 : s > tokens ? tokens : s);
+  };
+  for (int b = tid; b < kv.batch; b += kThreads) {
+    first[b] = start_of(b);
+    ends[b] = start_of(b + 1);
+    order[b] = b;
+    lens[b] = paged_len(kv, b, blockIdx.x == 0 ? a.err : nullptr);
   }
   __syncthreads();
+  const bool sorted = kv.batch > 1 && kv.batch <= kMaxSorted &&
+                      tokens * kv.kv_heads > int64_t(2) * a.per_tile * gridDim.x;
+  if (sorted) {
+    int rank = 0, s0 = 0, s1 = 0, n = 0;
+    if (tid < kv.batch) {
+      s0 = first[tid], s1 = ends[tid], n = lens[tid];
+      for (int c = 0; c < kv.batch; ++c) rank += lens[c] < n || (lens[c] == n && c < tid);
+    }
+    __syncthreads();
+    if (tid < kv.batch) first[rank] = s0, ends[rank] = s1, lens[rank] = n, order[rank] = tid;
+    __syncthreads();
+  }
   {
     constexpr int kPer = (kPagedMaxBatch + kThreads - 1) / kThreads;
     const int per = (kv.batch + kThreads - 1) / kThreads;
     int mine[kPer], sum = 0;
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
-      const int b = tid * per + i;
       mine[i] = 0;
-      if (i < per && b < kv.batch) {
-        const int n = first[b + 1] - first[b];
+      if (i < per && tid * per + i < kv.batch) {
+        const int n = ends[tid * per + i] - first[tid * per + i];
         mine[i] = n > 0 ? (n + 2 * a.per_tile - 1) / (2 * a.per_tile) : 0;
       }
       sum += mine[i];
@@ -521,41 +551,41 @@ __global__ void __launch_bounds__(Plan<D, FP8>::kThreads, 1)
   }
   const uint32_t tmem = uint32_t(misc[0]);
   const int tiles = line[kv.batch];
-  const int64_t pieces = int64_t(tiles) * kv.kv_heads;
+  const int pieces = tiles * kv.kv_heads;  // (tokens x heads fit 31 bits)
   const int sms = gridDim.x;
-  int split = a.may_split && pieces > 0 && pieces * 2 <= sms ? int(sms / pieces) : 1;
-  split = split < kMaxSplit ? split : kMaxSplit;
-  const int64_t items = pieces * split;
-  if (a.may_split && blockIdx.x == 0 && tid == 0)
-    a.joins[0] = make_int4(split > 1 ? int(pieces) : 0, split, 0, 0);
   const int G = a.group, heads = G * kv.kv_heads, TT = a.per_tile;
+  // Whole rounds of pieces, then the rest: where it has a piece for every second
+  // CTA at most, its pieces are split along their tokens.
+  const int whole = pieces / sms * sms;
+  const int rest = pieces - whole;
+  int split = a.may_split && rest > 0 && rest * 2 <= sms ? sms / rest : 1;
+  split = split < kMaxSplit ? split : kMaxSplit;
 
-  // The CTA's turns: the items, longest first, are dealt to the CTAs to and
-  // fro, which evens out what a falling order leaves uneven; -1 at the end.
-  auto turn_of = [&](int64_t turn) {
-    if (turn * sms >= items) return int64_t(-1);
-    return turn * sms + (turn & 1 ? sms - 1 - int(blockIdx.x) : int(blockIdx.x));
-  };
-  auto item_of = [&](int64_t idx) {
+  auto item_of = [&](int idx) {
     Item w;
-    w.part = int(idx % split);
-    const int64_t piece = idx / split;
-    w.base = split > 1 ? int(piece) : 0;
-    w.j = int(piece % kv.kv_heads);
-    const int u = tiles - 1 - int(piece / kv.kv_heads);  // the longest first
+    int piece = idx;
+    w.part = 0;
+    w.base = -1;
+    if (split > 1 && idx >= whole) {
+      w.base = (idx - whole) / split;
+      w.part = idx - whole - w.base * split;
+      piece = whole + w.base;
+    }
+    w.j = piece % kv.kv_heads;
+    const int u = tiles - 1 - piece / kv.kv_heads;  // the longest first
     int lo = 0, hi = kv.batch;
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
       if (line[mid] <= u) lo = mid; else hi = mid;
     }
-    w.b = lo;
-    const int s0 = first[lo], s1 = first[lo + 1];
+    w.b = order[lo];
+    const int s0 = first[lo], s1 = ends[lo];
     const int q0 = (u - line[lo]) * 2 * TT;
     w.tok0 = s0 + q0;
     w.new_tokens = s1 - w.tok0;
     w.len = lens[lo];
     w.p0 = w.len - w.new_tokens;
-    w.pre = a.prefix ? __ldcg(a.prefix + lo) : 0;
+    w.pre = a.prefix ? __ldcg(a.prefix + w.b) : 0;
     const int rows = w.new_tokens < 2 * TT ? w.new_tokens : 2 * TT;
     const int plast = w.p0 + rows - 1;
     int top = plast + 1 > w.pre ? plast + 1 : w.pre;
@@ -571,7 +601,7 @@ __global__ void __launch_bounds__(Plan<D, FP8>::kThreads, 1)
     const int nk = w.hi > w.lo ? kb - ka : 0;
     // two tiles a part at least (a part's start costs about as much)
     const int most = nk > 3 ? nk / 2 : 1;
-    w.parts = split < most ? split : most;
+    w.parts = w.base < 0 ? 1 : split < most ? split : most;
     w.k0 = w.k1 = ka;
     if (w.part < w.parts) {
       w.k0 = ka + int(int64_t(nk) * w.part / w.parts);
@@ -580,6 +610,22 @@ __global__ void __launch_bounds__(Plan<D, FP8>::kThreads, 1)
     return w;
   };
   auto has_b = [&](const Item& w) { return w.new_tokens > TT; };
+  // After whole rounds a split gains less than a round, and costs the parts' way
+  // through memory: short pieces stay whole.
+  if (split > 1 && whole > 0) {
+    const Item w = item_of(whole);
+    const int nk = (w.hi + kKeys - 1) / kKeys - w.lo / kKeys;
+    if (nk < kTailTiles) split = 1;
+  }
+  const int items = whole + rest * split;
+  if (a.may_split && blockIdx.x == 0 && tid == 0)
+    a.joins[0] = make_int4(split > 1 ? rest : 0, split, 0, 0);
+  // The CTA's turns: the items, longest first, are dealt to the CTAs to and
+  // fro, which evens out what a falling order leaves uneven; -1 at the end.
+  auto turn_of = [&](int turn) {
+    if (turn * sms >= items) return -1;
+    return turn * sms + (turn & 1 ? sms - 1 - int(blockIdx.x) : int(blockIdx.x));
+  };
   const int br_shift = kv.page_shift;  // rows of a box: a page, 16 .. 128
   const int boxes = kKeys >> br_shift;
 
@@ -591,7 +637,7 @@ __global__ void __launch_bounds__(Plan<D, FP8>::kThreads, 1)
       int seq = 0;     // items done
       uint32_t nt = 0; // tiles
       bool ok = true;
-      for (int64_t turn = 0, idx; ok && (idx = turn_of(turn)) >= 0; ++turn) {
+      for (int turn = 0, idx; ok && (idx = turn_of(turn)) >= 0; ++turn) {
         if (idx >= items) continue;
         const Item w = item_of(idx);
         if (w.k1 <= w.k0) continue;
@@ -714,7 +760,7 @@ __global__ void __launch_bounds__(Plan<D, FP8>::kThreads, 1)
       auto phase = [&](uint32_t m) { return (m / P::kSlots) & 1u; };
       using G0 = std::integral_constant<int, 0>;
       using G1 = std::integral_constant<int, 1>;
-      for (int64_t turn = 0, idx; ok && (idx = turn_of(turn)) >= 0; ++turn) {
+      for (int turn = 0, idx; ok && (idx = turn_of(turn)) >= 0; ++turn) {
         if (idx >= items) continue;
         const Item w = item_of(idx);
         const int nk = __shfl_sync(kAll, w.k1 - w.k0, 0);
@@ -802,7 +848,7 @@ __global__ void __launch_bounds__(Plan<D, FP8>::kThreads, 1)
       uint32_t n = 0, nt = 0;
       int seq = 0;
       bool ok = true;
-      for (int64_t turn = 0, idx; ok && (idx = turn_of(turn)) >= 0; ++turn) {
+      for (int turn = 0, idx; ok && (idx = turn_of(turn)) >= 0; ++turn) {
         if (idx >= items) continue;
         const Item w = item_of(idx);
         if (w.k1 <= w.k0) continue;
@@ -949,7 +995,7 @@ constexpr int kIlp = 4;  // pieces in work at once
     uint32_t slot = 0, done = 0;  // slot uses of the CTA; items of this row tile
     int seq = 0;
     bool ok = true;
-    for (int64_t turn = 0, idx; ok && (idx = turn_of(turn)) >= 0; ++turn) {
+    for (int turn = 0, idx; ok && (idx = turn_of(turn)) >= 0; ++turn) {
       if (idx >= items) continue;
       const Item w = item_of(idx);
       if (w.part >= w.parts) continue;
@@ -958,7 +1004,7 @@ constexpr int kIlp = 4;  // pieces in work at once
       const int tok = g * TT + rt;  // among the item's tokens
       const bool mine = rt < TT && tok < w.new_tokens;
       const int groups = has_b(w) ? 2 : 1;
-      if (split > 1 && w.part == 0 && r == 0 && (w.parts == 1 || (g == 1 && groups == 1)))
+      if (w.base >= 0 && w.part == 0 && r == 0 && (w.parts == 1 || (g == 1 && groups == 1)))
         a.joins[1 + 2 * w.base + g] = make_int4(0, 0, 0, 0);
       if (g == 1 && groups == 1) {
         nt += nk;
@@ -1364,10 +1410,13 @@ cudaError_t launch(const DeviceInfo& di, const PagedKv& kv, const PagedAttnArgs&
   d.prefix = a.prefix;
   d.out = a.out;
   d.lse = a.lse;
-  // Split where there may be fewer than half as many pieces as SMs (tokens
-  // that no sequence has only make this too careful).
+  // Whether a last round of half as many pieces as SMs or fewer is possible.
+  // One sequence has this many pieces (tokens that it does not have only make this
+  // too careful); several may have any number more, up to one q tile each.
   const int64_t pieces = (a.tokens + 2 * TT - 1) / (2 * TT) * kv.kv_heads;
-  d.may_split = pieces * 2 <= di.sms;
+  const int64_t rest = pieces % di.sms;
+  d.may_split = kv.batch == 1 ? rest > 0 && rest * 2 <= di.sms
+                              : pieces * 2 <= di.sms || pieces > di.sms;
   d.joins = reinterpret_cast<int4*>(static_cast<uint8_t*>(a.ws) + kCounters * 4);
   d.parts = reinterpret_cast<float*>(static_cast<uint8_t*>(a.ws) + kCounters * 4 + kJoinBytes);
   d.err = di.error_word;

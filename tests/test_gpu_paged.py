@@ -609,6 +609,20 @@ def test_prefill_more_pieces_than_sms(heads, kvh, d, batch, most, fp8):
     _prefill_case(batch, heads, kvh, d, 16, fp8, new, [int(n) for n in r.integers(0, 60, batch)])
 
 
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("heads,kvh,d,new,past,opt", [
+    (64, 4, 128, [641], [1300], {}),  # 152 pieces and some: those of the last round in parts
+    (64, 4, 64, [641], [1300], {"prefix": [1900], "sinks": True}),
+    (64, 4, 64, [700], [900], {"window": 500}),  # the last round's pieces are short
+    (64, 4, 128, [300, 1, 0, 260, 200], [100, 1500, 0, 0, 1400], {}),  # taken in order of their lengths
+    (64, 4, 64, [300, 30, 0, 260, 200, 300], [1300, 1500, 0, 700, 1400, 1300], {"prefix": [0, 1530, 0, 0, 1500, 900]}),
+])
+def test_prefill_rounds(heads, kvh, d, new, past, opt, fp8):
+    got = _prefill_case(len(new), heads, kvh, d, 64, fp8, new, past, **opt)
+    again = _prefill_case(len(new), heads, kvh, d, 64, fp8, new, past, **opt)
+    assert (got[0] == again[0]).all() and (got[1] == again[1]).all()
+
+
 @pytest.mark.parametrize("parts", [True, False])
 @pytest.mark.parametrize("bad", [0x7FC0, 0x7F80, 0xFF80], ids=["nan", "inf", "-inf"])
 def test_prefill_values_not_finite_reach_only_rows_that_see_them(bad, parts):
