@@ -9,7 +9,8 @@
 // rlo = p + 1 - window.  The work is 4 head_dim operations per row and
 // token, so it belongs to the tensor cores:
 //   S = Q K^T   128 rows x 128 tokens, tcgen05.mma, accumulator in TMEM
-//   P = 2^(S - m) in bf16, back to TMEM over S
+//   P = 2^(S - m) in bf16, back to TMEM: over S, or with 64 dims, where columns
+//                 are left, into its own, so that the next S need not wait for P V
 //   O += P V    A operand P from TMEM, B operand V as it lies in the cache
 //               (token rows: the "transposed" B of the instruction), O in TMEM
 //
@@ -18,8 +19,9 @@
 // two row tiles at once (A and B), each with a warpgroup for its softmax, one
 // thread a row, while the tensor cores are busy with the other's products:
 //   warps 0-3, 4-7  softmax of A and B (a thread holds a row's 128 scores)
-//   warp 8          the products, one thread
-//   warp 9          the copies (TMA: one box per page and 64 dims)
+//   warp 8          the products, issued by the warp in step, one elected lane
+//   warp 9          the copies (TMA: one box per page and 64 dims; FP8: bulk
+//                   copies of codes and scales)
 //   warps 10, 11    make the V tiles safe (below); FP8: warps 10-15, which
 //                   also turn E4M3 pages into bf16 tiles
 // The running maximum is only raised (and O rescaled, which takes a TMEM round
@@ -44,6 +46,18 @@
 // split along their tokens and a second kernel joins the parts, in order: 512
 // pieces of 64 tiles on 152 SMs are three rounds and a half then, not four (420
 // -> 384 us).  What the lengths are is read on the device.
+//
+// Measured (back to back in a graph): 8192 tokens, 16 / 4 heads of 128, all of a
+// prefix of 7411 seen: 384 us, 1.30 PFLOP/s; 8192 causal tokens, 64 / 8 heads of
+// 64: 705 us, 0.78 PFLOP/s (a token and row cost the same exponential and half
+// the products); over FP8 pages 0.52 PFLOP/s; four ragged chunks of 120 tokens
+// 21.7 us.  What bounds it: with 128 dims the chain S, softmax, P V, next S of a
+// row tile, of which the other tile's covers a part (products alone, with the
+// same handshakes, take 172 us where the kernel takes 218); with 64 dims the
+// softmax warps' own time (two thirds of a tile's 3000 cycles).  FP8: the
+// softmax threads read 256 scales a tile and row from shared memory, six warps
+// convert 2 x 128 rows a tile, and both share the issue slots (58% busy).
+// Exponentials left out (to see) change 0 with 128 dims and 7% with 64.
 #include <cmath>
 #include <type_traits>
 
@@ -823,7 +837,7 @@ __global__ void __launch_bounds__(Plan<D, FP8>::kThreads, 1)
           did |= tile(G1{}, v1, s1, my1);
           if (did) {
             idle = 0;
-          } else if ((++idle & 63u) == 0u) {
+          } else if ((++idle & 63u) == 0u) {  // (a sleep of 20 ns here: 222 us for 218.5)
             if (idle == 64u) since = globaltimer_ns();
             if (globaltimer_ns() - since > kWaitLimitNs && lane == 0) {
               *quit = 1;
