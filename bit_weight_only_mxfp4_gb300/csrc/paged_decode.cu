@@ -21,12 +21,12 @@
 // (cp.async), into a swizzled layout that the fragment loads read without bank
 // conflicts; a pair's queries come with its first tiles.  The ring spans pair
 // boundaries, so the copies run on while a pair is finished.  (One TMA box per
-// page and matrix, from one warp, moves a page of 16 rows of 64 bytes at a third
-// of the rate: 1 KB a box.  One copying warp in place of four: FP8 batch 140 us,
-// four 118.)  Two groups of four warps take the tiles in turn, 16 (or 2 x 16)
-// tokens a warp, each with its own running maximum, sum and output; a pair's
-// end joins them in shared memory.  (Four groups, with half the registers each:
-// 137 us where two take 117.)
+// page and matrix costs as much for a page of 1 KB as for one of 16: the FP8
+// batch below took 308 us that way; four warps that share every tile 134 to 140,
+// whole tiles each 117.)  Two groups of four warps take the tiles in turn, 16
+// (or 2 x 16) tokens a warp, each with its own running maximum, sum and output;
+// a pair's end joins them in shared memory.  (Four groups, with half the
+// registers each: 137 us where two take 117.)
 //
 // Products, on mma.sync m16n8k16 with the tokens (or dims) as the 16 rows and
 // the heads as the 8 columns, so that up to 8 heads fill it:
