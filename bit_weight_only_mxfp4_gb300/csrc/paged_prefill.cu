@@ -48,12 +48,12 @@
 // -> 384 us).  What the lengths are is read on the device.
 //
 // Measured (back to back in a graph): 8192 tokens, 16 / 4 heads of 128, all of a
-// prefix of 7411 seen: 384 us, 1.30 PFLOP/s; 8192 causal tokens, 64 / 8 heads of
-// 64: 705 us, 0.78 PFLOP/s (a token and row cost the same exponential and half
+// prefix of 7411 seen: 370 us, 1.35 PFLOP/s; 8192 causal tokens, 64 / 8 heads of
+// 64: 693 us, 0.79 PFLOP/s (a token and row cost the same exponential and half
 // the products); over FP8 pages 0.52 PFLOP/s; four ragged chunks of 120 tokens
 // 21.7 us.  What bounds it: with 128 dims the chain S, softmax, P V, next S of a
 // row tile, of which the other tile's covers a part (products alone, with the
-// same handshakes, take 172 us where the kernel takes 218); with 64 dims the
+// same handshakes, take 172 us where the kernel takes 214); with 64 dims the
 // softmax warps' own time (two thirds of a tile's 3000 cycles).  FP8: the
 // softmax threads read 256 scales a tile and row from shared memory, six warps
 // convert 2 x 128 rows a tile, and both share the issue slots (58% busy).
@@ -83,12 +83,13 @@ struct Plan {
   // warps 0-7 softmax, 8 products, 9 copies, and from kFixWarp on those that
   // make the V tiles safe: two; FP8: six, which convert.  Registers a thread:
   // at launch, for the softmax warps (a thread holds a row's 128 scores), for
-  // the others.
+  // the others (bf16 208 / 88: 383 us for the 370 below, 232 / 40: 381; FP8 200 /
+  // 56: 744 for 731, 216 / 40: 754).
   static constexpr int kThreads = FP8 ? 512 : 384;
   static constexpr int kFixers = kThreads - 32 * kFixWarp;
   static constexpr int kLaunchRegs = FP8 ? 128 : 168;
-  static constexpr int kSoftmaxRegs = FP8 ? 200 : 208;
-  static constexpr int kOtherRegs = FP8 ? 56 : 88;
+  static constexpr int kSoftmaxRegs = FP8 ? 208 : 224;
+  static constexpr int kOtherRegs = FP8 ? 48 : 56;
   static_assert(256 * kSoftmaxRegs + (kThreads - 256) * kOtherRegs <= kThreads * kLaunchRegs,
                 "register shares");
   static constexpr int kHalves = D / 64;            // 128-byte spans of a bf16 row
