@@ -51,4 +51,34 @@ __device__ __forceinline__ int paged_seq_of(const int32_t* starts, int batch, in
   return __reduce_add_sync(0xffffffffu, n);
 }
 
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// The end of a row from its maximum m (log2 units) and its sum l of weights
+// 2^(z - m): the sink, the logarithm; returns the factor of the sum of
+// weights times values.  l = 0: the row sees no key, its sink is all there is,
+// and the result 0.  A sink of -infinity adds nothing; one of +infinity has
+// the whole weight.
+__device__ __forceinline__ float close_row(float m, float l, const float* sinks, int h,
+                                           float* lse, int64_t row) {
+  float f = 1.f;
+  if (sinks) {
+    const float sink = __ldcg(sinks + h);
+    if (l == 0.f) {
+      if (lse) lse[row] = sink;
+      return 0.f;
+    }
+    const float z = sink * kLog2e, m2 = fmaxf(m, z);
+    f = m == -INFINITY ? 0.f : ex2(m - m2);
+    // z - m2 is no number where both are infinite
+    l = l * f + (z == -INFINITY ? 0.f : z == m2 ? 1.f : ex2(z - m2));
+    m = m2;
+  }
+  if (lse) lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+  return f * (l > 0.f ? 1.f / l : l == 0.f ? 0.f : l);  // a NaN stays one
+}
+
 }  // namespace tt

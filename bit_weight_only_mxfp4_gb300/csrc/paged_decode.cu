@@ -196,11 +196,6 @@ __device__ __forceinline__ float rcp(float x) {
 __device__ __forceinline__ void prefetch_l2(const void* p) {
   asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
 }
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
 template <int kConsumers>
 __device__ __forceinline__ void consumer_sync() {
   asm volatile("bar.sync %0, %1;" ::"r"(kConsumerBar), "n"(kConsumers) : "memory");
@@ -873,24 +868,11 @@ __global__ void __launch_bounds__(Plan<D, NH, FP8>::kThreads, 1)
     // final values from O, max (log2 units) and sum of head r
     auto finish = [&](int r, int u, float4 s, float M, float Lq) {
       const int h = j * G + r, ul = u & 31, qi = (u >> 5) % QI;
-      if (a.sinks) {
-        const float z = __ldcg(a.sinks + h) * kLog2e;
-        const float M2 = fmaxf(M, z);
-        const float f = M == -INFINITY ? 0.f : ex2(M - M2);
-        Lq = Lq * f + ex2(z - M2);
-        s.x *= f;
-        s.y *= f;
-        s.z *= f;
-        s.w *= f;
-        M = M2;
-      }
-      const float inv = Lq > 0.f ? 1.f / Lq : Lq == 0.f ? 0.f : Lq;  // a NaN stays one
       const int64_t row = int64_t(b) * heads + h;
       const int d0 = first_dim(qi, ul >> 2);
+      const float inv = close_row(M, Lq, a.sinks, h, d0 == 0 ? a.lse : nullptr, row);
       *reinterpret_cast<uint2*>(a.out + row * D + d0) =
           make_uint2(bf16x2(s.x * inv, s.y * inv), bf16x2(s.z * inv, s.w * inv));
-      if (a.lse && d0 == 0)
-        a.lse[row] = Lq == 0.f ? -INFINITY : (M + log2f(Lq)) * 0.6931471805599453f;
     };
     // head of unit u
     auto head_of = [](int u) {

@@ -326,11 +326,6 @@ __device__ __forceinline__ void bulk_copy(uint32_t dst, const void* src, uint32_
       : "memory");
 }
 
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
 // Two 32-bit lanes at once.
 __device__ __forceinline__ uint64_t f2(uint32_t lo, uint32_t hi) {
   uint64_t r;
@@ -411,22 +406,6 @@ __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile in
       }
     }
   }
-}
-
-// The end of a row from its maximum (log2 units) and sum: the sink, the
-// logarithm; returns the factor of O.
-__device__ __forceinline__ float close_row(float m, float l, const float* sinks, int h,
-                                           float* lse, int64_t row) {
-  float f = 1.f;
-  if (sinks) {
-    const float z = __ldcg(sinks + h) * kLog2e;
-    const float m2 = fmaxf(m, z);
-    f = m == -INFINITY ? 0.f : ex2(m - m2);
-    l = l * f + ex2(z - m2);
-    m = m2;
-  }
-  if (lse) lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
-  return f * (l > 0.f ? 1.f / l : l == 0.f ? 0.f : l);  // a NaN stays one
 }
 
 // GEN: a cap, a bias or a scale that is not positive (the plain kernel's loop

@@ -499,8 +499,8 @@ tt_status tt_paged_rope_append(const tt_paged_kv* kv, const uint16_t* q, const u
  *             f(s) = softcap * tanh(s / softcap) if softcap > 0, else s
  *   out[b][h] = bf16_rne( sum_t e^z v[j][t] / (sum_t e^z + e^sinks[h]) )
  *   lse[b][h] = log(sum_t e^z + e^sinks[h])
- * slopes, sinks: fp32 [heads] or NULL (no bias; no sink).  lse fp32
- * [batch][heads] or NULL.  A token that sees no key: out 0, lse = sinks[h]
+ * slopes, sinks: fp32 [heads] or NULL (no bias; no sink).  A head without a
+ * sink among others has -inf.  lse fp32 [batch][heads] or NULL.  A token that sees no key: out 0, lse = sinks[h]
  * (-inf without sinks).  q: row of sequence b at b * q_stride elements; out
  * [batch][heads][head_dim].
  * Requires heads a multiple of kv_heads, heads / kv_heads <= 16, scale and
