@@ -42,8 +42,13 @@
 //   FP8: codes become f16 exactly; q becomes f16 after an exact power-of-two
 //     prescale per head (its elements keep 11 bits down to 2^-29 of the
 //     largest); the scales multiply scores and weights in 32 bits; P * scale
-//     is rounded once to f16 (2^-11, against 2^-4 for a code), in units of
-//     the power of two of the largest scale so far, so that it is at most 2.
+//     is rounded once to f16 (2^-11, against 2^-4 for a code), in a unit per
+//     head that follows the largest P * scale so far, not the largest scale: a
+//     row of a large scale may have no weight, and one of a small scale all of
+//     it.  The unit puts the largest between 2^11 and 2^12 and is moved when one
+//     passes 2^15, so products down to 2^-25 of the largest keep their 11 bits,
+//     and smaller ones are off by 2^-36 of it.  When the maximum rises the unit
+//     shrinks with the old weights and O stays as it is.
 //
 // Measured (back to back in a graph): 64 ragged sequences up to 16384 tokens,
 // 64 / 8 heads of 64, FP8 pages of 16: 116 us, 4.8 TB/s (without the products
@@ -68,6 +73,7 @@ constexpr int kCopiers = 32 * kCopyWarps;
 constexpr int kMaxCtas = 1024;                // counters in the workspace
 constexpr int kSmemMax = 227 * 1024;
 constexpr int kConsumerBar = 1;
+constexpr float kLeastUnit = 0x1p-126f;       // of an FP8 cache's P * scale: the smallest normal number
 
 template <int D, int NH, bool FP8>
 struct Plan {
@@ -520,10 +526,11 @@ __global__ void __launch_bounds__(Plan<D, NH, FP8>::kThreads, 1)
     };
 
     float mrun[NH][2], lsum[NH][2], o[NH][MT][4];
-    float vref = 0x1p-120f;  // unit of o on an FP8 cache, a power of two
+    [[maybe_unused]] float ou[NH][2];  // FP8: the units of o
 #pragma unroll
     for (int nh = 0; nh < NH; ++nh) {
       mrun[nh][0] = mrun[nh][1] = -INFINITY;
+      ou[nh][0] = ou[nh][1] = kLeastUnit;
       lsum[nh][0] = lsum[nh][1] = 0.f;
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt)
@@ -583,12 +590,10 @@ __global__ void __launch_bounds__(Plan<D, NH, FP8>::kThreads, 1)
 #pragma unroll
           for (int e = 0; e < 4; ++e) sc[tm][nh][e] += s2[nh][e];
       }
-      // the scales of this lane's tokens, and the unit of the weights
+      // the scales of this lane's tokens
       [[maybe_unused]] float vs[kTm][2];
-      [[maybe_unused]] float keep = 1.f;  // what the unit's change makes of o
       if constexpr (FP8) {
         const float* ss = reinterpret_cast<const float*>(vb + P::kPart);
-        float vmax = 0.f;
 #pragma unroll
         for (int tm = 0; tm < kTm; ++tm)
 #pragma unroll
@@ -597,27 +602,12 @@ __global__ void __launch_bounds__(Plan<D, NH, FP8>::kThreads, 1)
             const float ks = ss[r];
             vs[tm][e] = ss[kTok + r];
             if (!FULLT && !visible(r)) vs[tm][e] = 0.f;
-            vmax = fmaxf(vmax, fabsf(vs[tm][e]));
 #pragma unroll
             for (int nh = 0; nh < NH; ++nh) {
               sc[tm][nh][2 * e] *= ks;
               sc[tm][nh][2 * e + 1] *= ks;
             }
           }
-        vmax = fmaxf(vmax, __shfl_xor_sync(kFull, vmax, 4));
-        vmax = fmaxf(vmax, __shfl_xor_sync(kFull, vmax, 8));
-        vmax = fmaxf(vmax, __shfl_xor_sync(kFull, vmax, 16));
-        const float top = fminf(__uint_as_float(__float_as_uint(vmax) & 0x7f800000u), 0x1p120f);
-        if (top > vref) {  // the same for the whole warp
-          keep = vref / top;
-          vref = top;
-        }
-        const float inv = __uint_as_float((254u << 23) - __float_as_uint(vref));
-#pragma unroll
-        for (int tm = 0; tm < kTm; ++tm) {
-          vs[tm][0] *= inv;
-          vs[tm][1] *= inv;
-        }
       }
       // to log2 units, mask, running maximum and sum
 #pragma unroll
@@ -660,15 +650,71 @@ __global__ void __launch_bounds__(Plan<D, NH, FP8>::kThreads, 1)
 #pragma unroll
           for (int tm = 0; tm < kTm; ++tm) t += sc[tm][nh][h] + sc[tm][nh][h + 2];
           lsum[nh][h] = lsum[nh][h] * alpha[h] + t;
-          if constexpr (FP8) alpha[h] *= keep;
+          if constexpr (FP8) ou[nh][h] *= alpha[h];
+        }
+        if constexpr (!FP8) {
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt) {
+            o[nh][mt][0] *= alpha[0];
+            o[nh][mt][1] *= alpha[1];
+            o[nh][mt][2] *= alpha[0];
+            o[nh][mt][3] *= alpha[1];
+          }
+        }
+      }
+      // FP8: weights times scales, in the heads' units
+      if constexpr (FP8) {
+        float top[NH][2], iu[NH][2];
+        bool move = false;
+#pragma unroll
+        for (int nh = 0; nh < NH; ++nh)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            float t = 0.f;
+#pragma unroll
+            for (int tm = 0; tm < kTm; ++tm)
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                float& w = sc[tm][nh][h + 2 * e];
+                w *= vs[tm][e];
+                t = fmaxf(t, fabsf(w));
+              }
+            top[nh][h] = t;
+            iu[nh][h] = rcp(ou[nh][h]);  // (of less than kLeastUnit: not used)
+            move |= ou[nh][h] < kLeastUnit || t * iu[nh][h] > 0x1p15f;
+          }
+        if (__any_sync(kFull, move)) {
+#pragma unroll
+          for (int nh = 0; nh < NH; ++nh) {
+            float f[2];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              float t = top[nh][h];
+              t = fmaxf(t, __shfl_xor_sync(kFull, t, 4));
+              t = fmaxf(t, __shfl_xor_sync(kFull, t, 8));
+              t = fmaxf(t, __shfl_xor_sync(kFull, t, 16));
+              // the power of two in t (of infinity: 2^127), 2^11 of which are the unit
+              t = fminf(__uint_as_float(__float_as_uint(t) & 0x7f800000u), 0x1p127f) * 0x1p-11f;
+              t = fmaxf(fmaxf(t, ou[nh][h]), kLeastUnit);
+              iu[nh][h] = rcp(t);
+              f[h] = ou[nh][h] * iu[nh][h];
+              ou[nh][h] = t;
+            }
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) {
+              o[nh][mt][0] *= f[0];
+              o[nh][mt][1] *= f[1];
+              o[nh][mt][2] *= f[0];
+              o[nh][mt][3] *= f[1];
+            }
+          }
         }
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
-          o[nh][mt][0] *= alpha[0];
-          o[nh][mt][1] *= alpha[1];
-          o[nh][mt][2] *= alpha[0];
-          o[nh][mt][3] *= alpha[1];
-        }
+        for (int tm = 0; tm < kTm; ++tm)
+#pragma unroll
+          for (int nh = 0; nh < NH; ++nh)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) sc[tm][nh][e] *= iu[nh][e & 1];
       }
       // O^T += V^T P^T
 #pragma unroll
@@ -679,8 +725,8 @@ __global__ void __launch_bounds__(Plan<D, NH, FP8>::kThreads, 1)
         for (int nh = 0; nh < NH; ++nh) {
           const float* c = sc[tm][nh];
           if constexpr (FP8) {
-            ph[nh][0] = transpose8x8(f16x2(c[0] * vs[tm][0], c[1] * vs[tm][0]));
-            ph[nh][1] = transpose8x8(f16x2(c[2] * vs[tm][1], c[3] * vs[tm][1]));
+            ph[nh][0] = transpose8x8(f16x2(c[0], c[1]));
+            ph[nh][1] = transpose8x8(f16x2(c[2], c[3]));
           } else {
             const uint32_t h0 = bf16x2(c[0], c[1]), h1 = bf16x2(c[2], c[3]);
             ph[nh][0] = transpose8x8(h0);
@@ -802,7 +848,7 @@ __global__ void __launch_bounds__(Plan<D, NH, FP8>::kThreads, 1)
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) o[nh][mt][e] *= vref;
+          for (int e = 0; e < 4; ++e) o[nh][mt][e] *= ou[nh][e & 1];
       }
     }
     // Unit (hf, qi) of a lane: head 8 (hf / 2) + 2 qd + hf % 2, four

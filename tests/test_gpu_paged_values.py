@@ -76,3 +76,93 @@ def test_a_sink_of_infinity_takes_everything(fp8):
         out, lse = _attend(_handle(c), _queries(202, tokens, 16, 128), starts, 0.125, sinks=sinks)
         assert not bf16_to_f64(out[:, ::2]).any() and np.isposinf(lse[:, ::2]).all()
         assert np.isfinite(bf16_to_f64(out)).all() and np.isfinite(lse[:, 1::2]).all()
+
+
+# ----------------------------------------------------------------------------------- weights times scales, FP8 decode
+@pytest.mark.parametrize("ratio", [-16, -20, -30, -60])
+@pytest.mark.parametrize("heads,kvh,d", [(16, 4, 128), (64, 8, 64), (12, 1, 64), (32, 2, 128)])
+def test_fp8_decode_small_scales_with_all_the_weight(heads, kvh, d, ratio):
+    """The last 4 tokens have all the softmax (a steep distance bias) and value scales 2^ratio of those of their
+    neighbours, which weigh e^-96 at most.  The bound is relative to what the 4 make: 2^-11, an f16 rounding of each
+    weight times scale."""
+    lens = [704, 304]
+    c = ref.Cache(203, lens, kvh, d, 16, True)
+    q = _queries(203, 2, heads, d)
+    for b, n in enumerate(lens):
+        t = np.arange(n - 4, n)
+        at = (c.table[b, t // 16], slice(None), t % 16)
+        c.v_scales[at] = (c.v_scales[at] * 2.0 ** ratio).astype(np.float32)
+    opt = dict(slopes=np.full(heads, 24.0, np.float32), window=48)
+    got = _attend(_handle(c), q, None, 0.125, **opt)
+    ref.check_attention(*got, ref.attention(c, q, None, 0.125, **opt), DECODE_EPS[True], f"2^{ratio}")
+
+
+def _flat_scores(seed, scores, v_scales, kvh, d):
+    """Keys and queries of ones: the score of token t is scores[t].  Values of one code and sign, so that an error of
+    the weights does not average out."""
+    n = len(scores)
+    c = ref.Cache(seed, [n], kvh, d, 16, True)
+    t = np.arange(n)
+    at = (c.table[0, t // 16], slice(None), t % 16)
+    c.k[at], c.v[at] = 0x38, 0x3D  # 1, and 1.625
+    c.k_scales[at] = np.asarray(scores, np.float32)[:, None]
+    c.v_scales[at] = np.asarray(v_scales, np.float32)[:, None]
+    return c
+
+
+@pytest.mark.parametrize("gap", [12.0, 14.3, 16.3, 18.0])
+@pytest.mark.parametrize("heads,kvh,d", [(16, 4, 128), (64, 8, 64), (12, 1, 64)])
+@pytest.mark.parametrize("where", [0, 200, -1])
+def test_fp8_decode_one_heavy_token_of_small_values(heads, kvh, d, where, gap):
+    """One token far above the rest whose value row is almost zero (an attention sink): the rest makes the output."""
+    n = 700
+    scores, vs = np.zeros(n), np.ones(n)
+    scores[where], vs[where] = gap, 2.0 ** -40
+    c = _flat_scores(204, scores, vs, kvh, d)
+    q = np.full((1, heads, d), 0x3F80, np.uint16)
+    got = _attend(_handle(c), q, None, 1.0 / d)
+    ref.check_attention(*got, ref.attention(c, q, None, 1.0 / d), DECODE_EPS[True], f"gap {gap}")
+
+
+@pytest.mark.parametrize("heads,kvh,d", [(16, 4, 128), (64, 8, 64)])
+@pytest.mark.parametrize("big", [100.0, 2.0 ** 20, 2.0 ** 24])
+def test_fp8_decode_one_large_scale_of_small_weight(heads, kvh, d, big):
+    """One token whose value scale is far above the others', 40 nats below them."""
+    n = 100
+    scores, vs = np.full(n, 40.0), np.full(n, 1.3)
+    vs[5], scores[5] = big, 0.0
+    scores[::3] = 37.0  # and others between
+    c = _flat_scores(205, scores, vs, kvh, d)
+    q = np.full((1, heads, d), 0x3F80, np.uint16)
+    got = _attend(_handle(c), q, None, 1.0 / d)
+    ref.check_attention(*got, ref.attention(c, q, None, 1.0 / d), DECODE_EPS[True], f"scale {big}")
+
+
+def test_fp8_decode_heads_of_one_group_with_different_tokens():
+    """Two heads of one kv head: one has all its weight on a row of a small scale, the other on one of a large scale."""
+    c = ref.Cache(206, [120], 1, 64, 16, True)
+    t = np.arange(120)
+    at = (c.table[0, t // 16], 0, t % 16)
+    c.k[at] = 0
+    code = np.where(t < 60, 0x38, 0xB8)[:, None]  # +1 or -1
+    c.k[at] = np.broadcast_to(code, (120, 64))
+    c.k_scales[at] = 0.5
+    c.v[at] = 0x3D
+    c.v_scales[at] = np.where(t < 60, 1.0, 2.0 ** -28).astype(np.float32)
+    q = np.empty((1, 2, 64), np.uint16)
+    q[0, 0], q[0, 1] = 0x3F80, 0xBF80  # the score of a token: +-32
+    got = _attend(_handle(c), q, None, 1.0)
+    ref.check_attention(*got, ref.attention(c, q, None, 1.0), DECODE_EPS[True], "two heads")
+
+
+@pytest.mark.parametrize("shift", [-120, -100, 100])
+def test_fp8_decode_scales_at_the_ends_of_the_range(shift):
+    """All value scales at 2^-120, 2^-100 and 2^100 of the usual ones (those below 2^-126 lose bits in 32 bits too)."""
+    c = ref.Cache(207, [700, 33], 4, 128, 16, True)
+    c.v_scales = (c.v_scales.astype(np.float64) * 2.0 ** shift).astype(np.float32)
+    q = _queries(207, 2, 16, 128)
+    out, lse = _attend(_handle(c), q, None, 0.125)
+    w_out, w_lse, spread, slack = ref.attention(c, q, None, 0.125)
+    y = bf16_to_f64(out).reshape(w_out.shape)
+    tol = 2.0 ** -8 * np.abs(w_out) + (2.0 ** -11 + 2 * slack[..., None] + 2.0 ** -16) * spread + 2.0 ** -133
+    assert np.isfinite(y).all() and np.all(np.abs(y - w_out) <= tol)
