@@ -38,7 +38,9 @@
 // 128 rows of queries for a product of at most 16, and K and V would pass
 // shared memory all the same.)
 //   bf16: exact products; P as bf16 high + low parts (2^-16), since a decode
-//     step's output should not lose to the cache's own precision.
+//     step's output should not lose to the cache's own precision.  The high part
+//     is the largest below P, so that the low one is above 0 and both take an
+//     infinite value to the same infinity (0 * infinity is NaN).
 //   FP8: codes become f16 exactly; q becomes f16 after an exact power-of-two
 //     prescale per head (its elements keep 11 bits down to 2^-29 of the
 //     largest); the scales multiply scores and weights in 32 bits; P * scale
@@ -183,6 +185,11 @@ __device__ __forceinline__ uint32_t word(const uint4& v, int i) {
 }
 __device__ __forceinline__ uint32_t halves(uint32_t a, uint32_t b, int h) {
   return __byte_perm(a, b, h ? 0x7632 : 0x5410);
+}
+
+// The largest bf16 value below x > 0 (32-bit pattern); 0 of 0, NaN of a NaN.
+__device__ __forceinline__ uint32_t bf16_below(float x) {
+  return (max(__float_as_uint(x), 1u) - 1u) & 0xffff0000u;
 }
 
 // 16 bytes to shared memory, past L1; counted by the thread's next
@@ -728,13 +735,15 @@ __global__ void __launch_bounds__(Plan<D, NH, FP8>::kThreads, 1)
             ph[nh][0] = transpose8x8(f16x2(c[0], c[1]));
             ph[nh][1] = transpose8x8(f16x2(c[2], c[3]));
           } else {
-            const uint32_t h0 = bf16x2(c[0], c[1]), h1 = bf16x2(c[2], c[3]);
-            ph[nh][0] = transpose8x8(h0);
-            ph[nh][1] = transpose8x8(h1);
-            pl[nh][0] = transpose8x8(bf16x2(c[0] - __uint_as_float(h0 << 16),
-                                            c[1] - __uint_as_float(h0 & 0xffff0000u)));
-            pl[nh][1] = transpose8x8(bf16x2(c[2] - __uint_as_float(h1 << 16),
-                                            c[3] - __uint_as_float(h1 & 0xffff0000u)));
+            uint32_t h[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) h[e] = bf16_below(c[e]);
+            ph[nh][0] = transpose8x8(halves(h[0], h[1], 1));
+            ph[nh][1] = transpose8x8(halves(h[2], h[3], 1));
+            pl[nh][0] = transpose8x8(
+                bf16x2(c[0] - __uint_as_float(h[0]), c[1] - __uint_as_float(h[1])));
+            pl[nh][1] = transpose8x8(
+                bf16x2(c[2] - __uint_as_float(h[2]), c[3] - __uint_as_float(h[3])));
           }
         }
         const int rv = 16 * (tm * kGroupWarps + gw) + 2 * qd;

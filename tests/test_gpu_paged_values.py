@@ -166,3 +166,22 @@ def test_fp8_decode_scales_at_the_ends_of_the_range(shift):
     y = bf16_to_f64(out).reshape(w_out.shape)
     tol = 2.0 ** -8 * np.abs(w_out) + (2.0 ** -11 + 2 * slack[..., None] + 2.0 ** -16) * spread + 2.0 ** -133
     assert np.isfinite(y).all() and np.all(np.abs(y - w_out) <= tol)
+
+
+# ------------------------------------------------------------------------------------------------ values in sight
+@pytest.mark.parametrize("heads,kvh,d", [(64, 8, 64), (16, 4, 128), (12, 1, 64)])
+@pytest.mark.parametrize("bad", [0x7F80, 0xFF80, 0x7FC0], ids=["inf", "-inf", "nan"])
+@pytest.mark.parametrize("n,t", [(1, 0), (100, 37), (100, 99), (5000, 4000)])
+def test_decode_infinite_values_in_sight(n, t, bad, heads, kvh, d):
+    """sum e^z v with v infinite and e^z > 0 is that infinity, whatever the weight's bits are."""
+    j, dim = kvh - 1, 9
+    c, clean = (ref.Cache(208, [n, 60], kvh, d, 16, False, junk=False) for _ in range(2))
+    c.v[c.table[0, t // 16], j, t % 16, dim] = bad
+    q = _queries(208, 2, heads, d)
+    got = bf16_to_f64(_attend(_handle(c), q, None, 0.125)[0]).reshape(2, heads, d)
+    want = bf16_to_f64(_attend(_handle(clean), q, None, 0.125)[0]).reshape(2, heads, d)
+    hit = np.zeros((2, heads, d), bool)
+    hit[0, j * (heads // kvh):(j + 1) * (heads // kvh), dim] = True
+    assert np.array_equal(got[~hit], want[~hit])
+    value = bf16_to_f64(np.uint16(bad))
+    assert np.isnan(got[hit]).all() if bad == 0x7FC0 else (got[hit] == value).all()
