@@ -55,6 +55,7 @@ bool has_registers(Kern kern, int regs) {
 
 constexpr int kPagedMaxBatch = 1024;
 constexpr int kPagedMaxGroup = 16;  // query heads per kv head
+constexpr float kCapSmall = 256.f;  // caps up to here are taken from the exponential alone
 
 // paged_append.cu
 cudaError_t launch_rope_turns(const double* inv_freq, int n, uint64_t* turns, cudaStream_t s);

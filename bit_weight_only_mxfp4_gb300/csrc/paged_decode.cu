@@ -201,11 +201,6 @@ __device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
 __device__ __forceinline__ void copies_arrive(uint32_t bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
 }
-__device__ __forceinline__ float rcp(float x) {
-  float y;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
 __device__ __forceinline__ void prefetch_l2(const void* p) {
   asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
 }
@@ -257,7 +252,7 @@ __device__ __forceinline__ At find(const Line& L, int batch, int item) {
   return {lo, rem / nt, rem % nt};
 }
 
-template <int D, int NH, bool FP8>
+template <int D, int NH, bool FP8, bool LARGE_CAP>
 __global__ void __launch_bounds__(Plan<D, NH, FP8>::kThreads, 1)
     paged_decode_kernel(const PagedKv kv, const DecodeArgs a) {
   using P = Plan<D, NH, FP8>;
@@ -453,12 +448,10 @@ __global__ void __launch_bounds__(Plan<D, NH, FP8>::kThreads, 1)
   constexpr int KP = P::kRow / 64;  // 16-byte pieces of a row per lane in the score product
   constexpr int QR = D / 8;         // registers of q per lane and head tile
   constexpr int MT = D / 16;        // 16-dim tiles of the output
-  // to log2 units; with a cap, cap tanh(x) = cap - 2 cap / (1 + e^2x) from
-  // v = 2x log2 e (e^2x may be infinite, its reciprocal is then 0): off by
-  // about cap 2^-22 absolutely, which is what counts in the exponent
-  const float cap2 = a.softcap * kLog2e;
-  const float unit = a.softcap > 0.f ? 2.f * kLog2e / a.softcap : kLog2e;
-  const bool plain = !(a.softcap > 0.f) && !a.slopes;
+  const Cap cap = cap_of(a.softcap);
+  // from the product's units: to log2 units, or with a small cap to its y
+  const float unit = kLog2e * (!LARGE_CAP && a.softcap > 0.f ? cap.per : 1.f);
+  const bool plain = LARGE_CAP ? !a.slopes : !(a.softcap > 0.f) && !a.slopes;
 
   uint32_t pairs = 0;  // done so far
   At at = find(L, kv.batch, i0);
@@ -527,8 +520,8 @@ __global__ void __launch_bounds__(Plan<D, NH, FP8>::kThreads, 1)
           }
           fac[nh][0] = fac[nh][1] = a.scale;
         }
-        fac[nh][0] *= unit;
-        fac[nh][1] *= unit;
+        fac[nh][0] = fminf(fmaxf(fac[nh][0] * unit, -kFiniteMax), kFiniteMax);
+        fac[nh][1] = fminf(fmaxf(fac[nh][1] * unit, -kFiniteMax), kFiniteMax);
       }
     };
 
@@ -617,6 +610,27 @@ __global__ void __launch_bounds__(Plan<D, NH, FP8>::kThreads, 1)
           }
       }
       // to log2 units, mask, running maximum and sum
+      if constexpr (LARGE_CAP) {
+        float far = 0.f;
+#pragma unroll
+        for (int tm = 0; tm < kTm; ++tm)
+#pragma unroll
+          for (int nh = 0; nh < NH; ++nh)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              sc[tm][nh][e] *= fac[nh][e & 1];
+              far = fmaxf(far, fabsf(sc[tm][nh][e]));
+            }
+        const bool large = __any_sync(kFull, far * cap.per >= kCapSeries);
+#pragma unroll
+        for (int tm = 0; tm < kTm; ++tm)
+#pragma unroll
+          for (int nh = 0; nh < NH; ++nh)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              sc[tm][nh][e] =
+                  large ? cap_large(sc[tm][nh][e], cap) : cap_series(sc[tm][nh][e], cap);
+      }
 #pragma unroll
       for (int nh = 0; nh < NH; ++nh) {
         float mx[2] = {-INFINITY, -INFINITY};
@@ -625,9 +639,9 @@ __global__ void __launch_bounds__(Plan<D, NH, FP8>::kThreads, 1)
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const int r = 16 * (tm * kGroupWarps + gw) + g + 8 * (e >> 1);
-            float v = sc[tm][nh][e] * fac[nh][e & 1];
+            float v = LARGE_CAP ? sc[tm][nh][e] : sc[tm][nh][e] * fac[nh][e & 1];
             if (!plain) {
-              if (a.softcap > 0.f) v = fmaf(-2.f * cap2, rcp(1.f + ex2(v)), cap2);
+              if (!LARGE_CAP && a.softcap > 0.f) v = cap_small(v, cap);
               v = fmaf(slope[nh][e & 1], float(t0 + r - (n - 1)), v);
             }
             if (!FULLT && !visible(r)) v = -INFINITY;
@@ -1051,11 +1065,11 @@ __global__ void __launch_bounds__(Plan<D, NH, FP8>::kThreads, 1)
   }
 }
 
-template <int D, int NH, bool FP8>
-cudaError_t launch(const DeviceInfo& di, const PagedKv& kv, const PagedAttnArgs& a,
-                   cudaStream_t s, bool pdl) {
+template <int D, int NH, bool FP8, bool LARGE_CAP>
+cudaError_t launch_as(const DeviceInfo& di, const PagedKv& kv, const PagedAttnArgs& a,
+                      cudaStream_t s, bool pdl) {
   using P = Plan<D, NH, FP8>;
-  auto kern = paged_decode_kernel<D, NH, FP8>;
+  auto kern = paged_decode_kernel<D, NH, FP8, LARGE_CAP>;
   static const bool fits = has_registers(kern, P::kLaunchRegs);
   if (!fits) return cudaErrorInvalidDeviceFunction;
   if (cudaError_t e = ensure_smem(di, kern, P::kSmem)) return e;
@@ -1090,6 +1104,13 @@ cudaError_t launch(const DeviceInfo& di, const PagedKv& kv, const PagedAttnArgs&
   cfg.attrs = attr;
   cfg.numAttrs = pdl ? 1 : 0;
   return cudaLaunchKernelEx(&cfg, kern, kv, d);
+}
+
+template <int D, int NH, bool FP8>
+cudaError_t launch(const DeviceInfo& di, const PagedKv& kv, const PagedAttnArgs& a,
+                   cudaStream_t s, bool pdl) {
+  return a.softcap > kCapSmall ? launch_as<D, NH, FP8, true>(di, kv, a, s, pdl)
+                               : launch_as<D, NH, FP8, false>(di, kv, a, s, pdl);
 }
 
 }  // namespace

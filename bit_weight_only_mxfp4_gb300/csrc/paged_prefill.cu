@@ -358,11 +358,6 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
   return y;
 }
-__device__ __forceinline__ float rcp(float x) {
-  float y;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
 __device__ __forceinline__ uint32_t bf16x2(float a, float b) {
   const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
   return *reinterpret_cast<const uint32_t*>(&h);
@@ -408,15 +403,17 @@ __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile in
   }
 }
 
-// GEN: a cap, a bias or a scale that is not positive (the plain kernel's loop
-// stays short without them).
-template <int D, bool FP8, bool GEN>
+// What is done to the scores: nothing but a positive scale; a cap, a bias or
+// another scale (the plain kernel's loop stays short without them); a large cap.
+enum Scores { kPlain, kGeneral, kLargeCap };
+template <int D, bool FP8, Scores SC>
 __global__ void __launch_bounds__(Plan<D, FP8>::kThreads, 1)
     paged_prefill_kernel(const __grid_constant__ CUtensorMap map_q,
                          const __grid_constant__ CUtensorMap map_k,
                          const __grid_constant__ CUtensorMap map_v, const PagedKv kv,
                          const PrefillArgs a) {
   using P = Plan<D, FP8>;
+  constexpr bool GEN = SC != kPlain;
   constexpr int kThreads = P::kThreads, kFixers = P::kFixers;
   extern __shared__ __align__(128) uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
@@ -980,10 +977,11 @@ constexpr int kIlp = 4;  // pieces in work at once
     const uint32_t lanes = uint32_t((warp & 3) * 32) << 16;
     const uint32_t ts = tmem + lanes + P::kColS(g), to = tmem + lanes + P::kColO(g),
                    tp = tmem + lanes + P::kColP(g);
-    // scores to log2 units: z = s mul without a cap; with one, e^2x is 2^(s cap_mul)
-    const float mul = a.scale * kLog2e;
-    const float cap2 = a.softcap * kLog2e;
-    const float cap_mul = a.softcap > 0.f ? 2.f * mul / a.softcap : 0.f;
+    const float mul = a.scale * kLog2e;  // scores to log2 units
+    const Cap cap = cap_of(a.softcap);
+    // with a small cap to its y
+    const float unit =
+        a.softcap > 0.f ? fminf(fmaxf(mul * cap.per, -kFiniteMax), kFiniteMax) : mul;
     const int rt = r / G, rh = r - rt * G;
     uint32_t nt = 0, my = 0;  // tiles of the CTA; tiles of this row tile
     uint32_t slot = 0, done = 0;  // slot uses of the CTA; items of this row tile
@@ -1065,19 +1063,45 @@ constexpr int kIlp = 4;  // pieces in work at once
             }
           }
         };
-        // to log2 units, the long way: the cap, the bias, a scale <= 0.
-        // cap tanh(x) = cap - 2 cap / (1 + e^2x); e^2x may be infinite, its
-        // reciprocal is then 0.  Off by cap * 2^-22 absolutely, which is what
-        // counts in the exponent.
-        auto capped = [&](float v) {
-          return fmaf(-2.f * cap2, rcp(1.f + ex2(v * cap_mul)), cap2);
+        // a large cap, two scores at a time where all are below the series' end
+        auto capped = [&](uint32_t* x) {
+          float far = 0.f;
+#pragma unroll
+          for (int e = 0; e < 32; ++e) {
+            const float v = __uint_as_float(x[e]) * mul;
+            far = fmaxf(far, fabsf(v));
+            x[e] = __float_as_uint(v);
+          }
+          if (__any_sync(kAll, far * cap.per >= kCapSeries)) {
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              x[e] = __float_as_uint(cap_large(__uint_as_float(x[e]), cap));
+            return;
+          }
+          auto both = [](float v) { return f2(v, v); };
+          const uint64_t k = both(cap.per * kHalfLn2);
+#pragma unroll
+          for (int e = 0; e < 32; e += 2) {
+            const uint64_t s2 = f2(x[e], x[e + 1]), xc = mul2(s2, k), x2 = mul2(xc, xc);
+            uint64_t p = fma2(x2, both(kCap4), both(kCap3));
+            p = fma2(x2, p, both(kCap2));
+            p = fma2(x2, p, both(kCap1));
+            float v[2];
+            un2(fma2(mul2(s2, x2), p, s2), v[0], v[1]);
+            x[e] = __float_as_uint(v[0]);
+            x[e + 1] = __float_as_uint(v[1]);
+          }
         };
+        // to log2 units, the long way: the cap, the bias, a scale <= 0
         auto general = [&](uint32_t* x, int c) {
           const float base = slope * float(t0 + 32 * c - p);
 #pragma unroll
           for (int e = 0; e < 32; ++e) {
             float v = __uint_as_float(x[e]);
-            v = a.softcap > 0.f ? capped(v) : v * mul;
+            if constexpr (SC != kLargeCap) {
+              v *= unit;
+              if (a.softcap > 0.f) v = cap_small(v, cap);
+            }
             x[e] = __float_as_uint(v + fmaf(slope, float(e), base));
           }
         };
@@ -1098,7 +1122,10 @@ constexpr int kIlp = 4;  // pieces in work at once
         }
         if constexpr (GEN) {
 #pragma unroll
-          for (int c = 0; c < 4; ++c) general(s + 32 * c, c);
+          for (int c = 0; c < 4; ++c) {
+            if constexpr (SC == kLargeCap) capped(s + 32 * c);
+            general(s + 32 * c, c);
+          }
         }
         if (__builtin_expect(!clear, 0)) {
 #pragma unroll
@@ -1367,11 +1394,11 @@ cudaError_t encode(CUtensorMap* map, const void* base, int rank, const cuuint64_
   return cudaSuccess;
 }
 
-template <int D, bool FP8, bool GEN>
-cudaError_t launch(const DeviceInfo& di, const PagedKv& kv, const PagedAttnArgs& a,
-                   cudaStream_t s, bool pdl) {
+template <int D, bool FP8, Scores SC>
+cudaError_t launch_as(const DeviceInfo& di, const PagedKv& kv, const PagedAttnArgs& a,
+                      cudaStream_t s, bool pdl) {
   using P = Plan<D, FP8>;
-  auto kern = paged_prefill_kernel<D, FP8, GEN>;
+  auto kern = paged_prefill_kernel<D, FP8, SC>;
   const int G = a.heads / kv.kv_heads, TT = kRows / G;
   CUtensorMap mq, mk = {}, mv = {};
   {
@@ -1433,6 +1460,15 @@ cudaError_t launch(const DeviceInfo& di, const PagedKv& kv, const PagedAttnArgs&
   return cudaLaunchKernelEx(&cfg, paged_prefill_join_kernel<D>, d, a.heads);
 }
 
+template <int D, bool FP8>
+cudaError_t launch(const DeviceInfo& di, const PagedKv& kv, const PagedAttnArgs& a,
+                   cudaStream_t s, bool pdl) {
+  if (a.softcap > kCapSmall) return launch_as<D, FP8, kLargeCap>(di, kv, a, s, pdl);
+  if (a.softcap > 0.f || a.slopes || !(a.scale > 0.f))
+    return launch_as<D, FP8, kGeneral>(di, kv, a, s, pdl);
+  return launch_as<D, FP8, kPlain>(di, kv, a, s, pdl);
+}
+
 }  // namespace
 
 size_t paged_prefill_workspace_bytes(int head_dim) {
@@ -1447,19 +1483,9 @@ cudaError_t launch_paged_prefill(const PagedKv& kv, int head_dim, bool fp8,
                                  const PagedAttnArgs& a, cudaStream_t s, bool pdl) {
   const DeviceInfo* di = device_info();
   if (!di) return cudaErrorNoDevice;
-  const bool gen = a.softcap > 0.f || a.slopes || !(a.scale > 0.f);
-  if (head_dim == 64) {
-    if (gen)
-      return fp8 ? launch<64, true, true>(*di, kv, a, s, pdl)
-                 : launch<64, false, true>(*di, kv, a, s, pdl);
-    return fp8 ? launch<64, true, false>(*di, kv, a, s, pdl)
-               : launch<64, false, false>(*di, kv, a, s, pdl);
-  }
-  if (gen)
-    return fp8 ? launch<128, true, true>(*di, kv, a, s, pdl)
-               : launch<128, false, true>(*di, kv, a, s, pdl);
-  return fp8 ? launch<128, true, false>(*di, kv, a, s, pdl)
-             : launch<128, false, false>(*di, kv, a, s, pdl);
+  if (head_dim == 64)
+    return fp8 ? launch<64, true>(*di, kv, a, s, pdl) : launch<64, false>(*di, kv, a, s, pdl);
+  return fp8 ? launch<128, true>(*di, kv, a, s, pdl) : launch<128, false>(*di, kv, a, s, pdl);
 }
 
 }  // namespace tt

@@ -1,5 +1,7 @@
 """The paged cache operators on values at the ends of their ranges, against 64-bit references: sinks that are not
 finite, value scales far apart, values that are not finite, large caps, and what such values cost."""
+import math
+
 import numpy as np
 import pytest
 
@@ -185,3 +187,34 @@ def test_decode_infinite_values_in_sight(n, t, bad, heads, kvh, d):
     assert np.array_equal(got[~hit], want[~hit])
     value = bf16_to_f64(np.uint16(bad))
     assert np.isnan(got[hit]).all() if bad == 0x7FC0 else (got[hit] == value).all()
+
+
+# ---------------------------------------------------------------------------------------------------------------- caps
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("heads,kvh,d", [(16, 4, 128), (64, 8, 64)])
+@pytest.mark.parametrize("cap", [1e3, 3e4, 1e5, 1e7, 1e20, 3.4e38])
+def test_large_caps(cap, heads, kvh, d, fp8):
+    """A cap far above the scores hardly bends them: its error must not grow with it.  c tanh(s / c) for |s| < c / 8 is
+    s less s^3 / (3 c^2), in 32 bits off by a few 2^-24 |s|, which is below the slack of the scores' own sums (2 d steps
+    of 2^-24 of sum |q k|, and |s| <= that sum), so the uncapped scores' slack is the bound, doubled for both."""
+    cap = float(np.float32(cap))
+    c = ref.Cache(209, [300, 41, 1], kvh, d, 16, fp8, k_std=3.0)
+    scale = float(np.float32(1.0 / math.sqrt(d)))
+    for starts, tokens, eps in ((None, 3, DECODE_EPS[fp8]), (np.array([0, 30, 41, 42], np.int32), 42, PREFILL_EPS)):
+        q = _queries(209, tokens, heads, d)
+        out, lse, spread, _ = ref.attention(c, q, starts, scale, softcap=cap)
+        slack = 2 * ref.attention(c, q, starts, scale)[3]
+        got = _attend(_handle(c), q, starts, scale, softcap=cap)
+        ref.check_attention(*got, (out, lse, spread, slack), eps, f"cap {cap}")
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("cap", [1e-40, 1e-30, 1e-3, 0.5, 255.0, 257.0, 1000.0])
+def test_caps_that_bend_the_scores(cap, fp8):
+    """Scores below, around and above the cap; tiny caps make all weights alike."""
+    cap = float(np.float32(cap))
+    c = ref.Cache(210, [300, 41], 4, 128, 16, fp8, k_std=min(60.0, 3.0 + cap / 4))
+    for starts, tokens, eps in ((None, 2, DECODE_EPS[fp8]), (np.array([0, 30, 41], np.int32), 41, PREFILL_EPS)):
+        q = _queries(210, tokens, 16, 128)
+        got = _attend(_handle(c), q, starts, 0.25, softcap=cap)
+        ref.check_attention(*got, ref.attention(c, q, starts, 0.25, softcap=cap), eps, f"cap {cap}")
