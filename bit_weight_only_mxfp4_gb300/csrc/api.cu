@@ -440,9 +440,10 @@ tt_status check_paged_kv(const tt_paged_kv* kv, tt::PagedKv* out) {
   if (kv->head_dim != 64 && kv->head_dim != 128) return TT_ERR_UNSUPPORTED;
   if (kv->kv_heads > tt::kGqaMaxKvHeads || kv->batch > tt::kPagedMaxBatch)
     return TT_ERR_UNSUPPORTED;
-  // row and token numbers fit 32 bits
+  // row and token numbers fit 32 bits, also those of a tile's end and of the
+  // pages (32 of 128 tokens at most) that a warp looks up from a tile's start on
   if (kv->num_pages > kMaxRows / kv->kv_heads / kv->page_size) return TT_ERR_UNSUPPORTED;
-  if (kv->pages_per_seq > kMaxRows / kv->page_size) return TT_ERR_UNSUPPORTED;
+  if (kv->pages_per_seq > (kMaxRows + 1 - 4096) / kv->page_size) return TT_ERR_UNSUPPORTED;
   if (!kv->k || !kv->v || !kv->page_table || !kv->lens) return TT_ERR_NULL;
   if (kv->type == TT_KV_FP8 && (!kv->k_scales || !kv->v_scales)) return TT_ERR_NULL;
   if (!aligned(kv->k, 16) || !aligned(kv->v, 16) || !aligned(kv->page_table, 4) ||

@@ -432,9 +432,9 @@ tt_status tt_gqa_decode_attention(const uint16_t* q_bf16, const uint16_t* k_cach
  * is clamped): nothing outside the pool is touched.  page_table, lens and
  * q_starts are read after the call waits for the preceding kernel.
  * Requires page_size 16, 32, 64 or 128; head_dim 64 or 128; kv_heads <= 64;
- * batch <= 1024; num_pages * kv_heads * page_size and pages_per_seq *
- * page_size <= 2^31 - 1 (else TT_ERR_UNSUPPORTED).  k, v and scales 16-byte
- * aligned, int32 arrays 4-byte.
+ * batch <= 1024; num_pages * kv_heads * page_size <= 2^31 - 1 and
+ * pages_per_seq * page_size <= 2^31 - 4096 (else TT_ERR_UNSUPPORTED).  k, v
+ * and scales 16-byte aligned, int32 arrays 4-byte.
  * --------------------------------------------------------------------- */
 #define TT_KV_BF16 0
 #define TT_KV_FP8 1

@@ -64,6 +64,17 @@ def test_bad_caches_are_refused_by_every_call(lib, bad, want):
     assert prefill(kv(**bad)) == want
 
 
+@pytest.mark.parametrize("page", [16, 32, 64, 128])
+def test_tables_of_almost_two_to_the_31_tokens(lib, page):
+    """Tokens are counted in 32 bits up to a tile's end and a warp's furthest page: the last 4096 are refused."""
+    most = ((1 << 31) - 4096) // page
+    for call in (append, decode, prefill):
+        for more in (1, 4096 // page - 1):
+            assert call(kv(page_size=page, batch=1, pages_per_seq=most + more, num_pages=10)) == 5
+        # accepted as a size: the next check refuses it
+        assert call(kv(page_size=page, batch=1, pages_per_seq=most, num_pages=10, k=A + 8)) == 3
+
+
 def test_no_cache(lib):
     assert append(None) == decode(None) == prefill(None) == 1
 
