@@ -403,6 +403,61 @@ __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile in
   }
 }
 
+// Which of the 32 dims from d0 on have a value of +infinity, -infinity, NaN (a
+// bit each) among the tokens [lo, hi) of sequence b and kv head j, in the tiles
+// whose values were kept out of the product: those that the mask cuts (not
+// within [all_lo, all_hi)), and with `holes` those of which pages are missing.
+// Only these are read, a page looked up once.  (The whole row, element by
+// element, took 45 ms for 17,000 tokens with one NaN in the last tile, and
+// would have been past a wait's limit for some 400,000.)
+template <int D, bool FP8>
+__device__ __noinline__ uint3 not_finite(const PagedKv& kv, int b, int j, int lo, int hi,
+                                         int all_lo, int all_hi, bool holes, int d0) {
+  uint3 x = make_uint3(0u, 0u, 0u);
+  const int rows = 1 << kv.page_shift;
+  for (int t0 = lo / kKeys * kKeys; t0 < hi; t0 += kKeys) {
+    if (t0 >= all_lo && t0 + kKeys <= all_hi) {
+      bool whole = true;
+      for (int t = t0; holes && t < t0 + kKeys; t += rows) whole &= paged_page(kv, b, t, nullptr) >= 0;
+      if (whole) continue;
+    }
+    for (int tp = t0; tp < t0 + kKeys; tp += rows) {
+      const int from = max(tp, lo), n = min(tp + rows, hi) - from;
+      if (n <= 0) continue;
+      const int page = paged_page(kv, b, tp, nullptr);
+      if (page < 0) continue;
+      const int64_t at = paged_row(kv, page, j, from);
+      const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(kv.v) +
+                                                        (at * D + d0) * (FP8 ? 1 : 2));
+#pragma unroll 4
+      for (int t = 0; t < n; ++t) {
+        if constexpr (FP8) {  // codes have NaN only; a scale that is not finite makes all of the row so
+          const uint4 q[2] = {__ldcg(src + t * (D / 16)), __ldcg(src + t * (D / 16) + 1)};
+          if (!(fabsf(__ldcg(kv.v_scales + at + t)) <= kFiniteMax)) x.z = kAll;
+#pragma unroll
+          for (int u = 0; u < 8; ++u) {
+            const uint32_t c = reinterpret_cast<const uint32_t*>(q)[u] & 0x7f7f7f7fu;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              x.z |= uint32_t(((c >> (8 * i)) & 0x7fu) == 0x7fu) << (4 * u + i);
+          }
+        } else {
+          const uint4 q[4] = {__ldcg(src + t * (D / 8)), __ldcg(src + t * (D / 8) + 1),
+                              __ldcg(src + t * (D / 8) + 2), __ldcg(src + t * (D / 8) + 3)};
+#pragma unroll
+          for (int d = 0; d < 32; ++d) {
+            const uint32_t v = (reinterpret_cast<const uint32_t*>(q)[d / 2] >> (16 * (d & 1))) & 0xffffu;
+            x.x |= uint32_t(v == 0x7f80u) << d;
+            x.y |= uint32_t(v == 0xff80u) << d;
+            x.z |= uint32_t((v & 0x7fffu) > 0x7f80u) << d;
+          }
+        }
+      }
+    }
+  }
+  return x;
+}
+
 // What is done to the scores: nothing but a positive scale; a cap, a bias or
 // another scale (the plain kernel's loop stays short without them); a large cap.
 enum Scores { kPlain, kGeneral, kLargeCap };
@@ -410,7 +465,8 @@ template <int D, bool FP8, Scores SC>
 __global__ void __launch_bounds__(Plan<D, FP8>::kThreads, 1)
     paged_prefill_kernel(const __grid_constant__ CUtensorMap map_q,
                          const __grid_constant__ CUtensorMap map_k,
-                         const __grid_constant__ CUtensorMap map_v, const PagedKv kv,
+                         const __grid_constant__ CUtensorMap map_v,
+                         const __grid_constant__ PagedKv kv,
                          const PrefillArgs a) {
   using P = Plan<D, FP8>;
   constexpr bool GEN = SC != kPlain;
@@ -1018,7 +1074,7 @@ constexpr int kIlp = 4;  // pieces in work at once
           for (int e = groups; e <= 2; ++e) mbar_arrive(smem_u32(&empty[use % P::kSlots]));
       };
       float m = -INFINITY, l = 0.f;
-      bool holes = false;  // in any tile
+      bool holes = false;  // pages missing of a tile that the mask does not cut
       for (int i = 0; i < nk; ++i, ++nt, ++my) {
         ok = __all_sync(kAll, wait(&s_full[g], my & 1u, quit, a.err));
         if (!ok) break;
@@ -1034,7 +1090,7 @@ constexpr int kIlp = 4;  // pieces in work at once
         const int t0 = (w.k0 + i) * kKeys;
         const uint32_t got = have[nt & 7u];
         const bool whole = got == kAll >> (32 - boxes);
-        holes |= !whole;
+        holes |= !whole && t0 >= w.all_lo && t0 + kKeys <= w.all_hi;
         const bool clear = __all_sync(kAll, t0 >= rlo && t0 + kKeys <= rhi) && whole;
         const float* ks = scales + ((nt & 3u) * 2) * kKeys;
         // All of the row's scores at once, and its weights at once: a TMEM access
@@ -1220,29 +1276,14 @@ constexpr int kIlp = 4;  // pieces in work at once
       }
       const int64_t row = int64_t(w.tok0 + tok) * heads + h;
       const bool poisoned = nk > 0 && *static_cast<volatile int*>(&dirty[seq & 3]) == seq;
-      // values that are not finite and were kept out of the product, from the
-      // tiles where that was done
       auto add_not_finite = [&](float* o, int d0) {
-        for (int t = rlo > w.k0 * kKeys ? rlo : w.k0 * kKeys; t < rhi && t < w.k1 * kKeys; ++t) {
-          const int t0 = t / kKeys * kKeys;
-          if (!holes && t0 >= w.all_lo && t0 + kKeys <= w.all_hi) {
-            t = t0 + kKeys - 1;
-            continue;
-          }
-          const int page = paged_page(kv, w.b, t, nullptr);
-          if (page < 0) continue;
-          const int64_t at = paged_row(kv, page, w.j, t) * D + d0;
-          for (int d = 0; d < 32; ++d) {
-            if constexpr (FP8) {
-              const float x = __ldcg(kv.v_scales + at / D);
-              if ((__ldcg(static_cast<const uint8_t*>(kv.v) + at + d) & 0x7f) == 0x7f ||
-                  !(fabsf(x) <= 3.4028234663852886e38f))
-                o[d] = NAN;
-            } else {
-              const float x = bf16_bits_to_f32(__ldcg(static_cast<const uint16_t*>(kv.v) + at + d));
-              if (!(fabsf(x) <= 3.4028234663852886e38f)) o[d] += x;
-            }
-          }
+        const uint3 x = not_finite<D, FP8>(kv, w.b, w.j, max(rlo, w.k0 * kKeys),
+                                           min(rhi, w.k1 * kKeys), w.all_lo, w.all_hi, holes, d0);
+#pragma unroll
+        for (int d = 0; d < 32; ++d) {
+          if ((x.x >> d) & 1u) o[d] += INFINITY;
+          if ((x.y >> d) & 1u) o[d] -= INFINITY;
+          if ((x.z >> d) & 1u) o[d] = NAN;
         }
       };
       auto store = [&](const float* o, int c, float inv) {  // 32 dims from 32 c on

@@ -5,12 +5,12 @@ import math
 import numpy as np
 import pytest
 
-from bit_weight_only_mxfp4_gb300 import synth
+from bit_weight_only_mxfp4_gb300 import synth, thinmx
 
 from . import gpu_util as gu
 from . import paged_ref as ref
 from .parity import bf16_to_f64
-from .test_gpu_paged import DECODE_EPS, PREFILL_EPS, WID, _attend, _handle
+from .test_gpu_paged import DECODE_EPS, PREFILL_EPS, WID, _attend, _handle, _workspace
 
 pytestmark = pytest.mark.gpu
 
@@ -218,3 +218,69 @@ def test_caps_that_bend_the_scores(cap, fp8):
         q = _queries(210, tokens, 16, 128)
         got = _attend(_handle(c), q, starts, 0.25, softcap=cap)
         ref.check_attention(*got, ref.attention(c, q, starts, 0.25, softcap=cap), eps, f"cap {cap}")
+
+
+# ---------------------------------------------------------------------------------- what a value that is not finite costs
+@pytest.mark.parametrize("fp8", [False, True])
+def test_prefill_one_value_not_finite_costs_little(fp8):
+    """One NaN in a tile that the mask cuts, behind a long past and with a length that ends inside a page: only the
+    tiles that were cleaned are read again.  (Read again whole, the past takes a hundred times the call.)"""
+    import torch
+    heads, kvh, d, new, past = 16, 4, 128, 2500, 17003
+    n = new + past
+    c = ref.Cache(211, [n], kvh, d, 64, fp8, junk=False)
+    kv = _handle(c)
+    g = torch.Generator(device="cuda").manual_seed(1)
+    q = torch.randn((new, heads, d), generator=g, device="cuda").bfloat16()
+    out = torch.empty_like(q)
+    starts = torch.tensor([0, new], dtype=torch.int32, device="cuda")
+    ws = _workspace(heads, kvh, d)
+
+    def call():
+        thinmx.tt_paged_prefill_attention(kv, q, heads * d, starts, new, heads, 0.088, 0.0, 0, None, None, None, out, None,
+                                          ws[0], ws[1])
+
+    def best():
+        call()
+        times = []
+        for _ in range(5):
+            a, b = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+            a.record()
+            call()
+            b.record()
+            b.synchronize()
+            times.append(a.elapsed_time(b))
+        return min(times)
+
+    clean, want = best(), out.clone()
+    t = past + 1201
+    kv.tensors[1][int(c.table[0, t // 64]), 2, t % 64, 17] = 0x7F if fp8 else 0x7FC0
+    dirty = best()
+    hit = torch.zeros_like(out, dtype=torch.bool)
+    hit[t - past:, 8:12, 17] = True
+    assert torch.equal(~torch.isfinite(out), hit)
+    assert torch.equal(out[~hit], want[~hit])
+    assert gu.device_error() == 0
+    assert dirty <= 3 * clean, f"{clean:.3f} ms clean, {dirty:.3f} ms with one NaN"
+
+
+def test_prefill_values_not_finite_between_holes():
+    """Holes in tiles that the mask does not cut: values that are not finite are found in those tiles, too."""
+    heads, kvh, d, n, new = 16, 4, 128, 1500, 100
+    c, clean = (ref.Cache(212, [n], kvh, d, 16, False, junk=False) for _ in range(2))
+    for x in (c, clean):
+        x.table[0, [3, 20, 21, 60]] = -1  # tokens 48.., 320.., 960..
+    at = (40, 330 + 30, 600, 975 + 20, 1450)  # beside holes, in a whole tile, and in a cut one
+    for i, t in enumerate(at):
+        c.v[c.table[0, t // 16], 1, t % 16, 7 + i] = 0x7F80 if i % 2 else 0x7FC0
+    starts = np.array([0, new], np.int32)
+    q = _queries(212, new, heads, d)
+    got, want = (bf16_to_f64(_attend(_handle(x), q, starts, 0.125)[0]).reshape(new, heads, d) for x in (c, clean))
+    hit = np.zeros((new, heads, d), bool)
+    p = np.arange(n - new, n)
+    for i, t in enumerate(at):
+        hit[p >= t, 4:8, 7 + i] = True
+        x = got[p >= t, 4:8, 7 + i]
+        assert np.isposinf(x).all() if i % 2 else np.isnan(x).all()
+    assert np.array_equal(~np.isfinite(got), hit)
+    assert np.array_equal(got[~hit], want[~hit])
