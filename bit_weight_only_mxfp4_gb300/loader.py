@@ -65,14 +65,17 @@ def moe_expert_from_f32(w_gate_up: torch.Tensor, w_down: torch.Tensor):
 def paged_kv(k: torch.Tensor, v: torch.Tensor, page_table: torch.Tensor, lens: torch.Tensor,
              k_scales: torch.Tensor | None = None, v_scales: torch.Tensor | None = None):
     """The cache description the paged entry points take: k, v
-    [pages, kv_heads, page_size, head_dim] in bf16, or in float8_e4m3fn / uint8
-    codes with fp32 scales [pages, kv_heads, page_size]; page_table int32
+    [pages, kv_heads, page_size, head_dim] in bf16 (or its bits in int16 /
+    uint16), or in float8_e4m3fn (or its codes in uint8 / int8) with fp32 scales
+    [pages, kv_heads, page_size]; page_table int32
     [batch, pages_per_seq]; lens int32 [batch].  It keeps its tensors alive;
     it is made once, and later steps write into page_table and lens."""
     fp8 = k_scales is not None
     for t in (k, v, page_table, lens, k_scales, v_scales):
         assert t is None or (t.is_cuda and t.is_contiguous())
-    assert k.shape == v.shape and k.dtype == v.dtype and k.element_size() == (1 if fp8 else 2)
+    assert k.shape == v.shape and k.dtype == v.dtype
+    assert k.dtype in ((torch.float8_e4m3fn, torch.uint8, torch.int8) if fp8 else
+                       (torch.bfloat16, torch.int16, torch.uint16))
     assert (v_scales is not None) == fp8
     pages, kv_heads, page_size, head_dim = k.shape
     assert page_table.dtype == lens.dtype == torch.int32

@@ -284,3 +284,23 @@ def test_prefill_values_not_finite_between_holes():
         assert np.isposinf(x).all() if i % 2 else np.isnan(x).all()
     assert np.array_equal(~np.isfinite(got), hit)
     assert np.array_equal(got[~hit], want[~hit])
+
+
+# ----------------------------------------------------------------------------------------------------------------- types
+def test_caches_of_other_types_are_refused():
+    import torch
+    from bit_weight_only_mxfp4_gb300 import loader
+    table, lens = (torch.zeros(s, dtype=torch.int32, device="cuda") for s in ((2, 4), (2,)))
+    scales = torch.ones((8, 2, 16), device="cuda")
+
+    def make(dtype, s=None):
+        x = torch.zeros((8, 2, 16, 64), dtype=dtype, device="cuda")
+        return loader.paged_kv(x, x.clone(), table, lens, s, s)
+
+    make(torch.bfloat16)
+    make(torch.float8_e4m3fn, scales)
+    make(torch.uint8, scales)
+    for dtype, s in ((torch.float16, None), (torch.float8_e5m2, scales), (torch.float8_e4m3fn, None),
+                     (torch.bfloat16, scales), (torch.float32, None)):
+        with pytest.raises(AssertionError):
+            make(dtype, s)
