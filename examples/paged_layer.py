@@ -111,11 +111,17 @@ def serve(fp8=False, steps=16, lens=(37, 5, 130)):
     cache = Cache(layer, most, fp8=fp8)
     prompt(layer, cache, [x[:n] for x, n in zip(xs, lens)])
     x, work = torch.zeros((len(lens), layer.hidden), dtype=torch.bfloat16, device="cuda"), layer.work(len(lens))
+
+    def step():
+        cache.lens += 1
+        layer(cache, x, None, work)
+
+    step()  # a call may be captured once it has been made
+    cache.lens -= 1  # (the row that it wrote is the next one to be written)
     graph = torch.cuda.CUDAGraph()
     torch.cuda.synchronize()
     with torch.cuda.graph(graph):
-        cache.lens += 1
-        layer(cache, x, None, work)
+        step()
     rows = []
     for i in range(steps):
         x.copy_(torch.stack([s[n + i] for s, n in zip(xs, lens)]))
