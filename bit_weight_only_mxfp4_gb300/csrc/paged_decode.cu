@@ -23,10 +23,10 @@
 // boundaries, so the copies run on while a pair is finished.  (One TMA box per
 // page and matrix costs as much for a page of 1 KB as for one of 16: the FP8
 // batch below took 308 us that way; four warps that share every tile 134 to 140,
-// whole tiles each 117.)  Two groups of four warps take the tiles in turn, 16
+// whole tiles each 117, before the units of the weights were a head's.)  Two groups of four warps take the tiles in turn, 16
 // (or 2 x 16) tokens a warp, each with its own running maximum, sum and output;
 // a pair's end joins them in shared memory.  (Four groups, with half the
-// registers each: 137 us where two take 117.)
+// registers each: 137 us where two took 117.)
 //
 // Products, on mma.sync m16n8k16 with the tokens (or dims) as the 16 rows and
 // the heads as the 8 columns, so that up to 8 heads fill it:
@@ -53,12 +53,12 @@
 //     shrinks with the old weights and O stays as it is.
 //
 // Measured (back to back in a graph): 64 ragged sequences up to 16384 tokens,
-// 64 / 8 heads of 64, FP8 pages of 16: 116 us, 4.8 TB/s (without the products
-// 100: issue slots are 48% busy, copies and products share them); 32 up to 8192,
-// 16 / 4 heads of 128, bf16: 46.7 us, 5.4 TB/s (without the products 43.8); one
-// of 32768 tokens, 64 / 8 heads of 64, bf16: 18.2 us, of which 5 until the first
+// 64 / 8 heads of 64, FP8 pages of 16: 113 us, 4.9 TB/s (without the products
+// 100: issue slots are 47% busy, copies and products share them); 32 up to 8192,
+// 16 / 4 heads of 128, bf16: 47 us, 5.4 TB/s (without the products 43.8); one
+// of 32768 tokens, 64 / 8 heads of 64, bf16: 18.3 us, of which 5 until the first
 // tile (lengths, table, page: three dependent loads) and 4 to write and join
-// the parts; one of 333 tokens 7.3 us.  The slowest CTA ends 10% after the mean.
+// the parts; one of 333 tokens 7.7 us.  The slowest CTA ends 11% after the mean.
 #include <cmath>
 #include <type_traits>
 
@@ -85,7 +85,7 @@ struct Plan {
   static constexpr int kConsumers = kGroups * kGroupWarps * 32;
   static constexpr int kThreads = kConsumers + kCopiers;
   // registers a thread: 65,536 less the copying warps' share
-  // (40: FP8 batch 128 us, 56: 117.5, 72: 115.5, 88: 118.5)
+  // (40: FP8 batch 125 us, 56: 114.8, 72: 113.2, 88: 116.2)
   static constexpr int kCopyRegs = 72;
   static constexpr int kLaunchRegs = 65536 / kThreads / 8 * 8;
   static constexpr int kRegs = (kLaunchRegs * kThreads - kCopyRegs * kCopiers) / kConsumers / 8 * 8;

@@ -48,16 +48,21 @@
 // -> 384 us).  What the lengths are is read on the device.
 //
 // Measured (back to back in a graph): 8192 tokens, 16 / 4 heads of 128, all of a
-// prefix of 7411 seen: 370 us, 1.35 PFLOP/s; 8192 causal tokens, 64 / 8 heads of
-// 64: 693 us, 0.79 PFLOP/s (a token and row cost the same exponential and half
-// the products); over FP8 pages 0.52 PFLOP/s; four ragged chunks of 120 tokens
-// 21.7 us.  What bounds it: with 128 dims the chain S, softmax, P V, next S of a
-// row tile, of which the other tile's covers a part (products alone, with the
-// same handshakes, take 172 us where the kernel takes 214); with 64 dims the
-// softmax warps' own time (two thirds of a tile's 3000 cycles).  FP8: the
-// softmax threads read 256 scales a tile and row from shared memory, six warps
-// convert 2 x 128 rows a tile, and both share the issue slots (58% busy).
-// Exponentials left out (to see) change 0 with 128 dims and 7% with 64.
+// prefix of 7411 seen: 374 us, 1.34 PFLOP/s; 8192 causal tokens 218, and of 64 / 8
+// heads of 64 699 us, 0.79 PFLOP/s (a token and row cost the same exponential and
+// half the products), over FP8 pages 384 and 1019; three chunks over FP8 pages 735,
+// 0.52 PFLOP/s; four ragged chunks of 120 tokens 21.9 us.  What bounds it: with 128
+// dims the chain S, softmax, P V, next S of a row tile, of which the other tile's
+// covers a part (products alone, with the same handshakes, take 172 us where the
+// kernel takes 218); with 64 dims the softmax warps' own time (two thirds of a
+// tile's 3000 cycles), which is latency: two warps a scheduler, each with a serial
+// run over 128 scores, leave the issue slots half empty (47% busy; tensor pipe and
+// special functions 34%).  FP8: the softmax threads read 256 scales a tile and row
+// from shared memory, six warps convert 2 x 128 rows a tile, and both share the
+// issue slots (59% busy).  Exponentials left out (to see) change 0 with 128 dims
+// and 7% with 64.  Registers spilled a thread: 156 bytes (bf16, 128 dims; with a
+// cap or bias up to 224), 312 to 372 (FP8, 128 dims), 136 to 196 (FP8, 64), 0 to 36
+// (bf16, 64).
 #include <cmath>
 #include <type_traits>
 
@@ -927,7 +932,7 @@ __global__ void __launch_bounds__(Plan<D, FP8>::kThreads, 1)
               const bool sure = !cut && got == whole;
               bool bad = false;
               constexpr int kC = D / 16;  // 16-byte pieces of a raw row
-constexpr int kIlp = 4;  // pieces in work at once
+              constexpr int kIlp = 4;  // pieces in work at once
 #pragma unroll 1
               for (int i0 = 0; i0 < kKeys * kC; i0 += kIlp * kFixers) {
                 uint4 x4[kIlp];

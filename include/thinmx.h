@@ -521,6 +521,8 @@ tt_status tt_paged_decode_attention(const tt_paged_kv* kv, const uint16_t* q, in
 /* The same for the new tokens of q_starts (required): each sees the keys
  * t <= p, and also t < prefix[b] (int32 [batch] or NULL: the part of a
  * sequence that its tokens see whole), t < lens[b], within the window.
+ * The bias is slopes[h] * (t - p) there, too: positive for the keys ahead.
+ * Requires tokens * heads < 2^31 (else TT_ERR_SHAPE).
  * q rows at token * q_stride; out [tokens][heads][head_dim], lse
  * [tokens][heads].  A token with p < 0 sees nothing. */
 tt_status tt_paged_prefill_attention(const tt_paged_kv* kv, const uint16_t* q, int64_t q_stride,
