@@ -67,11 +67,12 @@ __device__ __forceinline__ float rcp(float x) {
 // x = s / c and y = 2 x log2 e, tanh x = 1 - 2 / (1 + 2^y); 2^y may be infinite,
 // its reciprocal is then 0.  That is off by about c 2^-22 absolutely, which is
 // what counts in the exponent, also where s is far below c.  Caps above
-// kCapSmall (2^-14 there, against the 2^-9 and 2^-12 of weights rounded to bf16
+// kCapSmall (2^-14 there, against the 2^-8 and 2^-11 of weights rounded to bf16
 // and f16) have kernels of their own: they take it from |y| = kCapSeries
 // (|x| = 0.25) on only, and below it
 //   s (1 - x^2 / 3 + 2 x^4 / 15 - 17 x^6 / 315 + 62 x^8 / 2835)
-// whose next term is below 2^-26: off by a few 2^-24 of s.  Measured with a cap
+// whose next term is below 2^-26: off by a few 2^-24 of s, and by 2^-19 of it at
+// most beyond.  Measured with a cap
 // of 50 / 500: 8192 prompt tokens, 16 / 4 heads of 128, all of a prefix of 7411
 // seen, 765 / 774 us; the FP8 decode batch of 64 122.6 / 141.  (Both forms in one
 // kernel: 890 / 915 and 126 / 144, and that batch without a cap 116 for 113.)

@@ -497,7 +497,7 @@ tt_status tt_paged_rope_append(const tt_paged_kv* kv, const uint16_t* q, const u
  *   (t <= p; t > p - window if window > 0; no hole):
  *   z[h][t] = f(scale * q[b][h] . k[j][t]) + slopes[h] * (t - p),
  *             f(s) = softcap * tanh(s / softcap) if softcap > 0, else s
- *             (off by 2^-21 of softcap up to 256, of |s| above)
+ *             (off by 2^-21 of softcap up to 256, by 2^-19 of |s| above)
  *   out[b][h] = bf16_rne( sum_t e^z v[j][t] / (sum_t e^z + e^sinks[h]) )
  *   lse[b][h] = log(sum_t e^z + e^sinks[h])
  * slopes, sinks: fp32 [heads] or NULL (no bias; no sink).  A head without a
