@@ -89,6 +89,7 @@ inline cudaStream_t as_stream(void* s) { return static_cast<cudaStream_t>(s); }
 
 constexpr int64_t kMaxRows = (int64_t(1) << 31) - 1;
 constexpr int64_t kMaxK = 16384;
+constexpr int64_t kMaxVocab = int64_t(1) << 30;
 constexpr int64_t kTcMinBatch = 4;  // smallest m sent to the tensor-core path
 constexpr int64_t kMoeMaxHidden = 8192;
 static_assert(TT_MOE_STATIC_MAX_HIDDEN == tt::kMoeStaticMaxHidden,
@@ -456,8 +457,12 @@ tt_status check_paged_kv(const tt_paged_kv* kv, tt::PagedKv* out) {
   return TT_OK;
 }
 
+size_t attention_workspace(const tt_paged_kv* kv, int32_t heads) {
+  return kv ? tt_paged_attention_workspace_bytes(heads, kv->kv_heads, kv->head_dim) : 0;
+}
+
 tt_status check_paged_attention(const tt_paged_kv* kv, const tt::PagedAttnArgs& a,
-                                size_t ws_bytes, tt::PagedKv* out) {
+                                size_t ws_bytes, size_t ws_need, tt::PagedKv* out) {
   if (tt_status st = check_paged_kv(kv, out)) return st;
   if (a.heads < 1 || a.heads % kv->kv_heads != 0) return TT_ERR_SHAPE;
   if (a.heads / kv->kv_heads > tt::kPagedMaxGroup) return TT_ERR_UNSUPPORTED;
@@ -466,8 +471,7 @@ tt_status check_paged_attention(const tt_paged_kv* kv, const tt::PagedAttnArgs& 
   if (a.q_stride % 8 != 0 || a.q_stride < int64_t(a.heads) * kv->head_dim) return TT_ERR_SHAPE;
   if (a.tokens < 0 || a.tokens > kMaxRows / a.heads) return TT_ERR_SHAPE;
   if (!a.q || !a.out || !a.ws) return TT_ERR_NULL;
-  if (ws_bytes < tt_paged_attention_workspace_bytes(a.heads, kv->kv_heads, kv->head_dim))
-    return TT_ERR_SIZE;
+  if (ws_bytes < ws_need) return TT_ERR_SIZE;
   if (!aligned(a.q, 16) || !aligned(a.out, 16) || !aligned(a.ws, 16) || !aligned(a.lse, 4) ||
       !aligned(a.slopes, 4) || !aligned(a.sinks, 4) || !aligned(a.prefix, 4) ||
       !aligned(a.starts, 4))
@@ -529,7 +533,8 @@ tt_status tt_paged_decode_attention(const tt_paged_kv* kv, const uint16_t* q, in
   const tt::PagedAttnArgs a{q,      q_stride, nullptr, kv ? kv->batch : 0, heads, scale, softcap,
                             window, slopes,   sinks,   nullptr,            out,   lse,   workspace};
   tt::PagedKv c;
-  if (tt_status st = check_paged_attention(kv, a, workspace_bytes, &c)) return st;
+  if (tt_status st = check_paged_attention(kv, a, workspace_bytes, attention_workspace(kv, heads), &c))
+    return st;
   // tiles of all sequences and kv heads (of at least 64 tokens) are counted in 32 bits
   const int64_t tiles = ((int64_t(kv->pages_per_seq) * kv->page_size + 63) / 64) * kv->batch;
   if (tiles > kMaxRows / kv->kv_heads) return TT_ERR_UNSUPPORTED;
@@ -546,11 +551,200 @@ tt_status tt_paged_prefill_attention(const tt_paged_kv* kv, const uint16_t* q, i
   const tt::PagedAttnArgs a{q,      q_stride, q_starts, tokens, heads, scale, softcap,
                             window, slopes,   sinks,    prefix, out,   lse,   workspace};
   tt::PagedKv c;
-  if (tt_status st = check_paged_attention(kv, a, workspace_bytes, &c)) return st;
+  if (tt_status st = check_paged_attention(kv, a, workspace_bytes, attention_workspace(kv, heads), &c))
+    return st;
   if (!q_starts) return TT_ERR_NULL;
   if (tokens == 0) return TT_OK;
   return from_cuda(tt::launch_paged_prefill(c, kv->head_dim, kv->type == TT_KV_FP8, a,
                                             as_stream(stream), kPdl));
+}
+
+namespace {
+
+// Checks the descriptions of several layers' caches: all as the first, but for
+// their pools.
+tt_status check_paged_layers(const tt_paged_kv* layers, int32_t n, tt::PagedKv* out,
+                             tt::PagedPools* pools) {
+  if (n < 1 || n > tt::kMaxLayers) return TT_ERR_SHAPE;
+  if (!layers) return TT_ERR_NULL;
+  for (int i = n - 1; i >= 0; --i) {
+    const tt_paged_kv& l = layers[i];
+    const tt_paged_kv& f = layers[0];
+    if (tt_status st = check_paged_kv(&l, out)) return st;
+    if (l.page_table != f.page_table || l.lens != f.lens || l.num_pages != f.num_pages ||
+        l.type != f.type || l.page_size != f.page_size || l.kv_heads != f.kv_heads ||
+        l.head_dim != f.head_dim || l.batch != f.batch || l.pages_per_seq != f.pages_per_seq)
+      return TT_ERR_SHAPE;
+    pools->k[i] = l.k;
+    pools->v[i] = l.v;
+    pools->k_scales[i] = l.k_scales;
+    pools->v_scales[i] = l.v_scales;
+  }
+  pools->layers = n;
+  return TT_OK;
+}
+
+// What the calls that write the table share.
+tt_status check_pages(const tt_paged_kv& kv, const int32_t* table_out, const int32_t* count,
+                      const void* ws, size_t ws_bytes) {
+  if (!table_out || !ws) return TT_ERR_NULL;
+  if (ws_bytes < tt_paged_pages_workspace_bytes(&kv)) return TT_ERR_SIZE;
+  if (!aligned(table_out, 4) || !aligned(count, 4) || !aligned(ws, 16)) return TT_ERR_ALIGN;
+  return TT_OK;
+}
+
+}  // namespace
+
+tt_status tt_draft_tree(const int32_t* parents, const int32_t* q_starts, const int32_t* lens,
+                        int32_t batch, int64_t tokens, int32_t mask_words, uint32_t* masks,
+                        int32_t* positions, void* stream) {
+  if (batch < 1 || tokens < 0 || tokens > kMaxRows || mask_words < 1) return TT_ERR_SHAPE;
+  if (batch > tt::kPagedMaxBatch || mask_words > tt::kMaxMaskWords) return TT_ERR_UNSUPPORTED;
+  if (!parents || !q_starts || !lens || !masks || !positions) return TT_ERR_NULL;
+  if (!aligned(parents, 4) || !aligned(q_starts, 4) || !aligned(lens, 4) || !aligned(masks, 4) ||
+      !aligned(positions, 4))
+    return TT_ERR_ALIGN;
+  if (tokens == 0) return TT_OK;
+  return from_cuda(tt::launch_draft_tree(parents, q_starts, lens, batch, tokens, mask_words, masks,
+                                         positions, as_stream(stream), kPdl));
+}
+
+size_t tt_paged_tree_workspace_bytes(int32_t heads, int32_t kv_heads, int32_t head_dim) {
+  if (heads < 1 || kv_heads < 1 || heads % kv_heads != 0) return 0;
+  if (head_dim != 64 && head_dim != 128) return 0;
+  if (heads / kv_heads > tt::kPagedMaxGroup || kv_heads > tt::kGqaMaxKvHeads) return 0;
+  return tt::paged_tree_workspace_bytes(head_dim);
+}
+
+tt_status tt_paged_tree_attention(const tt_paged_kv* kv, const uint16_t* q, int64_t q_stride,
+                                  const int32_t* q_starts, int64_t tokens, int32_t heads,
+                                  float scale, float softcap, int32_t window,
+                                  const float* slopes, const float* sinks, const uint32_t* masks,
+                                  int32_t mask_words, uint16_t* out, float* lse, void* workspace,
+                                  size_t workspace_bytes, void* stream) {
+  const tt::TreeArgs a{{q, q_stride, q_starts, tokens, heads, scale, softcap, window, slopes, sinks,
+                        nullptr, out, lse, workspace},
+                       masks, mask_words};
+  tt::PagedKv c;
+  if (tt_status st = check_paged_attention(
+          kv, a.attn, workspace_bytes,
+          kv ? tt_paged_tree_workspace_bytes(heads, kv->kv_heads, kv->head_dim) : 0, &c))
+    return st;
+  if (mask_words < 1) return TT_ERR_SHAPE;
+  if (mask_words > tt::kMaxMaskWords) return TT_ERR_UNSUPPORTED;
+  if (!q_starts || !masks) return TT_ERR_NULL;
+  if (!aligned(masks, 4)) return TT_ERR_ALIGN;
+  if (tokens == 0) return TT_OK;
+  return from_cuda(
+      tt::launch_paged_tree(c, kv->head_dim, kv->type == TT_KV_FP8, a, as_stream(stream), kPdl));
+}
+
+tt_status tt_draft_accept(const int32_t* parents, const int32_t* drafts, const int32_t* chosen,
+                          const int32_t* q_starts, int32_t batch, int64_t tokens,
+                          int32_t path_width, int32_t* path, int32_t* counts, int32_t* next,
+                          void* stream) {
+  if (batch < 1 || tokens < 0 || tokens > kMaxRows || path_width < 1) return TT_ERR_SHAPE;
+  if (batch > tt::kPagedMaxBatch) return TT_ERR_UNSUPPORTED;
+  if (!q_starts || !path || !counts || !next) return TT_ERR_NULL;
+  if (tokens > 0 && (!parents || !drafts || !chosen)) return TT_ERR_NULL;
+  if (!aligned(parents, 4) || !aligned(drafts, 4) || !aligned(chosen, 4) || !aligned(q_starts, 4) ||
+      !aligned(path, 4) || !aligned(counts, 4) || !aligned(next, 4))
+    return TT_ERR_ALIGN;
+  return from_cuda(tt::launch_draft_accept(parents, drafts, chosen, q_starts, batch, tokens,
+                                           path_width, path, counts, next, as_stream(stream),
+                                           kPdl));
+}
+
+tt_status tt_paged_keep(const tt_paged_kv* layers, int32_t n_layers, const int32_t* q_starts,
+                        const int32_t* path, int32_t path_width, const int32_t* counts,
+                        int32_t* lens_out, void* stream) {
+  tt::PagedKv c;
+  tt::PagedPools pools;
+  if (tt_status st = check_paged_layers(layers, n_layers, &c, &pools)) return st;
+  if (path_width < 1) return TT_ERR_SHAPE;
+  if (!q_starts || !path || !counts || !lens_out) return TT_ERR_NULL;
+  if (!aligned(q_starts, 4) || !aligned(path, 4) || !aligned(counts, 4) || !aligned(lens_out, 4))
+    return TT_ERR_ALIGN;
+  return from_cuda(tt::launch_paged_keep(c, pools, layers->head_dim, layers->type == TT_KV_FP8,
+                                         q_starts, path, path_width, counts, lens_out,
+                                         as_stream(stream), kPdl));
+}
+
+size_t tt_paged_pages_workspace_bytes(const tt_paged_kv* kv) {
+  tt::PagedKv c;
+  if (check_paged_kv(kv, &c) != TT_OK) return 0;
+  return tt::paged_pages_workspace_bytes(kv->num_pages, kv->batch, kv->pages_per_seq);
+}
+
+tt_status tt_paged_resize(const tt_paged_kv* kv, const int32_t* want, const uint8_t* held,
+                          int32_t* table_out, int32_t* lens_out, int32_t* left, void* workspace,
+                          size_t workspace_bytes, void* stream) {
+  tt::PagedKv c;
+  if (tt_status st = check_paged_kv(kv, &c)) return st;
+  if (!want || !lens_out) return TT_ERR_NULL;
+  if (!aligned(want, 4) || !aligned(lens_out, 4)) return TT_ERR_ALIGN;
+  if (tt_status st = check_pages(*kv, table_out, left, workspace, workspace_bytes)) return st;
+  return from_cuda(tt::launch_paged_resize(c, want, held, table_out, lens_out, left, workspace,
+                                           as_stream(stream), kPdl));
+}
+
+tt_status tt_paged_fork(const tt_paged_kv* layers, int32_t n_layers, const int32_t* from,
+                        const uint8_t* held, int32_t* table_out, int32_t* lens_out,
+                        int32_t* left, void* workspace, size_t workspace_bytes, void* stream) {
+  tt::PagedKv c;
+  tt::PagedPools pools;
+  if (tt_status st = check_paged_layers(layers, n_layers, &c, &pools)) return st;
+  if (!from || !lens_out) return TT_ERR_NULL;
+  if (!aligned(from, 4) || !aligned(lens_out, 4)) return TT_ERR_ALIGN;
+  if (tt_status st = check_pages(*layers, table_out, left, workspace, workspace_bytes)) return st;
+  return from_cuda(tt::launch_paged_fork(c, pools, layers->head_dim, layers->type == TT_KV_FP8,
+                                         from, held, table_out, lens_out, left, workspace,
+                                         as_stream(stream), kPdl));
+}
+
+tt_status tt_paged_compact(const tt_paged_kv* layers, int32_t n_layers, const uint8_t* held,
+                           int32_t* table_out, int32_t* span, void* workspace,
+                           size_t workspace_bytes, void* stream) {
+  tt::PagedKv c;
+  tt::PagedPools pools;
+  if (tt_status st = check_paged_layers(layers, n_layers, &c, &pools)) return st;
+  if (tt_status st = check_pages(*layers, table_out, span, workspace, workspace_bytes)) return st;
+  return from_cuda(tt::launch_paged_compact(c, pools, layers->head_dim, layers->type == TT_KV_FP8,
+                                            held, table_out, span, workspace, as_stream(stream),
+                                            kPdl));
+}
+
+size_t tt_token_logprobs_workspace_bytes(int64_t rows, int64_t vocab, int32_t top_k) {
+  if (rows < 1 || vocab < 1 || vocab > kMaxVocab || top_k < 0 || top_k > tt::kMaxTop) return 0;
+  return tt::token_logprobs_workspace_bytes(rows, vocab, top_k);
+}
+
+tt_status tt_token_logprobs(const void* logits, int32_t type, int64_t rows, int64_t vocab,
+                            int64_t stride, float scale, const int32_t* targets, int32_t top_k,
+                            float* logp, float* entropy, int32_t* top_ids, float* top_logp,
+                            void* workspace, size_t workspace_bytes, void* stream) {
+  if (type != TT_LOGITS_F32 && type != TT_LOGITS_BF16) return TT_ERR_SHAPE;
+  if (rows < 0 || rows > kMaxRows || vocab < 1 || stride < vocab) return TT_ERR_SHAPE;
+  if (vocab > kMaxVocab || stride > kMaxRows) return TT_ERR_UNSUPPORTED;
+  if (top_k < 0 || top_k > vocab) return TT_ERR_SHAPE;
+  if (top_k > tt::kMaxTop) return TT_ERR_UNSUPPORTED;
+  if (!std::isfinite(scale)) return TT_ERR_NONFINITE;
+  if (!(scale > 0.f)) return TT_ERR_SHAPE;
+  if (!targets && logp) return TT_ERR_NULL;
+  if (top_k == 0 && (top_ids || top_logp)) top_ids = nullptr, top_logp = nullptr;
+  if (rows == 0) return TT_OK;
+  if (!logits || (top_k > 0 && !top_ids)) return TT_ERR_NULL;
+  const size_t need = tt_token_logprobs_workspace_bytes(rows, vocab, top_k);
+  if (need > 0 && !workspace) return TT_ERR_NULL;
+  if (workspace_bytes < need) return TT_ERR_SIZE;
+  if (!aligned(logits, type == TT_LOGITS_F32 ? 4 : 2) || !aligned(targets, 4) ||
+      !aligned(logp, 4) || !aligned(entropy, 4) || !aligned(top_ids, 4) || !aligned(top_logp, 4) ||
+      !aligned(workspace, 16))
+    return TT_ERR_ALIGN;
+  const tt::LogprobArgs a{logits, rows,    vocab,   stride,   scale,    targets,
+                          top_k,  logp,    entropy, top_ids,  top_logp, workspace};
+  return from_cuda(
+      tt::launch_token_logprobs(a, type == TT_LOGITS_BF16, as_stream(stream), kPdl));
 }
 
 size_t tt_lowbit_matrix_bytes(int32_t bits, int64_t n, int64_t k) {

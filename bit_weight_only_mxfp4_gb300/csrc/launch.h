@@ -122,6 +122,23 @@ cudaError_t launch_moe_lowbit(int bits, const uint16_t* x, int hidden, int inter
                               const uint8_t* const* dn, uint16_t* out, int32_t* out_idx,
                               float* out_prob, void* ws, cudaStream_t s, bool pdl);
 
+// logprobs.cu
+constexpr int kMaxTop = 32;  // TT_LOGPROBS_MAX_TOP
+struct LogprobArgs {
+  const void* logits;
+  int64_t rows, vocab, stride;
+  float scale;
+  const int32_t* targets;
+  int top;
+  float* logp;
+  float* entropy;
+  int32_t* top_ids;
+  float* top_logp;
+  void* ws;
+};
+size_t token_logprobs_workspace_bytes(int64_t rows, int64_t vocab, int top);
+cudaError_t launch_token_logprobs(const LogprobArgs& a, bool bf16, cudaStream_t s, bool pdl);
+
 // gemv_bf16.cu
 cudaError_t launch_swiglu_bf16(const uint16_t* wg, const uint16_t* wu, int n, int k,
                                const uint16_t* x, int m, uint16_t* h, cudaStream_t s, bool pdl);

@@ -93,6 +93,15 @@ def paged_kv(k: torch.Tensor, v: torch.Tensor, page_table: torch.Tensor, lens: t
     return kv
 
 
+def paged_layers(kvs):
+    """The caches of several layers (paged_kv, over one page_table and one lens) as
+    the array that tt_paged_keep, tt_paged_fork and tt_paged_compact take.  It keeps
+    their tensors alive."""
+    layers = (thinmx.tt_paged_kv * len(kvs))(*kvs)
+    layers.tensors = [getattr(kv, "tensors", None) for kv in kvs]
+    return layers
+
+
 def rope_turns(inv_freq: torch.Tensor) -> torch.Tensor:
     """Rotation frequencies, fp64 [n] in radians per position -> the table
     tt_paged_rope_append takes."""

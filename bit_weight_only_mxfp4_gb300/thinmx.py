@@ -73,11 +73,27 @@ SIGNATURES = {
     "tt_paged_prefill_attention": (ctypes.c_int, [_P, _P, _I64, _P, _I64, _I32, ctypes.c_float,
                                                    ctypes.c_float, _I32, _P, _P, _P, _P, _P, _P,
                                                    _SZ, _P]),
+    "tt_draft_tree": (ctypes.c_int, [_P, _P, _P, _I32, _I64, _I32, _P, _P, _P]),
+    "tt_paged_tree_workspace_bytes": (_SZ, [_I32, _I32, _I32]),
+    "tt_paged_tree_attention": (ctypes.c_int, [_P, _P, _I64, _P, _I64, _I32, ctypes.c_float,
+                                                ctypes.c_float, _I32, _P, _P, _P, _I32, _P, _P, _P,
+                                                _SZ, _P]),
+    "tt_draft_accept": (ctypes.c_int, [_P, _P, _P, _P, _I32, _I64, _I32, _P, _P, _P, _P]),
+    "tt_paged_keep": (ctypes.c_int, [_P, _I32, _P, _P, _I32, _P, _P, _P]),
+    "tt_paged_pages_workspace_bytes": (_SZ, [_P]),
+    "tt_paged_resize": (ctypes.c_int, [_P, _P, _P, _P, _P, _P, _P, _SZ, _P]),
+    "tt_paged_fork": (ctypes.c_int, [_P, _I32, _P, _P, _P, _P, _P, _P, _SZ, _P]),
+    "tt_paged_compact": (ctypes.c_int, [_P, _I32, _P, _P, _P, _P, _SZ, _P]),
+    "tt_token_logprobs_workspace_bytes": (_SZ, [_I64, _I64, _I32]),
+    "tt_token_logprobs": (ctypes.c_int, [_P, _I32, _I64, _I64, _I64, ctypes.c_float, _P, _I32, _P,
+                                          _P, _P, _P, _P, _SZ, _P]),
 }
 
 
 TT_KV_BF16 = 0
 TT_KV_FP8 = 1
+TT_LOGITS_F32 = 0
+TT_LOGITS_BF16 = 1
 
 
 class tt_paged_kv(ctypes.Structure):
@@ -322,6 +338,77 @@ def tt_paged_prefill_attention(kv, q, q_stride, q_starts, tokens, heads, scale, 
         _kv(kv), _ptr(q), q_stride, _ptr(q_starts), tokens, heads, scale, softcap, window,
         _ptr(slopes), _ptr(sinks), _ptr(prefix), _ptr(out), _ptr(lse), _ptr(workspace),
         workspace_bytes, _stream(stream)))
+
+
+def tt_draft_tree(parents, q_starts, lens, batch, tokens, mask_words, masks, positions,
+                  stream=None):
+    _check("tt_draft_tree", load().tt_draft_tree(
+        _ptr(parents), _ptr(q_starts), _ptr(lens), batch, tokens, mask_words, _ptr(masks),
+        _ptr(positions), _stream(stream)))
+
+
+def tt_paged_tree_workspace_bytes(heads, kv_heads, head_dim) -> int:
+    return int(load().tt_paged_tree_workspace_bytes(heads, kv_heads, head_dim))
+
+
+def tt_paged_tree_attention(kv, q, q_stride, q_starts, tokens, heads, scale, softcap, window,
+                            slopes, sinks, masks, mask_words, out, lse, workspace,
+                            workspace_bytes, stream=None):
+    _check("tt_paged_tree_attention", load().tt_paged_tree_attention(
+        _kv(kv), _ptr(q), q_stride, _ptr(q_starts), tokens, heads, scale, softcap, window,
+        _ptr(slopes), _ptr(sinks), _ptr(masks), mask_words, _ptr(out), _ptr(lse),
+        _ptr(workspace), workspace_bytes, _stream(stream)))
+
+
+def tt_draft_accept(parents, drafts, chosen, q_starts, batch, tokens, path_width, path, counts,
+                    next, stream=None):
+    _check("tt_draft_accept", load().tt_draft_accept(
+        _ptr(parents), _ptr(drafts), _ptr(chosen), _ptr(q_starts), batch, tokens, path_width,
+        _ptr(path), _ptr(counts), _ptr(next), _stream(stream)))
+
+
+def tt_paged_keep(layers, n_layers, q_starts, path, path_width, counts, lens_out, stream=None):
+    """layers: from loader.paged_layers (or one tt_paged_kv with n_layers = 1)."""
+    _check("tt_paged_keep", load().tt_paged_keep(
+        _kv(layers), n_layers, _ptr(q_starts), _ptr(path), path_width, _ptr(counts),
+        _ptr(lens_out), _stream(stream)))
+
+
+def tt_paged_pages_workspace_bytes(kv) -> int:
+    return int(load().tt_paged_pages_workspace_bytes(_kv(kv)))
+
+
+def tt_paged_resize(kv, want, held, table_out, lens_out, left, workspace, workspace_bytes,
+                    stream=None):
+    _check("tt_paged_resize", load().tt_paged_resize(
+        _kv(kv), _ptr(want), _ptr(held), _ptr(table_out), _ptr(lens_out), _ptr(left),
+        _ptr(workspace), workspace_bytes, _stream(stream)))
+
+
+def tt_paged_fork(layers, n_layers, from_, held, table_out, lens_out, left, workspace,
+                  workspace_bytes, stream=None):
+    _check("tt_paged_fork", load().tt_paged_fork(
+        _kv(layers), n_layers, _ptr(from_), _ptr(held), _ptr(table_out), _ptr(lens_out),
+        _ptr(left), _ptr(workspace), workspace_bytes, _stream(stream)))
+
+
+def tt_paged_compact(layers, n_layers, held, table_out, span, workspace, workspace_bytes,
+                     stream=None):
+    _check("tt_paged_compact", load().tt_paged_compact(
+        _kv(layers), n_layers, _ptr(held), _ptr(table_out), _ptr(span), _ptr(workspace),
+        workspace_bytes, _stream(stream)))
+
+
+def tt_token_logprobs_workspace_bytes(rows, vocab, top_k) -> int:
+    return int(load().tt_token_logprobs_workspace_bytes(rows, vocab, top_k))
+
+
+def tt_token_logprobs(logits, type, rows, vocab, stride, scale, targets, top_k, logp, entropy,
+                      top_ids, top_logp, workspace, workspace_bytes, stream=None):
+    _check("tt_token_logprobs", load().tt_token_logprobs(
+        _ptr(logits), type, rows, vocab, stride, scale, _ptr(targets), top_k, _ptr(logp),
+        _ptr(entropy), _ptr(top_ids), _ptr(top_logp), _ptr(workspace), workspace_bytes,
+        _stream(stream)))
 
 
 def tt_lowbit_matrix_bytes(bits, n, k) -> int:

@@ -11,7 +11,10 @@
  *   - FP8 (E4M3, one scale per row) matvec and gate/up SwiGLU matvec;
  *   - single-token grouped-query attention over a bf16 KV cache;
  *   - the paged KV cache (bf16 or FP8): append with position rotation,
- *     attention of one or of several new tokens per sequence;
+ *     attention of one or of several new tokens per sequence, or of a tree of
+ *     drafted ones; pages taken, shared, let go and moved together;
+ *   - log probabilities of given tokens, with entropy and top alternatives;
+ *   - the tree, the acceptance and the kept rows of a drafted step;
  *   - the MoE layer with Q1 / Q2 packed low-bit experts.
  *
  * Sources.  The method is the ThinTensor decode runtime's:
@@ -531,6 +534,169 @@ tt_status tt_paged_prefill_attention(const tt_paged_kv* kv, const uint16_t* q, i
                                      const float* slopes, const float* sinks,
                                      const int32_t* prefix, uint16_t* out, float* lse,
                                      void* workspace, size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Drafted trees.  A step may answer several drafted continuations at once:
+ * the new tokens of a sequence (q_starts, as above) are the nodes of a tree.
+ *   parents int32 [tokens]: a node's parent, as a number among the new tokens
+ *   of its sequence, below its own number; -1 for a node that follows the
+ *   cached tokens.
+ * Node i of sequence b lies in the cache at the place past + i, where past =
+ * lens[b] - n_b, and follows in the text on its parent.  The order of a step:
+ *   tt_draft_tree (masks, positions), per layer tt_paged_rope_append (with
+ *   those positions) and tt_paged_tree_attention; then from the logits of all
+ *   nodes the chosen tokens (tt_token_logprobs' first alternative, or a
+ *   sampler's), tt_draft_accept, tt_paged_keep.
+ * --------------------------------------------------------------------- */
+#define TT_TREE_MAX_WORDS 8 /* 32-bit words of a mask row: 256 nodes */
+
+/* masks uint32 [tokens][mask_words]: bit i of a node's row = the i-th new
+ * token of its sequence is the node itself or above it;  positions int32
+ * [tokens] = past + the number of nodes above it.
+ * A parent that is neither -1 nor a smaller number is reported as
+ * TT_ERR_SHAPE in the device error word and taken for -1; so is a sequence of
+ * more than 32 * mask_words new tokens, whose further ones get an empty mask
+ * and the position past.  Rows of flat tokens that no sequence has are left
+ * as they are.  Requires batch <= 1024, 1 <= mask_words <= 8, tokens >= 0. */
+tt_status tt_draft_tree(const int32_t* parents, const int32_t* q_starts, const int32_t* lens,
+                        int32_t batch, int64_t tokens, int32_t mask_words, uint32_t* masks,
+                        int32_t* positions, void* stream);
+
+/* Attention of the new tokens of q_starts (required), of which each sees the
+ * cached tokens t < past and the new tokens that its mask row names (masks
+ * uint32 [tokens][mask_words], of a tree or any other; bits of tokens that
+ * the sequence does not have are ignored, and its tokens past 32 * mask_words
+ * are seen by none).
+ *   depth(i) = the number of new tokens that i sees, less one, at least 0
+ *   place(i) = past + depth(i);  place of a cached token t: t
+ *   z = f(scale * q . k) + slopes[h] * (place of the key - place(i)); with
+ *   window > 0 the key is seen only if place(i) - its place < window
+ *   out, lse, f, sinks, slopes and holes as in tt_paged_decode_attention.
+ * A token that sees no key: out 0, lse = sinks[h] (-inf without sinks).  With
+ * lens[b] < n_b the tokens without a place in the cache see nothing and are
+ * seen by none.  Requires the same of heads, scale, softcap, window, q_stride
+ * and tokens as tt_paged_prefill_attention, and 1 <= mask_words <= 8.
+ * workspace: >= tt_paged_tree_workspace_bytes(...) bytes, no initial
+ * contents needed; one of that size and of tt_paged_attention_workspace_bytes
+ * may serve all three attentions.  Calls that share one must be ordered on
+ * one stream. */
+size_t tt_paged_tree_workspace_bytes(int32_t heads, int32_t kv_heads, int32_t head_dim);
+tt_status tt_paged_tree_attention(const tt_paged_kv* kv, const uint16_t* q, int64_t q_stride,
+                                  const int32_t* q_starts, int64_t tokens, int32_t heads,
+                                  float scale, float softcap, int32_t window,
+                                  const float* slopes, const float* sinks, const uint32_t* masks,
+                                  int32_t mask_words, uint16_t* out, float* lse, void* workspace,
+                                  size_t workspace_bytes, void* stream);
+
+/* The walk down each tree: the first new token of a sequence is accepted (it
+ * was chosen by the step before); from an accepted node i the walk goes on
+ * to its lowest child c with drafts[c] == chosen[i], if it has one.
+ *   drafts, chosen int32 [tokens]: a node's own token, and the token that the
+ *   model chose after it;
+ *   path int32 [batch][path_width] = the accepted nodes, then -1;
+ *   counts int32 [batch] = how many (0 for a sequence without new tokens; the
+ *   walk ends when the path is full);
+ *   next int32 [batch] = chosen of the last of them (-1 without one).
+ * Requires batch <= 1024, path_width >= 1, tokens >= 0. */
+tt_status tt_draft_accept(const int32_t* parents, const int32_t* drafts, const int32_t* chosen,
+                          const int32_t* q_starts, int32_t batch, int64_t tokens,
+                          int32_t path_width, int32_t* path, int32_t* counts, int32_t* next,
+                          void* stream);
+
+/* ------------------------------------------------------------------------
+ * Rows and pages.  These take the caches of all layers at once: an array (host
+ * memory, read during the call) of n_layers descriptions, 1 <= n_layers <=
+ * TT_PAGED_MAX_LAYERS, which share page_table and lens and agree in all sizes
+ * (else TT_ERR_SHAPE).  table_out int32 [batch][pages_per_seq] may be the
+ * page_table itself, lens_out int32 [batch] the lens; otherwise they may not
+ * overlap.  A table entry >= num_pages is reported as TT_ERR_SHAPE in the device
+ * error word and taken for a hole.
+ * --------------------------------------------------------------------- */
+#define TT_PAGED_MAX_LAYERS 128
+
+/* Keeps the accepted rows of a step: in every layer and kv head the cache row
+ * of the new token path[b][j] is moved to the place past + j, for j <
+ * counts[b], and lens_out[b] = past + counts[b] (at least 0).  path int32
+ * [batch][path_width], ascending in each sequence, from 0 to n_b - 1; where it is
+ * not, or counts[b] is not in 0 .. min(n_b, path_width), that is reported as
+ * TT_ERR_SHAPE in the device error word and the count ends there.  A move from
+ * or to a place without a row (a hole, a negative place) is dropped.  A page
+ * that is listed twice makes two tokens share its rows (then either may win). */
+tt_status tt_paged_keep(const tt_paged_kv* layers, int32_t n_layers, const int32_t* q_starts,
+                        const int32_t* path, int32_t path_width, const int32_t* counts,
+                        int32_t* lens_out, void* stream);
+
+/* Pages.  A page is in use if the table names it (however often: sequences
+ * may share pages) or held[page] != 0 (uint8 [num_pages] or NULL: pages that
+ * others have).  Free pages are taken lowest first.  left int32 [1] or NULL:
+ * the free pages after the call, or, where they did not suffice, minus the
+ * number that were missing: those entries stay holes and TT_ERR_SIZE is
+ * reported in the device error word.  workspace: device, >=
+ * tt_paged_pages_workspace_bytes(kv) bytes, 16-byte aligned, no initial contents
+ * needed; calls that share one must be ordered on one stream.  The table is
+ * read by one CTA (64K entries take about 10 us).
+ *
+ * tt_paged_resize: sequence b gets the pages of want[b] tokens (int32
+ * [batch]): entries from ceil(want / page_size) on are let go, and the negative
+ * ones from ceil(lens[b] / page_size) up to there take free pages, in order of
+ * sequences and entries.  lens_out[b] = min(lens[b], want[b]).  want[b] < 0: the
+ * sequence stays as it is; a want past the table is reported as TT_ERR_SHAPE and
+ * clamped.  Holes below the length stay holes. */
+size_t tt_paged_pages_workspace_bytes(const tt_paged_kv* kv);
+tt_status tt_paged_resize(const tt_paged_kv* kv, const int32_t* want, const uint8_t* held,
+                          int32_t* table_out, int32_t* lens_out, int32_t* left, void* workspace,
+                          size_t workspace_bytes, void* stream);
+
+/* tt_paged_fork: sequence b becomes what sequence from[b] was before the call
+ * (int32 [batch]); from[b] == b: it stays, with all its entries; from[b] < 0: it
+ * ends (no pages, length 0).  A copy names the pages of the sequence's length;
+ * its whole pages are shared.  Of a last page that is not full the first
+ * copy takes over the page if the sequence does not stay itself, and every
+ * other copy takes a free page (in order of b; pages that this call lets go are
+ * free), into which the rows are copied in every layer.  from[b] >= batch
+ * is reported as TT_ERR_SHAPE in the device error word and the sequence stays. */
+tt_status tt_paged_fork(const tt_paged_kv* layers, int32_t n_layers, const int32_t* from,
+                        const uint8_t* held, int32_t* table_out, int32_t* lens_out,
+                        int32_t* left, void* workspace, size_t workspace_bytes, void* stream);
+
+/* tt_paged_compact: moves the pages of the table together, in every layer: with
+ * M pages in use that are not held, those that are not among the first M pages
+ * that are not held move, in order, to the free ones among these, and the table
+ * follows.  span int32 [1] or NULL: all pages of the table that are not held are
+ * below it.  The contents of pages that are free after the call are undefined. */
+tt_status tt_paged_compact(const tt_paged_kv* layers, int32_t n_layers, const uint8_t* held,
+                           int32_t* table_out, int32_t* span, void* workspace,
+                           size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Log probabilities of given tokens, with entropy and top alternatives.
+ *   x[i] = scale * logits[row][i], i < vocab;  lse = log sum_i e^x[i]
+ *   logp[row]     = x[targets[row]] - lse
+ *   entropy[row]  = lse - sum_i x[i] e^(x[i] - lse)
+ *   top_ids, top_logp [row][top_k] = the largest logits in falling order, equal
+ *                   ones by rising index, and their x - lse
+ * logits: TT_LOGITS_F32 or TT_LOGITS_BF16, row r at r * stride elements.
+ * targets int32 [rows] or NULL (then logp NULL): a negative one is no token
+ * (logp 0); one >= vocab is reported as TT_ERR_SHAPE in the device error word
+ * (logp NaN).  logp, entropy fp32 [rows], each may be NULL; top_ids int32,
+ * top_logp fp32 [rows][top_k], top_logp may be NULL, both with top_k = 0.
+ * Sums are 32-bit.  A logit of -infinity has probability 0.  A row with a NaN or
+ * +infinity, or without a logit above -infinity, has NaN for all
+ * probabilities and its entropy; NaN comes first in the order of logits.
+ * Requires rows >= 0, 1 <= vocab <= 2^30, stride >= vocab, scale finite and above
+ * 0, 0 <= top_k <= min(32, vocab).  logits aligned to their type, the rest 4 bytes;
+ * workspace: >= tt_token_logprobs_workspace_bytes(...) bytes (may be 0 and
+ * NULL), 16-byte aligned, no initial contents needed; calls that share one must
+ * be ordered on one stream.
+ * --------------------------------------------------------------------- */
+#define TT_LOGITS_F32 0
+#define TT_LOGITS_BF16 1
+#define TT_LOGPROBS_MAX_TOP 32
+size_t tt_token_logprobs_workspace_bytes(int64_t rows, int64_t vocab, int32_t top_k);
+tt_status tt_token_logprobs(const void* logits, int32_t type, int64_t rows, int64_t vocab,
+                            int64_t stride, float scale, const int32_t* targets, int32_t top_k,
+                            float* logp, float* entropy, int32_t* top_ids, float* top_logp,
+                            void* workspace, size_t workspace_bytes, void* stream);
 
 /* ------------------------------------------------------------------------
  * Q1 / Q2 packed low-bit experts  [SHIP 97.87 tok/s notes:
