@@ -66,22 +66,17 @@
 #include <cmath>
 #include <type_traits>
 
-#include "launch.h"
-#include "paged.cuh"
-#include "tensor_map.h"
+#include "paged_mma.cuh"
 
 namespace tt {
 namespace {
 
-constexpr int kRows = 128;   // rows of a row tile
-constexpr int kKeys = 128;   // tokens of a K / V tile
 constexpr int kMmaWarp = 8, kLoadWarp = 9, kFixWarp = 10;
 constexpr int kCounters = 1024;  // the decode kernel's, at the workspace's start: left alone
 constexpr int kJoinBytes = (kCounters + 1) * 16;
 constexpr int kMaxSplit = 32;
 constexpr int kMaxSorted = 64;   // sequences that are put in order of length
 constexpr int kTailTiles = 8;    // tiles a piece of the last round has to have to be split
-constexpr uint32_t kAll = 0xffffffffu;
 
 template <int D, bool FP8>
 struct Plan {
@@ -141,242 +136,6 @@ struct PrefillArgs {
   int32_t* err;
 };
 
-// ---- tcgen05
-__device__ __forceinline__ uint64_t desc_base() {
-  return (uint64_t(1024 >> 4) << 32)  // stride: 8 rows of 128 bytes
-         | (uint64_t(1) << 46)        // descriptor version
-         | (uint64_t(2) << 61);       // 128-byte swizzle
-}
-// K-major operand (rows of 64 contiguous elements of the contraction).
-__device__ __forceinline__ uint64_t desc_k(uint32_t addr) {
-  return desc_base() | (uint64_t(1) << 16) | uint64_t((addr >> 4) & 0x3fffu);
-}
-// MN-major operand (rows = steps of the contraction); `leading` bytes from
-// one 64-element span of the outer dimension to the next.
-__device__ __forceinline__ uint64_t desc_mn(uint32_t addr, uint32_t leading) {
-  return desc_base() | (uint64_t(leading >> 4) << 16) | uint64_t((addr >> 4) & 0x3fffu);
-}
-// bf16 x bf16 -> f32, 128 rows, n columns; mn: B is MN-major.
-__device__ __forceinline__ constexpr uint32_t idesc(int n, bool mn) {
-  return (1u << 4) | (1u << 7) | (1u << 10) | (mn ? 1u << 16 : 0u) | (uint32_t(n >> 3) << 17) |
-         (uint32_t(kRows >> 4) << 24);
-}
-// The products are issued by a whole warp in step, one elected lane each:
-// the compiler then knows that their operands are the same in all lanes and
-// keeps them in uniform registers.  (In a branch of one lane every operand is
-// moved there first: 60 to 110 cycles an instruction, more than the products
-// themselves take.)
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t id,
-                                       uint32_t acc) {
-  asm volatile(
-      "{\n\t.reg .pred p, e;\n\tsetp.ne.b32 p, %4, 0;\n\telect.sync _|e, 0xffffffff;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(id), "r"(acc)
-      : "memory");
-}
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t id,
-                                       uint32_t acc) {
-  asm volatile(
-      "{\n\t.reg .pred p, e;\n\tsetp.ne.b32 p, %4, 0;\n\telect.sync _|e, 0xffffffff;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-      "r"(a), "l"(b), "r"(id), "r"(acc)
-      : "memory");
-}
-__device__ __forceinline__ void commit(uint32_t bar) {
-  asm volatile(
-      "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
-      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(
-          bar)
-      : "memory");
-}
-__device__ __forceinline__ void fence_after() {
-  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-}
-__device__ __forceinline__ void fence_before() {
-  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-}
-// Waits for this thread's tcgen05.ld; the registers pass through, so that
-// nothing that uses them is moved before it.
-__device__ __forceinline__ void wait_ld(uint32_t (&r)[32]) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;"
-               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]),
-                 "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]),
-                 "+r"(r[14]), "+r"(r[15]), "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]),
-                 "+r"(r[21]), "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]),
-                 "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
-               :
-               : "memory");
-}
-__device__ __forceinline__ void wait_st() {
-  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-}
-// 32 columns of this warp's 32 lanes (complete after wait_ld).
-__device__ __forceinline__ void tmem_ld32(uint32_t addr, uint32_t (&r)[32]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
-      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
-        "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]),
-        "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]),
-        "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-      : "r"(addr));
-}
-__device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t (&r)[32]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
-      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
-      "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(
-          addr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
-      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
-      "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]),
-      "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]),
-      "r"(r[29]), "r"(r[30]), "r"(r[31])
-      : "memory");
-}
-
-// 64 columns of this warp's 32 lanes into r[first ..] (complete after
-// wait_ld128).
-template <int first>
-__device__ __forceinline__ void tmem_ld64(uint32_t addr, uint32_t (&r)[128]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x64.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17,"
-      "%18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32, %33,"
-      "%34, %35, %36, %37, %38, %39, %40, %41, %42, %43, %44, %45, %46, %47, %48, %49,"
-      "%50, %51, %52, %53, %54, %55, %56, %57, %58, %59, %60, %61, %62, %63}, [%64];"
-      : "=r"(r[first + 0]), "=r"(r[first + 1]), "=r"(r[first + 2]), "=r"(r[first + 3]), "=r"(r[first + 4]), "=r"(r[first + 5]), "=r"(r[first + 6]),
-      "=r"(r[first + 7]), "=r"(r[first + 8]), "=r"(r[first + 9]), "=r"(r[first + 10]), "=r"(r[first + 11]), "=r"(r[first + 12]), "=r"(r[first + 13]),
-      "=r"(r[first + 14]), "=r"(r[first + 15]), "=r"(r[first + 16]), "=r"(r[first + 17]), "=r"(r[first + 18]), "=r"(r[first + 19]), "=r"(r[first + 20]),
-      "=r"(r[first + 21]), "=r"(r[first + 22]), "=r"(r[first + 23]), "=r"(r[first + 24]), "=r"(r[first + 25]), "=r"(r[first + 26]), "=r"(r[first + 27]),
-      "=r"(r[first + 28]), "=r"(r[first + 29]), "=r"(r[first + 30]), "=r"(r[first + 31]), "=r"(r[first + 32]), "=r"(r[first + 33]), "=r"(r[first + 34]),
-      "=r"(r[first + 35]), "=r"(r[first + 36]), "=r"(r[first + 37]), "=r"(r[first + 38]), "=r"(r[first + 39]), "=r"(r[first + 40]), "=r"(r[first + 41]),
-      "=r"(r[first + 42]), "=r"(r[first + 43]), "=r"(r[first + 44]), "=r"(r[first + 45]), "=r"(r[first + 46]), "=r"(r[first + 47]), "=r"(r[first + 48]),
-      "=r"(r[first + 49]), "=r"(r[first + 50]), "=r"(r[first + 51]), "=r"(r[first + 52]), "=r"(r[first + 53]), "=r"(r[first + 54]), "=r"(r[first + 55]),
-      "=r"(r[first + 56]), "=r"(r[first + 57]), "=r"(r[first + 58]), "=r"(r[first + 59]), "=r"(r[first + 60]), "=r"(r[first + 61]), "=r"(r[first + 62]),
-      "=r"(r[first + 63])
-      : "r"(addr));
-}
-// Waits for this thread's loads; the registers pass through, so that nothing
-// that uses them is moved before.
-__device__ __forceinline__ void wait_ld128(uint32_t (&r)[128]) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;"
-      : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]),
-      "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]),
-      "+r"(r[14]), "+r"(r[15]), "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]),
-      "+r"(r[21]), "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]),
-      "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31]), "+r"(r[32]), "+r"(r[33]), "+r"(r[34]),
-      "+r"(r[35]), "+r"(r[36]), "+r"(r[37]), "+r"(r[38]), "+r"(r[39]), "+r"(r[40]), "+r"(r[41]),
-      "+r"(r[42]), "+r"(r[43]), "+r"(r[44]), "+r"(r[45]), "+r"(r[46]), "+r"(r[47]), "+r"(r[48]),
-      "+r"(r[49]), "+r"(r[50]), "+r"(r[51]), "+r"(r[52]), "+r"(r[53]), "+r"(r[54]), "+r"(r[55]),
-      "+r"(r[56]), "+r"(r[57]), "+r"(r[58]), "+r"(r[59]), "+r"(r[60]), "+r"(r[61]), "+r"(r[62]),
-      "+r"(r[63])
-      :
-      : "memory");
-  asm volatile(""
-      : "+r"(r[64]), "+r"(r[65]), "+r"(r[66]), "+r"(r[67]), "+r"(r[68]), "+r"(r[69]), "+r"(r[70]),
-      "+r"(r[71]), "+r"(r[72]), "+r"(r[73]), "+r"(r[74]), "+r"(r[75]), "+r"(r[76]), "+r"(r[77]),
-      "+r"(r[78]), "+r"(r[79]), "+r"(r[80]), "+r"(r[81]), "+r"(r[82]), "+r"(r[83]), "+r"(r[84]),
-      "+r"(r[85]), "+r"(r[86]), "+r"(r[87]), "+r"(r[88]), "+r"(r[89]), "+r"(r[90]), "+r"(r[91]),
-      "+r"(r[92]), "+r"(r[93]), "+r"(r[94]), "+r"(r[95]), "+r"(r[96]), "+r"(r[97]), "+r"(r[98]),
-      "+r"(r[99]), "+r"(r[100]), "+r"(r[101]), "+r"(r[102]), "+r"(r[103]), "+r"(r[104]),
-      "+r"(r[105]), "+r"(r[106]), "+r"(r[107]), "+r"(r[108]), "+r"(r[109]), "+r"(r[110]),
-      "+r"(r[111]), "+r"(r[112]), "+r"(r[113]), "+r"(r[114]), "+r"(r[115]), "+r"(r[116]),
-      "+r"(r[117]), "+r"(r[118]), "+r"(r[119]), "+r"(r[120]), "+r"(r[121]), "+r"(r[122]),
-      "+r"(r[123]), "+r"(r[124]), "+r"(r[125]), "+r"(r[126]), "+r"(r[127])
-      :
-      : "memory");
-}
-__device__ __forceinline__ void tmem_st64(uint32_t addr, const uint32_t (&r)[64]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x64.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18,"
-      "%19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32, %33, %34,"
-      "%35, %36, %37, %38, %39, %40, %41, %42, %43, %44, %45, %46, %47, %48, %49, %50,"
-      "%51, %52, %53, %54, %55, %56, %57, %58, %59, %60, %61, %62, %63, %64};" ::"r"(addr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
-      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
-      "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]),
-      "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]),
-      "r"(r[29]), "r"(r[30]), "r"(r[31]), "r"(r[32]), "r"(r[33]), "r"(r[34]), "r"(r[35]),
-      "r"(r[36]), "r"(r[37]), "r"(r[38]), "r"(r[39]), "r"(r[40]), "r"(r[41]), "r"(r[42]),
-      "r"(r[43]), "r"(r[44]), "r"(r[45]), "r"(r[46]), "r"(r[47]), "r"(r[48]), "r"(r[49]),
-      "r"(r[50]), "r"(r[51]), "r"(r[52]), "r"(r[53]), "r"(r[54]), "r"(r[55]), "r"(r[56]),
-      "r"(r[57]), "r"(r[58]), "r"(r[59]), "r"(r[60]), "r"(r[61]), "r"(r[62]), "r"(r[63])
-      : "memory");
-}
-
-__device__ __forceinline__ void tma_q(uint32_t dst, const CUtensorMap* map, int x, int h, int t,
-                                      uint32_t bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(h), "r"(t), "r"(bar)
-      : "memory");
-}
-__device__ __forceinline__ void tma_rows(uint32_t dst, const CUtensorMap* map, int x, int row,
-                                         uint32_t bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(row), "r"(bar)
-      : "memory");
-}
-__device__ __forceinline__ void bulk_copy(uint32_t dst, const void* src, uint32_t bytes,
-                                          uint32_t bar) {
-  asm volatile(
-      "cp.async.bulk.shared::cta.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-          dst),
-      "l"(src), "r"(bytes), "r"(bar)
-      : "memory");
-}
-
-// Two 32-bit lanes at once.
-__device__ __forceinline__ uint64_t f2(uint32_t lo, uint32_t hi) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(lo), "r"(hi));
-  return r;
-}
-__device__ __forceinline__ uint64_t f2(float lo, float hi) {
-  return f2(__float_as_uint(lo), __float_as_uint(hi));
-}
-__device__ __forceinline__ void un2(uint64_t v, float& lo, float& hi) {
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ float max3(float a, float b, float c) {
-  float y;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
-  return y;
-}
-__device__ __forceinline__ uint32_t bf16x2(float a, float b) {
-  const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
-// Two E4M3 codes (low 16 bits) -> bf16x2, exact.
-__device__ __forceinline__ uint32_t e4m3x2_bf16x2(uint32_t w) {
-  uint32_t h;
-  asm("{\n\t.reg .b16 l, u;\n\tmov.b32 {l, u}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\t}"
-      : "=r"(h)
-      : "r"(w));
-  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
-  return bf16x2(f.x, f.y);
-}
-
 // What one piece of work is: the row tiles A and B of q tile `qt` of sequence
 // b, kv head j, the part [k0, k1) of its K / V tiles.
 struct Item {
@@ -388,25 +147,6 @@ struct Item {
   int k0, k1, parts, part;
   int base;              // number among the joined pieces, or -1
 };
-
-// Waits for a phase; gives up after kWaitLimitNs, or when another thread has.
-__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile int* quit,
-                                     int32_t* err) {
-  const uint32_t a = smem_u32(bar);
-  if (mbar_try_wait(a, parity)) return true;
-  const uint64_t t0 = globaltimer_ns();
-  for (uint32_t it = 1;; ++it) {
-    if (mbar_try_wait(a, parity)) return true;
-    if ((it & 15u) == 0u) {
-      if (*quit) return false;
-      if (globaltimer_ns() - t0 > kWaitLimitNs) {
-        *quit = 1;
-        flag_error(err, kErrTimeout);
-        return false;
-      }
-    }
-  }
-}
 
 // Which of the 32 dims from d0 on have a value of +infinity, -infinity, NaN (a
 // bit each) among the tokens [lo, hi) of sequence b and kv head j, in the tiles
@@ -1436,18 +1176,6 @@ __global__ void __launch_bounds__(kJoinThreads)
         make_uint4(bf16x2(o[0] * inv, o[1] * inv), bf16x2(o[2] * inv, o[3] * inv),
                    bf16x2(o[4] * inv, o[5] * inv), bf16x2(o[6] * inv, o[7] * inv));
   }
-}
-
-cudaError_t encode(CUtensorMap* map, const void* base, int rank, const cuuint64_t* dims,
-                   const cuuint64_t* strides, const cuuint32_t* box) {
-  EncodeTiledFn enc = tensor_map_encoder();
-  if (!enc) return cudaErrorNotSupported;
-  const cuuint32_t estr[3] = {1u, 1u, 1u};
-  if (enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, cuuint32_t(rank), const_cast<void*>(base), dims,
-          strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
-    return cudaErrorInvalidValue;
-  return cudaSuccess;
 }
 
 template <int D, bool FP8, Scores SC>
