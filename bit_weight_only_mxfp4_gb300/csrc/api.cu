@@ -634,6 +634,11 @@ tt_status tt_paged_tree_attention(const tt_paged_kv* kv, const uint16_t* q, int6
   if (mask_words > tt::kMaxMaskWords) return TT_ERR_UNSUPPORTED;
   if (!q_starts || !masks) return TT_ERR_NULL;
   if (!aligned(masks, 4)) return TT_ERR_ALIGN;
+  // K / V tiles of all row tiles (of 64 rows at least, but for a sequence's last) stay
+  // far from 64 bits, and those of one CTA within 32
+  const int64_t tiles = (int64_t(kv->pages_per_seq) * kv->page_size + 127) / 128;
+  const int64_t pieces = tokens * heads / 64 + int64_t(kv->batch) * kv->kv_heads;
+  if (tiles > (int64_t(1) << 40) / pieces) return TT_ERR_UNSUPPORTED;
   if (tokens == 0) return TT_OK;
   return from_cuda(
       tt::launch_paged_tree(c, kv->head_dim, kv->type == TT_KV_FP8, a, as_stream(stream), kPdl));

@@ -14,21 +14,24 @@
 //
 // Split.  A piece is a row tile (floor(128 / G) tokens x G heads) of a sequence and
 // kv head; it has ceil(length / 128) K / V tiles.  The tiles of all pieces form
-// one line, of which each CTA takes an equal stretch, whatever the lengths are.  A
-// piece that lies in several CTAs is written in parts, joined in order by a second
-// kernel.
+// one line, of which each of two groups of four softmax warps a CTA takes an equal
+// stretch, whatever the lengths are.  A piece that lies in several stretches is
+// written in parts, joined in order by a second kernel.
 //
-// Inside a CTA the tiles of a piece go in turn to two groups of four warps, each
-// with its own maximum, sum and O: while one group turns its scores into weights,
-// the other's products run.  At the end of a piece (or of its part) both groups
-// read both O's, half of the dims each.  (With one row tile for each group, as in
-// the prompt kernel, a piece of one row tile would leave a group idle.)
-//   warps 0-3, 4-7  softmax of the even and the odd tiles, one thread a row
-//   warp 8          the products, issued by the warp in step, one elected lane
-//   warp 9          the copies (TMA: one box per page and 64 dims; FP8: bulk
-//                   copies of codes and scales)
-//   warps 10, 11    make the V tiles safe (below); FP8: warps 10-15, which
-//                   also turn E4M3 pages into bf16 tiles
+// Inside a CTA the two groups have nothing to do with each other but that they share
+// the SM: while one turns its scores into weights, or writes a piece's end, the
+// other's products and copies run.  (Even and odd tiles of one stretch, joined in the
+// CTA at a piece's end, left the copies idle for 5 us there.)
+//   warps 0-3, 4-7  softmax of the groups, one thread a row
+//   warp 8          the products, issued by the warp in step, one elected lane; Q
+//   warps 9-12      a group's K tiles, or V tiles: asked for (TMA: one box per page
+//                   and 64 dims; FP8: one bulk copy per page), and once there turned
+//                   into bf16 in their place, if E4M3 codes, and made safe (below)
+//   warps 13, 14    what is next of a group: pages looked up, FP8: scales
+// Several warps ask for the copies because the asking bounds one: some 100 cycles a
+// box.  Measured on copies alone, boxes of 2 KB from memory: one warp 2.8 TB/s, two
+// 4.9, four 6.7; from L2 3.1, 6.0, 10.9.  (Copied 16 bytes a lane by cp.async, an
+// instruction took 100 cycles.)
 // The running maximum is only raised (and O rescaled) when a row's maximum has
 // grown by more than 2^8.
 //
@@ -36,10 +39,10 @@
 // (2^-8 of each weight); the sum of weights is taken from the unrounded ones.
 // FP8: codes become bf16 exactly, the scales multiply S and P in 32 bits.
 //
-// Masked values.  0 * NaN is NaN, so where the mask cuts a tile (the new tokens'
-// tiles, the window's first ones) or pages are missing, V rows of no token are
-// zeroed, elements that are not finite too, and the rows that do see them get
-// them added at the end.  Tiles that all rows see whole need nothing of it.
+// Masked values.  0 * NaN is NaN, so a V row that some row must not see (a new
+// token's, or one that the window cuts) may not enter the product with NaN or
+// infinities in it: those elements are zeroed, and the rows that do see them get
+// them added at the end.  Rows of no token are zeroed.
 #include <cmath>
 #include <type_traits>
 
@@ -48,33 +51,46 @@
 namespace tt {
 namespace {
 
-constexpr int kMmaWarp = 8, kLoadWarp = 9, kFixWarp = 10;
+constexpr int kMmaWarp = 8, kCopyWarp = 9, kPlanWarp = 13;
 constexpr int kMaxCtas = 1024;
 constexpr int kCounters = 1024;  // the decode kernel's, at the workspace's start: left alone
-constexpr int kDirty = 16;
+constexpr int kAhead = 4;        // tiles of a group that are planned at once
+constexpr int kDirty = 8;
+
+// What the warps of a group know of a tile.
+struct Tile {
+  int32_t row[8];    // first cache row of its pages, or -1
+  uint32_t got;      // pages present, a bit each
+  int16_t from, upto;  // its rows of tokens
+  int16_t seen0, seen1;  // those that every row of S sees
+  int32_t segment;   // 1, 2, ..
+  int32_t ends;      // bit 0: first of the segment, bit 1: last
+  int32_t next_token, next_head;  // of the last: where the next segment's Q is, or -1
+};
 
 template <int D, bool FP8>
 struct Plan {
-  static constexpr int kThreads = FP8 ? 512 : 384;
-  static constexpr int kFixers = kThreads - 32 * kFixWarp;
+  static constexpr int kThreads = 512;
   // registers a thread: at launch, of the softmax warps, of the others
-  static constexpr int kLaunchRegs = FP8 ? 128 : 168;
-  static constexpr int kSoftmaxRegs = FP8 ? 208 : 224;
-  static constexpr int kOtherRegs = FP8 ? 48 : 56;
+  static constexpr int kLaunchRegs = 128;
+  static constexpr int kSoftmaxRegs = 200;
+  static constexpr int kOtherRegs = 56;
   static_assert(256 * kSoftmaxRegs + (kThreads - 256) * kOtherRegs <= kThreads * kLaunchRegs,
                 "register shares");
   static constexpr int kHalves = D / 64;            // 128-byte spans of a bf16 row
   static constexpr int kSpan = kKeys * 128;         // bytes of a tile's one span
   static constexpr int kTile = kSpan * kHalves;     // a K or V tile, or a Q tile
-  static constexpr int kSlots = FP8 ? (D == 128 ? 3 : 6) : (D == 128 ? 4 : 8);
-  static constexpr int kRaw = FP8 ? kKeys * D + 2 * kKeys * 4 : 0;  // codes, both scales (with K)
-  static constexpr int kRaws = FP8 ? (D == 128 ? 2 : 4) : 0;
-  static constexpr int kOffKv = 2 * kTile;                      // (two Q tiles before)
-  static constexpr int kOffRaw = kOffKv + kSlots * kTile;
-  static constexpr int kOffScale = kOffRaw + kRaws * kRaw;      // [4 tiles][key, value][128]
-  static constexpr int kOffDepth = kOffScale + (FP8 ? 4 * 2 * kKeys * 4 : 0);  // [2][2][128] floats
-  static constexpr int kOffStat = kOffDepth + 4 * kKeys * 4;    // [2][128] maximum and sum
-  static constexpr int kOffLine = kOffStat + 2 * kRows * 8;     // int64 [batch + 1]
+  static constexpr int kSlots = D == 128 ? 4 : 8;
+  static constexpr int kRow = FP8 ? D : 2 * D;      // bytes of a cache row
+  // Slots of a group's K or V: tile i of the group lies in slot i % kDepth.  A slot
+  // is one warp's, and one group's, so that all wait for every phase of its barriers
+  // in turn.
+  static constexpr int kDepth = kSlots / 4;
+  static constexpr int kOffKv = 2 * kTile;                      // (each group's Q before)
+  static constexpr int kOffScale = kOffKv + kSlots * kTile;     // [2][kAhead][key, value][128]
+  static constexpr int kOffDepth = kOffScale + (FP8 ? 2 * kAhead * 2 * kKeys * 4 : 0);  // [2][2][128] floats
+  static constexpr int kOffTiles = kOffDepth + 4 * kKeys * 4;   // Tile [2][kAhead]
+  static constexpr int kOffLine = kOffTiles + (2 * kAhead * int(sizeof(Tile)) + 7) / 8 * 8;  // int64 [batch + 1]
   static constexpr int kOffStart = kOffLine + (kPagedMaxBatch + 2) * 8;
   static constexpr int kOffCount = kOffStart + kPagedMaxBatch * 4;
   static constexpr int kOffLen = kOffCount + kPagedMaxBatch * 4;
@@ -104,12 +120,12 @@ struct KernelArgs {
   int words;
   uint16_t* out;
   float* lse;
-  int4* joins;   // a record for each CTA whose last piece goes on in the next one's
-  float* parts;  // [CTA][2]: of a piece that began before, of one that goes on
+  int4* joins;   // a record for each group whose last piece goes on in the next one's
+  float* parts;  // [group][2]: of a piece that began before, of one that goes on
   int32_t* err;
 };
 
-// A CTA's part of a piece: K / V tiles [k0, k1) of the row tile that begins at
+// A group's part of a piece: K / V tiles [k0, k1) of the row tile that begins at
 // flat token tok0.
 struct Segment {
   int b, j, len, past;
@@ -149,48 +165,104 @@ struct Sight {
 };
 
 // Which of the 32 dims from d0 on have a value of +infinity, -infinity, NaN (a bit
-// each) among the tokens of the tiles [k0, k1) that the row sees, in those tiles
-// whose values were kept out of the product.
+// each) among the tokens of [t0, t1) that the row sees and that were kept out of
+// the product: those that not every row sees.
 template <int D, bool FP8>
-__device__ __noinline__ uint3 tree_not_finite(const PagedKv& kv, const Sight& s, int b, int j, int k0,
-                                              int k1, int all_lo, int all_hi, bool holes, int d0) {
+__device__ __noinline__ uint3 tree_not_finite(const PagedKv& kv, const Sight& s, int b, int j, int t0,
+                                              int t1, int all_lo, int all_hi, int d0) {
   uint3 x = make_uint3(0u, 0u, 0u);
-  const int rows = 1 << kv.page_shift;
-  for (int kt = k0; kt < k1; ++kt) {
-    const int t0 = kt * kKeys;
-    if (t0 >= all_lo && t0 + kKeys <= all_hi) {
-      bool whole = true;
-      for (int t = t0; holes && t < t0 + kKeys; t += rows) whole &= paged_page(kv, b, t, nullptr) >= 0;
-      if (whole) continue;
+  for (int t = t0; t < t1; ++t) {
+    if (t >= all_lo && t < all_hi) {
+      t = all_hi - 1;
+      continue;
     }
-    for (int tp = t0; tp < t0 + kKeys && tp < s.len; tp += rows) {
-      const int page = paged_page(kv, b, tp, nullptr);
-      if (page < 0) continue;
-      for (int t = tp; t < tp + rows && t < s.len; ++t) {
-        if (!s.sees(t)) continue;
-        const int64_t at = paged_row(kv, page, j, t);
-        const uint8_t* src = static_cast<const uint8_t*>(kv.v) + (at * D + d0) * (FP8 ? 1 : 2);
-        if constexpr (FP8) {
-          if (!(fabsf(__ldcg(kv.v_scales + at)) <= kFiniteMax)) x.z = kAll;
-          for (int d = 0; d < 32; d += 4) {
-            const uint32_t v = __ldcg(reinterpret_cast<const uint32_t*>(src + d));
-            for (int e = 0; e < 4; ++e) x.z |= uint32_t(((v >> (8 * e)) & 0x7fu) == 0x7fu) << (d + e);
-          }
-        } else {
-          for (int d = 0; d < 32; d += 2) {
-            const uint32_t w = __ldcg(reinterpret_cast<const uint32_t*>(src + 2 * d));
-            for (int e = 0; e < 2; ++e) {
-              const uint32_t v = (w >> (16 * e)) & 0xffffu;
-              x.x |= uint32_t(v == 0x7f80u) << (d + e);
-              x.y |= uint32_t(v == 0xff80u) << (d + e);
-              x.z |= uint32_t((v & 0x7fffu) > 0x7f80u) << (d + e);
-            }
-          }
+    if (!s.sees(t)) continue;
+    const int page = paged_page(kv, b, t, nullptr);
+    if (page < 0) continue;
+    const int64_t at = paged_row(kv, page, j, t);
+    const uint8_t* src = static_cast<const uint8_t*>(kv.v) + (at * D + d0) * (FP8 ? 1 : 2);
+    if constexpr (FP8) {
+      if (!(fabsf(__ldcg(kv.v_scales + at)) <= kFiniteMax)) x.z = kAll;
+      for (int d = 0; d < 32; d += 4) {
+        const uint32_t v = __ldcg(reinterpret_cast<const uint32_t*>(src + d));
+        for (int e = 0; e < 4; ++e) x.z |= uint32_t(((v >> (8 * e)) & 0x7fu) == 0x7fu) << (d + e);
+      }
+    } else {
+      for (int d = 0; d < 32; d += 2) {
+        const uint32_t w = __ldcg(reinterpret_cast<const uint32_t*>(src + 2 * d));
+        for (int e = 0; e < 2; ++e) {
+          const uint32_t v = (w >> (16 * e)) & 0xffffu;
+          x.x |= uint32_t(v == 0x7f80u) << (d + e);
+          x.y |= uint32_t(v == 0xff80u) << (d + e);
+          x.z |= uint32_t((v & 0x7fffu) > 0x7f80u) << (d + e);
         }
       }
     }
   }
   return x;
+}
+
+// Four E4M3 codes -> two bf16x2, exact (NaN becomes 480): with exponent and mantissa
+// moved to bf16's places a code is its value times 2^-120, subnormal ones too.
+// (Conversion instructions, three for two codes, share the unit with the softmax
+// warps' exponentials.)
+__device__ __forceinline__ void e4m3x4_bf16(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  auto half = [](uint32_t t) {
+    const uint32_t u = ((t >> 4) & 0x07f007f0u) | (t & 0x80008000u);
+    const uint32_t up = 0x7b807b80u;  // 2^120
+    const __nv_bfloat162 y = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&u),
+                                     *reinterpret_cast<const __nv_bfloat162*>(&up));
+    return *reinterpret_cast<const uint32_t*>(&y);
+  };
+  lo = half(__byte_perm(w, 0u, 0x1404));
+  hi = half(__byte_perm(w, 0u, 0x3424));
+}
+
+// What few K and V tiles need, by a whole warp; all are bf16 here.  V: rows of no token
+// become zeros, and elements that are not finite in rows that not every row of S sees
+// (true: some were).  E4M3 codes of NaN, `nan`, are 480 so far, which no other is.
+template <int D, bool FP8>
+__device__ __noinline__ bool tree_make_safe(uint8_t* tile, const Tile* d, int value, bool nan,
+                                            int page_shift) {
+  constexpr int kPieces = D / 8, kStep = 32 / kPieces;  // 16-byte pieces of a row; rows at once
+  const int lane = threadIdx.x & 31, c = lane % kPieces, r0 = lane / kPieces;
+  const int from = d->from, upto = d->upto, seen0 = d->seen0, seen1 = d->seen1;
+  const uint32_t got = d->got;
+  uint8_t* column = tile + (c >> 3) * kKeys * 128;
+  auto piece = [&](int r) {
+    return reinterpret_cast<uint4*>(column + r * 128 + (((c & 7) ^ (r & 7)) << 4));
+  };
+  bool bad = false;
+  auto scan = [&](int r, int end, bool hidden) {
+    for (r += r0; r < end; r += kStep) {
+      uint4 x = *piece(r);
+      auto fixed = [&](uint32_t h) {  // one element
+        if (FP8 ? (h & 0x7fffu) != 0x43f0u : (h & 0x7f80u) != 0x7f80u) return h;
+        bad |= hidden;
+        return hidden ? 0u : 0x7fc0u;
+      };
+      auto both = [&](uint32_t w) { return fixed(w & 0xffffu) | fixed(w >> 16) << 16; };
+      *piece(r) = make_uint4(both(x.x), both(x.y), both(x.z), both(x.w));
+    }
+  };
+  if (!value) {
+    scan(from, upto, false);
+    return false;
+  }
+  auto clear = [&](int r, int end) {
+#pragma unroll 4
+    for (r += r0; r < end; r += kStep) *piece(r) = make_uint4(0u, 0u, 0u, 0u);
+  };
+  clear(0, from);
+  clear(upto, kKeys);
+  for (int t = from; t < upto; t = ((t >> page_shift) + 1) << page_shift)
+    if (!((got >> (t >> page_shift)) & 1u)) clear(t, min(((t >> page_shift) + 1) << page_shift, upto));
+  __syncwarp();
+  if (FP8 && !nan) return false;
+  if (seen0 > from) scan(from, min(seen0, upto), true);
+  if (FP8) scan(max(from, seen0), min(seen1, upto), false);
+  if (seen1 < upto) scan(max(seen1, from), upto, true);
+  return bad;
 }
 
 // What is done to the scores: nothing but a positive scale; a cap, a bias or
@@ -204,63 +276,55 @@ __global__ void __launch_bounds__(Plan<D, FP8>::kThreads, 1)
                       const __grid_constant__ PagedKv kv, const KernelArgs a) {
   using P = Plan<D, FP8>;
   constexpr bool GEN = SC != kPlain;
-  constexpr int kThreads = P::kThreads, kFixers = P::kFixers;
+  constexpr int kThreads = P::kThreads;
   extern __shared__ __align__(128) uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
   const uint32_t sbase = smem_u32(smem);
   float* scales = reinterpret_cast<float*>(smem + P::kOffScale);
   float* shifts = reinterpret_cast<float*>(smem + P::kOffDepth);
-  float2* stat = reinterpret_cast<float2*>(smem + P::kOffStat);
+  Tile* plans = reinterpret_cast<Tile*>(smem + P::kOffTiles);  // [group][kAhead]
   int64_t* line = reinterpret_cast<int64_t*>(smem + P::kOffLine);  // tiles before a sequence's
   int32_t* first = reinterpret_cast<int32_t*>(smem + P::kOffStart);
   int32_t* count = reinterpret_cast<int32_t*>(smem + P::kOffCount);
   int32_t* lens = reinterpret_cast<int32_t*>(smem + P::kOffLen);
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + P::kOffBar);
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + P::kOffBar);  // of the slots
   uint64_t* empty = full + P::kSlots;
-  uint64_t* ready = empty + P::kSlots;   // slot made safe, or converted
-  uint64_t* raw_full = ready + P::kSlots;
-  uint64_t* raw_empty = raw_full + 4;
-  uint64_t* q_full = raw_empty + 4;      // [2], of the Q tiles
-  uint64_t* q_free = q_full + 2;         // [2]
-  uint64_t* s_full = q_free + 2;         // [2], of the groups, and so on
+  uint64_t* ready = empty + P::kSlots;   // made safe, or converted
+  uint64_t* planned = ready + P::kSlots;  // [2][kAhead]
+  uint64_t* freed = planned + 2 * kAhead;   // [2][kAhead], when a tile is used up
+  uint64_t* q_full = freed + 2 * kAhead;    // [2], of the groups, and so on
+  uint64_t* s_full = q_full + 2;
   uint64_t* p_full = s_full + 2;
   uint64_t* o_done = p_full + 2;
   uint64_t* s_read = o_done + 2;
   uint64_t* shifted = s_read + 2;
-  uint64_t* posted = shifted + 2;        // both groups' maxima and sums
-  uint64_t* taken = posted + 1;          // both groups' O's
-  uint64_t* drained = taken + 1;
-  uint32_t* have = reinterpret_cast<uint32_t*>(drained + 1);  // [8] boxes present, per tile
-  int* dirty = reinterpret_cast<int*>(have + 8);              // [kDirty] segment number + 1
-  int* misc = dirty + kDirty;  // [0] TMEM address, [1] quit, [2, 3] holes of the groups
+  uint64_t* drained = shifted + 2;
+  int* dirty = reinterpret_cast<int*>(drained + 1);  // [2][kDirty] segment
+  int* misc = dirty + 2 * kDirty;  // [0] TMEM address, [1] quit
   volatile int* quit = misc + 1;
-  int64_t* scan = reinterpret_cast<int64_t*>(stat);  // [warps], before the main loop
-  static_assert(kThreads / 32 * 8 <= 2 * kRows * 8, "scan");
+  int64_t* scan = reinterpret_cast<int64_t*>(smem);  // [warps], before the main loop
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if (tid == 0) {
     for (int i = 0; i < P::kSlots; ++i) {
       mbar_init(smem_u32(&full[i]), 1);
       mbar_init(smem_u32(&empty[i]), 1);
-      mbar_init(smem_u32(&ready[i]), kFixers);
+      mbar_init(smem_u32(&ready[i]), 1);
     }
-    for (int i = 0; i < 4; ++i) {
-      mbar_init(smem_u32(&raw_full[i]), 1);
-      mbar_init(smem_u32(&raw_empty[i]), kFixers);
+    for (int i = 0; i < 2 * kAhead; ++i) {
+      mbar_init(smem_u32(&planned[i]), 1);
+      mbar_init(smem_u32(&freed[i]), 1);
     }
     for (int g = 0; g < 2; ++g) {
       mbar_init(smem_u32(&q_full[g]), 1);
-      mbar_init(smem_u32(&q_free[g]), 2);
       mbar_init(smem_u32(&s_full[g]), 1);
       mbar_init(smem_u32(&p_full[g]), kRows);
       mbar_init(smem_u32(&o_done[g]), 1);
       mbar_init(smem_u32(&s_read[g]), kRows);
       mbar_init(smem_u32(&shifted[g]), kRows);
     }
-    mbar_init(smem_u32(posted), 2 * kRows);
-    mbar_init(smem_u32(taken), 2 * kRows);
     mbar_init(smem_u32(drained), 1);
-    for (int i = 0; i < kDirty; ++i) dirty[i] = 0;
+    for (int i = 0; i < 2 * kDirty; ++i) dirty[i] = 0;
     misc[1] = 0;
     fence_mbar_init();
   }
@@ -326,398 +390,424 @@ __global__ void __launch_bounds__(Plan<D, FP8>::kThreads, 1)
     fence_after();
   }
   const uint32_t tmem = uint32_t(misc[0]);
-  // The CTA's stretch [begin, end) of the line: an equal share; two tiles at least,
-  // one for each group.
+  // The groups' stretches of the line: equal shares of it, two tiles at least.
   const int64_t total = line[kv.batch];
-  const int sms = gridDim.x, cta = blockIdx.x;
-  const int ctas = total >= 2 * sms ? sms : int((total + 1) / 2);
-  const int64_t begin = cta < ctas ? total * cta / ctas : 0;
-  const int64_t end = cta < ctas ? total * (cta + 1) / ctas : 0;
+  const int all = 2 * gridDim.x, own = 2 * blockIdx.x;  // groups, this CTA's first one
+  const int groups = total >= 2 * all ? all : int((total + 1) / 2);
+  auto stretch = [&](int i) { return i < groups ? total * i / groups : total; };
+  const int64_t begins[2] = {stretch(own), stretch(own + 1)}, ends[2] = {begins[1], stretch(own + 2)};
 
-  // the piece that tile `at` of the line belongs to: its sequence, its first tile
-  auto piece_at = [&](int64_t at, int& b, int& piece, int& tile) {
+  // A walk over a group's segments: at a piece (its number in the sequence) and a
+  // tile of it; `left` tiles of the stretch.
+  struct Walk {
+    int64_t left;
+    int b, piece, tile, tiles, pieces;
+  };
+  auto walk_to = [&](int64_t at, int64_t end) {
+    Walk k;
+    k.left = end - at;
+    if (k.left <= 0) return k;
     int lo = 0, hi = kv.batch;  // the last b with line[b] <= at
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
       if (line[mid] <= at) lo = mid; else hi = mid;
     }
-    b = lo;
+    k.b = lo;
+    k.tiles = tiles_of(lo);
+    k.pieces = row_tiles(lo) * kv.kv_heads;
     const int64_t rem = at - line[lo];
-    const int nt = tiles_of(lo);
-    piece = int(rem / nt);
-    tile = int(rem - int64_t(piece) * nt);
+    k.piece = rem >> 31 ? int(rem / k.tiles) : int(uint32_t(rem) / uint32_t(k.tiles));
+    k.tile = int(rem - int64_t(k.piece) * k.tiles);
+    return k;
   };
-  auto segment_at = [&](int64_t at) {
+  auto next_segment = [&](Walk& k) {
     Segment w;
-    int piece, tile;
-    piece_at(at, w.b, piece, tile);
-    const int rts = row_tiles(w.b), nt = tiles_of(w.b), n = count[w.b];
-    w.j = piece / rts;
-    w.i0 = (piece - w.j * rts) * TT;
-    w.tok0 = first[w.b] + w.i0;
+    const int b = k.b, rts = row_tiles(b), n = count[b];
+    w.b = b;
+    w.j = k.piece / rts;
+    w.i0 = (k.piece - w.j * rts) * TT;
+    w.tok0 = first[b] + w.i0;
     w.rows = n - w.i0 < TT ? n - w.i0 : TT;
-    w.len = lens[w.b];
+    w.len = lens[b];
     w.past = w.len - n;
     w.most = n < 32 * a.words ? n : 32 * a.words;
     w.lo = low_of(w.past);
     w.all_hi = w.past > 0 ? w.past : 0;
     // the deepest row's window
     w.all_lo = a.window > 0 && w.past + w.most > a.window ? w.past + w.most - a.window : 0;
-    const int64_t left = end - at;
-    w.k0 = w.lo / kKeys + tile;
-    w.k1 = w.k0 + (left < nt - tile ? int(left) : nt - tile);
-    w.begins = tile == 0;
-    w.ends = left >= nt - tile;
+    w.begins = k.tile == 0;
+    w.ends = k.left >= k.tiles - k.tile;
+    const int nk = w.ends ? k.tiles - k.tile : int(k.left);
+    w.k0 = w.lo / kKeys + k.tile;
+    w.k1 = w.k0 + nk;
+    k.left -= nk;
+    k.tile = 0;
+    if (++k.piece == k.pieces && k.left > 0) {
+      do ++k.b; while (line[k.b + 1] == line[k.b]);
+      k.piece = 0;
+      k.tiles = tiles_of(k.b);
+      k.pieces = row_tiles(k.b) * kv.kv_heads;
+    }
     return w;
   };
-  // the record of the piece that begins here and goes on in the next CTAs
-  if (tid == 0 && a.joins) {
+  // the record of the piece that begins in a group's stretch and goes on in the next
+  if (tid < 2 && a.joins) {
     int4 rec = make_int4(0, 0, 0, 0);
+    const int64_t begin = begins[tid], end = ends[tid];
     if (end > begin) {
-      int b, piece, tile;
-      piece_at(end - 1, b, piece, tile);
-      const int nt = tiles_of(b);
-      const int64_t from = end - 1 - tile;
-      if (from >= begin && from + nt > end) {
-        const int last = int(((from + nt) * ctas + total - 1) / total) - 1;
-        const int rts = row_tiles(b), i0 = (piece % rts) * TT, n = count[b] - i0;
-        rec = make_int4(last - cta + 1, first[b] + i0, n < TT ? n : TT, piece / rts);
+      const Walk k = walk_to(end - 1, end);
+      const int64_t from = end - 1 - k.tile;
+      if (from >= begin && from + k.tiles > end) {
+        const int last = int(((from + k.tiles) * groups + total - 1) / total) - 1;
+        const int rts = row_tiles(k.b), i0 = (k.piece % rts) * TT, n = count[k.b] - i0;
+        rec = make_int4(last - (own + tid) + 1, first[k.b] + i0, n < TT ? n : TT, k.piece / rts);
       }
     }
-    a.joins[cta] = rec;
+    a.joins[own + tid] = rec;
   }
-  const int br_shift = kv.page_shift;  // rows of a box: a page, 16 .. 128
-  const int boxes = kKeys >> br_shift;
+  const int boxes = kKeys >> kv.page_shift;  // pages of a tile
+
+  // A group's Q, rows of TT tokens from a token on, of a kv head.
+  auto load_q = [&](int g, int token, int j) {
+    const uint32_t bar = smem_u32(&q_full[g]);
+    mbar_arrive_expect_tx(bar, uint32_t(TT * G * 128 * P::kHalves));
+    for (int h = 0; h < P::kHalves; ++h)
+      tma_q(sbase + g * P::kTile + h * P::kSpan, &map_q, 64 * h, j * G, token, bar);
+  };
 
   if (warp >= kMmaWarp) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(P::kOtherRegs));
-    if (warp == kLoadWarp) {
-      // ============================================================ copies
-      uint32_t n = 0;   // slots used
-      uint32_t seq = 0, asked = 0;  // segments, Q tiles
-      uint32_t nt = 0;  // tiles
-      bool ok = true;
-      for (int64_t at = begin; ok && at < end; ++seq) {
-        const Segment w = segment_at(at);
-        at += w.k1 - w.k0;
-        const uint32_t qb = seq & 1u;
-        // a Q tile is free when the last score products of the segment are done
-        if (seq >= 2)
-          ok = __all_sync(kAll, wait(&q_free[qb], ((seq >> 1) - 1) & 1u, quit, a.err));
-        if (!ok) break;
-        if (lane == 0) {
-          const uint32_t bar = smem_u32(&q_full[qb]);
-          mbar_arrive_expect_tx(bar, uint32_t(TT * G * 128 * P::kHalves));
-          for (int h = 0; h < P::kHalves; ++h)
-            tma_q(sbase + qb * P::kTile + h * P::kSpan, &map_q, 64 * h, w.j * G, w.tok0, bar);
-        }
-        __syncwarp();
-        ++asked;
-        auto look = [&](int kt) {
-          const int t = kt * kKeys + (lane << br_shift);
-          const bool in = lane < boxes && t < w.len && t + (1 << br_shift) > w.lo;
-          return in ? paged_page(kv, w.b, t, a.err) : -1;
-        };
-        int ahead = look(w.k0);
-        for (int kt = w.k0; ok && kt < w.k1; ++kt, ++nt) {
-          const int page = ahead;
-          if (kt + 1 < w.k1) ahead = look(kt + 1);  // the next tile's, while this one is copied
-          const uint32_t got = __ballot_sync(kAll, page >= 0);
-          const int64_t row =
-              page >= 0 ? paged_row(kv, page, w.j, kt * kKeys + (lane << br_shift)) : 0;
-          const uint32_t bytes_row = 128u * P::kHalves;
-          for (int part = 0; part < 2; ++part, ++n) {  // K, then V
-            if constexpr (FP8) {
-              const uint32_t s = n % P::kRaws, turn = n / P::kRaws;
-              ok = turn == 0 || wait(&raw_empty[s], (turn - 1) & 1u, quit, a.err);
-              ok = __all_sync(kAll, ok);
-              if (!ok) break;
-              const uint32_t bar = smem_u32(&raw_full[s]);
-              if (lane == 0) {
-                have[nt & 7u] = got;
-                mbar_arrive_expect_tx(bar, __popc(got) * (uint32_t(part ? D : D + 8) << br_shift));
-              }
-              __syncwarp();
-              if (page >= 0) {
-                const uint32_t dst = sbase + P::kOffRaw + s * P::kRaw;
-                const uint8_t* src = static_cast<const uint8_t*>(part ? kv.v : kv.k) + row * D;
-                bulk_copy(dst + ((uint32_t(lane) * D) << br_shift), src, uint32_t(D) << br_shift,
-                          bar);
-                if (part == 0) {  // both scales with K: the softmax needs them after S
-                  const uint32_t so = dst + kKeys * D + (uint32_t(lane) << (br_shift + 2));
-                  bulk_copy(so, kv.k_scales + row, 4u << br_shift, bar);
-                  bulk_copy(so + kKeys * 4, kv.v_scales + row, 4u << br_shift, bar);
-                }
-              }
-            } else {
-              const uint32_t s = n % P::kSlots, turn = n / P::kSlots;
-              ok = turn == 0 || wait(&empty[s], (turn - 1) & 1u, quit, a.err);
-              ok = __all_sync(kAll, ok);
-              if (!ok) break;
-              const uint32_t bar = smem_u32(&full[s]);
-              if (lane == 0) {
-                have[nt & 7u] = got;
-                mbar_arrive_expect_tx(bar, __popc(got) * (bytes_row << br_shift));
-              }
-              __syncwarp();
-              if (page >= 0) {
-                const uint32_t dst =
-                    sbase + P::kOffKv + s * P::kTile + (uint32_t(lane) << (br_shift + 7));
-                for (int h = 0; h < P::kHalves; ++h)
-                  tma_rows(dst + h * P::kSpan, part ? &map_v : &map_k, 64 * h, int(row), bar);
-              }
-            }
+    const int64_t tiles_all[2] = {ends[0] - begins[0], ends[1] - begins[1]};
+    // the slot of a group's tile i, K or V
+    auto slot_of = [](int g, int value, uint32_t i) {
+      return ((i % P::kDepth) * 2 + g) * 2 + value;
+    };
+    const int in_page = (1 << kv.page_shift) - 1;
+    if (warp >= kPlanWarp && warp < kPlanWarp + 2) {
+      // ============================================================== plans
+      // A lane a page, then (FP8) four tokens a lane.  A tile's entries are asked for
+      // two tiles ahead, its scales one; it is planned when the one kAhead before it is
+      // used up: its places in the rings are free then.
+      const int g = warp - kPlanWarp;
+      Walk walk = walk_to(begins[g], ends[g]);
+      struct Next {  // a tile: what is needed of its segment
+        int b, j, kt, k0, k1, lo, len, all_lo, all_hi, segment;
+      };
+      Next u;
+      u.segment = 0;
+      u.kt = u.k1 = 0;
+      int token = -1;
+      // goes on to the next tile; false at the end
+      auto advance = [&] {
+        if (++u.kt < u.k1) return true;
+        if (walk.left <= 0) return false;
+        const Segment w = next_segment(walk);
+        u = {w.b, w.j, w.k0, w.k0, w.k1, w.lo, w.len, w.all_lo, w.all_hi, u.segment + 1};
+        token = w.tok0;
+        return true;
+      };
+      auto look = [&] {  // the table's entry of this lane's page
+        const int t = u.kt * kKeys + (lane << kv.page_shift);
+        const bool in = lane < boxes && t < u.len && t + (1 << kv.page_shift) > u.lo;
+        return in ? __ldcg(kv.page_table + int64_t(u.b) * kv.pages_per_seq + (t >> kv.page_shift))
+                  : -1;
+      };
+      float v[2][kKeys / 32];
+      auto load_scales = [&](const Next& n, int row0) {
+        if constexpr (FP8) {
+#pragma unroll
+          for (int i = 0; i < kKeys / 32; ++i) {
+            const int r = 32 * i + lane, t = n.kt * kKeys + r;
+            const int first_row = __shfl_sync(kAll, row0, r >> kv.page_shift);
+            const bool some = first_row >= 0 && t >= n.lo && t < n.len;
+            v[0][i] = some ? __ldcg(kv.k_scales + first_row + (r & in_page)) : 0.f;
+            v[1][i] = some ? __ldcg(kv.v_scales + first_row + (r & in_page)) : 0.f;
           }
         }
+      };
+      auto row_of = [&](int entry, int j) {
+        if (entry >= kv.num_pages) {
+          flag_error(a.err, kErrShape);
+          entry = -1;
+        }
+        return entry >= 0 ? (entry * kv.kv_heads + j) << kv.page_shift : -1;
+      };
+      bool more = advance();
+      if (more) {
+        if (lane == 0) load_q(g, token, u.j);
+        Next now = u;
+        int row = row_of(look(), u.j);
+        load_scales(now, row);
+        more = advance();
+        int entry = more ? look() : -1;
+        for (uint32_t i = 0;; ++i) {
+          const uint32_t ring = i % kAhead;
+          if (i >= kAhead &&
+              !__all_sync(kAll, wait(&freed[g * kAhead + ring], (i / kAhead - 1u) & 1u, quit, a.err)))
+            break;
+          const uint32_t got = __ballot_sync(kAll, row >= 0);
+          const int t0 = now.kt * kKeys;
+          auto within = [&](int t) { return int16_t(t < t0 ? 0 : t - t0 > kKeys ? kKeys : t - t0); };
+          Tile* d = plans + g * kAhead + ring;
+          if (lane < 8) d->row[lane] = row;
+          if (lane == 0) {
+            const bool last = now.kt + 1 == now.k1;
+            d->got = got;
+            d->from = within(now.lo);
+            d->upto = within(now.len);
+            d->seen0 = within(now.all_lo);
+            d->seen1 = within(now.all_hi);
+            d->segment = now.segment;
+            d->ends = (now.kt == now.k0 ? 1 : 0) | (last ? 2 : 0);
+            d->next_token = last && more ? token : -1;
+            d->next_head = u.j;
+          }
+          if constexpr (FP8) {
+            float* to = scales + (g * kAhead + ring) * 2 * kKeys;
+            bool bad = false;
+#pragma unroll
+            for (int e = 0; e < kKeys / 32; ++e) {
+              const int r = 32 * e + lane, t = t0 + r;
+              // a value row's scale, as an element of V
+              if ((t < now.all_lo || t >= now.all_hi) && !(fabsf(v[1][e]) <= kFiniteMax)) {
+                v[1][e] = 0.f;
+                bad = true;
+              }
+              to[r] = v[0][e];
+              to[kKeys + r] = v[1][e];
+            }
+            if (bad) dirty[g * kDirty + now.segment % kDirty] = now.segment;
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&planned[g * kAhead + ring]));
+          if (!more) break;
+          now = u;
+          row = row_of(entry, u.j);
+          load_scales(now, row);
+          more = advance();
+          if (more) entry = look();
+        }
       }
-      if (!ok) {  // gave up: the copies in flight land before the CTA ends
-        uint64_t* f = FP8 ? raw_full : full;
-        const uint32_t m = FP8 ? (P::kRaws ? P::kRaws : 1) : P::kSlots;
-        for (uint32_t i = 1; i <= m && i <= n; ++i)
-          (void)mbar_wait_bounded(smem_u32(&f[(n - i) % m]), ((n - i) / m) & 1u);
-        for (uint32_t i = 1; i <= 2 && i <= asked; ++i)
-          (void)mbar_wait_bounded(smem_u32(&q_full[(asked - i) & 1u]), ((asked - i) >> 1) & 1u);
+    } else if (warp >= kCopyWarp && warp < kPlanWarp) {
+      // ============================================================ copies
+      const int g = (warp - kCopyWarp) >> 1, value = (warp - kCopyWarp) & 1;
+      const uint32_t parts = uint32_t(tiles_all[g]);
+      // E4M3 codes are copied into their slot's last bytes (64 dims), or second span
+      // (128)
+      constexpr uint32_t kRaw = FP8 ? P::kTile / 2 : 0;
+      constexpr int kPieces = P::kRow / 16, kStep = 32 / kPieces;  // rows for 32 lanes
+      const int c = lane % kPieces, r0 = lane / kPieces;
+      const uint32_t whole = kAll >> (32 - boxes);
+      // Whether part i may be asked for: its tile is planned, its slot is free.
+      auto may_ask = [&](uint32_t i, bool block) {
+        uint64_t* p = &planned[g * kAhead + i % kAhead];
+        uint64_t* e = &empty[slot_of(g, value, i)];
+        const uint32_t pp = (i / kAhead) & 1u, ep = (i / P::kDepth - 1u) & 1u;
+        bool go;
+        if (block)
+          go = wait(p, pp, quit, a.err) && (i < P::kDepth || wait(e, ep, quit, a.err));
+        else
+          go = mbar_test_wait(smem_u32(p), pp) && (i < P::kDepth || mbar_test_wait(smem_u32(e), ep));
+        return bool(__all_sync(kAll, go));
+      };
+      auto ask = [&](uint32_t i) {
+        const Tile* d = plans + g * kAhead + i % kAhead;
+        const uint32_t s = slot_of(g, value, i), bar = smem_u32(&full[s]);
+        if (lane == 0)
+          mbar_arrive_expect_tx(bar, __popc(d->got) * (uint32_t(P::kRow) << kv.page_shift));
+        __syncwarp();
+        const int row = lane < boxes ? d->row[lane] : -1;
+        const uint32_t dst = sbase + P::kOffKv + s * P::kTile + kRaw;
+        if (row >= 0) {
+          if constexpr (FP8) {
+            const uint8_t* pool = static_cast<const uint8_t*>(value ? kv.v : kv.k);
+            bulk_copy(dst + ((uint32_t(lane) * P::kRow) << kv.page_shift),
+                      pool + int64_t(row) * P::kRow, uint32_t(P::kRow) << kv.page_shift, bar);
+          } else {
+            for (int h = 0; h < P::kHalves; ++h)
+              tma_rows(dst + (uint32_t(lane) << (kv.page_shift + 7)) + h * P::kSpan,
+                       value ? &map_v : &map_k, 64 * h, row, bar);
+          }
+        }
+        __syncwarp();
+      };
+      // A part that has landed is turned into bf16, made safe, handed to the tensor
+      // cores.  E4M3 codes: in place, in rising order of rows: a row's bf16 elements
+      // end before the codes of the next ones begin, or lie where its own were.  (What
+      // few tiles need is a function of its own: in the loop it cost 80 us of 320, 48
+      // ragged sequences of 64 / 8 heads of 64.)
+      constexpr int kIlp = 4;
+      constexpr int kSteps = FP8 ? kKeys / (kStep * kIlp) : 1;
+      uint32_t odd = 0u;  // carries into the top bits of bytes from 0x7f and 0xff, NaN
+      bool bad = false;
+      auto work = [&](uint32_t n, int step) {
+        uint8_t* tile = smem + P::kOffKv + slot_of(g, value, n) * P::kTile;
+        if constexpr (FP8) {
+          uint4 x[kIlp];
+#pragma unroll
+          for (int i = 0; i < kIlp; ++i)
+            x[i] = *reinterpret_cast<const uint4*>(
+                tile + kRaw + ((step * kIlp + i) * kStep + r0) * P::kRow + 16 * c);
+          __syncwarp();
+#pragma unroll
+          for (int i = 0; i < kIlp; ++i) {
+            const int r = (step * kIlp + i) * kStep + r0;
+            odd |= ((x[i].x & 0x7f7f7f7fu) + 0x01010101u) | ((x[i].y & 0x7f7f7f7fu) + 0x01010101u) |
+                   ((x[i].z & 0x7f7f7f7fu) + 0x01010101u) | ((x[i].w & 0x7f7f7f7fu) + 0x01010101u);
+            uint4 d0, d1;
+            e4m3x4_bf16(x[i].x, d0.x, d0.y);
+            e4m3x4_bf16(x[i].y, d0.z, d0.w);
+            e4m3x4_bf16(x[i].z, d1.x, d1.y);
+            e4m3x4_bf16(x[i].w, d1.z, d1.w);
+            uint8_t* dst = tile + (c >> 2) * P::kSpan + r * 128;
+            const int ch = (c & 3) * 2;
+            *reinterpret_cast<uint4*>(dst + ((ch ^ (r & 7)) << 4)) = d0;
+            *reinterpret_cast<uint4*>(dst + (((ch + 1) ^ (r & 7)) << 4)) = d1;
+          }
+          __syncwarp();
+        }
+        if (step + 1 == kSteps) {
+          const Tile* d = plans + g * kAhead + n % kAhead;
+          const bool edge = d->from > 0 || d->upto < kKeys || d->got != whole;
+          const bool cut = d->seen0 > d->from || d->seen1 < d->upto;
+          const bool nan = FP8 && __any_sync(kAll, (odd & 0x80808080u) != 0u);
+          if (nan || (value && (edge || (!FP8 && cut)))) {
+            bad = tree_make_safe<D, FP8>(tile, d, value, nan, kv.page_shift);
+            __syncwarp();
+          }
+          odd = 0u;
+        }
+      };
+      auto hand_over = [&](uint32_t n) {
+        const Tile* d = plans + g * kAhead + n % kAhead;
+        if (bad) dirty[g * kDirty + d->segment % kDirty] = d->segment;
+        bad = false;
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&ready[slot_of(g, value, n)]));
+      };
+      uint32_t asked = 0, done = 0;
+      if (!FP8 && !value) {  // bf16 keys need nothing: scores of masked tokens are replaced
+        for (; asked < parts && may_ask(asked, true); ++asked) ask(asked);
+      } else {
+        for (int step = 0; done < parts;) {
+          // as many parts on their way as there are slots; it is waited for one only where
+          // nothing else is left to do
+          while (asked < parts && asked - done < P::kDepth && may_ask(asked, false)) ask(asked++);
+          if (asked == done) {
+            if (!may_ask(asked, true)) break;
+            continue;
+          }
+          if (step == 0 && !__all_sync(kAll, wait(&full[slot_of(g, value, done)],
+                                                   (done / P::kDepth) & 1u, quit, a.err)))
+            break;
+          work(done, step);
+          if (++step < kSteps) continue;
+          step = 0;
+          hand_over(done++);
+        }
       }
+      // nothing lands after the CTA's end (where the warp gave up)
+      for (uint32_t i = 1; i <= P::kDepth && i <= asked; ++i)
+        (void)mbar_wait_bounded(smem_u32(&full[slot_of(g, value, asked - i)]),
+                                ((asked - i) / P::kDepth) & 1u);
     } else if (warp == kMmaWarp) {
       // ========================================================== products
-      // One warp for both groups, whichever is ready.  The commits free the slots,
-      // so that a copy begins as soon as the products are through with its place.
-      // Products finish in order, so scores that are there say that the P V issued
-      // before them is done.
+      // One warp for both groups, whichever is ready: eight lanes a group each test
+      // what one of its next products waits for.  The commits free the slots, so that
+      // a copy begins as soon as the products are through with its place.  Products
+      // finish in order, so scores that are there say that the P V issued before them
+      // is done.
       const uint32_t kv0 = sbase + P::kOffKv;
-      uint32_t n = 0, seq = 0, my0 = 0, my1 = 0;  // slots; segments; tiles of the groups
       bool ok = tmem == 0;  // all columns are ours, so they begin at 0
       if (!ok && lane == 0) {
         *quit = 1;
         flag_error(a.err, kErrShape);
       }
-      auto scores = [&](auto gc, uint32_t slot) {
-        constexpr int g = decltype(gc)::value;
-        const uint64_t q = desc_k(sbase + (seq & 1u) * P::kTile), k = desc_k(kv0 + slot * P::kTile);
-#pragma unroll
-        for (int i = 0; i < D / 16; ++i) {
-          const uint64_t off = ((i >> 2) * P::kSpan + (i & 3) * 32) >> 4;
-          mma_ss(P::kColS(g), q + off, k + off, idesc(kKeys, false), i > 0);
+      // (Loops that are not unrolled, and one code for both groups: the instructions of
+      // all roles have to fit the caches.  Unrolled, 78 us for 68, 32 ragged sequences
+      // of 16 / 4 heads of 128.)
+      auto scores = [&](uint32_t g, uint32_t i) {
+        const uint32_t slot = slot_of(g, 0, i);
+        const uint64_t q = desc_k(sbase + g * P::kTile), k = desc_k(kv0 + slot * P::kTile);
+#pragma unroll 1
+        for (int e = 0; e < D / 16; ++e) {
+          const uint64_t off = ((e >> 2) * P::kSpan + (e & 3) * 32) >> 4;
+          mma_ss(P::kColS(g), q + off, k + off, idesc(kKeys, false), e > 0);
         }
         commit(smem_u32(&s_full[g]));
         commit(smem_u32(&empty[slot]));
       };
-      auto values = [&](auto gc, uint32_t slot, uint32_t more) {
-        constexpr int g = decltype(gc)::value;
+      auto values = [&](uint32_t g, uint32_t i, int ends) {
+        const uint32_t slot = slot_of(g, 1, i);
         const uint64_t v = desc_mn(kv0 + slot * P::kTile, P::kHalves > 1 ? P::kSpan : 1024);
-#pragma unroll
+#pragma unroll 1
         for (int k = 0; k < kKeys / 16; ++k)
-          mma_ts(P::kColO(g), P::kColP(g) + 8 * k, v + k * (2048 >> 4),
-                 idesc(D, true), k > 0 ? 1u : more);
+          mma_ts(P::kColO(g), P::kColP(g) + 8 * k, v + k * (2048 >> 4), idesc(D, true),
+                 k > 0 ? 1u : uint32_t(!(ends & 1)));
+        commit(smem_u32(&empty[slot]));
+        if (P::kOwnP || __any_sync(kAll, ends & 2)) commit(smem_u32(&o_done[g]));
       };
-      auto key_bar = [&](uint32_t m) {
-        return smem_u32(FP8 ? &ready[m % P::kSlots] : &full[m % P::kSlots]);
-      };
-      auto phase = [&](uint32_t m) { return (m / P::kSlots) & 1u; };
-      using G0 = std::integral_constant<int, 0>;
-      using G1 = std::integral_constant<int, 1>;
-      for (int64_t at = begin; ok && at < end; ++seq) {
-        const Segment w = segment_at(at);
-        const uint32_t nk = __shfl_sync(kAll, w.k1 - w.k0, 0);
-        at += nk;
-        ok = __all_sync(kAll, wait(&q_full[seq & 1u], (seq >> 1) & 1u, quit, a.err));
-        if (!ok) break;
-        const uint32_t nk0 = (nk + 1) / 2, nk1 = nk / 2;
-        // of each group: products P V issued, scores issued
-        uint32_t v0 = 0, s0 = 0, v1 = 0, s1 = 0;
-        uint64_t since = 0;  // of the idle stretch
-        auto tile = [&](auto gc, uint32_t nkg, uint32_t& vi, uint32_t& si, uint32_t& my) {
-          constexpr int g = decltype(gc)::value;
-          bool did = false;
-          const uint32_t m = n + 2 * (2 * vi + g);  // the tile's K
-          if (vi < si) {
-            const bool go =
-                mbar_test_wait(smem_u32(&p_full[g]), my & 1u) &&
-                mbar_test_wait(smem_u32(&ready[(m + 1) % P::kSlots]), phase(m + 1));
-            if (__all_sync(kAll, go)) {
-              fence_after();
-              values(gc, (m + 1) % P::kSlots, vi > 0);
-              commit(smem_u32(&empty[(m + 1) % P::kSlots]));
-              if (P::kOwnP || vi + 1 == nkg) commit(smem_u32(&o_done[g]));
-              ++vi;
-              ++my;
-              did = true;
-            }
-          }
-          // the next scores: with 128 dims once the P V that lie there are issued,
-          // else once those before are read (my - vi tiles were before this segment)
-          if (si < nkg && (P::kOwnP || si == vi)) {
-            const uint32_t ms = n + 2 * (2 * si + g);
-            const bool go =
-                (!P::kOwnP || mbar_test_wait(smem_u32(&s_read[g]), (my - vi + si - 1) & 1u)) &&
-                mbar_test_wait(key_bar(ms), phase(ms));
-            if (__all_sync(kAll, go)) {
-              fence_after();
-              scores(gc, ms % P::kSlots);
-              ++si;
-              did = true;
-            }
-          }
-          return did;
+      // Of each group: tiles, P V issued, scores issued, segments whose scores are all
+      // issued.  A test of a barrier takes some 150 cycles, so all of a round go out
+      // together, asked for in one vote each.  (One after the other, as needed, a round
+      // of both groups' products took 6000 cycles; a lane for each test, whose
+      // addresses then differ, 700 without any product.)
+      uint32_t n0 = uint32_t(tiles_all[0]), n1 = uint32_t(tiles_all[1]);
+      uint32_t v0 = 0, s0 = 0, e0 = 0, v1 = 0, s1 = 0, e1 = 0;
+      uint64_t since = 0;  // of the idle stretch
+      uint32_t g = 0;      // the group whose turn it is: that of v0, s0, e0, n0
+      bool before = true;  // the other had something in its turn
+      for (uint32_t idle = 0; ok && (v0 < n0 || v1 < n1);) {
+        auto there = [](uint64_t* bar, uint32_t phase) {
+          return mbar_test_wait(smem_u32(bar), phase & 1u);
         };
-        for (uint32_t idle = 0; v0 < nk0 || v1 < nk1;) {
-          bool did = tile(G0{}, nk0, v0, s0, my0);
-          did |= tile(G1{}, nk1, v1, s1, my1);
-          if (did) {
-            idle = 0;
-          } else if ((++idle & 63u) == 0u) {
-            if (idle == 64u) since = globaltimer_ns();
-            if (globaltimer_ns() - since > kWaitLimitNs && lane == 0) {
-              *quit = 1;
-              flag_error(a.err, kErrTimeout);
-            }
-            if (__any_sync(kAll, *quit)) {
-              ok = false;
-              break;
-            }
-          }
+        const bool weights = there(&p_full[g], v0);
+        const bool value = there(&ready[slot_of(g, 1, v0)], v0 / P::kDepth);
+        const bool key = there((FP8 ? ready : full) + slot_of(g, 0, s0), s0 / P::kDepth);
+        const bool read = !P::kOwnP || there(&s_read[g], s0 - 1u);
+        const bool query = there(&q_full[g], e0);
+        const int v_ends = plans[g * kAhead + v0 % kAhead].ends;
+        const int s_ends = plans[g * kAhead + s0 % kAhead].ends;
+        const bool pv = __all_sync(kAll, weights && value) && v0 < s0;
+        // the next scores: with 128 dims once the P V that lie there are issued, else once
+        // those before are read
+        const bool qk = __all_sync(kAll, key && read && query) && s0 < n0 &&
+                        (P::kOwnP || s0 == v0 + pv);
+        if (pv | qk) fence_after();
+        if (pv) values(g, v0++, v_ends);
+        if (qk) {
+          scores(g, s0++);
+          e0 += (s_ends >> 1) & 1;
         }
-        if (!ok) break;
-        n += 2 * nk;
+        const bool did = pv | qk | before;
+        before = pv | qk;
+        // the other group's turn
+        auto swap = [](uint32_t& x, uint32_t& y) {
+          const uint32_t t = x;
+          x = y;
+          y = t;
+        };
+        swap(n0, n1);
+        swap(v0, v1);
+        swap(s0, s1);
+        swap(e0, e1);
+        g ^= 1u;
+        if (did) {
+          idle = 0;
+        } else if ((++idle & 63u) == 0u) {
+          if (idle == 64u) since = globaltimer_ns();
+          if (globaltimer_ns() - since > kWaitLimitNs && lane == 0) {
+            *quit = 1;
+            flag_error(a.err, kErrTimeout);
+          }
+          if (__any_sync(kAll, *quit)) ok = false;
+        }
       }
       // nothing of the tensor cores is under way when the CTA ends
       commit(smem_u32(drained));
       (void)mbar_wait_bounded(smem_u32(drained), 0);
       __syncwarp();
-    } else if (warp >= kFixWarp) {
-      // ===================================== V tiles made safe; FP8 -> bf16
-      const int ft = tid - kFixWarp * 32;
-      uint32_t n = 0, nt = 0;
-      int seq = 0;
-      bool ok = true;
-      for (int64_t at = begin; ok && at < end;) {
-        const Segment w = segment_at(at);
-        at += w.k1 - w.k0;
-        ++seq;
-        for (int kt = w.k0; ok && kt < w.k1; ++kt, ++nt) {
-          const int t0 = kt * kKeys;
-          const bool cut = t0 < w.all_lo || t0 + kKeys > w.all_hi;
-          for (int part = 0; part < 2; ++part, ++n) {
-            const uint32_t s = n % P::kSlots, turn = n / P::kSlots;
-            uint8_t* tile = smem + P::kOffKv + s * P::kTile;
-            if constexpr (FP8) {
-              const uint32_t rs = n % P::kRaws;
-              ok = wait(&raw_full[rs], (n / P::kRaws) & 1u, quit, a.err) &&
-                   (turn == 0 || wait(&empty[s], (turn - 1) & 1u, quit, a.err));
-              if (!ok) break;
-              const uint8_t* raw = smem + P::kOffRaw + rs * P::kRaw;
-              const uint32_t got = have[nt & 7u];
-              const uint32_t whole = kAll >> (32 - boxes);
-              const bool sure = !cut && got == whole;
-              bool bad = false;
-              constexpr int kC = D / 16;  // 16-byte pieces of a raw row
-              constexpr int kIlp = 4;  // pieces in work at once
-#pragma unroll 1
-              for (int i0 = 0; i0 < kKeys * kC; i0 += kIlp * kFixers) {
-                uint4 x4[kIlp];
-#pragma unroll
-                for (int i = 0; i < kIlp; ++i) {
-                  const int u = i0 + i * kFixers + ft;
-                  x4[i] = u < kKeys * kC ? *reinterpret_cast<const uint4*>(raw + u * 16)
-                                         : make_uint4(0u, 0u, 0u, 0u);
-                }
-#pragma unroll
-                for (int i = 0; i < kIlp; ++i) {
-                  const int u = i0 + i * kFixers + ft, r = u / kC, c = u % kC;
-                  if (u >= kKeys * kC) break;
-                  uint4 x = x4[i];
-                  if (!sure) {
-                    const int t = t0 + r;
-                    if (t < w.lo || t >= w.len || !((got >> (r >> br_shift)) & 1u)) {
-                      x = make_uint4(0u, 0u, 0u, 0u);
-                    } else if (part) {
-                      uint32_t* xs[4] = {&x.x, &x.y, &x.z, &x.w};
-#pragma unroll
-                      for (int e = 0; e < 4; ++e) {
-                        // bytes 0x7f and 0xff, NaN, become 0
-                        const uint32_t nan = __vcmpeq4(*xs[e] & 0x7f7f7f7fu, 0x7f7f7f7fu);
-                        bad |= nan != 0u;
-                        *xs[e] &= ~nan;
-                      }
-                    }
-                  }
-                  const uint4 d0 = make_uint4(e4m3x2_bf16x2(x.x), e4m3x2_bf16x2(x.x >> 16),
-                                              e4m3x2_bf16x2(x.y), e4m3x2_bf16x2(x.y >> 16));
-                  const uint4 d1 = make_uint4(e4m3x2_bf16x2(x.z), e4m3x2_bf16x2(x.z >> 16),
-                                              e4m3x2_bf16x2(x.w), e4m3x2_bf16x2(x.w >> 16));
-                  uint8_t* dst = tile + (c >> 2) * P::kSpan + r * 128;
-                  const int ch = (c & 3) * 2;
-                  *reinterpret_cast<uint4*>(dst + ((ch ^ (r & 7)) << 4)) = d0;
-                  *reinterpret_cast<uint4*>(dst + (((ch + 1) ^ (r & 7)) << 4)) = d1;
-                }
-              }
-              if (part == 0) {
-                const float* sc = reinterpret_cast<const float*>(raw + kKeys * D);
-                for (int i = ft; i < 2 * kKeys; i += kFixers) {
-                  const int r = i & (kKeys - 1), t = t0 + r;
-                  float v = sc[i];
-                  if (!sure) {
-                    if (t < w.lo || t >= w.len || !((got >> (r >> br_shift)) & 1u)) {
-                      v = 0.f;
-                    } else if (i >= kKeys && !(fabsf(v) <= kFiniteMax)) {
-                      v = 0.f;  // a value row that some must not see: as an element of V
-                      bad = true;
-                    }
-                  }
-                  scales[(nt & 3u) * 2 * kKeys + i] = v;
-                }
-              }
-              if (bad) dirty[seq & (kDirty - 1)] = seq;
-              asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-              mbar_arrive(smem_u32(&raw_empty[rs]));
-              mbar_arrive(smem_u32(&ready[s]));
-            } else {
-              if (part == 0) continue;  // K: scores of masked tokens are replaced
-              ok = wait(&full[s], turn & 1u, quit, a.err);
-              if (!ok) break;
-              const uint32_t got = have[nt & 7u];
-              if (cut || got != kAll >> (32 - boxes)) {
-                bool bad = false;
-                for (int r = ft; r < kKeys; r += kFixers) {
-                  const int t = t0 + r;
-                  const bool none =
-                      t < w.lo || t >= w.len || !((got >> (r >> br_shift)) & 1u);
-                  for (int c = 0; c < 8 * P::kHalves; ++c) {
-                    // pieces in another order for every row: no bank conflicts
-                    uint4* p = reinterpret_cast<uint4*>(tile + (c >> 3) * P::kSpan + r * 128 +
-                                                        ((((c & 7) + r) & 7) << 4));
-                    if (none) {
-                      *p = make_uint4(0u, 0u, 0u, 0u);
-                      continue;
-                    }
-                    uint4 x = *p;
-                    uint32_t* xs[4] = {&x.x, &x.y, &x.z, &x.w};
-                    bool hit = false;
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                      if ((*xs[e] & 0x7f80u) == 0x7f80u) {
-                        *xs[e] &= 0xffff0000u;
-                        hit = true;
-                      }
-                      if ((*xs[e] & 0x7f800000u) == 0x7f800000u) {
-                        *xs[e] &= 0x0000ffffu;
-                        hit = true;
-                      }
-                    }
-                    if (hit) {
-                      *p = x;
-                      bad = true;
-                    }
-                  }
-                }
-                if (bad) dirty[seq & (kDirty - 1)] = seq;
-                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-              }
-              mbar_arrive(smem_u32(&ready[s]));
-            }
-          }
-        }
-      }
     }
   } else {
     // ============================================================== softmax
@@ -733,15 +823,12 @@ __global__ void __launch_bounds__(Plan<D, FP8>::kThreads, 1)
         a.softcap > 0.f ? fminf(fmaxf(mul * cap.per, -kFiniteMax), kFiniteMax) : mul;
     const int rt = r / G, rh = r - rt * G;
     const bool placed = a.window > 0 || a.slopes;  // depths matter
-    uint32_t tile0 = 0;          // tiles of the CTA before the segment
-    uint32_t my = 0, other = 0;  // tiles of this group, of the other
-    uint32_t done[2] = {0, 0};   // segments of the groups
-    uint32_t seq = 0, moved = 0;
+    uint32_t my = 0, seq = 0, moved = 0;  // tiles; segments; tiles where depths mattered
+    uint32_t asked = 1;  // Q tiles
     bool ok = true;
-    for (int64_t at = begin; ok && at < end; ++seq) {
-      const Segment w = segment_at(at);
-      const int nk = w.k1 - w.k0, nkg = (nk + 1 - g) / 2;
-      at += nk;
+    for (Walk walk = walk_to(begins[g], ends[g]); ok && walk.left > 0; ++seq) {
+      const Segment w = next_segment(walk);
+      const int nk = w.k1 - w.k0;
       const bool mine = rt < w.rows;
       const int h = w.j * G + rh;
       Sight see;
@@ -764,21 +851,24 @@ __global__ void __launch_bounds__(Plan<D, FP8>::kThreads, 1)
       }
       const float slope = GEN && a.slopes && mine ? __ldcg(a.slopes + h) * kLog2e : 0.f;
       float m = -INFINITY, l = 0.f;
-      bool holes = false;  // pages missing of a tile that the mask does not cut
-      if (nkg == 0 && r == 0) mbar_arrive(smem_u32(&q_free[seq & 1u]));
-      for (int i = 0; i < nkg; ++i, ++my) {
+      for (int i = 0; i < nk; ++i, ++my) {
         ok = __all_sync(kAll, wait(&s_full[g], my & 1u, quit, a.err));
         if (!ok) break;
         fence_after();
-        const uint32_t nt = tile0 + 2 * i + g;
-        if (i + 1 == nkg && r == 0) mbar_arrive(smem_u32(&q_free[seq & 1u]));
         [[maybe_unused]] bool seen_o = false;
-        const int t0 = (w.k0 + 2 * i + g) * kKeys;
-        const uint32_t got = have[nt & 7u];
+        const int t0 = (w.k0 + i) * kKeys;
+        const uint32_t ring = g * kAhead + my % kAhead;
+        const uint32_t got = plans[ring].got;
+        // the P V issued before these scores are done
+        if (!P::kOwnP && i > 0 && r == 0) mbar_arrive(smem_u32(&freed[g * kAhead + (my - 1) % kAhead]));
+        // Q is done with when the segment's last scores are there
+        if (r == 0 && i + 1 == nk && plans[ring].next_token >= 0) {
+          load_q(g, plans[ring].next_token, plans[ring].next_head);
+          ++asked;
+        }
         const bool whole = got == kAll >> (32 - boxes);
-        holes |= !whole && t0 >= w.all_lo && t0 + kKeys <= w.all_hi;
         const bool clear = __all_sync(kAll, t0 >= rlo && t0 + kKeys <= rhi) && whole;
-        const float* ks = scales + ((nt & 3u) * 2) * kKeys;
+        const float* ks = scales + ring * 2 * kKeys;
         // where the tile has new tokens and depths matter: how much higher in the
         // text a key lies than in the cache
         const float* shift = shifts + (2 * g + (moved & 1u)) * kKeys;
@@ -857,8 +947,8 @@ __global__ void __launch_bounds__(Plan<D, FP8>::kThreads, 1)
             }
             bits |= named;
           }
-          if (!((got >> ((32 * c) >> br_shift)) & 1u)) bits &= 0xffff0000u;
-          if (!((got >> ((32 * c + 16) >> br_shift)) & 1u)) bits &= 0x0000ffffu;
+          if (!((got >> ((32 * c) >> kv.page_shift)) & 1u)) bits &= 0xffff0000u;
+          if (!((got >> ((32 * c + 16) >> kv.page_shift)) & 1u)) bits &= 0x0000ffffu;
 #pragma unroll
           for (int e = 0; e < 32; ++e)
             if (!((bits >> e) & 1u)) x[e] = 0xff800000u;
@@ -942,6 +1032,7 @@ __global__ void __launch_bounds__(Plan<D, FP8>::kThreads, 1)
             if (!ok) break;
             fence_after();
           }
+          if (i > 0 && r == 0) mbar_arrive(smem_u32(&freed[g * kAhead + (my - 1) % kAhead]));
         }
         __syncwarp();
         tmem_st64(tp, pk);
@@ -956,55 +1047,31 @@ __global__ void __launch_bounds__(Plan<D, FP8>::kThreads, 1)
       }
       if (!ok) break;
 
-      // ---- the segment's end: both groups' maxima and sums, then their O's
-      const int nko = (nk + g) / 2;  // the other group's tiles
-      other += nko;
-      stat[g * kRows + r] = make_float2(m, l);
-      if (r == 0) misc[2 + g] = holes;
-      auto o_wait = [&](int e, uint32_t tiles_of_e) {
-        return wait(&o_done[e], (P::kOwnP ? tiles_of_e - 1 : done[e]) & 1u, quit, a.err);
-      };
-      if (nkg > 0) {
-        ok = __all_sync(kAll, o_wait(g, my));
-        if (!ok) break;
-      }
-      mbar_arrive(smem_u32(posted));
-      ok = __all_sync(kAll, wait(posted, seq & 1u, quit, a.err));
+      // ---- the segment's end
+      ok = __all_sync(kAll, wait(&o_done[g], (P::kOwnP ? my - 1 : seq) & 1u, quit, a.err));
       if (!ok) break;
-      if (nko > 0) {
-        ok = __all_sync(kAll, o_wait(1 - g, other));
-        if (!ok) break;
-      }
       fence_after();
-      const bool two = nk > 1;
-      const float2 sa = stat[r], sb = two ? stat[kRows + r] : make_float2(-INFINITY, 0.f);
-      const float mm = fmaxf(sa.x, sb.x), base = mm == -INFINITY ? 0.f : mm;
-      const float fa = ex2(sa.x - base), fb = ex2(sb.x - base);
-      const float ll = sa.y * fa + sb.y * fb;
+      if (r == 0) mbar_arrive(smem_u32(&freed[g * kAhead + (my - 1) % kAhead]));
       const int64_t row = int64_t(w.tok0 + rt) * heads + h;
-      const bool poisoned = *static_cast<volatile int*>(&dirty[(seq + 1) & (kDirty - 1)]) == int(seq + 1);
+      const bool poisoned =
+          *static_cast<volatile int*>(&dirty[g * kDirty + (seq + 1) % kDirty]) == int(seq + 1);
       const bool direct = w.begins && w.ends;
       float inv = 0.f;
-      if (direct && mine) inv = close_row(mm, ll, a.sinks, h, g == 0 ? a.lse : nullptr, row);
-      float* mypart = a.parts + (int64_t(cta) * 2 + (w.begins ? 1 : 0)) * P::kPartFloats;
+      if (direct && mine) inv = close_row(m, l, a.sinks, h, a.lse, row);
+      float* mypart = a.parts + (int64_t(own + g) * 2 + (w.begins ? 1 : 0)) * P::kPartFloats;
 #pragma unroll 1
-      for (int c = g * (D / 64); c < (g + 1) * (D / 64); ++c) {
+      for (int c = 0; c < D / 32; ++c) {
         uint32_t o[32];
         float of[32];
         __syncwarp();
-        tmem_ld32(tmem + lanes + P::kColO(0) + 32 * c, o);
+        tmem_ld32(to + 32 * c, o);
         wait_ld(o);
 #pragma unroll
-        for (int e = 0; e < 32; ++e) of[e] = __uint_as_float(o[e]) * fa;
-        if (two) {
-          tmem_ld32(tmem + lanes + P::kColO(1) + 32 * c, o);
-          wait_ld(o);
-#pragma unroll
-          for (int e = 0; e < 32; ++e) of[e] = fmaf(__uint_as_float(o[e]), fb, of[e]);
-        }
+        for (int e = 0; e < 32; ++e) of[e] = __uint_as_float(o[e]);
         if (mine && poisoned) {
-          const uint3 x = tree_not_finite<D, FP8>(kv, see, w.b, w.j, w.k0, w.k1, w.all_lo, w.all_hi,
-                                                  misc[2] || misc[3], 32 * c);
+          const uint3 x =
+              tree_not_finite<D, FP8>(kv, see, w.b, w.j, max(w.k0 * kKeys, w.lo),
+                                      min(w.k1 * kKeys, w.len), w.all_lo, w.all_hi, 32 * c);
 #pragma unroll
           for (int d = 0; d < 32; ++d) {
             if ((x.x >> d) & 1u) of[d] += INFINITY;
@@ -1027,17 +1094,14 @@ __global__ void __launch_bounds__(Plan<D, FP8>::kThreads, 1)
                 make_float4(of[4 * e], of[4 * e + 1], of[4 * e + 2], of[4 * e + 3]);
         }
       }
-      if (!direct && mine && g == 0) {
-        mypart[kRows * D + r] = mm;
-        mypart[kRows * (D + 1) + r] = ll;
+      if (!direct && mine) {
+        mypart[kRows * D + r] = m;
+        mypart[kRows * (D + 1) + r] = l;
       }
       fence_before();
-      mbar_arrive(smem_u32(taken));
-      ok = __all_sync(kAll, wait(taken, seq & 1u, quit, a.err));
-      ++done[0];
-      if (two) ++done[1];
-      tile0 += nk;
     }
+    // no copy of Q is under way when the CTA ends
+    if (r == 0 && begins[g] < ends[g]) (void)mbar_wait_bounded(smem_u32(&q_full[g]), (asked - 1) & 1u);
   }
   // ---- every role is done (or has given up): free the tensor memory
   fence_before();
@@ -1053,21 +1117,21 @@ __global__ void __launch_bounds__(Plan<D, FP8>::kThreads, 1)
 constexpr int kJoinThreads = kRows;
 template <int D>
 __global__ void __launch_bounds__(kJoinThreads)
-    paged_tree_join_kernel(const KernelArgs a, int ctas, int heads) {
+    paged_tree_join_kernel(const KernelArgs a, int groups, int heads) {
   constexpr int kJoin = 8;
   constexpr int kPartFloats = kRows * (D + 2);
   const int r = threadIdx.x;
   pdl_allow_next_grid();
   pdl_wait_prior_grid();
-  const int units = ctas * (D / 8);
+  const int units = groups * (D / 8);
   const int rt = r / a.group, rh = r - rt * a.group;
   for (int u = blockIdx.x; u < units; u += gridDim.x) {
-    const int cta = u / (D / 8), c = u % (D / 8);  // where the piece begins; dims 8c ..
-    const int4 rec = __ldcg(a.joins + cta);        // parts, first token, tokens, kv head
-    if (rt >= rec.z) continue;                     // (no parts: no tokens)
-    // the first part is its CTA's second one, the others their CTAs' first ones
+    const int from = u / (D / 8), c = u % (D / 8);  // where the piece begins; dims 8c ..
+    const int4 rec = __ldcg(a.joins + from);        // parts, first token, tokens, kv head
+    if (rt >= rec.z) continue;                      // (no parts: no tokens)
+    // the first part is its group's second one, the others their groups' first ones
     auto part_at = [&](int q) {
-      return a.parts + (int64_t(cta + q) * 2 + (q == 0 ? 1 : 0)) * kPartFloats;
+      return a.parts + (int64_t(from + q) * 2 + (q == 0 ? 1 : 0)) * kPartFloats;
     };
     float o[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
     float m = -INFINITY, l = 0.f;
@@ -1159,7 +1223,7 @@ cudaError_t launch_as(const DeviceInfo& di, const PagedKv& kv, const TreeArgs& t
   const bool may_split = int64_t(kv.pages_per_seq) << kv.page_shift > kKeys;
   uint8_t* ws = static_cast<uint8_t*>(a.ws) + kCounters * 4;
   d.joins = may_split ? reinterpret_cast<int4*>(ws) : nullptr;
-  d.parts = reinterpret_cast<float*>(ws + kMaxCtas * 16);
+  d.parts = reinterpret_cast<float*>(ws + 2 * kMaxCtas * 16);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(unsigned(ctas));
   cfg.blockDim = dim3(P::kThreads);
@@ -1176,7 +1240,7 @@ cudaError_t launch_as(const DeviceInfo& di, const PagedKv& kv, const TreeArgs& t
   cfg.blockDim = dim3(kJoinThreads);
   cfg.dynamicSmemBytes = 0;
   cfg.numAttrs = 1;  // the join always follows programmatically
-  return cudaLaunchKernelEx(&cfg, paged_tree_join_kernel<D>, d, ctas, a.heads);
+  return cudaLaunchKernelEx(&cfg, paged_tree_join_kernel<D>, d, 2 * ctas, a.heads);
 }
 
 template <int D, bool FP8>
@@ -1192,10 +1256,11 @@ cudaError_t launch(const DeviceInfo& di, const PagedKv& kv, const TreeArgs& t, c
 
 size_t paged_tree_workspace_bytes(int head_dim) {
   // (the decode kernel's counters,) the records of the join, two parts of a row
-  // tile per CTA
+  // tile per group
   const DeviceInfo* di = device_info();
   const int64_t ctas = di && di->sms < kMaxCtas ? di->sms : kMaxCtas;
-  return size_t(kCounters) * 4 + kMaxCtas * 16 + size_t(ctas) * 2 * kRows * (head_dim + 2) * 4;
+  return size_t(kCounters) * 4 + 2 * kMaxCtas * 16 +
+         size_t(ctas) * 4 * kRows * (head_dim + 2) * 4;
 }
 
 cudaError_t launch_paged_tree(const PagedKv& kv, int head_dim, bool fp8, const TreeArgs& a,

@@ -254,3 +254,30 @@ def test_draft_tree_reports_what_is_no_tree():
     assert list(got[:4]) == [1, 2, 4, 8 | 2]
     assert list(got[4:36]) == [1 << i for i in range(32)] and list(got[36:]) == [0] * 4  # 36 nodes, 32 bits
     assert list(gu.host(positions)[:5]) == [5, 5, 5, 6, 4] and list(gu.host(positions)[36:]) == [4] * 4
+
+
+def test_every_code_of_an_fp8_cache():
+    """Keys and values of all 256 codes, subnormal ones and NaN too: with one token to see, its value row is the
+    output and its score the log of the sum."""
+    from . import paged_ref
+    d, kvh, batch = 64, 4, 4
+    cache = ref.Cache(21, [1] * batch, kvh, d, 16, fp8=True)
+    codes = np.arange(256, dtype=np.uint8).reshape(kvh, d)
+    for b in range(batch):
+        at = cache.table[b, 0], slice(None), 0
+        cache.k[at] = cache.v[at] = codes
+        cache.k_scales[at] = cache.v_scales[at] = 1.0
+    q = np.zeros((batch, 16 * kvh, d), np.uint16)
+    for b in range(batch):
+        for h in range(16 * kvh):
+            q[b, h, 16 * b + h % 16] = 0x3F80  # picks one element of the key
+    want = paged_ref.e4m3_to_f64(codes)
+    # NaN in a key poisons only products with it; 0 * NaN is NaN as well: leave those keys to one row each
+    for b in range(batch):
+        cache.k[cache.table[b, 0], :, 0][np.isnan(want)] = 0
+    out, lse = attend(_handle(cache), q, list(range(batch + 1)), [1] * batch, 1, 1.0)
+    y = bf16_to_f64(out).reshape(batch, kvh, 16, d)
+    assert np.array_equal(y, np.broadcast_to(want[None, :, None], y.shape), equal_nan=True)
+    for b in range(batch):
+        z = np.where(np.isnan(want), 0.0, want)[:, 16 * b:16 * b + 16].ravel()
+        assert np.abs(lse[b] - z).max() <= 2.0 ** -22 * 448
