@@ -2,14 +2,69 @@
 //
 //   x = scale * logit;  lse = m + log sum e^(x - m)
 //   logp = x[target] - lse;  H = log sum e^(x - m) - sum (x - m) e^(x - m) / sum e^(x - m)
+//
+// One pass over the logits, which are read once: bound by their bytes.  A thread
+// keeps a running maximum m, s = sum 2^y and t = sum y 2^y over its elements, with
+// y = x log2 e - m; where the maximum rises by d, s becomes 2^-d s and t becomes
+// 2^-d (t - d s).  Five instructions an element, so the exponentials and additions
+// hide behind the loads (bf16: 12 elements a cycle and SM).
+//
+// Top alternatives.  Logit and index make one key, larger for a larger logit and
+// for the smaller index of equal ones, so that all keys differ.  From the first
+// chunk of a row the CTA takes a bound that at least top_k keys reach: the top_k-th
+// of 32 groups' largest.  After that only what reaches the bound, a few hundred
+// elements of a row, is collected in shared memory and ranked at the end, each key by
+// counting those above it.
+//
+// Split.  A row is cut into chunks of 16 KB, the chunks of all rows form one line,
+// and each CTA takes an equal stretch.  A row that lies in several stretches is
+// written in parts, joined by a second kernel.
 #include "launch.h"
 #include "common.cuh"
 
 namespace tt {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 256, kWarps = kThreads / 32;
+constexpr int kCtasPerSm = 4;
+constexpr int kMaxCtas = 1024;
+constexpr int kBuffer = 2048;                   // keys that are collected
+constexpr int kCheck = 8;                       // chunks from one look at their number to the next
+constexpr uint32_t kAll = 0xffffffffu;
 constexpr int kErrShape = 2;
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+
+// A part of a row: maximum and sums of all its logits, its largest keys.
+struct alignas(16) Part {
+  float m, s, t, pad;
+  uint64_t keys[kMaxTop];
+};
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// The larger one; NaN if either is.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float y;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+  return y;
+}
+
+// Larger for a larger logit, and of equal ones for the smaller index; never 0.
+// -0 counts as 0, NaN as the largest.
+__device__ __forceinline__ uint64_t key_of(float x, uint32_t i) {
+  uint32_t u = __float_as_uint(x + 0.f);
+  if (x != x) u = 0x7fffffffu;
+  u = u & 0x80000000u ? ~u : u | 0x80000000u;
+  return uint64_t(u) << 32 | (kAll - i);
+}
+__device__ __forceinline__ float logit_of(uint64_t key) {
+  const uint32_t u = uint32_t(key >> 32);
+  return __uint_as_float(u & 0x80000000u ? u & 0x7fffffffu : ~u);
+}
+__device__ __forceinline__ int32_t id_of(uint64_t key) { return int32_t(kAll - uint32_t(key)); }
 
 template <bool BF16>
 __device__ __forceinline__ float logit(const void* row, int64_t i) {
@@ -17,83 +72,491 @@ __device__ __forceinline__ float logit(const void* row, int64_t i) {
   return __ldcg(static_cast<const float*>(row) + i);
 }
 
-// Larger for a larger logit, and of equal ones for the smaller index; never 0.
-__device__ __forceinline__ uint64_t key_of(float x, uint32_t i) {
-  uint32_t u = __float_as_uint(x + 0.f);  // -0 as 0
-  if (x != x) u = 0x7fffffffu;
-  u = u & 0x80000000u ? ~u : u | 0x80000000u;
-  return uint64_t(u) << 32 | (0xffffffffu - i);
+// Maximum and sums of the union.
+struct Sums {
+  float m, s, t;
+};
+__device__ __forceinline__ Sums join(const Sums& a, const Sums& b) {
+  Sums r;
+  r.m = max_nan(a.m, b.m);
+  r.s = r.t = 0.f;
+  if (a.m != -INFINITY) {
+    const float d = r.m - a.m, f = ex2(-d);
+    r.s += a.s * f;
+    r.t += (a.t - d * a.s) * f;
+  }
+  if (b.m != -INFINITY) {
+    const float d = r.m - b.m, f = ex2(-d);
+    r.s += b.s * f;
+    r.t += (b.t - d * b.s) * f;
+  }
+  return r;
 }
 
-template <typename T, typename F>
-__device__ __forceinline__ T block_reduce(T v, F f, T* part) {
-  for (int o = 16; o > 0; o >>= 1) v = f(v, __shfl_xor_sync(0xffffffffu, v, o));
-  if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
-  __syncthreads();
-  v = part[0];
-  for (int w = 1; w < kThreads / 32; ++w) v = f(v, part[w]);
-  __syncthreads();
-  return v;
-}
-
+// The results of row r from its sums and its largest keys (in shared memory); by all
+// threads of the CTA.
 template <bool BF16>
-__global__ void __launch_bounds__(kThreads) logprobs_kernel(const LogprobArgs a, int32_t* err) {
-  __shared__ float fpart[kThreads / 32];
-  __shared__ uint64_t kpart[kThreads / 32];
-  pdl_allow_next_grid();
-  pdl_wait_prior_grid();
-  const int64_t r = blockIdx.x;
+__device__ __forceinline__ void write_row(const LogprobArgs& a, int64_t r, const Sums& z,
+                                          const uint64_t* keys, int32_t* err) {
+  const float k = a.scale * kLog2e;
+  // NaN unless the maximum is finite
+  const float ls = log2f(z.s) + (z.m - z.m);
   const int tid = threadIdx.x;
-  const uint8_t* row = static_cast<const uint8_t*>(a.logits) + r * a.stride * (BF16 ? 2 : 4);
-  float m = -INFINITY;
-  for (int64_t i = tid; i < a.vocab; i += kThreads) {
-    const float x = logit<BF16>(row, i) * a.scale;
-    m = x != x || m != m ? NAN : fmaxf(m, x);
-  }
-  m = block_reduce(m, [](float x, float y) { return x != x || y != y ? NAN : fmaxf(x, y); }, fpart);
-  float s = 0.f, e = 0.f;
-  for (int64_t i = tid; i < a.vocab; i += kThreads) {
-    const float y = logit<BF16>(row, i) * a.scale - m, w = expf(y);
-    s += w;
-    e += w > 0.f ? y * w : 0.f;
-  }
-  s = block_reduce(s, [](float x, float y) { return x + y; }, fpart);
-  e = block_reduce(e, [](float x, float y) { return x + y; }, fpart);
-  const float bad = m - m;  // NaN unless m is finite
-  const float ls = logf(s) + bad;
   if (tid == 0) {
-    if (a.entropy) a.entropy[r] = ls - e / s;
+    if (a.entropy) a.entropy[r] = (ls - z.t / z.s) * kLn2;
     if (a.logp) {
       const int t = __ldcg(a.targets + r);
+      float y = t < 0 ? 0.f : NAN;
       if (t >= a.vocab) flag_error(err, kErrShape);
-      a.logp[r] = t < 0 ? 0.f : t >= a.vocab ? NAN : logit<BF16>(row, t) * a.scale - m - ls;
+      if (t >= 0 && t < a.vocab) {
+        const void* row = static_cast<const uint8_t*>(a.logits) + r * a.stride * (BF16 ? 2 : 4);
+        y = (fmaf(logit<BF16>(row, t), k, -z.m) - ls) * kLn2;
+      }
+      a.logp[r] = y;
     }
   }
+  if (tid < a.top) {
+    a.top_ids[r * a.top + tid] = id_of(keys[tid]);
+    if (a.top_logp) a.top_logp[r * a.top + tid] = (fmaf(logit_of(keys[tid]), k, -z.m) - ls) * kLn2;
+  }
+}
+
+// The `top` largest of n keys in falling order, zeros behind them if there are fewer:
+// each by the number of those above it.
+__device__ __forceinline__ void rank_keys(const uint64_t* from, int n, int top, uint64_t* to) {
+  for (int i = threadIdx.x; i < top; i += kThreads)
+    if (i >= n) to[i] = 0;
+  for (int i = threadIdx.x; i < n; i += kThreads) {
+    const uint64_t key = from[i];
+    int above = 0;
+#pragma unroll 4
+    for (int j = 0; j < n; ++j) above += from[j] > key;
+    if (above < top) to[above] = key;
+  }
+}
+
+// The largest keys of the elements [lo, hi) one after the other: where more of them
+// reached the bound than can be collected.
+template <bool BF16>
+__device__ __noinline__ void keys_by_rounds(const void* row, int64_t lo, int64_t hi, int top,
+                                            uint64_t* to, uint64_t* part) {
   uint64_t last = ~0ull;
-  for (int k = 0; k < a.top; ++k) {
+  for (int k = 0; k < top; ++k) {
     uint64_t best = 0;
-    for (int64_t i = tid; i < a.vocab; i += kThreads) {
+    for (int64_t i = lo + threadIdx.x; i < hi; i += kThreads) {
       const uint64_t key = key_of(logit<BF16>(row, i), uint32_t(i));
       if (key < last && key > best) best = key;
     }
-    last = block_reduce(best, [](uint64_t x, uint64_t y) { return x > y ? x : y; }, kpart);
-    if (tid == 0) {
-      const int32_t id = int32_t(0xffffffffu - uint32_t(last));
-      a.top_ids[r * a.top + k] = id;
-      if (a.top_logp) a.top_logp[r * a.top + k] = logit<BF16>(row, id) * a.scale - m - ls;
+    for (int o = 16; o > 0; o >>= 1) {
+      const uint64_t other = __shfl_xor_sync(kAll, best, o);
+      best = other > best ? other : best;
     }
+    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = best;
+    __syncthreads();
+    for (int w = 0; w < kWarps; ++w) best = part[w] > best ? part[w] : best;
+    last = best;
+    if (threadIdx.x == 0) to[k] = best;
+    __syncthreads();
   }
 }
 
-}  // namespace
+__device__ __forceinline__ uint64_t f2(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ void un2(uint64_t v, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
 
-size_t token_logprobs_workspace_bytes(int64_t rows, int64_t vocab, int top) { return 0; }
+// Elements [i, i + 16 bytes) of a row, -infinity where they are outside of it.
+template <bool BF16>
+__device__ __noinline__ uint4 piece_at_end(const void* row, int64_t i, int64_t vocab) {
+  uint32_t w[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    if constexpr (BF16) {
+      const uint16_t* p = static_cast<const uint16_t*>(row);
+      const int64_t i0 = i + 2 * e, i1 = i0 + 1;
+      const uint32_t lo = i0 >= 0 && i0 < vocab ? __ldcg(p + i0) : 0xff80u;
+      const uint32_t hi = i1 >= 0 && i1 < vocab ? __ldcg(p + i1) : 0xff80u;
+      w[e] = lo | hi << 16;
+    } else {
+      const int64_t i0 = i + e;
+      w[e] = i0 >= 0 && i0 < vocab ? __ldcg(static_cast<const uint32_t*>(row) + i0) : 0xff800000u;
+    }
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
 
-cudaError_t launch_token_logprobs(const LogprobArgs& a, bool bf16, cudaStream_t s, bool pdl) {
-  const DeviceInfo* di = device_info();
-  if (!di) return cudaErrorNoDevice;
+// The largest key among `pieces` pieces of a row, from element i on and `step` apart;
+// read again, which only threads without anything above -infinity do.
+template <bool BF16>
+__device__ __noinline__ uint64_t largest_key(const void* row, int64_t i, int pieces, int step,
+                                             int64_t vocab) {
+  uint64_t most = 0;
+  for (int j = 0; j < pieces; ++j, i += step) {
+    for (int e = 0; e < (BF16 ? 8 : 4); ++e) {
+      if (i + e < 0 || i + e >= vocab) continue;
+      const uint64_t key = key_of(logit<BF16>(row, i + e), uint32_t(i + e));
+      most = key > most ? key : most;
+    }
+  }
+  return most;
+}
+
+// kVectors: 16-byte pieces a thread and chunk.
+template <bool BF16, int kVectors>
+__global__ void __launch_bounds__(kThreads, kCtasPerSm)
+    logprobs_kernel(const LogprobArgs a, int chunks, int64_t total, Part* parts, int32_t* err) {
+  constexpr int kPer = BF16 ? 8 : 4;  // elements of a piece
+  constexpr int kBytes = BF16 ? 2 : 4;
+  constexpr int kChunk = kPer * kVectors * kThreads;
+  __shared__ uint64_t buffer[kBuffer];
+  __shared__ uint64_t best[kMaxTop];
+  __shared__ uint64_t groups[32];
+  __shared__ Sums sums[kWarps];
+  __shared__ int s_count;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  pdl_allow_next_grid();
+  pdl_wait_prior_grid();
+  const int64_t begin = total * blockIdx.x / gridDim.x, end = total * (blockIdx.x + 1) / gridDim.x;
+  const float k = a.scale * kLog2e;
+  const uint64_t k2 = f2(k, k);
+
+  for (int64_t at = begin; at < end;) {
+    const int64_t r = at / chunks;
+    const int c0 = int(at - r * chunks);
+    const int c1 = end - at < chunks - c0 ? c0 + int(end - at) : chunks;
+    at += c1 - c0;
+    const uint8_t* row = static_cast<const uint8_t*>(a.logits) + r * a.stride * kBytes;
+    // pieces are cut from the 16-byte boundary before the row on: element i of the row
+    // is element i + shift of them
+    const int shift = int(reinterpret_cast<uintptr_t>(row) & 15u) / kBytes;
+    const int64_t mine0 = int64_t(tid) * kPer - shift;  // this thread's first element
+    auto load = [&](int c, uint4 (&x)[kVectors]) {
+      const int64_t i0 = int64_t(c) * kChunk + mine0;
+      const int64_t low = int64_t(c) * kChunk - shift;
+      if (low >= 0 && low + kChunk <= a.vocab) {
+        const uint4* p = reinterpret_cast<const uint4*>(row + i0 * kBytes);
+#pragma unroll
+        for (int j = 0; j < kVectors; ++j) x[j] = __ldcg(p + j * kThreads);
+      } else {  // one of the row's ends
+#pragma unroll 1
+        for (int j = 0; j < kVectors; ++j) {
+          const int64_t i = i0 + int64_t(j) * kThreads * kPer;
+          const uint4 v = i >= 0 && i + kPer <= a.vocab
+                              ? __ldcg(reinterpret_cast<const uint4*>(row + i * kBytes))
+                              : piece_at_end<BF16>(row, i, a.vocab);
+#pragma unroll
+          for (int e = 0; e < kVectors; ++e)
+            if (e == j) x[e] = v;
+        }
+      }
+    };
+    Sums z{-INFINITY, 0.f, 0.f};
+    uint64_t bound = 0;
+    float least = -INFINITY;  // the bound's logit
+    bool whole = true;        // all that reached the bound was collected
+    if (tid == 0) s_count = 0;
+    uint4 x[kVectors], ahead[kVectors];
+    load(c0, x);
+#pragma unroll 1
+    for (int c = c0; c < c1; ++c) {
+      if (c + 1 < c1) load(c + 1, ahead);
+      // ---- the largest
+      float top;
+      if constexpr (BF16) {
+        auto two = [](uint32_t w) { return *reinterpret_cast<const __nv_bfloat162*>(&w); };
+        __nv_bfloat162 m2 = two(x[0].x);
+#pragma unroll
+        for (int j = 0; j < kVectors; ++j) {
+          if (j > 0) m2 = __hmax2_nan(m2, two(x[j].x));
+          m2 = __hmax2_nan(__hmax2_nan(m2, two(x[j].y)), __hmax2_nan(two(x[j].z), two(x[j].w)));
+        }
+        top = max_nan(__low2float(m2), __high2float(m2));
+      } else {
+        top = __uint_as_float(x[0].x);
+#pragma unroll
+        for (int j = 0; j < kVectors; ++j) {
+          if (j > 0) top = max_nan(top, __uint_as_float(x[j].x));
+          top = max_nan(max_nan(top, __uint_as_float(x[j].y)),
+                        max_nan(__uint_as_float(x[j].z), __uint_as_float(x[j].w)));
+        }
+      }
+      // ---- the sums
+      const float m = top * k;
+      if (!(m <= z.m)) {
+        const float d = m - z.m, f = ex2(-d);
+        z.t = z.m == -INFINITY ? 0.f : (z.t - d * z.s) * f;
+        z.s *= f;
+        z.m = m;
+      }
+      // what is 1000 below the maximum or more, -infinity too, has no weight (and no
+      // product of infinity and 0)
+      const float base = z.m == -INFINITY ? 0.f : -z.m;
+      const uint64_t base2 = f2(base, base);
+      uint64_t s2 = 0, t2 = 0;
+      auto add = [&](float lo, float hi) {
+        const uint64_t y = fma2(f2(lo, hi), k2, base2);
+        un2(y, lo, hi);
+        const uint64_t w = f2(ex2(lo), ex2(hi));
+        s2 = add2(s2, w);
+        t2 = fma2(y, w, t2);
+      };
+      const float low = (-base - 1000.f) / k;
+      if constexpr (BF16) {
+        const __nv_bfloat162 low2 = __float2bfloat162_rn(low);
+#pragma unroll
+        for (int j = 0; j < kVectors; ++j) {
+          const uint32_t ws[4] = {x[j].x, x[j].y, x[j].z, x[j].w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const __nv_bfloat162 v =
+                __hmax2(*reinterpret_cast<const __nv_bfloat162*>(&ws[e]), low2);
+            const uint32_t w = *reinterpret_cast<const uint32_t*>(&v);
+            add(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+          }
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < kVectors; ++j) {
+          add(fmaxf(__uint_as_float(x[j].x), low), fmaxf(__uint_as_float(x[j].y), low));
+          add(fmaxf(__uint_as_float(x[j].z), low), fmaxf(__uint_as_float(x[j].w), low));
+        }
+      }
+      float lo, hi;
+      un2(s2, lo, hi);
+      z.s += lo + hi;
+      un2(t2, lo, hi);
+      z.t += lo + hi;
+      // ---- the largest keys
+      if (a.top > 0) {
+        const int64_t i0 = int64_t(c) * kChunk + mine0;
+        auto element = [&](int e) {
+          const uint4& v = x[e / kPer];
+          const int q = e % kPer;
+          if constexpr (BF16) {
+            const uint32_t w = q < 2 ? v.x : q < 4 ? v.y : q < 6 ? v.z : v.w;
+            return __uint_as_float(q & 1 ? w & 0xffff0000u : w << 16);
+          } else {
+            return __uint_as_float(q == 0 ? v.x : q == 1 ? v.y : q == 2 ? v.z : v.w);
+          }
+        };
+        auto index = [&](int e) { return i0 + int64_t(e / kPer) * kThreads * kPer + e % kPer; };
+        // what reaches the bound, into the buffer (as far as there is room)
+        auto collect = [&] {
+#pragma unroll
+          for (int e = 0; e < kPer * kVectors; ++e) {
+            const float v = element(e);
+            if (v < least) continue;
+            const int64_t i = index(e);
+            const uint64_t key = key_of(v, uint32_t(i));
+            if (i < 0 || i >= a.vocab || key < bound) continue;
+            const int n = atomicAdd(&s_count, 1);
+            if (n < kBuffer) buffer[n] = key;
+          }
+        };
+        if (c == c0) {
+          // this thread's largest: its first element that is not below the largest (one
+          // of -infinity may lie outside the row)
+          uint64_t mine;
+          if (top == -INFINITY) {
+            mine = largest_key<BF16>(row, i0, kVectors, kThreads * kPer, a.vocab);
+          } else {
+            int first = 0;
+#pragma unroll
+            for (int e = kPer * kVectors - 1; e >= 0; --e) {
+              const float y = element(e);
+              if (top != top ? y != y : y == top) first = e;
+            }
+            mine = key_of(top, uint32_t(i0 + int64_t(first / kPer) * kThreads * kPer + first % kPer));
+          }
+          uint64_t group = mine;
+#pragma unroll
+          for (int o = 4; o > 0; o >>= 1) {
+            const uint64_t other = __shfl_xor_sync(kAll, group, o);
+            group = other > group ? other : group;
+          }
+          if ((lane & 7) == 0) groups[warp * 4 + lane / 8] = group;
+          __syncthreads();
+          // every warp ranks the groups for itself
+          const uint64_t g = groups[lane];
+          int above = 0;
+#pragma unroll 8
+          for (int o = 0; o < 32; ++o) {
+            const uint64_t other = groups[o];
+            above += other > g || (other == g && o < lane);
+          }
+          const int owner = __ffs(__ballot_sync(kAll, above == a.top - 1)) - 1;
+          bound = __shfl_sync(kAll, g, owner);
+          least = bound ? logit_of(bound) : -INFINITY;
+        }
+        // (one place for both: the code is long)
+        if (!(top < least)) collect();
+        if ((c - c0) % kCheck == kCheck - 1 && c + 1 < c1) {
+          __syncthreads();
+          const int n = s_count;
+          whole &= n <= kBuffer;
+          if (n >= 2 * a.top + 8 && whole) {  // a better bound
+            rank_keys(buffer, n, a.top, best);
+            __syncthreads();
+            for (int i = tid; i < a.top; i += kThreads) buffer[i] = best[i];
+            if (tid == 0) s_count = a.top;
+            bound = best[a.top - 1];
+            least = logit_of(bound);
+          }
+          __syncthreads();
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < kVectors; ++j) x[j] = ahead[j];
+    }
+    // ---- the part's end
+#pragma unroll 1
+    for (int o = 16; o > 0; o >>= 1) {
+      Sums other;
+      other.m = __shfl_xor_sync(kAll, z.m, o);
+      other.s = __shfl_xor_sync(kAll, z.s, o);
+      other.t = __shfl_xor_sync(kAll, z.t, o);
+      z = join(z, other);
+    }
+    if (lane == 0) sums[warp] = z;
+    __syncthreads();
+    if (a.top > 0) {
+      const int n = s_count;
+      if (whole && n <= kBuffer) {
+        rank_keys(buffer, n, a.top, best);
+      } else {
+        int64_t lo = int64_t(c0) * kChunk - shift, hi = int64_t(c1) * kChunk - shift;
+        lo = lo < 0 ? 0 : lo;
+        hi = hi < a.vocab ? hi : a.vocab;
+        keys_by_rounds<BF16>(row, lo, hi, a.top, best, groups);
+      }
+      __syncthreads();
+    }
+    z = sums[0];
+#pragma unroll 1
+    for (int w = 1; w < kWarps; ++w) z = join(z, sums[w]);
+    if (c0 == 0 && c1 == chunks) {
+      write_row<BF16>(a, r, z, best, err);
+    } else {
+      Part* p = parts + blockIdx.x * 2 + (c0 == 0 ? 1 : 0);
+      if (tid == 0) p->m = z.m, p->s = z.s, p->t = z.t;
+      if (tid < a.top) p->keys[tid] = best[tid];
+    }
+    __syncthreads();
+  }
+}
+
+// Joins the parts of the rows that lie in several stretches: block b has the row
+// that goes on from stretch b into the next, if it began in b.
+template <bool BF16>
+__global__ void __launch_bounds__(kThreads)
+    logprobs_join_kernel(const LogprobArgs a, int chunks, int64_t total, const Part* parts,
+                         int32_t* err) {
+  __shared__ uint64_t buffer[kMaxTop * kMaxTop];
+  __shared__ uint64_t firsts[kMaxCtas];
+  __shared__ uint64_t best[kMaxTop];
+  __shared__ Sums sums[kWarps];
+  __shared__ uint64_t s_bound;
+  __shared__ int s_count;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int64_t ctas = gridDim.x + 1;
+  pdl_allow_next_grid();
+  pdl_wait_prior_grid();
+  const int64_t edge = total * (blockIdx.x + 1) / ctas;  // between the stretches
+  const int64_t r = edge / chunks, first = r * chunks;
+  if (edge == first || first < total * blockIdx.x / ctas) return;
+  // the stretch of the row's last chunk: the last that begins at or before it
+  const int n = int(((first + chunks) * ctas + total - 1) / total) - 1 - int(blockIdx.x) + 1;
+  auto part = [&](int i) { return parts + (int64_t(blockIdx.x) + i) * 2 + (i == 0 ? 1 : 0); };
+  if (tid == 0) s_count = 0, s_bound = 0;
+  Sums z{-INFINITY, 0.f, 0.f};
+  for (int i = tid; i < n; i += kThreads) {
+    const float4 p = __ldcg(reinterpret_cast<const float4*>(part(i)));
+    if (a.top > 0) firsts[i] = __ldcg(part(i)->keys);
+    z = join(z, Sums{p.x, p.y, p.z});
+  }
+#pragma unroll 1
+  for (int o = 16; o > 0; o >>= 1) {
+    Sums other;
+    other.m = __shfl_xor_sync(kAll, z.m, o);
+    other.s = __shfl_xor_sync(kAll, z.s, o);
+    other.t = __shfl_xor_sync(kAll, z.t, o);
+    z = join(z, other);
+  }
+  if (lane == 0) sums[warp] = z;
+  __syncthreads();
+  if (a.top > 0) {
+    // What reaches the top_k-th largest of the parts' first keys is at most top_k keys
+    // of top_k parts.
+    if (n >= a.top) {
+      for (int i = tid; i < n; i += kThreads) {
+        const uint64_t key = firsts[i];
+        int above = 0;
+#pragma unroll 8
+        for (int j = 0; j < n; ++j) {
+          const uint64_t other = firsts[j];
+          above += other > key || (other == key && j < i);
+        }
+        if (above == a.top - 1) s_bound = key;
+      }
+    }
+    __syncthreads();
+    const uint64_t bound = s_bound;
+    // a part a warp, a key a lane, four parts on their way
+    for (int i0 = warp; i0 < n; i0 += 4 * kWarps) {
+      uint64_t key[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int i = i0 + e * kWarps;
+        key[e] = i < n && firsts[i] >= bound && lane < a.top ? __ldcg(part(i)->keys + lane) : 0;
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        if (key[e] != 0 && key[e] >= bound) {
+          const int at = atomicAdd(&s_count, 1);
+          if (at < kMaxTop * kMaxTop) buffer[at] = key[e];
+        }
+      }
+    }
+    __syncthreads();
+    rank_keys(buffer, s_count < kMaxTop * kMaxTop ? s_count : kMaxTop * kMaxTop, a.top, best);
+    __syncthreads();
+  }
+  z = sums[0];
+#pragma unroll 1
+  for (int w = 1; w < kWarps; ++w) z = join(z, sums[w]);
+  write_row<BF16>(a, r, z, best, err);
+}
+
+// Chunks of a row, wherever it begins.
+int64_t chunks_of(int64_t vocab, bool bf16, int vectors) {
+  const int64_t per = bf16 ? 8 : 4;
+  const int64_t chunk = per * vectors * kThreads;
+  return (vocab + per - 1 + chunk - 1) / chunk;
+}
+
+template <bool BF16, int kVectors>
+cudaError_t launch(const DeviceInfo& di, const LogprobArgs& a, cudaStream_t s, bool pdl) {
+  const int chunks = int(chunks_of(a.vocab, BF16, kVectors));
+  const int64_t total = a.rows * chunks;
+  int64_t ctas = int64_t(di.sms) * kCtasPerSm;
+  if (ctas > kMaxCtas) ctas = kMaxCtas;
+  if (ctas > total) ctas = total;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(unsigned(a.rows));
+  cfg.gridDim = dim3(unsigned(ctas));
   cfg.blockDim = dim3(kThreads);
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
@@ -101,8 +564,39 @@ cudaError_t launch_token_logprobs(const LogprobArgs& a, bool bf16, cudaStream_t 
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = pdl ? 1 : 0;
-  return bf16 ? cudaLaunchKernelEx(&cfg, logprobs_kernel<true>, a, di->error_word)
-              : cudaLaunchKernelEx(&cfg, logprobs_kernel<false>, a, di->error_word);
+  Part* parts = static_cast<Part*>(a.ws);
+  if (cudaError_t e = cudaLaunchKernelEx(&cfg, logprobs_kernel<BF16, kVectors>, a, chunks, total,
+                                         parts, di.error_word))
+    return e;
+  // rows of one chunk, or as many CTAs as divide the rows evenly: nothing to join
+  if (chunks == 1 || ctas == 1 || a.rows % ctas == 0) return cudaSuccess;
+  cfg.gridDim = dim3(unsigned(ctas - 1));
+  cfg.numAttrs = 1;  // the join always follows programmatically
+  return cudaLaunchKernelEx(&cfg, logprobs_join_kernel<BF16>, a, chunks, total,
+                            static_cast<const Part*>(parts), di.error_word);
+}
+
+template <bool BF16>
+cudaError_t launch(const DeviceInfo& di, const LogprobArgs& a, cudaStream_t s, bool pdl) {
+  // Few rows: chunks of a quarter, so that more SMs have one.
+  if (a.rows * chunks_of(a.vocab, BF16, 4) <= di.sms) return launch<BF16, 1>(di, a, s, pdl);
+  return launch<BF16, 4>(di, a, s, pdl);
+}
+
+}  // namespace
+
+size_t token_logprobs_workspace_bytes(int64_t rows, int64_t vocab, int top) {
+  // two parts a CTA
+  (void)rows, (void)vocab, (void)top;
+  const DeviceInfo* di = device_info();
+  const int64_t ctas = di && di->sms * kCtasPerSm < kMaxCtas ? di->sms * kCtasPerSm : kMaxCtas;
+  return size_t(ctas) * 2 * sizeof(Part);
+}
+
+cudaError_t launch_token_logprobs(const LogprobArgs& a, bool bf16, cudaStream_t s, bool pdl) {
+  const DeviceInfo* di = device_info();
+  if (!di) return cudaErrorNoDevice;
+  return bf16 ? launch<true>(*di, a, s, pdl) : launch<false>(*di, a, s, pdl);
 }
 
 }  // namespace tt
