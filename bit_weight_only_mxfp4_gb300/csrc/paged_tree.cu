@@ -23,7 +23,7 @@
 // other's products and copies run.  (Even and odd tiles of one stretch, joined in the
 // CTA at a piece's end, left the copies idle for 5 us there.)
 //   warps 0-3, 4-7  softmax of the groups, one thread a row
-//   warp 8          the products, issued by the warp in step, one elected lane; Q
+//   warps 8, 15     a group's products, issued by the warp in step, one elected lane
 //   warps 9-12      a group's K tiles, or V tiles: asked for (TMA: one box per page
 //                   and 64 dims; FP8: one bulk copy per page), and once there turned
 //                   into bf16 in their place, if E4M3 codes, and made safe (below)
@@ -51,7 +51,7 @@
 namespace tt {
 namespace {
 
-constexpr int kMmaWarp = 8, kCopyWarp = 9, kPlanWarp = 13;
+constexpr int kMmaWarp = 8, kCopyWarp = 9, kPlanWarp = 13, kMmaWarp2 = 15;
 constexpr int kMaxCtas = 1024;
 constexpr int kCounters = 1024;  // the decode kernel's, at the workspace's start: left alone
 constexpr int kAhead = 4;        // tiles of a group that are planned at once
@@ -299,7 +299,7 @@ __global__ void __launch_bounds__(Plan<D, FP8>::kThreads, 1)
   uint64_t* s_read = o_done + 2;
   uint64_t* shifted = s_read + 2;
   uint64_t* drained = shifted + 2;
-  int* dirty = reinterpret_cast<int*>(drained + 1);  // [2][kDirty] segment
+  int* dirty = reinterpret_cast<int*>(drained + 2);  // [2][kDirty] segment
   int* misc = dirty + 2 * kDirty;  // [0] TMEM address, [1] quit
   volatile int* quit = misc + 1;
   int64_t* scan = reinterpret_cast<int64_t*>(smem);  // [warps], before the main loop
@@ -322,8 +322,8 @@ __global__ void __launch_bounds__(Plan<D, FP8>::kThreads, 1)
       mbar_init(smem_u32(&o_done[g]), 1);
       mbar_init(smem_u32(&s_read[g]), kRows);
       mbar_init(smem_u32(&shifted[g]), kRows);
+      mbar_init(smem_u32(&drained[g]), 1);
     }
-    mbar_init(smem_u32(drained), 1);
     for (int i = 0; i < 2 * kDirty; ++i) dirty[i] = 0;
     misc[1] = 0;
     fence_mbar_init();
@@ -711,23 +711,25 @@ __global__ void __launch_bounds__(Plan<D, FP8>::kThreads, 1)
       for (uint32_t i = 1; i <= P::kDepth && i <= asked; ++i)
         (void)mbar_wait_bounded(smem_u32(&full[slot_of(g, value, asked - i)]),
                                 ((asked - i) / P::kDepth) & 1u);
-    } else if (warp == kMmaWarp) {
+    } else {
       // ========================================================== products
-      // One warp for both groups, whichever is ready: eight lanes a group each test
-      // what one of its next products waits for.  The commits free the slots, so that
-      // a copy begins as soon as the products are through with its place.  Products
-      // finish in order, so scores that are there say that the P V issued before them
-      // is done.
+      // A warp for each group, issued by the warp in step.  (One for both took 2700
+      // cycles for a round of both groups' products: 75.9 us for 64.3, one sequence of 32768
+      // tokens, 64 new ones of 64 / 8 heads of 64.)  The commits free the slots, so
+      // that a copy begins as soon as the products are through with its place.  Products
+      // finish in order, so scores that are there say that the P V issued before them is
+      // done.
+      // (asked for by a vote, so that the compiler knows it to be the same in all lanes)
+      const uint32_t g = __any_sync(kAll, warp == kMmaWarp2) ? 1 : 0;
       const uint32_t kv0 = sbase + P::kOffKv;
       bool ok = tmem == 0;  // all columns are ours, so they begin at 0
       if (!ok && lane == 0) {
         *quit = 1;
         flag_error(a.err, kErrShape);
       }
-      // (Loops that are not unrolled, and one code for both groups: the instructions of
-      // all roles have to fit the caches.  Unrolled, 78 us for 68, 32 ragged sequences
+      // (Loops that are not unrolled: the instructions of all roles have to fit the caches.  Unrolled, 78 us for 68, 32 ragged sequences
       // of 16 / 4 heads of 128.)
-      auto scores = [&](uint32_t g, uint32_t i) {
+      auto scores = [&](uint32_t i) {
         const uint32_t slot = slot_of(g, 0, i);
         const uint64_t q = desc_k(sbase + g * P::kTile), k = desc_k(kv0 + slot * P::kTile);
 #pragma unroll 1
@@ -738,7 +740,7 @@ __global__ void __launch_bounds__(Plan<D, FP8>::kThreads, 1)
         commit(smem_u32(&s_full[g]));
         commit(smem_u32(&empty[slot]));
       };
-      auto values = [&](uint32_t g, uint32_t i, int ends) {
+      auto values = [&](uint32_t i, int ends) {
         const uint32_t slot = slot_of(g, 1, i);
         const uint64_t v = desc_mn(kv0 + slot * P::kTile, P::kHalves > 1 ? P::kSpan : 1024);
 #pragma unroll 1
@@ -748,51 +750,35 @@ __global__ void __launch_bounds__(Plan<D, FP8>::kThreads, 1)
         commit(smem_u32(&empty[slot]));
         if (P::kOwnP || __any_sync(kAll, ends & 2)) commit(smem_u32(&o_done[g]));
       };
-      // Of each group: tiles, P V issued, scores issued, segments whose scores are all
-      // issued.  A test of a barrier takes some 150 cycles, so all of a round go out
-      // together, asked for in one vote each.  (One after the other, as needed, a round
-      // of both groups' products took 6000 cycles; a lane for each test, whose
-      // addresses then differ, 700 without any product.)
-      uint32_t n0 = uint32_t(tiles_all[0]), n1 = uint32_t(tiles_all[1]);
-      uint32_t v0 = 0, s0 = 0, e0 = 0, v1 = 0, s1 = 0, e1 = 0;
+      // Tiles, P V issued, scores issued, segments whose scores are all issued.  A test
+      // of a barrier takes some 150 cycles, so all of a round go out together, asked for
+      // in one vote each.
+      const uint32_t n = uint32_t(tiles_all[g]);
+      uint32_t v = 0, sc = 0, seg = 0;
       uint64_t since = 0;  // of the idle stretch
-      uint32_t g = 0;      // the group whose turn it is: that of v0, s0, e0, n0
-      bool before = true;  // the other had something in its turn
-      for (uint32_t idle = 0; ok && (v0 < n0 || v1 < n1);) {
+      for (uint32_t idle = 0; ok && v < n;) {
         auto there = [](uint64_t* bar, uint32_t phase) {
           return mbar_test_wait(smem_u32(bar), phase & 1u);
         };
-        const bool weights = there(&p_full[g], v0);
-        const bool value = there(&ready[slot_of(g, 1, v0)], v0 / P::kDepth);
-        const bool key = there((FP8 ? ready : full) + slot_of(g, 0, s0), s0 / P::kDepth);
-        const bool read = !P::kOwnP || there(&s_read[g], s0 - 1u);
-        const bool query = there(&q_full[g], e0);
-        const int v_ends = plans[g * kAhead + v0 % kAhead].ends;
-        const int s_ends = plans[g * kAhead + s0 % kAhead].ends;
-        const bool pv = __all_sync(kAll, weights && value) && v0 < s0;
+        const bool weights = there(&p_full[g], v);
+        const bool value = there(&ready[slot_of(g, 1, v)], v / P::kDepth);
+        const bool key = there((FP8 ? ready : full) + slot_of(g, 0, sc), sc / P::kDepth);
+        const bool read = !P::kOwnP || there(&s_read[g], sc - 1u);
+        const bool query = there(&q_full[g], seg);
+        const int v_ends = plans[g * kAhead + v % kAhead].ends;
+        const int s_ends = plans[g * kAhead + sc % kAhead].ends;
+        const bool pv = __all_sync(kAll, weights && value) && v < sc;
         // the next scores: with 128 dims once the P V that lie there are issued, else once
         // those before are read
-        const bool qk = __all_sync(kAll, key && read && query) && s0 < n0 &&
-                        (P::kOwnP || s0 == v0 + pv);
+        const bool qk = __all_sync(kAll, key && read && query) && sc < n &&
+                        (P::kOwnP || sc == v + pv);
         if (pv | qk) fence_after();
-        if (pv) values(g, v0++, v_ends);
+        if (pv) values(v++, v_ends);
         if (qk) {
-          scores(g, s0++);
-          e0 += (s_ends >> 1) & 1;
+          scores(sc++);
+          seg += (s_ends >> 1) & 1;
         }
-        const bool did = pv | qk | before;
-        before = pv | qk;
-        // the other group's turn
-        auto swap = [](uint32_t& x, uint32_t& y) {
-          const uint32_t t = x;
-          x = y;
-          y = t;
-        };
-        swap(n0, n1);
-        swap(v0, v1);
-        swap(s0, s1);
-        swap(e0, e1);
-        g ^= 1u;
+        const bool did = pv | qk;
         if (did) {
           idle = 0;
         } else if ((++idle & 63u) == 0u) {
@@ -805,8 +791,8 @@ __global__ void __launch_bounds__(Plan<D, FP8>::kThreads, 1)
         }
       }
       // nothing of the tensor cores is under way when the CTA ends
-      commit(smem_u32(drained));
-      (void)mbar_wait_bounded(smem_u32(drained), 0);
+      commit(smem_u32(&drained[g]));
+      (void)mbar_wait_bounded(smem_u32(&drained[g]), 0);
       __syncwarp();
     }
   } else {
@@ -1236,7 +1222,7 @@ cudaError_t launch_as(const DeviceInfo& di, const PagedKv& kv, const TreeArgs& t
   cfg.numAttrs = pdl ? 1 : 0;
   if (cudaError_t e = cudaLaunchKernelEx(&cfg, kern, mq, mk, mv, kv, d)) return e;
   if (!may_split) return cudaSuccess;
-  cfg.gridDim = dim3(unsigned(di.sms * 4));
+  cfg.gridDim = dim3(unsigned(di.sms * 8));  // (4 an SM: 65 us for 59.7, the long context)
   cfg.blockDim = dim3(kJoinThreads);
   cfg.dynamicSmemBytes = 0;
   cfg.numAttrs = 1;  // the join always follows programmatically
