@@ -734,7 +734,7 @@ tt_status tt_token_logprobs(const void* logits, int32_t type, int64_t rows, int6
   if (top_k < 0 || top_k > vocab) return TT_ERR_SHAPE;
   if (top_k > tt::kMaxTop) return TT_ERR_UNSUPPORTED;
   if (!std::isfinite(scale)) return TT_ERR_NONFINITE;
-  if (!(scale > 0.f)) return TT_ERR_SHAPE;
+  if (!(scale >= 0x1p-100f && scale <= 0x1p100f)) return TT_ERR_SHAPE;
   if (!targets && logp) return TT_ERR_NULL;
   if (top_k == 0 && (top_ids || top_logp)) top_ids = nullptr, top_logp = nullptr;
   if (rows == 0) return TT_OK;

@@ -4,10 +4,10 @@
 //   logp = x[target] - lse;  H = log sum e^(x - m) - sum (x - m) e^(x - m) / sum e^(x - m)
 //
 // One pass over the logits, which are read once: bound by their bytes.  A thread
-// keeps a running maximum m, s = sum 2^y and t = sum y 2^y over its elements, with
-// y = x log2 e - m; where the maximum rises by d, s becomes 2^-d s and t becomes
-// 2^-d (t - d s).  Five instructions an element, so the exponentials and additions
-// hide behind the loads (bf16: 12 elements a cycle and SM).
+// keeps a running maximum m of the logits, s = sum 2^y and t = sum y 2^y over its
+// elements, with y = (logit - m) scale log2 e; where y falls by d, s becomes 2^-d s and t
+// becomes 2^-d (t - d s).  The difference comes first: logits of any size and scales of
+// any size overflow nowhere but towards weight 0.
 //
 // Top alternatives.  Logit and index make one key, larger for a larger logit and
 // for the smaller index of equal ones, so that all keys differ.  From the first
@@ -21,6 +21,8 @@
 // written in parts, joined by a second kernel.
 #include "launch.h"
 #include "common.cuh"
+
+#include <cfloat>
 
 namespace tt {
 namespace {
@@ -72,24 +74,24 @@ __device__ __forceinline__ float logit(const void* row, int64_t i) {
   return __ldcg(static_cast<const float*>(row) + i);
 }
 
+// How far y falls where the maximum rises from `from` to `to`; 2^-kFar is 0, and times a
+// sum it is finite.
+constexpr float kFar = 1000.f;
+__device__ __forceinline__ float fall(float to, float from, float k) {
+  return fminf((to - from) * k, kFar);
+}
+
 // Maximum and sums of the union.
 struct Sums {
   float m, s, t;
 };
-__device__ __forceinline__ Sums join(const Sums& a, const Sums& b) {
+__device__ __forceinline__ Sums join(const Sums& a, const Sums& b, float k) {
   Sums r;
   r.m = max_nan(a.m, b.m);
-  r.s = r.t = 0.f;
-  if (a.m != -INFINITY) {
-    const float d = r.m - a.m, f = ex2(-d);
-    r.s += a.s * f;
-    r.t += (a.t - d * a.s) * f;
-  }
-  if (b.m != -INFINITY) {
-    const float d = r.m - b.m, f = ex2(-d);
-    r.s += b.s * f;
-    r.t += (b.t - d * b.s) * f;
-  }
+  const float da = fall(r.m, a.m, k), db = fall(r.m, b.m, k);
+  const float fa = ex2(-da), fb = ex2(-db);
+  r.s = a.s * fa + b.s * fb;
+  r.t = (a.t - da * a.s) * fa + (b.t - db * b.s) * fb;
   return r;
 }
 
@@ -98,26 +100,25 @@ __device__ __forceinline__ Sums join(const Sums& a, const Sums& b) {
 template <bool BF16>
 __device__ __forceinline__ void write_row(const LogprobArgs& a, int64_t r, const Sums& z,
                                           const uint64_t* keys, int32_t* err) {
-  const float k = a.scale * kLog2e;
   // NaN unless the maximum is finite
-  const float ls = log2f(z.s) + (z.m - z.m);
+  const float ls = logf(z.s) + (z.m - z.m);
   const int tid = threadIdx.x;
   if (tid == 0) {
-    if (a.entropy) a.entropy[r] = (ls - z.t / z.s) * kLn2;
+    if (a.entropy) a.entropy[r] = ls - z.t / z.s * kLn2;
     if (a.logp) {
       const int t = __ldcg(a.targets + r);
       float y = t < 0 ? 0.f : NAN;
       if (t >= a.vocab) flag_error(err, kErrShape);
       if (t >= 0 && t < a.vocab) {
         const void* row = static_cast<const uint8_t*>(a.logits) + r * a.stride * (BF16 ? 2 : 4);
-        y = (fmaf(logit<BF16>(row, t), k, -z.m) - ls) * kLn2;
+        y = fmaf(logit<BF16>(row, t) - z.m, a.scale, -ls);
       }
       a.logp[r] = y;
     }
   }
   if (tid < a.top) {
     a.top_ids[r * a.top + tid] = id_of(keys[tid]);
-    if (a.top_logp) a.top_logp[r * a.top + tid] = (fmaf(logit_of(keys[tid]), k, -z.m) - ls) * kLn2;
+    if (a.top_logp) a.top_logp[r * a.top + tid] = fmaf(logit_of(keys[tid]) - z.m, a.scale, -ls);
   }
 }
 
@@ -173,6 +174,11 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
   return r;
 }
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
 __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   uint64_t r;
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
@@ -215,6 +221,28 @@ __device__ __noinline__ uint64_t largest_key(const void* row, int64_t i, int pie
   return most;
 }
 
+// Sums of a piece's weights and of y times weight, -infinity told from the lowest logit.
+template <bool BF16>
+__device__ __noinline__ float2 sums_of_piece(uint4 v, float m, float k) {
+  const uint32_t ws[4] = {v.x, v.y, v.z, v.w};
+  float2 r{0.f, 0.f};
+  auto add = [&](float x) {
+    const float y = fmaxf((x - m) * k, -kFar), w = ex2(y);
+    r.x += w;
+    r.y = fmaf(y, w, r.y);
+  };
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    if constexpr (BF16) {
+      add(__uint_as_float(ws[e] << 16));
+      add(__uint_as_float(ws[e] & 0xffff0000u));
+    } else {
+      add(__uint_as_float(ws[e]));
+    }
+  }
+  return r;
+}
+
 // kVectors: 16-byte pieces a thread and chunk.
 template <bool BF16, int kVectors>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm)
@@ -233,6 +261,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
   const int64_t begin = total * blockIdx.x / gridDim.x, end = total * (blockIdx.x + 1) / gridDim.x;
   const float k = a.scale * kLog2e;
   const uint64_t k2 = f2(k, k);
+  const float far = __fdiv_ru(kFar, k);  // kFar in logits
 
   for (int64_t at = begin; at < end;) {
     const int64_t r = at / chunks;
@@ -295,44 +324,60 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
         }
       }
       // ---- the sums
-      const float m = top * k;
-      if (!(m <= z.m)) {
-        const float d = m - z.m, f = ex2(-d);
-        z.t = z.m == -INFINITY ? 0.f : (z.t - d * z.s) * f;
+      if (!(top <= z.m)) {
+        const float d = fall(top, z.m, k), f = ex2(-d);
+        z.t = (z.t - d * z.s) * f;
         z.s *= f;
-        z.m = m;
+        z.m = max_nan(z.m, top);
       }
-      // what is 1000 below the maximum or more, -infinity too, has no weight (and no
-      // product of infinity and 0)
-      const float base = z.m == -INFINITY ? 0.f : -z.m;
-      const uint64_t base2 = f2(base, base);
+      const float m = z.m == -INFINITY ? 0.f : z.m;
+      const uint64_t m2 = f2(-m, -m);
       uint64_t s2 = 0, t2 = 0;
-      auto add = [&](float lo, float hi) {
-        const uint64_t y = fma2(f2(lo, hi), k2, base2);
-        un2(y, lo, hi);
-        const uint64_t w = f2(ex2(lo), ex2(hi));
-        s2 = add2(s2, w);
-        t2 = fma2(y, w, t2);
-      };
-      const float low = (-base - 1000.f) / k;
-      if constexpr (BF16) {
-        const __nv_bfloat162 low2 = __float2bfloat162_rn(low);
+      // What is `far` below the maximum or more has no weight, and is taken for `low`:
+      // -infinity times weight 0 is NaN.  Rounded down, so that no logit is taken for one
+      // with weight.
+      float low = __fsub_rd(m, far);
+      if constexpr (BF16) low = __bfloat162float(__float2bfloat16_rd(low));
+      low = fmaxf(low, BF16 ? __uint_as_float(0xff7f0000u) : -FLT_MAX);
+      const float least_y = (low - m) * k;
+      if (least_y <= -200.f && least_y >= -FLT_MAX) {
+        auto add = [&](float lo, float hi) {
+          const uint64_t y = mul2(add2(f2(lo, hi), m2), k2);
+          un2(y, lo, hi);
+          const uint64_t w = f2(ex2(lo), ex2(hi));
+          s2 = add2(s2, w);
+          t2 = fma2(y, w, t2);
+        };
+        if constexpr (BF16) {
+          const __nv_bfloat162 low2 = __float2bfloat162_rn(low);
 #pragma unroll
-        for (int j = 0; j < kVectors; ++j) {
-          const uint32_t ws[4] = {x[j].x, x[j].y, x[j].z, x[j].w};
+          for (int j = 0; j < kVectors; ++j) {
+            const uint32_t ws[4] = {x[j].x, x[j].y, x[j].z, x[j].w};
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const __nv_bfloat162 v =
-                __hmax2(*reinterpret_cast<const __nv_bfloat162*>(&ws[e]), low2);
-            const uint32_t w = *reinterpret_cast<const uint32_t*>(&v);
-            add(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+            for (int e = 0; e < 4; ++e) {
+              const __nv_bfloat162 v =
+                  __hmax2(*reinterpret_cast<const __nv_bfloat162*>(&ws[e]), low2);
+              const uint32_t w = *reinterpret_cast<const uint32_t*>(&v);
+              add(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+            }
+          }
+        } else {
+#pragma unroll
+          for (int j = 0; j < kVectors; ++j) {
+            add(fmaxf(__uint_as_float(x[j].x), low), fmaxf(__uint_as_float(x[j].y), low));
+            add(fmaxf(__uint_as_float(x[j].z), low), fmaxf(__uint_as_float(x[j].w), low));
           }
         }
-      } else {
-#pragma unroll
+      } else {  // the lowest finite logit has weight, or one step below the maximum is too far
+#pragma unroll 1
         for (int j = 0; j < kVectors; ++j) {
-          add(fmaxf(__uint_as_float(x[j].x), low), fmaxf(__uint_as_float(x[j].y), low));
-          add(fmaxf(__uint_as_float(x[j].z), low), fmaxf(__uint_as_float(x[j].w), low));
+          uint4 v = x[0];
+#pragma unroll
+          for (int e = 1; e < kVectors; ++e)
+            if (e == j) v = x[e];
+          const float2 part = sums_of_piece<BF16>(v, m, k);
+          z.s += part.x;
+          z.t += part.y;
         }
       }
       float lo, hi;
@@ -429,7 +474,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
       other.m = __shfl_xor_sync(kAll, z.m, o);
       other.s = __shfl_xor_sync(kAll, z.s, o);
       other.t = __shfl_xor_sync(kAll, z.t, o);
-      z = join(z, other);
+      z = join(z, other, k);
     }
     if (lane == 0) sums[warp] = z;
     __syncthreads();
@@ -447,7 +492,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     }
     z = sums[0];
 #pragma unroll 1
-    for (int w = 1; w < kWarps; ++w) z = join(z, sums[w]);
+    for (int w = 1; w < kWarps; ++w) z = join(z, sums[w], k);
     if (c0 == 0 && c1 == chunks) {
       write_row<BF16>(a, r, z, best, err);
     } else {
@@ -473,6 +518,7 @@ __global__ void __launch_bounds__(kThreads)
   __shared__ int s_count;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int64_t ctas = gridDim.x + 1;
+  const float k = a.scale * kLog2e;
   pdl_allow_next_grid();
   pdl_wait_prior_grid();
   const int64_t edge = total * (blockIdx.x + 1) / ctas;  // between the stretches
@@ -486,7 +532,7 @@ __global__ void __launch_bounds__(kThreads)
   for (int i = tid; i < n; i += kThreads) {
     const float4 p = __ldcg(reinterpret_cast<const float4*>(part(i)));
     if (a.top > 0) firsts[i] = __ldcg(part(i)->keys);
-    z = join(z, Sums{p.x, p.y, p.z});
+    z = join(z, Sums{p.x, p.y, p.z}, k);
   }
 #pragma unroll 1
   for (int o = 16; o > 0; o >>= 1) {
@@ -494,7 +540,7 @@ __global__ void __launch_bounds__(kThreads)
     other.m = __shfl_xor_sync(kAll, z.m, o);
     other.s = __shfl_xor_sync(kAll, z.s, o);
     other.t = __shfl_xor_sync(kAll, z.t, o);
-    z = join(z, other);
+    z = join(z, other, k);
   }
   if (lane == 0) sums[warp] = z;
   __syncthreads();
@@ -537,7 +583,7 @@ __global__ void __launch_bounds__(kThreads)
   }
   z = sums[0];
 #pragma unroll 1
-  for (int w = 1; w < kWarps; ++w) z = join(z, sums[w]);
+  for (int w = 1; w < kWarps; ++w) z = join(z, sums[w], k);
   write_row<BF16>(a, r, z, best, err);
 }
 

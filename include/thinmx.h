@@ -680,11 +680,12 @@ tt_status tt_paged_compact(const tt_paged_kv* layers, int32_t n_layers, const ui
  * (logp 0); one >= vocab is reported as TT_ERR_SHAPE in the device error word
  * (logp NaN).  logp, entropy fp32 [rows], each may be NULL; top_ids int32,
  * top_logp fp32 [rows][top_k], top_logp may be NULL, both with top_k = 0.
- * Sums are 32-bit.  A logit of -infinity has probability 0.  A row with a NaN or
+ * Sums are 32-bit, of differences from the row's largest logit (one past the type's
+ * range counts as infinite).  A logit of -infinity has probability 0.  A row with a NaN or
  * +infinity, or without a logit above -infinity, has NaN for all
  * probabilities and its entropy; NaN comes first in the order of logits.
- * Requires rows >= 0, 1 <= vocab <= 2^30, stride >= vocab, scale finite and above
- * 0, 0 <= top_k <= min(32, vocab).  logits aligned to their type, the rest 4 bytes;
+ * Requires rows >= 0, 1 <= vocab <= 2^30, stride >= vocab, 2^-100 <= scale <=
+ * 2^100, 0 <= top_k <= min(32, vocab).  logits aligned to their type, the rest 4 bytes;
  * workspace: >= tt_token_logprobs_workspace_bytes(...) bytes (may be 0 and
  * NULL), 16-byte aligned, no initial contents needed; calls that share one must
  * be ordered on one stream.

@@ -136,7 +136,7 @@ def test_logprobs_refusals(lib):
     assert logprobs(kind=2) == logprobs(kind=-1) == logprobs(rows=-1) == logprobs(rows=1 << 31) == 2
     assert logprobs(vocab=0) == logprobs(stride=999) == logprobs(top=-1) == logprobs(vocab=4, top=5) == 2
     assert logprobs(vocab=(1 << 30) + 1, stride=1 << 31) == logprobs(top=33) == 5
-    assert logprobs(scale=0.0) == logprobs(scale=-1.0) == 2
+    assert logprobs(scale=0.0) == logprobs(scale=-1.0) == logprobs(scale=2.0 ** -101) == logprobs(scale=2.0 ** 101) == 2
     assert logprobs(scale=float("inf")) == logprobs(scale=float("nan")) == 4
     assert logprobs(targets=None) == logprobs(logits=None) == logprobs(ids=None) == 1
     assert logprobs(logits=A + 1) == logprobs(kind=0, logits=A + 2) == 3

@@ -207,3 +207,56 @@ def test_same_results_each_time_and_in_a_graph():
         torch.cuda.synchronize()
         want = first if scale else run(normal(9, 3, 150000, True), 150000, 1.0, [5, 6, 7], 20)
         assert all(np.array_equal(gu.host(a), b) for a, b in zip((logp, ent, ids, tops), want))
+
+
+LOWEST = {True: float(np.uint32(0xff7f0000).view(np.float32)), False: float(np.finfo(np.float32).min)}
+
+
+@pytest.mark.parametrize("bf16", [True, False])
+@pytest.mark.parametrize("vocab", [50, 9000])
+@pytest.mark.parametrize("scale", [2.0 ** -100, 1e-6, 0.3, 1.0, 40.0, 1e4, 2.0 ** 100])
+def test_logits_and_scales_of_any_size(scale, vocab, bf16):
+    """Large logits beside small ones, the lowest finite logit beside -infinity: what counts is differences."""
+    r = synth.rng(WID, vocab, 6)
+    x = r.standard_normal((12, vocab)).astype(np.float32)
+    for i, big in enumerate((2.0 ** 11, 2.0 ** 18, 2.0 ** 24, 2.0 ** 40, 2.0 ** 100, 1.7e38)):
+        x[i] = np.where(r.random(vocab) < 0.1, big * (1 - 2.0 ** -7 * r.integers(0, 3, vocab)), x[i])
+        x[i, vocab // 2] = big
+    x[6] -= np.float32(2.0 ** 60)
+    x[7] = np.where(r.random(vocab) < 0.7, LOWEST[bf16], x[7])
+    x[8] = np.where(r.random(vocab) < 0.7, LOWEST[bf16], -np.inf)
+    x[9] = LOWEST[bf16]
+    x[10] = -np.inf
+    x[10, vocab // 3] = LOWEST[bf16]
+    x[11] = np.where(r.random(vocab) < 0.5, -np.inf, np.clip(x[11], -3, 3) * 1e38)
+    x[8, 3], x[11, 3] = LOWEST[bf16], 1e38
+    logits = synth.f32_to_bf16_bits(x) if bf16 else x
+    v = values(logits)
+    targets = [3] * 10 + [vocab // 3, 3]
+    logp, ent, ids, tops = run(logits, vocab, scale, targets, 5)
+    y = (v - v.max(1, keepdims=True)) * float(np.float32(scale))
+    gone = y < -800
+    p = np.where(gone, 0.0, np.exp(np.where(gone, 0.0, y)))
+    s = p.sum(1)
+    p /= s[:, None]
+    y0 = np.where(gone, 0.0, y)
+    # as above, and without the sums' own size: differences come first, each rounded to half a step
+    a1, a2 = (p * np.abs(y0)).sum(1), (p * y0 * y0).sum(1)
+    chain = (vocab / 128 + 64) * 2.0 ** -24
+    tol = chain + 2.0 ** -22 * (2 + a1) + 2.0 ** -22 * np.log(s)
+
+    def near(got, want, tol, what, far=False):
+        far = far | (want < -3e38)  # past what 32 bits hold
+        assert (got[far] < -2e38).all(), what
+        off = np.abs(got[~far] - want[~far]) - (np.broadcast_to(tol, want.shape) + 2.0 ** -21 * np.abs(want))[~far]
+        assert off.size == 0 or off.max() <= 0, f"{what} off by {off.max():.3e} over its bound"
+
+    with np.errstate(over="ignore"):  # differences past the type's range
+        past = np.isinf(v.astype(np.float32) - v.max(1, keepdims=True).astype(np.float32))
+    near(logp, y[np.arange(12), targets] - np.log(s), tol, "logp", past[np.arange(12), targets])
+    near(ent, np.log(s) - (p * y0).sum(1), tol + a1 * (2 * chain + 2.0 ** -21) + 2.0 ** -22 * a2, "entropy")
+    order = np.argsort(-v, axis=1, kind="stable")[:, :5]
+    assert np.array_equal(ids, order)
+    near(tops, np.take_along_axis(y, order, 1) - np.log(s)[:, None], tol[:, None], "top",
+         np.take_along_axis(past, order, 1))
+    assert gu.device_error() == 0
