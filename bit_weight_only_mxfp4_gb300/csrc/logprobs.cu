@@ -95,8 +95,22 @@ __device__ __forceinline__ Sums join(const Sums& a, const Sums& b, float k) {
   return r;
 }
 
-// The results of row r from its sums and its largest keys (in shared memory); by all
-// threads of the CTA.
+// The union of the warp's, in every lane.
+__device__ __forceinline__ Sums join_warp(Sums z, float k) {
+  float m = z.m;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(kAll, m, o));
+  const float d = fall(m, z.m, k), f = ex2(-d);
+  float s = z.s * f, t = (z.t - d * z.s) * f;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    s += __shfl_xor_sync(kAll, s, o);
+    t += __shfl_xor_sync(kAll, t, o);
+  }
+  return {m, s, t};
+}
+
+// The results of row r from its sums and its largest keys (in shared memory); by a warp.
 template <bool BF16>
 __device__ __forceinline__ void write_row(const LogprobArgs& a, int64_t r, const Sums& z,
                                           const uint64_t* keys, int32_t* err) {
@@ -221,6 +235,36 @@ __device__ __noinline__ uint64_t largest_key(const void* row, int64_t i, int pie
   return most;
 }
 
+// The largest of a piece's logits.
+template <bool BF16>
+__device__ __forceinline__ float largest_of(const uint4& v) {
+  if constexpr (BF16) {
+    auto two = [](uint32_t w) { return *reinterpret_cast<const __nv_bfloat162*>(&w); };
+    const __nv_bfloat162 m2 = __hmax2_nan(__hmax2_nan(two(v.x), two(v.y)), __hmax2_nan(two(v.z), two(v.w)));
+    return max_nan(__low2float(m2), __high2float(m2));
+  } else {
+    return max_nan(max_nan(__uint_as_float(v.x), __uint_as_float(v.y)),
+                   max_nan(__uint_as_float(v.z), __uint_as_float(v.w)));
+  }
+}
+
+// A bit for each of a piece's logits that is not below `least`.
+template <bool BF16>
+__device__ __forceinline__ uint32_t not_below(const uint4& v, float least) {
+  const uint32_t ws[4] = {v.x, v.y, v.z, v.w};
+  uint32_t bits = 0;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    if constexpr (BF16) {
+      bits |= uint32_t(!(__uint_as_float(ws[e] << 16) < least)) << (2 * e);
+      bits |= uint32_t(!(__uint_as_float(ws[e] & 0xffff0000u) < least)) << (2 * e + 1);
+    } else {
+      bits |= uint32_t(!(__uint_as_float(ws[e]) < least)) << e;
+    }
+  }
+  return bits;
+}
+
 // Sums of a piece's weights and of y times weight, -infinity told from the lowest logit.
 template <bool BF16>
 __device__ __noinline__ float2 sums_of_piece(uint4 v, float m, float k) {
@@ -298,11 +342,10 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     float least = -INFINITY;  // the bound's logit
     bool whole = true;        // all that reached the bound was collected
     if (tid == 0) s_count = 0;
-    uint4 x[kVectors], ahead[kVectors];
-    load(c0, x);
+    uint4 x[kVectors];
 #pragma unroll 1
     for (int c = c0; c < c1; ++c) {
-      if (c + 1 < c1) load(c + 1, ahead);
+      load(c, x);
       // ---- the largest
       float top;
       if constexpr (BF16) {
@@ -388,44 +431,20 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
       // ---- the largest keys
       if (a.top > 0) {
         const int64_t i0 = int64_t(c) * kChunk + mine0;
-        auto element = [&](int e) {
-          const uint4& v = x[e / kPer];
-          const int q = e % kPer;
-          if constexpr (BF16) {
-            const uint32_t w = q < 2 ? v.x : q < 4 ? v.y : q < 6 ? v.z : v.w;
-            return __uint_as_float(q & 1 ? w & 0xffff0000u : w << 16);
-          } else {
-            return __uint_as_float(q == 0 ? v.x : q == 1 ? v.y : q == 2 ? v.z : v.w);
-          }
-        };
-        auto index = [&](int e) { return i0 + int64_t(e / kPer) * kThreads * kPer + e % kPer; };
-        // what reaches the bound, into the buffer (as far as there is room)
-        auto collect = [&] {
-#pragma unroll
-          for (int e = 0; e < kPer * kVectors; ++e) {
-            const float v = element(e);
-            if (v < least) continue;
-            const int64_t i = index(e);
-            const uint64_t key = key_of(v, uint32_t(i));
-            if (i < 0 || i >= a.vocab || key < bound) continue;
-            const int n = atomicAdd(&s_count, 1);
-            if (n < kBuffer) buffer[n] = key;
-          }
-        };
         if (c == c0) {
-          // this thread's largest: its first element that is not below the largest (one
-          // of -infinity may lie outside the row)
-          uint64_t mine;
+          // A key of this thread's that is no larger than its largest: the largest logit,
+          // with the last index of the first piece that has it (one of -infinity may lie
+          // outside the row).
+          uint64_t mine = 0;
           if (top == -INFINITY) {
             mine = largest_key<BF16>(row, i0, kVectors, kThreads * kPer, a.vocab);
           } else {
-            int first = 0;
 #pragma unroll
-            for (int e = kPer * kVectors - 1; e >= 0; --e) {
-              const float y = element(e);
-              if (top != top ? y != y : y == top) first = e;
+            for (int j = 0; j < kVectors; ++j) {
+              const uint64_t key = key_of(largest_of<BF16>(x[j]),
+                                          uint32_t(i0 + int64_t(j) * kThreads * kPer + kPer - 1));
+              mine = key > mine ? key : mine;
             }
-            mine = key_of(top, uint32_t(i0 + int64_t(first / kPer) * kThreads * kPer + first % kPer));
           }
           uint64_t group = mine;
 #pragma unroll
@@ -435,20 +454,30 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
           }
           if ((lane & 7) == 0) groups[warp * 4 + lane / 8] = group;
           __syncthreads();
-          // every warp ranks the groups for itself
+          // every warp ranks the groups for itself; those without elements have 0
           const uint64_t g = groups[lane];
           int above = 0;
 #pragma unroll 8
-          for (int o = 0; o < 32; ++o) {
-            const uint64_t other = groups[o];
-            above += other > g || (other == g && o < lane);
-          }
+          for (int o = 0; o < 32; ++o) above += groups[o] > g;
           const int owner = __ffs(__ballot_sync(kAll, above == a.top - 1)) - 1;
-          bound = __shfl_sync(kAll, g, owner);
+          bound = owner >= 0 ? __shfl_sync(kAll, g, owner) : 0;
           least = bound ? logit_of(bound) : -INFINITY;
         }
-        // (one place for both: the code is long)
-        if (!(top < least)) collect();
+        // what reaches the bound goes into the buffer, as far as there is room
+        if (!(top < least)) {
+          uint32_t hits = 0;
+#pragma unroll
+          for (int j = 0; j < kVectors; ++j) hits |= not_below<BF16>(x[j], least) << (j * kPer);
+          for (; hits; hits &= hits - 1u) {
+            const int e = __ffs(hits) - 1;
+            const int64_t i = i0 + int64_t(e / kPer) * kThreads * kPer + e % kPer;
+            if (i < 0 || i >= a.vocab) continue;
+            const uint64_t key = key_of(logit<BF16>(row, i), uint32_t(i));
+            if (key < bound) continue;
+            const int n = atomicAdd(&s_count, 1);
+            if (n < kBuffer) buffer[n] = key;
+          }
+        }
         if ((c - c0) % kCheck == kCheck - 1 && c + 1 < c1) {
           __syncthreads();
           const int n = s_count;
@@ -464,18 +493,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
           __syncthreads();
         }
       }
-#pragma unroll
-      for (int j = 0; j < kVectors; ++j) x[j] = ahead[j];
     }
     // ---- the part's end
-#pragma unroll 1
-    for (int o = 16; o > 0; o >>= 1) {
-      Sums other;
-      other.m = __shfl_xor_sync(kAll, z.m, o);
-      other.s = __shfl_xor_sync(kAll, z.s, o);
-      other.t = __shfl_xor_sync(kAll, z.t, o);
-      z = join(z, other, k);
-    }
+    z = join_warp(z, k);
     if (lane == 0) sums[warp] = z;
     __syncthreads();
     if (a.top > 0) {
@@ -490,15 +510,15 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
       }
       __syncthreads();
     }
-    z = sums[0];
-#pragma unroll 1
-    for (int w = 1; w < kWarps; ++w) z = join(z, sums[w], k);
-    if (c0 == 0 && c1 == chunks) {
-      write_row<BF16>(a, r, z, best, err);
-    } else {
-      Part* p = parts + blockIdx.x * 2 + (c0 == 0 ? 1 : 0);
-      if (tid == 0) p->m = z.m, p->s = z.s, p->t = z.t;
-      if (tid < a.top) p->keys[tid] = best[tid];
+    if (warp == 0) {
+      z = join_warp(lane < kWarps ? sums[lane] : Sums{-INFINITY, 0.f, 0.f}, k);
+      if (c0 == 0 && c1 == chunks) {
+        write_row<BF16>(a, r, z, best, err);
+      } else {
+        Part* p = parts + blockIdx.x * 2 + (c0 == 0 ? 1 : 0);
+        if (tid == 0) p->m = z.m, p->s = z.s, p->t = z.t;
+        if (tid < a.top) p->keys[tid] = best[tid];
+      }
     }
     __syncthreads();
   }
@@ -534,14 +554,7 @@ __global__ void __launch_bounds__(kThreads)
     if (a.top > 0) firsts[i] = __ldcg(part(i)->keys);
     z = join(z, Sums{p.x, p.y, p.z}, k);
   }
-#pragma unroll 1
-  for (int o = 16; o > 0; o >>= 1) {
-    Sums other;
-    other.m = __shfl_xor_sync(kAll, z.m, o);
-    other.s = __shfl_xor_sync(kAll, z.s, o);
-    other.t = __shfl_xor_sync(kAll, z.t, o);
-    z = join(z, other, k);
-  }
+  z = join_warp(z, k);
   if (lane == 0) sums[warp] = z;
   __syncthreads();
   if (a.top > 0) {
@@ -581,9 +594,8 @@ __global__ void __launch_bounds__(kThreads)
     rank_keys(buffer, s_count < kMaxTop * kMaxTop ? s_count : kMaxTop * kMaxTop, a.top, best);
     __syncthreads();
   }
-  z = sums[0];
-#pragma unroll 1
-  for (int w = 1; w < kWarps; ++w) z = join(z, sums[w], k);
+  if (warp != 0) return;
+  z = join_warp(lane < kWarps ? sums[lane] : Sums{-INFINITY, 0.f, 0.f}, k);
   write_row<BF16>(a, r, z, best, err);
 }
 
