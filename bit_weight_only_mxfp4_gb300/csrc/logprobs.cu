@@ -23,8 +23,9 @@
 // written in parts, joined by a second kernel.
 //
 // Four CTAs an SM, without loads ahead: the other warps cover them (5 CTAs: 54.6 / 153.4 us
-// for the two below, 6: 68.0 / 202; with the next chunk's loads in flight, registers
-// spilled: 63.6 -> 65.2 and 161 -> 169, before ranking was cut down).
+// for the two below, 6: 68.0 / 202; the next chunk's loads into registers, some spilled:
+// 63.6 -> 65.2 and 161 -> 169, before ranking was cut down; two chunks ahead into shared
+// memory, by bulk copies of 2 KB a warp: 73 / 211, by cp.async: 65 / 187).
 //
 // Measured (back to back in a graph): 512 rows of 201088 in bf16, the best token, 52.7 us
 // (3.9 TB/s; 45 without any ranking: issue slots); 2047 rows of 100352 in 32 bits, five
