@@ -16,7 +16,10 @@
 // of 32 groups' largest.  After that only what reaches the bound, a few hundred
 // elements of a row, is collected in shared memory and ranked at the end, each key by
 // counting those above it; every eight chunks the ones collected so far give a better
-// bound (4: 53.2 / 156.7 us for the two below, 16: 53.4 / 160.3).
+// bound (4: 53.2 / 156.7 us for the two below, 16: 53.4 / 160.3).  The groups' bound is
+// the looser, the more keys are asked for: from eight on the first looks come after 1, 2
+// and 4 chunks (twenty tokens of the rows below: 90.5 -> 74.2 us, 209 -> 181; one or five:
+// 52.8 -> 53.6, 155 -> 157).
 //
 // Split.  A row is cut into chunks of 16 KB, the chunks of all rows form one line,
 // and each CTA takes an equal stretch.  A row that lies in several stretches is
@@ -30,7 +33,7 @@
 // Measured (back to back in a graph): 512 rows of 201088 in bf16, the best token, 52.7 us
 // (3.9 TB/s; 45 without any ranking: issue slots); 2047 rows of 100352 in 32 bits, five
 // tokens, 155 us (5.3 TB/s; 131 without ranking); one row of 128256 in bf16, twenty
-// tokens, 10.4 us (two launches, a few dependent loads and barriers each).
+// tokens, 9.9 us (two launches, a few dependent loads and barriers each).
 #include "launch.h"
 #include "common.cuh"
 
@@ -43,6 +46,7 @@ constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kCtasPerSm = 4;
 constexpr int kMaxCtas = 1024;
 constexpr int kBuffer = 2048;                   // keys that are collected
+constexpr int kEarly = 8;                       // keys from which the first looks come early
 constexpr int kCheck = 8;                       // chunks from one look at their number to the next
 constexpr uint32_t kAll = 0xffffffffu;
 constexpr int kErrShape = 2;
@@ -277,6 +281,21 @@ __device__ __forceinline__ uint32_t not_below(const uint4& v, float least) {
   return bits;
 }
 
+// Element e of a thread's pieces, by halves of what is left.
+template <bool BF16, int kVectors>
+__device__ __forceinline__ float element(const uint4 (&x)[kVectors], int e) {
+  const int at = BF16 ? e >> 1 : e;
+  uint32_t w[4 * kVectors];
+#pragma unroll
+  for (int j = 0; j < kVectors; ++j) w[4 * j] = x[j].x, w[4 * j + 1] = x[j].y, w[4 * j + 2] = x[j].z, w[4 * j + 3] = x[j].w;
+#pragma unroll
+  for (int half = 2 * kVectors; half > 0; half /= 2) {
+#pragma unroll
+    for (int i = 0; i < half; ++i) w[i] = at & half ? w[i + half] : w[i];
+  }
+  return __uint_as_float(!BF16 ? w[0] : e & 1 ? w[0] & 0xffff0000u : w[0] << 16);
+}
+
 // Sums of a piece's weights and of y times weight, -infinity told from the lowest logit.
 template <bool BF16>
 __device__ __noinline__ float2 sums_of_piece(uint4 v, float m, float k) {
@@ -449,7 +468,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
           // outside the row).
           uint64_t mine = 0;
           if (top == -INFINITY) {
-            mine = largest_key<BF16>(row, i0, kVectors, kThreads * kPer, a.vocab);
+            if (i0 < a.vocab) mine = largest_key<BF16>(row, i0, kVectors, kThreads * kPer, a.vocab);
           } else {
 #pragma unroll
             for (int j = 0; j < kVectors; ++j) {
@@ -484,13 +503,14 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
             const int e = __ffs(hits) - 1;
             const int64_t i = i0 + int64_t(e / kPer) * kThreads * kPer + e % kPer;
             if (i < 0 || i >= a.vocab) continue;
-            const uint64_t key = key_of(logit<BF16>(row, i), uint32_t(i));
+            const uint64_t key = key_of(element<BF16>(x, e), uint32_t(i));
             if (key < bound) continue;
             const int n = atomicAdd(&s_count, 1);
             if (n < kBuffer) buffer[n] = key;
           }
         }
-        if ((c - c0) % kCheck == kCheck - 1 && c + 1 < c1) {
+        const int done = c - c0 + 1;
+        if ((done % kCheck == 0 || (a.top >= kEarly && (done & (done - 1)) == 0)) && c + 1 < c1) {
           __syncthreads();
           const int n = s_count;
           whole &= n <= kBuffer;
