@@ -35,11 +35,11 @@
 // The running maximum is only raised (and O rescaled) when a row's maximum has
 // grown by more than 2^8.
 //
-// Measured (back to back in a graph): 8 new tokens on 332, 16 / 4 heads of 128, 15.3 us (a
-// start, one or two tiles, the join); 64 on 32767, 64 / 8 heads of 64, 59.6 us (0.3 of the
+// Measured (back to back in a graph): 8 new tokens on 332, 16 / 4 heads of 128, 15.1 us (a
+// start, one or two tiles, the join); 64 on 32767, 64 / 8 heads of 64, 59.2 us (0.3 of the
 // bf16 rate: S -> softmax -> P V of a row tile, 47% of issue slots; without softmax 51 to
-// 56); 32 ragged sequences, up to 16 on up to 8191, 16 / 4 heads of 128, 64.0 us (4.3 TB/s;
-// without softmax 59); 48, up to 24 on up to 12000, 64 / 8 heads of 64 in FP8, 255 us
+// 56); 32 ragged sequences, up to 16 on up to 8191, 16 / 4 heads of 128, 63.8 us (4.3 TB/s;
+// without softmax 59); 48, up to 24 on up to 12000, 64 / 8 heads of 64 in FP8, 249 us
 // (without conversion 182, without softmax 212, without both 140: four converting and
 // eight softmax warps share the issue slots, 52% busy).
 //
@@ -758,44 +758,33 @@ __global__ void __launch_bounds__(Plan<D, FP8>::kThreads, 1)
         commit(smem_u32(&empty[slot]));
         if (P::kOwnP || __any_sync(kAll, ends & 2)) commit(smem_u32(&o_done[g]));
       };
-      // Tiles, P V issued, scores issued, segments whose scores are all issued.  A test
-      // of a barrier takes some 150 cycles, so all of a round go out together, asked for
-      // in one vote each.
+      // Tiles, P V issued, scores issued, segments whose scores are all issued.  With 64
+      // dims a tile's scores go out before the P V of the tile before, unless a new
+      // segment begins with it, whose Q may be late; with 128 dims P lies over S, and P V
+      // goes first.
       const uint32_t n = uint32_t(tiles_all[g]);
       uint32_t v = 0, sc = 0, seg = 0;
-      uint64_t since = 0;  // of the idle stretch
-      for (uint32_t idle = 0; ok && v < n;) {
-        auto there = [](uint64_t* bar, uint32_t phase) {
-          return mbar_test_wait(smem_u32(bar), phase & 1u);
-        };
-        const bool weights = there(&p_full[g], v);
-        const bool value = there(&ready[slot_of(g, 1, v)], v / P::kDepth);
-        const bool key = there((FP8 ? ready : full) + slot_of(g, 0, sc), sc / P::kDepth);
-        const bool read = !P::kOwnP || there(&s_read[g], sc - 1u);
-        const bool query = there(&q_full[g], seg);
-        const int v_ends = plans[g * kAhead + v % kAhead].ends;
-        const int s_ends = plans[g * kAhead + sc % kAhead].ends;
-        const bool pv = __all_sync(kAll, weights && value) && v < sc;
-        // the next scores: with 128 dims once the P V that lie there are issued, else once
-        // those before are read
-        const bool qk = __all_sync(kAll, key && read && query) && sc < n &&
-                        (P::kOwnP || sc == v + pv);
-        if (pv | qk) fence_after();
-        if (pv) values(v++, v_ends);
-        if (qk) {
+      auto await = [&](uint64_t* bar, uint32_t phase) {
+        ok = ok && __all_sync(kAll, wait(bar, phase & 1u, quit, a.err));
+      };
+      while (ok && v < n) {
+        const bool ahead = P::kOwnP && sc == v + 1 && !(plans[g * kAhead + v % kAhead].ends & 2);
+        if (__any_sync(kAll, sc < n && (sc == v || ahead))) {
+          await((FP8 ? ready : full) + slot_of(g, 0, sc), sc / P::kDepth);
+          if (P::kOwnP) await(&s_read[g], sc - 1u);
+          await(&q_full[g], seg);
+          if (!ok) break;
+          fence_after();
+          const int ends = plans[g * kAhead + sc % kAhead].ends;
           scores(sc++);
-          seg += (s_ends >> 1) & 1;
-        }
-        const bool did = pv | qk;
-        if (did) {
-          idle = 0;
-        } else if ((++idle & 63u) == 0u) {
-          if (idle == 64u) since = globaltimer_ns();
-          if (globaltimer_ns() - since > kWaitLimitNs && lane == 0) {
-            *quit = 1;
-            flag_error(a.err, kErrTimeout);
-          }
-          if (__any_sync(kAll, *quit)) ok = false;
+          seg += (ends >> 1) & 1;
+        } else {
+          await(&ready[slot_of(g, 1, v)], v / P::kDepth);
+          await(&p_full[g], v);
+          if (!ok) break;
+          fence_after();
+          values(v, plans[g * kAhead + v % kAhead].ends);
+          ++v;
         }
       }
       // nothing of the tensor cores is under way when the CTA ends
