@@ -575,7 +575,9 @@ tt_status tt_draft_tree(const int32_t* parents, const int32_t* q_starts, const i
  * A token that sees no key: out 0, lse = sinks[h] (-inf without sinks).  With
  * lens[b] < n_b the tokens without a place in the cache see nothing and are
  * seen by none.  Requires the same of heads, scale, softcap, window, q_stride
- * and tokens as tt_paged_prefill_attention, and 1 <= mask_words <= 8.
+ * and tokens as tt_paged_prefill_attention, and 1 <= mask_words <= 8; the table's
+ * tiles of 128 keys times (tokens * heads / 64 + batch * kv_heads) may not pass
+ * 2^40 (TT_ERR_UNSUPPORTED).
  * workspace: >= tt_paged_tree_workspace_bytes(...) bytes, no initial
  * contents needed; one of that size and of tt_paged_attention_workspace_bytes
  * may serve all three attentions.  Calls that share one must be ordered on

@@ -86,6 +86,8 @@ def test_tree_attention_refusals(lib):
     assert attend(c, tokens=-1) == attend(c, tokens=1 << 31) == 2
     assert attend(c, words=0) == 2
     assert attend(c, words=9) == 5
+    # 2^17 tiles of keys for each of some 2^24 tiles of rows
+    assert attend(kv(pages_per_seq=1 << 20, page_size=16), tokens=1 << 26) == 5
     for name in ("q", "starts", "masks", "out", "ws"):
         assert attend(c, **{name: None}) == 1
     assert attend(c, q=A + 8) == attend(c, out=A + 2) == attend(c, ws=A + 8) == attend(c, starts=A + 2) == 3
