@@ -30,10 +30,10 @@
 // 63.6 -> 65.2 and 161 -> 169, before ranking was cut down; two chunks ahead into shared
 // memory, by bulk copies of 2 KB a warp: 73 / 211, by cp.async: 65 / 187).
 //
-// Measured (back to back in a graph): 512 rows of 201088 in bf16, the best token, 52.7 us
-// (3.9 TB/s; 45 without any ranking: issue slots); 2047 rows of 100352 in 32 bits, five
-// tokens, 155 us (5.3 TB/s; 131 without ranking); one row of 128256 in bf16, twenty
-// tokens, 9.9 us (two launches, a few dependent loads and barriers each).
+// Measured (back to back in a graph): 512 rows of 201088 in bf16, the best token, 51.8 us
+// (4.0 TB/s; some 44 without any ranking: issue slots); 2047 rows of 100352 in 32 bits, five
+// tokens, 151 us (5.4 TB/s; some 130 without ranking); one row of 128256 in bf16, twenty
+// tokens, 10.0 us (two launches, a few dependent loads and barriers each).
 #include "launch.h"
 #include "common.cuh"
 
@@ -126,23 +126,28 @@ __device__ __forceinline__ Sums join_warp(Sums z, float k) {
   return {m, s, t};
 }
 
+// Row r's target (in the first thread, and if there are any), and its logit.
+__device__ __forceinline__ int target_of(const LogprobArgs& a, int64_t r) {
+  return threadIdx.x == 0 && a.logp ? __ldcg(a.targets + r) : -1;
+}
+template <bool BF16>
+__device__ __forceinline__ float target_logit(const LogprobArgs& a, const void* row, int t) {
+  return t >= 0 && t < a.vocab ? logit<BF16>(row, t) : 0.f;
+}
+
 // The results of row r from its sums and its largest keys (in shared memory); by a warp.
 template <bool BF16>
 __device__ __forceinline__ void write_row(const LogprobArgs& a, int64_t r, const Sums& z,
-                                          const uint64_t* keys, int32_t* err) {
+                                          const uint64_t* keys, int t, float x, int32_t* err) {
   // NaN unless the maximum is finite
   const float ls = logf(z.s) + (z.m - z.m);
   const int tid = threadIdx.x;
   if (tid == 0) {
     if (a.entropy) a.entropy[r] = ls - z.t / z.s * kLn2;
     if (a.logp) {
-      const int t = __ldcg(a.targets + r);
       float y = t < 0 ? 0.f : NAN;
       if (t >= a.vocab) flag_error(err, kErrShape);
-      if (t >= 0 && t < a.vocab) {
-        const void* row = static_cast<const uint8_t*>(a.logits) + r * a.stride * (BF16 ? 2 : 4);
-        y = fmaf(logit<BF16>(row, t) - z.m, a.scale, -ls);
-      }
+      if (t >= 0 && t < a.vocab) y = fmaf(x - z.m, a.scale, -ls);
       a.logp[r] = y;
     }
   }
@@ -356,18 +361,29 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
 #pragma unroll
         for (int j = 0; j < kVectors; ++j) x[j] = __ldcg(p + j * kThreads);
       } else {  // one of the row's ends
-#pragma unroll 1
+        const uint32_t none = BF16 ? 0xff80ff80u : 0xff800000u;
+        uint32_t cut = 0;
+#pragma unroll
         for (int j = 0; j < kVectors; ++j) {
           const int64_t i = i0 + int64_t(j) * kThreads * kPer;
-          const uint4 v = i >= 0 && i + kPer <= a.vocab
-                              ? __ldcg(reinterpret_cast<const uint4*>(row + i * kBytes))
-                              : piece_at_end<BF16>(row, i, a.vocab);
+          x[j] = make_uint4(none, none, none, none);
+          if (i >= 0 && i + kPer <= a.vocab)
+            x[j] = __ldcg(reinterpret_cast<const uint4*>(row + i * kBytes));
+          else if (i < a.vocab && i + kPer > 0)
+            cut |= 1u << j;
+        }
+        for (; cut; cut &= cut - 1u) {
+          const int j = __ffs(cut) - 1;
+          const uint4 v = piece_at_end<BF16>(row, i0 + int64_t(j) * kThreads * kPer, a.vocab);
 #pragma unroll
           for (int e = 0; e < kVectors; ++e)
             if (e == j) x[e] = v;
         }
       }
     };
+    // asked for early: with its logit two round trips, which a short row would wait for
+    const int t = c0 == 0 && c1 == chunks ? target_of(a, r) : -1;
+    float t_logit = 0.f;
     Sums z{-INFINITY, 0.f, 0.f};
     uint64_t bound = 0;
     float least = -INFINITY;  // the bound's logit
@@ -377,6 +393,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
 #pragma unroll 1
     for (int c = c0; c < c1; ++c) {
       load(c, x);
+      if (c == c0) t_logit = target_logit<BF16>(a, row, t);
       // ---- the largest
       float top;
       if constexpr (BF16) {
@@ -545,7 +562,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     if (warp == 0) {
       z = join_warp(lane < kWarps ? sums[lane] : Sums{-INFINITY, 0.f, 0.f}, k);
       if (c0 == 0 && c1 == chunks) {
-        write_row<BF16>(a, r, z, best, err);
+        write_row<BF16>(a, r, z, best, t, t_logit, err);
       } else {
         Part* p = parts + blockIdx.x * 2 + (c0 == 0 ? 1 : 0);
         if (tid == 0) p->m = z.m, p->s = z.s, p->t = z.t;
@@ -580,6 +597,8 @@ __global__ void __launch_bounds__(kThreads)
   const int n = int(((first + chunks) * ctas + total - 1) / total) - 1 - int(blockIdx.x) + 1;
   auto part = [&](int i) { return parts + (int64_t(blockIdx.x) + i) * 2 + (i == 0 ? 1 : 0); };
   if (tid == 0) s_count = 0, s_bound = 0;
+  const int t = target_of(a, r);
+  const float t_logit = target_logit<BF16>(a, static_cast<const uint8_t*>(a.logits) + r * a.stride * (BF16 ? 2 : 4), t);
   Sums z{-INFINITY, 0.f, 0.f};
   for (int i = tid; i < n; i += kThreads) {
     const float4 p = __ldcg(reinterpret_cast<const float4*>(part(i)));
@@ -628,7 +647,7 @@ __global__ void __launch_bounds__(kThreads)
   }
   if (warp != 0) return;
   z = join_warp(lane < kWarps ? sums[lane] : Sums{-INFINITY, 0.f, 0.f}, k);
-  write_row<BF16>(a, r, z, best, err);
+  write_row<BF16>(a, r, z, best, t, t_logit, err);
 }
 
 // Chunks of a row, wherever it begins.
