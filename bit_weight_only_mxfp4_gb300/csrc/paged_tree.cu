@@ -37,11 +37,11 @@
 //
 // Measured (back to back in a graph): 8 new tokens on 332, 16 / 4 heads of 128, 15.1 us (a
 // start, one or two tiles, the join); 64 on 32767, 64 / 8 heads of 64, 59.2 us (0.3 of the
-// bf16 rate: S -> softmax -> P V of a row tile, 47% of issue slots; without softmax 51 to
+// bf16 rate: S -> softmax -> P V of a row tile, 46% of issue slots; without softmax 51 to
 // 56); 32 ragged sequences, up to 16 on up to 8191, 16 / 4 heads of 128, 63.8 us (4.3 TB/s;
 // without softmax 59); 48, up to 24 on up to 12000, 64 / 8 heads of 64 in FP8, 249 us
 // (without conversion 182, without softmax 212, without both 140: four converting and
-// eight softmax warps share the issue slots, 52% busy).
+// eight softmax warps share the issue slots, 51% busy).
 //
 // Rounding.  Q and K products are exact, sums 32-bit; P is rounded once to bf16
 // (2^-8 of each weight); the sum of weights is taken from the unrounded ones.
