@@ -92,6 +92,7 @@ SIGNATURES = {
 
 TT_KV_BF16 = 0
 TT_KV_FP8 = 1
+TT_PAGED_MAX_LAYERS = 128
 TT_LOGITS_F32 = 0
 TT_LOGITS_BF16 = 1
 
@@ -312,6 +313,14 @@ def _kv(kv):
     return None if kv is None else ctypes.addressof(kv)
 
 
+def _layers(kvs, n):
+    """The same of n of them: an array of fewer would be read past its end."""
+    have = len(kvs) if isinstance(kvs, ctypes.Array) else 1
+    if kvs is not None and have < n <= TT_PAGED_MAX_LAYERS:
+        raise ValueError(f"{n} layers of {have}")
+    return _kv(kvs)
+
+
 def tt_paged_rope_append(kv, q, k, v, q_stride, kv_stride, tokens, q_starts, heads, turns, rot_dim,
                          interleaved, positions, axes, pair_axis, q_out, stream=None):
     _check("tt_paged_rope_append", load().tt_paged_rope_append(
@@ -370,7 +379,7 @@ def tt_draft_accept(parents, drafts, chosen, q_starts, batch, tokens, path_width
 def tt_paged_keep(layers, n_layers, q_starts, path, path_width, counts, lens_out, stream=None):
     """layers: from loader.paged_layers (or one tt_paged_kv with n_layers = 1)."""
     _check("tt_paged_keep", load().tt_paged_keep(
-        _kv(layers), n_layers, _ptr(q_starts), _ptr(path), path_width, _ptr(counts),
+        _layers(layers, n_layers), n_layers, _ptr(q_starts), _ptr(path), path_width, _ptr(counts),
         _ptr(lens_out), _stream(stream)))
 
 
@@ -388,14 +397,14 @@ def tt_paged_resize(kv, want, held, table_out, lens_out, left, workspace, worksp
 def tt_paged_fork(layers, n_layers, from_, held, table_out, lens_out, left, workspace,
                   workspace_bytes, stream=None):
     _check("tt_paged_fork", load().tt_paged_fork(
-        _kv(layers), n_layers, _ptr(from_), _ptr(held), _ptr(table_out), _ptr(lens_out),
+        _layers(layers, n_layers), n_layers, _ptr(from_), _ptr(held), _ptr(table_out), _ptr(lens_out),
         _ptr(left), _ptr(workspace), workspace_bytes, _stream(stream)))
 
 
 def tt_paged_compact(layers, n_layers, held, table_out, span, workspace, workspace_bytes,
                      stream=None):
     _check("tt_paged_compact", load().tt_paged_compact(
-        _kv(layers), n_layers, _ptr(held), _ptr(table_out), _ptr(span), _ptr(workspace),
+        _layers(layers, n_layers), n_layers, _ptr(held), _ptr(table_out), _ptr(span), _ptr(workspace),
         workspace_bytes, _stream(stream)))
 
 

@@ -609,9 +609,9 @@ tt_status tt_draft_accept(const int32_t* parents, const int32_t* drafts, const i
  * Rows and pages.  These take the caches of all layers at once: an array (host
  * memory, read during the call) of n_layers descriptions, 1 <= n_layers <=
  * TT_PAGED_MAX_LAYERS, which share page_table and lens and agree in all sizes
- * (else TT_ERR_SHAPE).  table_out int32 [batch][pages_per_seq] may be the
- * page_table itself, lens_out int32 [batch] the lens; otherwise they may not
- * overlap.  A table entry >= num_pages is reported as TT_ERR_SHAPE in the device
+ * (else TT_ERR_SHAPE), and whose pools do not overlap.  table_out int32
+ * [batch][pages_per_seq] may be the page_table itself, lens_out int32 [batch] the
+ * lens; otherwise they may not overlap.  A table entry >= num_pages is reported as TT_ERR_SHAPE in the device
  * error word and taken for a hole.
  * --------------------------------------------------------------------- */
 #define TT_PAGED_MAX_LAYERS 128

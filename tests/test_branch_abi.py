@@ -152,3 +152,12 @@ def test_logprobs_refusals(lib):
     thinmx.tt_token_logprobs(None, 1, 0, 1000, 1000, 1.0, None, 0, None, None, None, None, None, 0, stream=0)
     for bad in ((0, 1000, 5), (3, 0, 0), (3, 1000, -1), (3, 1000, 33)):
         assert thinmx.tt_token_logprobs_workspace_bytes(*bad) == 0
+
+
+def test_more_layers_than_there_are(lib):
+    two = loader.paged_layers([kv(), kv()])
+    for call in (keep, fork, compact):
+        with pytest.raises(ValueError):
+            call(two, n=3)
+        with pytest.raises(ValueError):
+            call(kv(), n=2)
