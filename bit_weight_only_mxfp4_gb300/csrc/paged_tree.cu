@@ -9,7 +9,7 @@
 // to about 280 rows a kv head (140 on an FP8 cache), and by the products beyond;
 // the products belong to the tensor cores either way:
 //   S = Q K^T   128 rows x 128 tokens, tcgen05.mma, accumulator in TMEM
-//   P = 2^(S - m) in bf16, back to TMEM
+//   P = 2^(S - m) as bf16 high + low parts, back to TMEM
 //   O += P V    A operand P from TMEM, B operand V as it lies in the cache
 //
 // Split.  A piece is a row tile (floor(128 / G) tokens x G heads) of a sequence and
@@ -35,17 +35,18 @@
 // The running maximum is only raised (and O rescaled) when a row's maximum has
 // grown by more than 2^8.
 //
-// Measured (back to back in a graph): 8 new tokens on 332, 16 / 4 heads of 128, 15.1 us (a
-// start, one or two tiles, the join); 64 on 32767, 64 / 8 heads of 64, 59.2 us (0.3 of the
-// bf16 rate: S -> softmax -> P V of a row tile, 46% of issue slots; without softmax 51 to
-// 56); 32 ragged sequences, up to 16 on up to 8191, 16 / 4 heads of 128, 63.8 us (4.3 TB/s;
-// without softmax 59); 48, up to 24 on up to 12000, 64 / 8 heads of 64 in FP8, 249 us
-// (without conversion 182, without softmax 212, without both 140: four converting and
-// eight softmax warps share the issue slots, 51% busy).
+// Measured (back to back in a graph): 8 new tokens on 332, 16 / 4 heads of 128, 16.7 us (a
+// start, one or two tiles, the join); 64 on 32767, 64 / 8 heads of 64, 86.8 us (0.21 of the
+// bf16 rate: S -> softmax -> P V of a row tile; without softmax 68); 32 ragged sequences, up
+// to 16 on up to 8191, 16 / 4 heads of 128, 69.7 us (3.9 TB/s; without softmax 64.5); 48, up
+// to 24 on up to 12000, 64 / 8 heads of 64 in FP8, 284 us (without conversion 259, without
+// softmax 226, without both 176: four converting and eight softmax warps share the issue
+// slots).  With weights rounded once to bf16 these were 15.1, 59.2, 63.8 and 249.
 //
-// Rounding.  Q and K products are exact, sums 32-bit; P is rounded once to bf16
-// (2^-8 of each weight); the sum of weights is taken from the unrounded ones.
-// FP8: codes become bf16 exactly, the scales multiply S and P in 32 bits.
+// Rounding.  Q and K products are exact, sums 32-bit; P is a bf16 high and low part
+// (2^-16 of each weight, as in the decode kernel: a drafted step's output should not
+// lose to the step that it takes the place of); the sum of weights is taken from the
+// unrounded ones.  FP8: codes become bf16 exactly, the scales multiply S and P in 32 bits.
 //
 // Masked values.  0 * NaN is NaN, so a V row that some row must not see (a new
 // token's, or one that the window cuts) may not enter the product with NaN or
@@ -64,6 +65,7 @@ constexpr int kMaxCtas = 1024;
 constexpr int kCounters = 1024;  // the decode kernel's, at the workspace's start: left alone
 constexpr int kAhead = 4;        // tiles of a group that are planned at once
 constexpr int kDirty = 8;
+constexpr float kBelowOne = 0x1.fffffep-1f;  // times it a weight falls by its last bit or two
 
 // What the warps of a group know of a tile.
 struct Tile {
@@ -106,13 +108,21 @@ struct Plan {
   static constexpr int kSmem = 1024 + kOffBar + 768;
   static_assert(kSmem <= 227 * 1024, "shared memory");
   static_assert(kOffBar % 8 == 0 && kOffLine % 8 == 0, "alignment");
-  // TMEM columns of the groups: S, O and P.  With 128 dims P lies over S and the
-  // next scores wait for P V; with 64 it has its own, and they wait only until S
-  // is read.
-  static constexpr bool kOwnP = D == 64;
+  // TMEM columns of the groups: S, O and P, for every kChunk tokens the high parts and
+  // then the low ones.  P lies over S, and the next scores wait for P V; with 64 dims of
+  // bf16 the next scores wait only until S is read, and one half of P at a time has
+  // columns of its own: the second one waits for the first one's products.
+  static constexpr bool kOwnP = D == 64 && !FP8;
+  static constexpr int kPass = FP8 ? kKeys : kKeys / 2;  // tokens that P goes to the products with
+  static constexpr int kPasses = kKeys / kPass;
+  // (FP8, the batch below: 64 tokens 316 us, 32 285, 128 283)
+  static constexpr int kChunk = FP8 ? 32 : 64;
+  static_assert(!kOwnP || kChunk == kPass, "a wait for each pass");
   __host__ __device__ static constexpr int kColS(int g) { return 128 * g; }
   __host__ __device__ static constexpr int kColO(int g) { return 256 + D * g; }
-  __host__ __device__ static constexpr int kColP(int g) { return kOwnP ? 384 + 64 * g : kColS(g); }
+  __host__ __device__ static constexpr int kColP(int g, int pass) {
+    return kOwnP ? 384 + 64 * g : kColS(g) + kPass * pass;
+  }
   static constexpr int kPartFloats = kRows * (D + 2);
 };
 
@@ -273,6 +283,10 @@ __device__ __noinline__ bool tree_make_safe(uint8_t* tile, const Tile* d, int va
   return bad;
 }
 
+// A chunk of P to its columns (complete after wait_st).
+__device__ __forceinline__ void tmem_put(uint32_t addr, const uint32_t (&r)[32]) { tmem_st32(addr, r); }
+__device__ __forceinline__ void tmem_put(uint32_t addr, const uint32_t (&r)[64]) { tmem_st64(addr, r); }
+
 // What is done to the scores: nothing but a positive scale; a cap, a bias or
 // another scale; a large cap.
 enum Scores { kPlain, kGeneral, kLargeCap };
@@ -302,9 +316,10 @@ __global__ void __launch_bounds__(Plan<D, FP8>::kThreads, 1)
   uint64_t* freed = planned + 2 * kAhead;   // [2][kAhead], when a tile is used up
   uint64_t* q_full = freed + 2 * kAhead;    // [2], of the groups, and so on
   uint64_t* s_full = q_full + 2;
-  uint64_t* p_full = s_full + 2;
-  uint64_t* o_done = p_full + 2;
-  uint64_t* s_read = o_done + 2;
+  uint64_t* p_full = s_full + 2;  // [pass][2]
+  uint64_t* o_done = p_full + 4;
+  uint64_t* half_done = o_done + 2;
+  uint64_t* s_read = half_done + 2;
   uint64_t* shifted = s_read + 2;
   uint64_t* drained = shifted + 2;
   int* dirty = reinterpret_cast<int*>(drained + 2);  // [2][kDirty] segment
@@ -327,7 +342,9 @@ __global__ void __launch_bounds__(Plan<D, FP8>::kThreads, 1)
       mbar_init(smem_u32(&q_full[g]), 1);
       mbar_init(smem_u32(&s_full[g]), 1);
       mbar_init(smem_u32(&p_full[g]), kRows);
+      mbar_init(smem_u32(&p_full[2 + g]), kRows);
       mbar_init(smem_u32(&o_done[g]), 1);
+      mbar_init(smem_u32(&half_done[g]), 1);
       mbar_init(smem_u32(&s_read[g]), kRows);
       mbar_init(smem_u32(&shifted[g]), kRows);
       mbar_init(smem_u32(&drained[g]), 1);
@@ -748,20 +765,26 @@ __global__ void __launch_bounds__(Plan<D, FP8>::kThreads, 1)
         commit(smem_u32(&s_full[g]));
         commit(smem_u32(&empty[slot]));
       };
-      auto values = [&](uint32_t i, int ends) {
+      auto values = [&](uint32_t i, int pass, int ends) {
         const uint32_t slot = slot_of(g, 1, i);
         const uint64_t v = desc_mn(kv0 + slot * P::kTile, P::kHalves > 1 ? P::kSpan : 1024);
 #pragma unroll 1
-        for (int k = 0; k < kKeys / 16; ++k)
-          mma_ts(P::kColO(g), P::kColP(g) + 8 * k, v + k * (2048 >> 4), idesc(D, true),
-                 k > 0 ? 1u : uint32_t(!(ends & 1)));
-        commit(smem_u32(&empty[slot]));
-        if (P::kOwnP || __any_sync(kAll, ends & 2)) commit(smem_u32(&o_done[g]));
+        for (int k = 0; k < 2 * P::kPass / 16; ++k) {  // (16 tokens' high or low parts)
+          constexpr int kIn = P::kChunk / 16;
+          const int at = pass * (P::kPass / 16) + k / (2 * kIn) * kIn + k % kIn;
+          mma_ts(P::kColO(g), P::kColP(g, pass) + 8 * k, v + at * (2048 >> 4), idesc(D, true),
+                 pass + k > 0 ? 1u : uint32_t(!(ends & 1)));
+        }
+        if (pass + 1 < P::kPasses) {
+          if (P::kOwnP) commit(smem_u32(&half_done[g]));
+        } else {
+          commit(smem_u32(&empty[slot]));
+          if (P::kOwnP || __any_sync(kAll, ends & 2)) commit(smem_u32(&o_done[g]));
+        }
       };
-      // Tiles, P V issued, scores issued, segments whose scores are all issued.  With 64
-      // dims a tile's scores go out before the P V of the tile before, unless a new
-      // segment begins with it, whose Q may be late; with 128 dims P lies over S, and P V
-      // goes first.
+      // Tiles, P V issued, scores issued, segments whose scores are all issued.  Where P has
+      // its own columns a tile's scores go out before the P V of the tile before, unless a
+      // new segment begins with it, whose Q may be late; where P lies over S, P V goes first.
       const uint32_t n = uint32_t(tiles_all[g]);
       uint32_t v = 0, sc = 0, seg = 0;
       auto await = [&](uint64_t* bar, uint32_t phase) {
@@ -780,10 +803,14 @@ __global__ void __launch_bounds__(Plan<D, FP8>::kThreads, 1)
           seg += (ends >> 1) & 1;
         } else {
           await(&ready[slot_of(g, 1, v)], v / P::kDepth);
-          await(&p_full[g], v);
-          if (!ok) break;
-          fence_after();
-          values(v, plans[g * kAhead + v % kAhead].ends);
+          const int ends = plans[g * kAhead + v % kAhead].ends;
+#pragma unroll 1
+          for (int pass = 0; pass < P::kPasses; ++pass) {
+            await(&p_full[2 * pass + g], v);
+            if (!ok) break;
+            fence_after();
+            values(v, pass, ends);
+          }
           ++v;
         }
       }
@@ -797,8 +824,7 @@ __global__ void __launch_bounds__(Plan<D, FP8>::kThreads, 1)
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(P::kSoftmaxRegs));
     const int g = warp >> 2, r = tid & (kRows - 1);
     const uint32_t lanes = uint32_t((warp & 3) * 32) << 16;
-    const uint32_t ts = tmem + lanes + P::kColS(g), to = tmem + lanes + P::kColO(g),
-                   tp = tmem + lanes + P::kColP(g);
+    const uint32_t ts = tmem + lanes + P::kColS(g), to = tmem + lanes + P::kColO(g);
     const float mul = a.scale * kLog2e;  // scores to log2 units
     const Cap cap = cap_of(a.softcap);
     // with a small cap to its y
@@ -991,7 +1017,21 @@ __global__ void __launch_bounds__(Plan<D, FP8>::kThreads, 1)
         const uint64_t mul_2 = GEN ? f2(1.f, 1.f) : f2(mul, mul);
         uint64_t sum[2] = {0ull, 0ull};
         const float* vsc = ks + kKeys;
-        uint32_t pk[64];
+        // The weights as high + low bf16 parts.  Over a bf16 cache the high one is cut off
+        // below the weight, so that the low one is above 0 and both take an infinite value to
+        // the same infinity (0 * infinity is NaN); an FP8 cache has none, and its weights
+        // times scales may be below 0.
+        constexpr int kChunk = P::kChunk;
+        uint32_t pk[kChunk];  // high parts, low parts
+        auto split = [&](int at, float x, float y) {
+          const uint64_t z = f2(x, y);
+          float a, b;
+          un2(FP8 ? z : mul2(z, f2(kBelowOne, kBelowOne)), a, b);
+          const uint32_t ha = __float_as_uint(a) & 0xffff0000u, hb = __float_as_uint(b) & 0xffff0000u;
+          pk[at] = __byte_perm(ha, hb, 0x7632);
+          un2(fma2(f2(ha, hb), f2(-1.f, -1.f), z), a, b);
+          pk[kChunk / 2 + at] = bf16x2(a, b);
+        };
 #pragma unroll
         for (int e = 0; e < 128; e += 4) {
           float z[4];
@@ -1006,27 +1046,33 @@ __global__ void __launch_bounds__(Plan<D, FP8>::kThreads, 1)
             un2(mul2(f2(z[0], z[1]), f2(v.x, v.y)), z[0], z[1]);
             un2(mul2(f2(z[2], z[3]), f2(v.z, v.w)), z[2], z[3]);
           }
-          pk[e / 2] = bf16x2(z[0], z[1]);
-          pk[e / 2 + 1] = bf16x2(z[2], z[3]);
-        }
-        if constexpr (P::kOwnP) {  // the weights before these are read
-          if (!seen_o) {
-            ok = __all_sync(kAll, i == 0 || wait(&o_done[g], (my - 1) & 1u, quit, a.err));
+          split(e % kChunk / 2, z[0], z[1]);
+          split(e % kChunk / 2 + 1, z[2], z[3]);
+          if ((e + 4) % kChunk != 0) continue;
+          if constexpr (P::kOwnP) {  // the weights before these are read
+            if (e >= P::kPass) {
+              ok = __all_sync(kAll, wait(&half_done[g], my & 1u, quit, a.err));
+            } else {
+              ok = __all_sync(kAll, i == 0 || seen_o || wait(&o_done[g], (my - 1) & 1u, quit, a.err));
+              if (ok && i > 0 && r == 0) mbar_arrive(smem_u32(&freed[g * kAhead + (my - 1) % kAhead]));
+            }
             if (!ok) break;
             fence_after();
           }
-          if (i > 0 && r == 0) mbar_arrive(smem_u32(&freed[g * kAhead + (my - 1) % kAhead]));
+          __syncwarp();
+          tmem_put(tmem + lanes + P::kColP(g, e / P::kPass) + e % P::kPass / kChunk * kChunk, pk);
+          if ((e + 4) % P::kPass == 0) {
+            wait_st();
+            fence_before();
+            mbar_arrive(smem_u32(&p_full[e / P::kPass * 2 + g]));
+          }
         }
-        __syncwarp();
-        tmem_st64(tp, pk);
+        if (!ok) break;
         {
           float s0, s1;
           un2(add2(sum[0], sum[1]), s0, s1);
           l += s0 + s1;
         }
-        wait_st();
-        fence_before();
-        mbar_arrive(smem_u32(&p_full[g]));
       }
       if (!ok) break;
 
