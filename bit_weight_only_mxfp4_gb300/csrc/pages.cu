@@ -9,13 +9,14 @@
 // Plan, one CTA: the table's entries set bits (of shared memory, or of the
 // workspace where the pool has more pages than that holds), a scan over the words
 // gives every free page its number, a scan over the sequences says who gets
-// which.  Copy, all SMs: a warp per (page, layer, k or v, kv head) moves the
+// which.  A fork marks the pages that sequences end inside of last: one that is marked
+// by then is named elsewhere, and nobody may go on in it.  Copy, all SMs: a warp per (page, layer, k or v, kv head) moves the
 // rows, 16 bytes a lane.  The plan is latency (a few scans and round trips; the
 // table streams through one SM), the copy is bytes.
 //
 // Measured (back to back in a graph).  Fork and resize: 4 beams of up to 1000 tokens, 36
-// layers of 4 kv heads of 128, 9.4 us; 128 sequences, 24 layers of 8 kv heads of 64 in
-// FP8, 71 MB read and written, 26.5 us (single launches from cold caches: the copy 13.7, a
+// layers of 4 kv heads of 128, 9.8 us; 128 sequences, 24 layers of 8 kv heads of 64 in
+// FP8, 71 MB read and written, 26.7 us (single launches from cold caches: the copy 13.7, a
 // plan 8.5).  Compaction: 2.5 GB read and written in 402 us (6.2 TB/s, 0.92 of the rate of
 // a copy).
 #include "launch.h"
@@ -216,12 +217,43 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
+// A page that some sequences would end inside of and write on: whose it is.  The first of
+// these that stays, else the first one, may keep it, unless another entry of the new table
+// names it.  What is kept is marked.  `page`: the one that this thread's sequence ends
+// inside of, or -1; `first`: it is the first of those that come from one source; ends, sources
+// [batch].  The other entries' pages are marked.  By all threads.
+struct Shared {
+  int twice[kPagedMaxBatch];  // pages that first ones of several sources end inside of
+  int count;
+};
+__device__ __forceinline__ bool keeps_page(uint32_t* bits, int page, bool first, int* ends,
+                                           const int* sources, int batch, Shared& s) {
+  const int tid = threadIdx.x;
+  const uint32_t bit = 1u << (page & 31);
+  bool keeps = first && page >= 0;
+  if (tid < batch) ends[tid] = keeps ? page : -1;
+  if (tid == 0) s.count = 0;
+  if (keeps) keeps = !(bits[page >> 5] & bit);
+  __syncthreads();
+  if (keeps && (atomicOr(bits + (page >> 5), bit) & bit)) s.twice[atomicAdd(&s.count, 1)] = page;
+  __syncthreads();
+  bool more = false;
+  for (int i = 0; keeps && i < s.count; ++i) more |= s.twice[i] == page;
+  const bool stays = more && sources[tid] == tid;
+  for (int i = 0; more && i < batch; ++i) {
+    const bool other = sources[i] == i;
+    if (ends[i] == page && (other != stays ? other : i < tid)) keeps = false;
+  }
+  return keeps;
+}
+
 __global__ void __launch_bounds__(kThreads, 1)
     fork_kernel(const PagedKv kv, const int32_t* from, const uint8_t* held, int32_t* table_out,
                 int32_t* lens_out, int32_t* left, Space ws, bool shared, int32_t* err) {
   __shared__ int part[kWarps + 1];
   __shared__ int owner[kPagedMaxBatch], source[kPagedMaxBatch], upto[kPagedMaxBatch];
-  __shared__ int tail[kPagedMaxBatch];
+  __shared__ int tail[kPagedMaxBatch], ends[kPagedMaxBatch];
+  __shared__ Shared s_shared;
   uint32_t* bits = shared ? s_bits : ws.bits;
   const int tid = threadIdx.x, W = kv.pages_per_seq, page = 1 << kv.page_shift;
   pdl_allow_next_grid();
@@ -238,24 +270,21 @@ __global__ void __launch_bounds__(kThreads, 1)
     owner[tid] = kPagedMaxBatch;
   }
   __syncthreads();
-  // who has a source's last page: the source if it stays, else its first copy
+  // who comes first of a source's: the source if it stays, else its first copy
   if (src >= 0) atomicMin(&owner[src], src == tid ? -1 : tid);
-  __syncthreads();
-  bool copies = false;
-  int old = -1;  // the page that is copied
+  int old = -1;  // the page that the sequence ends inside of
   if (tid < kv.batch) {
     const int last = len >> kv.page_shift;
-    copies = src >= 0 && src != tid && owner[src] != tid && (len & (page - 1)) != 0;
-    if (copies) {
+    if (src >= 0 && (len & (page - 1)) != 0) {
       old = __ldcg(kv.page_table + int64_t(src) * W + last);
-      copies = old >= 0 && old < kv.num_pages;
+      if (old >= kv.num_pages) old = -1;
     }
     source[tid] = src;
     upto[tid] = src < 0 ? 0 : src == tid ? W : (len + page - 1) >> kv.page_shift;
-    tail[tid] = copies ? last : -1;
-    lens_out[tid] = len;
+    tail[tid] = old >= 0 ? last : -1;
   }
   __syncthreads();
+  if (tid < kv.batch) lens_out[tid] = len;
   int32_t* rows = table_out == kv.page_table ? ws.rows : table_out;
   const Team t = team_of(kv.batch);
   for (int b = t.row; b < kv.batch; b += t.rows) {
@@ -278,9 +307,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   }
   __syncthreads();
+  const bool first = src >= 0 && owner[src] == (src == tid ? -1 : tid);
+  const bool keeps = keeps_page(bits, old, first, ends, source, kv.batch, s_shared);
+  const bool copies = old >= 0 && !keeps;
   int all;
   const int at = scan(copies ? 1 : 0, part, all);
   const int have = free_pages(bits, held, kv.num_pages, all, ws.list, part);
+  if (keeps) rows[int64_t(tid) * W + tail[tid]] = old;
   if (copies && at < have) {
     const int to = ws.list[at];
     rows[int64_t(tid) * W + tail[tid]] = to;

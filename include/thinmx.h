@@ -630,7 +630,8 @@ tt_status tt_paged_keep(const tt_paged_kv* layers, int32_t n_layers, const int32
 
 /* Pages.  A page is in use if the table names it (however often: sequences
  * may share pages) or held[page] != 0 (uint8 [num_pages] or NULL: pages that
- * others have).  Free pages are taken lowest first.  left int32 [1] or NULL:
+ * others have; they are not taken, but a sequence that ends inside one writes on
+ * there, so that its holder may count on the rows below that length only).  Free pages are taken lowest first.  left int32 [1] or NULL:
  * the free pages after the call, or, where they did not suffice, minus the
  * number that were missing: those entries stay holes and TT_ERR_SIZE is
  * reported in the device error word.  workspace: device, >=
@@ -652,11 +653,15 @@ tt_status tt_paged_resize(const tt_paged_kv* kv, const int32_t* want, const uint
 /* tt_paged_fork: sequence b becomes what sequence from[b] was before the call
  * (int32 [batch]); from[b] == b: it stays, with all its entries; from[b] < 0: it
  * ends (no pages, length 0).  A copy names the pages of the sequence's length;
- * its whole pages are shared.  Of a last page that is not full the first
- * copy takes over the page if the sequence does not stay itself, and every
- * other copy takes a free page (in order of b; pages that this call lets go are
- * free), into which the rows are copied in every layer.  from[b] >= batch
- * is reported as TT_ERR_SHAPE in the device error word and the sequence stays. */
+ * its whole pages are shared.  A last page that is not full is one sequence's,
+ * which will write its further rows: the first that stays with it keeps it, else
+ * the first that came to it as a copy; but nobody does if the new table names it
+ * elsewhere, too (another sequence's page below its length, or past it).  Every
+ * other sequence that ends in it, one that stays or a copy, takes a free page (in
+ * order of b; pages that this call lets go are free), into which the rows are
+ * copied in every layer.  So from[b] == b for all gives sequences that share more
+ * than whole pages pages of their own.  from[b] >= batch is reported as
+ * TT_ERR_SHAPE in the device error word and the sequence stays. */
 tt_status tt_paged_fork(const tt_paged_kv* layers, int32_t n_layers, const int32_t* from,
                         const uint8_t* held, int32_t* table_out, int32_t* lens_out,
                         int32_t* left, void* workspace, size_t workspace_bytes, void* stream);
