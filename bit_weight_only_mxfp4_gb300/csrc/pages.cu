@@ -15,8 +15,8 @@
 // table streams through one SM), the copy is bytes.
 //
 // Measured (back to back in a graph).  Fork and resize: 4 beams of up to 1000 tokens, 36
-// layers of 4 kv heads of 128, 9.8 us; 128 sequences, 24 layers of 8 kv heads of 64 in
-// FP8, 71 MB read and written, 26.7 us (single launches from cold caches: the copy 13.7, a
+// layers of 4 kv heads of 128, 10.2 us; 128 sequences, 24 layers of 8 kv heads of 64 in
+// FP8, 71 MB read and written, 27.5 us (single launches from cold caches: the copy 13.7, a
 // plan 8.5).  Compaction: 2.5 GB read and written in 402 us (6.2 TB/s, 0.92 of the rate of
 // a copy).
 #include "launch.h"
@@ -137,6 +137,48 @@ __device__ __forceinline__ Team team_of(int batch) {
   return {warp / team, kWarps / team, (warp % team) * 32 + int(threadIdx.x & 31), team * 32};
 }
 
+// Pages that sequences end inside of and would write on.  The other entries' pages are
+// marked; these are marked here, and those of several threads listed in `twice` (room for
+// one a thread).  Whether `page` (of this thread; -1: none) was marked before.  By all
+// threads.
+__device__ __forceinline__ bool named_before(uint32_t* bits, int page, int* twice, int* count) {
+  const uint32_t bit = 1u << (page & 31);
+  if (threadIdx.x == 0) *count = 0;
+  const bool named = page >= 0 && (bits[page >> 5] & bit);
+  __syncthreads();
+  if (page >= 0 && !named && (atomicOr(bits + (page >> 5), bit) & bit))
+    twice[atomicAdd(count, 1)] = page;
+  __syncthreads();
+  return named;
+}
+__device__ __forceinline__ bool is_twice(int page, const int* twice, const int* count) {
+  bool more = false;
+  for (int i = 0; i < *count; ++i) more |= twice[i] == page;
+  return more;
+}
+// Whether another entry names the thread's page.
+__device__ __forceinline__ bool shares_page(uint32_t* bits, int page, int* twice, int* count) {
+  return named_before(bits, page, twice, count) || (page >= 0 && is_twice(page, twice, count));
+}
+// Whether the thread's sequence keeps its page: the first one of those that stay, else the
+// first one, unless another entry names it.  `first`: it is the first of those that come
+// from one source; ends, sources [batch].
+__device__ __forceinline__ bool keeps_page(uint32_t* bits, int page, bool first, int* ends,
+                                           const int* sources, int batch, int* twice, int* count) {
+  const int tid = threadIdx.x;
+  if (!first) page = -1;
+  if (tid < batch) ends[tid] = page;
+  bool keeps = !named_before(bits, page, twice, count) && page >= 0;
+  if (keeps && is_twice(page, twice, count)) {
+    const bool stays = sources[tid] == tid;
+    for (int i = 0; i < batch; ++i) {
+      const bool other = sources[i] == i;
+      if (ends[i] == page && (other != stays ? other : i < tid)) keeps = false;
+    }
+  }
+  return keeps;
+}
+
 extern __shared__ uint32_t s_bits[];
 
 __global__ void __launch_bounds__(kThreads, 1)
@@ -144,11 +186,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                   int32_t* lens_out, int32_t* left, Space ws, bool shared, int32_t* err) {
   __shared__ int part[kWarps + 1];
   __shared__ int count[kPagedMaxBatch], from[kPagedMaxBatch], upto[kPagedMaxBatch];
+  __shared__ int s_twice;
   uint32_t* bits = shared ? s_bits : ws.bits;
   const int tid = threadIdx.x, lane = tid & 31, W = kv.pages_per_seq, page = 1 << kv.page_shift;
   pdl_allow_next_grid();
   pdl_wait_prior_grid();
   clear(bits, kv.num_pages);
+  int cut_page = -1;
   if (tid < kv.batch) {
     int w = __ldcg(want + tid);
     const int len = paged_len(kv, tid, err);
@@ -160,8 +204,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     from[tid] = w < 0 ? W : (len + page - 1) >> kv.page_shift;
     upto[tid] = w < 0 ? W : (w + page - 1) >> kv.page_shift;
     lens_out[tid] = w < 0 || w > len ? len : w;
+    if (w >= 0 && w < len && (w & (page - 1)) != 0) {
+      cut_page = __ldcg(kv.page_table + int64_t(tid) * W + (w >> kv.page_shift));
+      if (cut_page >= kv.num_pages) cut_page = -1;
+    }
+    if (cut_page >= 0) from[tid] = W + 1;  // (no entry is taken)
   }
-  __syncthreads();
+  const bool cuts = __syncthreads_or(cut_page >= 0);
   const Team t = team_of(kv.batch);
   for (int b = t.row; b < kv.batch; b += t.rows) {
     const int64_t row = int64_t(b) * W;
@@ -192,6 +241,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lane == 0 && missing) atomicAdd(&count[b], missing);
   }
   __syncthreads();
+  if (cuts) {  // the marks again, but for the pages that sequences are cut inside of
+    clear(bits, kv.num_pages);
+    __syncthreads();
+    for (int b = t.row; b < kv.batch; b += t.rows)
+      for (int e = t.lane; e < upto[b]; e += t.lanes)
+        if (from[b] <= W || e + 1 < upto[b])
+          mark(bits, table_out[int64_t(b) * W + e], kv.num_pages, nullptr);
+    __syncthreads();
+    if (shares_page(bits, cut_page, reinterpret_cast<int*>(ws.copies), &s_twice))
+      flag_error(err, kErrSize);
+  }
   int all;
   const int mine = tid < kv.batch ? count[tid] : 0;
   const int before = scan(mine, part, all);
@@ -217,43 +277,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-// A page that some sequences would end inside of and write on: whose it is.  The first of
-// these that stays, else the first one, may keep it, unless another entry of the new table
-// names it.  What is kept is marked.  `page`: the one that this thread's sequence ends
-// inside of, or -1; `first`: it is the first of those that come from one source; ends, sources
-// [batch].  The other entries' pages are marked.  By all threads.
-struct Shared {
-  int twice[kPagedMaxBatch];  // pages that first ones of several sources end inside of
-  int count;
-};
-__device__ __forceinline__ bool keeps_page(uint32_t* bits, int page, bool first, int* ends,
-                                           const int* sources, int batch, Shared& s) {
-  const int tid = threadIdx.x;
-  const uint32_t bit = 1u << (page & 31);
-  bool keeps = first && page >= 0;
-  if (tid < batch) ends[tid] = keeps ? page : -1;
-  if (tid == 0) s.count = 0;
-  if (keeps) keeps = !(bits[page >> 5] & bit);
-  __syncthreads();
-  if (keeps && (atomicOr(bits + (page >> 5), bit) & bit)) s.twice[atomicAdd(&s.count, 1)] = page;
-  __syncthreads();
-  bool more = false;
-  for (int i = 0; keeps && i < s.count; ++i) more |= s.twice[i] == page;
-  const bool stays = more && sources[tid] == tid;
-  for (int i = 0; more && i < batch; ++i) {
-    const bool other = sources[i] == i;
-    if (ends[i] == page && (other != stays ? other : i < tid)) keeps = false;
-  }
-  return keeps;
-}
-
 __global__ void __launch_bounds__(kThreads, 1)
     fork_kernel(const PagedKv kv, const int32_t* from, const uint8_t* held, int32_t* table_out,
                 int32_t* lens_out, int32_t* left, Space ws, bool shared, int32_t* err) {
   __shared__ int part[kWarps + 1];
   __shared__ int owner[kPagedMaxBatch], source[kPagedMaxBatch], upto[kPagedMaxBatch];
-  __shared__ int tail[kPagedMaxBatch], ends[kPagedMaxBatch];
-  __shared__ Shared s_shared;
+  __shared__ int tail[kPagedMaxBatch];
+  __shared__ int s_twice;
   uint32_t* bits = shared ? s_bits : ws.bits;
   const int tid = threadIdx.x, W = kv.pages_per_seq, page = 1 << kv.page_shift;
   pdl_allow_next_grid();
@@ -308,7 +338,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   __syncthreads();
   const bool first = src >= 0 && owner[src] == (src == tid ? -1 : tid);
-  const bool keeps = keeps_page(bits, old, first, ends, source, kv.batch, s_shared);
+  const bool keeps = keeps_page(bits, old, first, upto, source, kv.batch,
+                                reinterpret_cast<int*>(ws.copies), &s_twice);
   const bool copies = old >= 0 && !keeps;
   int all;
   const int at = scan(copies ? 1 : 0, part, all);

@@ -644,7 +644,12 @@ tt_status tt_paged_keep(const tt_paged_kv* layers, int32_t n_layers, const int32
  * ones from ceil(lens[b] / page_size) up to there take free pages, in order of
  * sequences and entries.  lens_out[b] = min(lens[b], want[b]).  want[b] < 0: the
  * sequence stays as it is; a want past the table is reported as TT_ERR_SHAPE and
- * clamped.  Holes below the length stay holes. */
+ * clamped.  Holes below the length stay holes.
+ * A cut (want[b] < lens[b]) that ends inside a page which the new table names
+ * elsewhere, too, would have two sequences write its rows: it is made, and reported
+ * as TT_ERR_SIZE, since the sequence lacks a page of its own; before its next append
+ * tt_paged_fork (from[b] = b) has to give it one.  Lengths are cut by this call
+ * alone: it lets the entries past them go. */
 size_t tt_paged_pages_workspace_bytes(const tt_paged_kv* kv);
 tt_status tt_paged_resize(const tt_paged_kv* kv, const int32_t* want, const uint8_t* held,
                           int32_t* table_out, int32_t* lens_out, int32_t* left, void* workspace,
