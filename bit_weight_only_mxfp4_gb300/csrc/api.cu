@@ -90,6 +90,8 @@ inline cudaStream_t as_stream(void* s) { return static_cast<cudaStream_t>(s); }
 constexpr int64_t kMaxRows = (int64_t(1) << 31) - 1;
 constexpr int64_t kMaxK = 16384;
 constexpr int64_t kMaxVocab = int64_t(1) << 30;
+// nodes and places that a kernel walks in strides of up to 256, in 32 bits
+constexpr int64_t kMaxWalk = (int64_t(1) << 31) - 4096;
 constexpr int64_t kTcMinBatch = 4;  // smallest m sent to the tensor-core path
 constexpr int64_t kMoeMaxHidden = 8192;
 static_assert(TT_MOE_STATIC_MAX_HIDDEN == tt::kMoeStaticMaxHidden,
@@ -649,7 +651,8 @@ tt_status tt_draft_accept(const int32_t* parents, const int32_t* drafts, const i
                           int32_t path_width, int32_t* path, int32_t* counts, int32_t* next,
                           void* stream) {
   if (batch < 1 || tokens < 0 || tokens > kMaxRows || path_width < 1) return TT_ERR_SHAPE;
-  if (batch > tt::kPagedMaxBatch) return TT_ERR_UNSUPPORTED;
+  if (batch > tt::kPagedMaxBatch || tokens > kMaxWalk || path_width > kMaxWalk)
+    return TT_ERR_UNSUPPORTED;
   if (!q_starts || !path || !counts || !next) return TT_ERR_NULL;
   if (tokens > 0 && (!parents || !drafts || !chosen)) return TT_ERR_NULL;
   if (!aligned(parents, 4) || !aligned(drafts, 4) || !aligned(chosen, 4) || !aligned(q_starts, 4) ||
@@ -667,6 +670,7 @@ tt_status tt_paged_keep(const tt_paged_kv* layers, int32_t n_layers, const int32
   tt::PagedPools pools;
   if (tt_status st = check_paged_layers(layers, n_layers, &c, &pools)) return st;
   if (path_width < 1) return TT_ERR_SHAPE;
+  if (path_width > kMaxWalk) return TT_ERR_UNSUPPORTED;
   if (!q_starts || !path || !counts || !lens_out) return TT_ERR_NULL;
   if (!aligned(q_starts, 4) || !aligned(path, 4) || !aligned(counts, 4) || !aligned(lens_out, 4))
     return TT_ERR_ALIGN;

@@ -599,7 +599,8 @@ tt_status tt_paged_tree_attention(const tt_paged_kv* kv, const uint16_t* q, int6
  *   counts int32 [batch] = how many (0 for a sequence without new tokens; the
  *   walk ends when the path is full);
  *   next int32 [batch] = chosen of the last of them (-1 without one).
- * Requires batch <= 1024, path_width >= 1, tokens >= 0. */
+ * Requires batch <= 1024, path_width >= 1, tokens >= 0, and at most 2^31 - 4096 of
+ * both (else TT_ERR_UNSUPPORTED). */
 tt_status tt_draft_accept(const int32_t* parents, const int32_t* drafts, const int32_t* chosen,
                           const int32_t* q_starts, int32_t batch, int64_t tokens,
                           int32_t path_width, int32_t* path, int32_t* counts, int32_t* next,
@@ -623,7 +624,8 @@ tt_status tt_draft_accept(const int32_t* parents, const int32_t* drafts, const i
  * not, or counts[b] is not in 0 .. min(n_b, path_width), that is reported as
  * TT_ERR_SHAPE in the device error word and the count ends there.  A move from
  * or to a place without a row (a hole, a negative place) is dropped.  A page
- * that is listed twice makes two tokens share its rows (then either may win). */
+ * that is listed twice makes two tokens share its rows (then either may win).
+ * Requires 1 <= path_width <= 2^31 - 4096 (beyond: TT_ERR_UNSUPPORTED). */
 tt_status tt_paged_keep(const tt_paged_kv* layers, int32_t n_layers, const int32_t* q_starts,
                         const int32_t* path, int32_t path_width, const int32_t* counts,
                         int32_t* lens_out, void* stream);
