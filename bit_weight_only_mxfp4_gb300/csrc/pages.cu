@@ -10,9 +10,9 @@
 // workspace where the pool has more pages than that holds), a scan over the words
 // gives every free page its number, a scan over the sequences says who gets
 // which.  A fork marks the pages that sequences end inside of last: one that is marked
-// by then is named elsewhere, and nobody may go on in it.  Copy, all SMs: a warp per (page, layer, k or v, kv head) moves the
-// rows, 16 bytes a lane.  The plan is latency (a few scans and round trips; the
-// table streams through one SM), the copy is bytes.
+// by then is named elsewhere, and nobody may go on in it.  Copy, all SMs: a warp per
+// (page, layer, k or v, kv head) moves the rows, 16 bytes a lane.  The plan is latency
+// (a few scans and round trips; the table streams through one SM), the copy is bytes.
 //
 // Measured (back to back in a graph).  Fork and resize: 4 beams of up to 1000 tokens, 36
 // layers of 4 kv heads of 128, 10.2 us; 128 sequences, 24 layers of 8 kv heads of 64 in
