@@ -3,8 +3,10 @@
 //   x = scale * logit;  lse = m + log sum e^(x - m)
 //   logp = x[target] - lse;  H = log sum e^(x - m) - sum (x - m) e^(x - m) / sum e^(x - m)
 //
-// One pass over the logits, which are read once: bound by their bytes with 32-bit
-// logits, nearly as much by issue slots with bf16.  A thread
+// One pass over the logits: near their bytes with 32-bit logits.  With bf16 neither the
+// bytes (52% of the DRAM's peak) nor the issue slots (60%) are used up: a warp's loads and
+// its arithmetic take turns, and waiting for a chunk's loads is the largest stall, barriers
+// the next.  A thread
 // keeps a running maximum m of the logits, s = sum 2^y and t = sum y 2^y over its
 // elements, with y = (logit - m) scale log2 e; where y falls by d, s becomes 2^-d s and t
 // becomes 2^-d (t - d s).  The difference comes first: logits of any size and scales of
@@ -21,6 +23,13 @@
 // and 4 chunks (twenty tokens of the rows below: 90.5 -> 74.2 us, 209 -> 181; one or five:
 // 52.8 -> 53.6, 155 -> 157).
 //
+// Where more than kBuffer elements reach the bound before it gets better (a row that
+// rises, or whose first chunk is masked), the part is read again, once for each key:
+// with the first 8192 logits at -infinity, 512 rows of 201088 take 404 us for the best
+// token and 2055 for twenty, where others take 55 and 75; 2047 rows of 100352 in 32 bits 892
+// and 4906 for 143 and 179; rising rows up to 2565 and 5205; one row 11.8 and 81 for 10.2
+// and 12.5.
+//
 // Split.  A row is cut into chunks of 16 KB, the chunks of all rows form one line,
 // and each CTA takes an equal stretch.  A row that lies in several stretches is
 // written in parts, joined by a second kernel.
@@ -31,8 +40,8 @@
 // memory, by bulk copies of 2 KB a warp: 73 / 211, by cp.async: 65 / 187).
 //
 // Measured (back to back in a graph): 512 rows of 201088 in bf16, the best token, 51.8 us
-// (4.0 TB/s; some 44 without any ranking: issue slots); 2047 rows of 100352 in 32 bits, five
-// tokens, 151 us (5.4 TB/s; some 130 without ranking); one row of 128256 in bf16, twenty
+// (4.0 TB/s; 44 without any ranking); 2047 rows of 100352 in 32 bits, five
+// tokens, 151 us (5.4 TB/s; 128 without ranking); one row of 128256 in bf16, twenty
 // tokens, 10.0 us (two launches, a few dependent loads and barriers each).
 #include "launch.h"
 #include "common.cuh"
@@ -687,7 +696,8 @@ cudaError_t launch(const DeviceInfo& di, const LogprobArgs& a, cudaStream_t s, b
 
 template <bool BF16>
 cudaError_t launch(const DeviceInfo& di, const LogprobArgs& a, cudaStream_t s, bool pdl) {
-  // Few rows: chunks of a quarter, so that more SMs have one.
+  // Few rows: chunks of a quarter, so that more SMs have one (one row of 128256: 14.7 us with
+  // whole ones, 10.0).
   if (a.rows * chunks_of(a.vocab, BF16, 4) <= di.sms) return launch<BF16, 1>(di, a, s, pdl);
   return launch<BF16, 4>(di, a, s, pdl);
 }

@@ -37,11 +37,14 @@
 //
 // Measured (back to back in a graph): 8 new tokens on 332, 16 / 4 heads of 128, 16.7 us (a
 // start, one or two tiles, the join); 64 on 32767, 64 / 8 heads of 64, 86.8 us (0.21 of the
-// bf16 rate: S -> softmax -> P V of a row tile; without softmax 68); 32 ragged sequences, up
+// bf16 rate: S -> softmax -> P V of a row tile, 5132 warp instructions, 46% of the issue
+// slots; without softmax 68); 32 ragged sequences, up
 // to 16 on up to 8191, 16 / 4 heads of 128, 69.7 us (3.9 TB/s; without softmax 64.5); 48, up
 // to 24 on up to 12000, 64 / 8 heads of 64 in FP8, 284 us (without conversion 259, without
 // softmax 226, without both 176: four converting and eight softmax warps share the issue
-// slots).  With weights rounded once to bf16 these were 15.1, 59.2, 63.8 and 249.
+// slots, 51% busy, 7543 instructions a tile).  With weights rounded once to bf16 these
+// were 15.1, 59.2, 63.8 and 249; their low parts alone, left out, give 16.5, 81.1, 68.6 and
+// 271 (the rest: two stores and waits for P, and its products twice).
 //
 // Rounding.  Q and K products are exact, sums 32-bit; P is a bf16 high and low part
 // (2^-16 of each weight, as in the decode kernel: a drafted step's output should not
@@ -1275,6 +1278,10 @@ cudaError_t launch_as(const DeviceInfo& di, const PagedKv& kv, const TreeArgs& t
 template <int D, bool FP8>
 cudaError_t launch(const DeviceInfo& di, const PagedKv& kv, const TreeArgs& t, cudaStream_t s,
                    bool pdl) {
+  // A kernel for each, since all of it is done for every score.  The three batches and
+  // contexts above (32 ragged / FP8 / one long): plain 69.5 / 284 / 86.8 us, in the general
+  // kernel 100 / 384 / 132; a cap of 30 in that one 122 / 510 / 171, in the one for large
+  // caps 178 / 768 / 246; a bias 105 / 400 / 137.
   if (t.attn.softcap > kCapSmall) return launch_as<D, FP8, kLargeCap>(di, kv, t, s, pdl);
   if (t.attn.softcap > 0.f || t.attn.slopes || !(t.attn.scale > 0.f))
     return launch_as<D, FP8, kGeneral>(di, kv, t, s, pdl);
